@@ -338,6 +338,146 @@ moe_status moe_router_topk_noalloc(const void *x, int32_t T, int32_t hidden, int
                                    int32_t *topk_ids, float *topk_w, int32_t *key_status,
                                    void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Linear operators with 4-bit weights
+ *
+ * One handle holds one weight matrix, or a gate/up pair, in the 4-bit formats
+ * the routed experts use, for the projections around the MoE layer:
+ *
+ *   act NONE    out = x W^T (+ bias)
+ *   act SWIGLU  out = silu(x Wg^T) * (x Wu^T)     (both products, the activation
+ *   act RELU2   out = max(x Wu^T, 0)^2             and the product in one pass)
+ *
+ * Sums, pre-activations and activations are fp32; out is rounded once.
+ * ------------------------------------------------------------------------- */
+typedef enum moe_qlinear_act {
+  MOE_QLINEAR_SWIGLU = 0,   /* the values of moe_act */
+  MOE_QLINEAR_RELU2 = 1,
+  MOE_QLINEAR_NONE = 2
+} moe_qlinear_act;
+
+typedef struct moe_qlinear_config {
+  int32_t in_features;    /* K: a multiple of group_size (and of 16), 16..65536 */
+  int32_t out_features;   /* N: any width, 1..2^24 */
+  int32_t group_size;     /* affine: 32, 64 or 128; NVFP4: 16; MXFP4: 32 */
+  int32_t weight_format;  /* moe_weight_format (4-bit codes) */
+  int32_t act_dtype;      /* BF16|FP16: x, out and bias */
+  int32_t scale_dtype;    /* BF16|FP16: affine scales and biases (ignored by fp4) */
+  int32_t act;            /* moe_qlinear_act */
+  int32_t has_bias;       /* a bias vector, added after the product (act NONE only) */
+  int32_t max_tokens;     /* largest T a forward call may pass, >= 1 */
+} moe_qlinear_config;
+
+/* Weights, DEVICE pointers owned by the caller (laid out as the experts' of
+ * moe_layer_weights, without the expert axis); create copies them into the
+ * handle's layout, after which they may be freed.
+ *   q [N, K/8] uint32     the codes (SWIGLU: of the up matrix)
+ *   s, b                  affine: [N, K/G] scale_dtype; NVFP4: s [N, K/16]
+ *                         uint8 E4M3, b one fp32 matrix scale; MXFP4: s
+ *                         [N, K/32] uint8 E8M0, b unused
+ *   gate_q, gate_s, gate_b  the gate matrix (SWIGLU only, else NULL)
+ *   bias [N]              act_dtype (has_bias only, else NULL) */
+typedef struct moe_qlinear_weights {
+  const uint32_t *q;
+  const void *s, *b;
+  const uint32_t *gate_q;
+  const void *gate_s, *gate_b;
+  const void *bias;
+} moe_qlinear_weights;
+
+typedef struct moe_qlinear moe_qlinear;
+
+/* Host-only validation (w may be NULL to check the config alone); touches no
+ * device.  MOE_ERR_INVALID_ARG: null cfg, sizes < 1, bad enum values, missing
+ * weights.  MOE_ERR_SHAPE: group_size not of the format, K not a multiple of
+ * it, a gate or a bias given where the config has none.  MOE_ERR_UNSUPPORTED:
+ * fp32 activations or scales, K > 65536, N > 2^24, a bias with an activation. */
+moe_status moe_qlinear_validate(const moe_qlinear_config *cfg, const moe_qlinear_weights *w);
+
+/* Create on the current CUDA device: validates, re-lays the weights out on
+ * `stream` and synchronises it.  On failure everything is freed and *out is
+ * NULL. */
+moe_status moe_qlinear_create(const moe_qlinear_config *cfg, const moe_qlinear_weights *w, void *stream,
+                              moe_qlinear **out);
+
+/* out[T, N] = the operator of x[T, K].  DEVICE pointers on the handle's
+ * device (the call makes it current and restores the caller's); rows of x are
+ * ldx elements apart (ldx >= K, a multiple of 8, x 16-byte aligned), rows of
+ * out ldo elements apart (ldo >= N); x and out must not overlap.  0 <= T <=
+ * max_tokens; T = 0 does nothing.  Asynchronous on `stream`, and may be
+ * captured into a CUDA graph.  Like a layer, a handle has one workspace: its
+ * calls (and replays of graphs that hold them) must not overlap on the GPU. */
+moe_status moe_qlinear_forward(moe_qlinear *h, const void *x, int64_t ldx, int32_t T, void *out, int64_t ldo,
+                               void *stream);
+
+/* Synchronises `stream`, reads and clears the status word: MOE_OK, or
+ * MOE_ERR_TIMEOUT when a bounded device-side wait ran out since the last call. */
+moe_status moe_qlinear_device_status(moe_qlinear *h, void *stream);
+int64_t moe_qlinear_device_bytes(const moe_qlinear *h);          /* weights and workspace */
+int32_t moe_qlinear_last_launch_count(const moe_qlinear *h);     /* kernels of the last forward */
+moe_status moe_qlinear_destroy(moe_qlinear *h);                  /* NULL is a no-op */
+/* Last error of a handle; NULL: of the last failed create or validate on this thread. */
+const char *moe_qlinear_last_error(const moe_qlinear *h);
+
+/* ---------------------------------------------------------------------------
+ * Gated feed-forward block with 16-bit weights, forward and backward
+ *
+ * The shared expert's input half as an operator of its own, for serving and
+ * for training (the weights are the caller's tensors, read as they lie):
+ *
+ *   g = x Wg^T, u = x Wu^T
+ *   act SWIGLU  out = silu(g) * u          act RELU2  out = max(u, 0)^2  (no gate)
+ *
+ * and, for e = the gradient of out, with p = 1 / (1 + exp(-g)):
+ *   SWIGLU  du = e g p,  dg = e u p (1 + g (1 - p));   RELU2  du = 2 e max(u, 0)
+ *   d_x = dg Wg + du Wu,  d_gate_w = dg^T x,  d_up_w = du^T x
+ *
+ * Sums and pre-activations are fp32; outputs and gradients are rounded once
+ * from fp32.  (dg and du are rounded to act_dtype on their way into the
+ * tensor-core products.)
+ * ------------------------------------------------------------------------- */
+typedef struct moe_gated_config {
+  int32_t in_features;    /* K: a multiple of 8, 8..65536 */
+  int32_t out_features;   /* N: a multiple of 8, 8..2^24 */
+  int32_t act;            /* moe_act */
+  int32_t act_dtype;      /* BF16|FP16: every 16-bit tensor */
+  int32_t max_tokens;     /* largest T of a call, >= 1 */
+  int32_t training;       /* 1: the handle has the backward pass's workspace */
+} moe_gated_config;
+
+typedef struct moe_gated moe_gated;
+
+/* MOE_ERR_INVALID_ARG: null cfg, sizes < 1, bad enum values.  MOE_ERR_SHAPE: K
+ * or N not a multiple of 8.  MOE_ERR_UNSUPPORTED: fp32, K > 65536, N > 2^24. */
+moe_status moe_gated_validate(const moe_gated_config *cfg);
+/* Create on the current CUDA device (workspace only: a handle holds no weights). */
+moe_status moe_gated_create(const moe_gated_config *cfg, moe_gated **out);
+
+/* out[T, N] from x[T, K] and gate_w, up_w [N, K] (row-major, contiguous; gate_w
+ * NULL for RELU2).  save_gate, save_up: NULL, or [T, N] fp32 buffers that
+ * receive the pre-activations g and u for the backward pass (both for SWIGLU,
+ * save_up alone for RELU2).  All pointers 16-byte aligned except out; ldx and
+ * ldo as in moe_qlinear_forward.  T = 0 does nothing.  Streams, devices, graphs
+ * and overlap as moe_qlinear_forward. */
+moe_status moe_gated_forward(moe_gated *h, const void *x, int64_t ldx, int32_t T, const void *gate_w, const void *up_w,
+                             void *out, int64_t ldo, float *save_gate, float *save_up, void *stream);
+
+/* The gradients for d_out[T, N] (rows ldd apart): d_x[T, K] (rows lddx apart),
+ * d_gate_w and d_up_w [N, K] contiguous, in act_dtype; each may be NULL when it
+ * is not wanted.  They are overwritten, not added to (T = 0 writes zero weight
+ * gradients).  x, the weights and the saved buffers are those of the forward
+ * call.  d_x must overlap none of the inputs.  MOE_ERR_UNSUPPORTED on a handle
+ * created without training. */
+moe_status moe_gated_backward(moe_gated *h, const void *d_out, int64_t ldd, int32_t T, const void *x, int64_t ldx,
+                              const void *gate_w, const void *up_w, const float *save_gate, const float *save_up,
+                              void *d_x, int64_t lddx, void *d_gate_w, void *d_up_w, void *stream);
+
+moe_status moe_gated_device_status(moe_gated *h, void *stream);
+int64_t moe_gated_device_bytes(const moe_gated *h);
+int32_t moe_gated_last_launch_count(const moe_gated *h);
+moe_status moe_gated_destroy(moe_gated *h);
+const char *moe_gated_last_error(const moe_gated *h);
+
 /* Device allocations currently held by all handles of this process (for leak
  * checks around refused creates). */
 int64_t moe_debug_live_allocations(void);

@@ -9,3 +9,6 @@ from ._capi import (  # noqa: F401
     moe_layer_device_status, moe_layer_forward, moe_layer_forward_ex, moe_layer_forward_host,
     moe_layer_set_path, moe_layer_validate, moe_router_topk_noalloc, torch_act_dtype, upload_arrays, SIGNATURES, LIB_PATH,
 )
+from ._ops import (  # noqa: F401
+    GatedBlock, GatedConfig, GatedGrads, QLinear, QLinearConfig,
+)

@@ -27,6 +27,7 @@ ACT = {"swiglu": 0, "relu2": 1}
 ROUTER = {"softmax": 0, "sigmoid": 1}
 DTYPE = {"bf16": 0, "fp16": 1, "fp32": 2}
 WFMT = {"affine": 0, "nvfp4": 1, "mxfp4": 2}
+QLINEAR_ACT = {"swiglu": 0, "relu2": 1, "none": 2}
 PATH = {"auto": 0, "gemv": 1, "grouped": 2}
 NUM_STAGES = 5
 STAGE_NAMES = ["dense_in", "route", "expert_up", "expert_down", "dense_out"]
@@ -58,6 +59,21 @@ _WEIGHT_FIELDS = ["router_w", "router_bias", "fc1_latent", "fc2_latent", "gate_q
 
 class moe_layer_weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in _WEIGHT_FIELDS]
+
+
+class moe_qlinear_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("in_features", "out_features", "group_size", "weight_format", "act_dtype", "scale_dtype", "act",
+                 "has_bias", "max_tokens")]
+
+
+class moe_qlinear_weights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "s", "b", "gate_q", "gate_s", "gate_b", "bias")]
+
+
+class moe_gated_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("in_features", "out_features", "act", "act_dtype", "max_tokens", "training")]
 
 
 # symbol -> (restype, argtypes)
@@ -93,6 +109,32 @@ SIGNATURES = {
                                                ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
                                                ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                                ctypes.c_void_p]),
+    "moe_qlinear_validate": (ctypes.c_int, [ctypes.POINTER(moe_qlinear_config),
+                                            ctypes.POINTER(moe_qlinear_weights)]),
+    "moe_qlinear_create": (ctypes.c_int, [ctypes.POINTER(moe_qlinear_config),
+                                          ctypes.POINTER(moe_qlinear_weights), ctypes.c_void_p,
+                                          ctypes.POINTER(ctypes.c_void_p)]),
+    "moe_qlinear_forward": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
+                                           ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
+    "moe_qlinear_device_status": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
+    "moe_qlinear_device_bytes": (ctypes.c_int64, [ctypes.c_void_p]),
+    "moe_qlinear_last_launch_count": (ctypes.c_int32, [ctypes.c_void_p]),
+    "moe_qlinear_destroy": (ctypes.c_int, [ctypes.c_void_p]),
+    "moe_qlinear_last_error": (ctypes.c_char_p, [ctypes.c_void_p]),
+    "moe_gated_validate": (ctypes.c_int, [ctypes.POINTER(moe_gated_config)]),
+    "moe_gated_create": (ctypes.c_int, [ctypes.POINTER(moe_gated_config), ctypes.POINTER(ctypes.c_void_p)]),
+    "moe_gated_forward": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
+                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "moe_gated_backward": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
+                                          ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "moe_gated_device_status": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
+    "moe_gated_device_bytes": (ctypes.c_int64, [ctypes.c_void_p]),
+    "moe_gated_last_launch_count": (ctypes.c_int32, [ctypes.c_void_p]),
+    "moe_gated_destroy": (ctypes.c_int, [ctypes.c_void_p]),
+    "moe_gated_last_error": (ctypes.c_char_p, [ctypes.c_void_p]),
     "moe_debug_live_allocations": (ctypes.c_int64, []),
     "moe_debug_fail_allocation": (None, [ctypes.c_int32]),
 }

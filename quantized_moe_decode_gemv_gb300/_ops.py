@@ -1,0 +1,311 @@
+"""Python handles of the operators around the MoE layer (include/moe_layer.h):
+the linear operators with 4-bit weights and the 16-bit gated block.
+
+Argument checks and marshalling; the arithmetic runs in the CUDA library.
+Outputs are allocated on the stream of the call: with ``stream=None`` the
+current one, otherwise the given one, where a consumer on another stream has to
+order itself after the call as after any kernel.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import dataclasses
+from typing import Any, Dict, NamedTuple, Optional, Tuple
+
+from ._capi import (ACT, DTYPE, MOE_OK, QLINEAR_ACT, WFMT, MoEError, load_library, moe_gated_config,
+                    moe_qlinear_config, moe_qlinear_weights, torch_act_dtype)
+
+_INVALID_ARG, _SHAPE = 1, 5
+
+
+def _name_of(table: Dict[str, int], key: str, what: str) -> int:
+    if key not in table:
+        raise MoEError(_INVALID_ARG, f"unknown {what} {key!r} (one of {', '.join(table)})")
+    return table[key]
+
+
+class _Handle:
+    """What the operator handles share: device, streams, status, lifetime."""
+
+    _prefix = ""
+
+    def _fn(self, name: str):
+        return getattr(self._lib, f"{self._prefix}_{name}")
+
+    def _check(self, status: int) -> None:
+        if status != MOE_OK:
+            raise MoEError(status, self._fn("last_error")(self.handle).decode())
+
+    def _rows(self, x, cols: int, what: str, dtype=None) -> Tuple[int, int]:
+        """(pointer, row stride) of a [T, cols] tensor; a single row has no stride."""
+        if x.dim() != 2 or x.shape[1] != cols:
+            raise MoEError(_SHAPE, f"{what} must be [T, {cols}], not {tuple(x.shape)}")
+        if x.dtype != (dtype or self._dtype):
+            raise MoEError(_INVALID_ARG, f"{what} must be {dtype or self._dtype}, not {x.dtype}")
+        if x.device != self.device:
+            raise MoEError(_INVALID_ARG, f"{what} is on {x.device}, the handle on {self.device}")
+        if x.stride(1) != 1 and x.shape[0] and cols > 1:
+            raise MoEError(_INVALID_ARG, f"{what} needs consecutive columns")
+        T = x.shape[0]
+        if T > 1 and x.stride(0) < cols:
+            raise MoEError(_INVALID_ARG, f"{what} has overlapping rows")
+        return x.data_ptr(), (x.stride(0) if T > 1 else cols)
+
+    def _matrix(self, w, rows: int, cols: int, what: str) -> int:
+        if w is None:
+            raise MoEError(_INVALID_ARG, f"{what} is missing")
+        if tuple(w.shape) != (rows, cols):
+            raise MoEError(_SHAPE, f"{what} must be [{rows}, {cols}], not {tuple(w.shape)}")
+        if w.dtype != self._dtype or w.device != self.device or not w.is_contiguous():
+            raise MoEError(_INVALID_ARG, f"{what} must be a contiguous {self._dtype} tensor on {self.device}")
+        return w.data_ptr()
+
+    def _stream(self, stream):
+        """(stream handle, context in which outputs are allocated)."""
+        torch = self._torch
+        if stream is None:
+            return torch.cuda.current_stream(self.device).cuda_stream, contextlib.nullcontext()
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+        return int(stream.cuda_stream), torch.cuda.stream(stream)
+
+    def device_status(self, stream=None) -> int:
+        """Synchronises the stream and returns the status recorded by the kernels since the last call."""
+        return self._fn("device_status")(self.handle, ctypes.c_void_p(self._stream(stream)[0]))
+
+    def device_bytes(self) -> int:
+        return int(self._fn("device_bytes")(self.handle))
+
+    def last_launch_count(self) -> int:
+        return int(self._fn("last_launch_count")(self.handle))
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            handle, self.handle = self.handle, None
+            self._fn("destroy")(handle)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ---------------------------------------------------------------------------
+# linear operators with 4-bit weights
+# ---------------------------------------------------------------------------
+
+@dataclasses.dataclass
+class QLinearConfig:
+    """Mirror of ``moe_qlinear_config``."""
+    in_features: int
+    out_features: int
+    fmt: str = "affine"          # "affine", "nvfp4" or "mxfp4"
+    group_size: int = 64
+    act_dtype: str = "bf16"
+    scale_dtype: str = "bf16"
+    act: str = "none"            # "none", "swiglu" or "relu2"
+    bias: bool = False
+    max_tokens: int = 16
+
+    def to_c(self) -> moe_qlinear_config:
+        return moe_qlinear_config(
+            in_features=self.in_features, out_features=self.out_features, group_size=self.group_size,
+            weight_format=_name_of(WFMT, self.fmt, "fmt"), act_dtype=_name_of(DTYPE, self.act_dtype, "act_dtype"),
+            scale_dtype=_name_of(DTYPE, self.scale_dtype, "scale_dtype"), act=_name_of(QLINEAR_ACT, self.act, "act"),
+            has_bias=int(bool(self.bias)), max_tokens=self.max_tokens)
+
+
+class QLinear(_Handle):
+    """``out = x W^T (+ bias)``, ``silu(x Wg^T) * (x W^T)`` or ``max(x W^T, 0)^2`` with 4-bit weights.
+
+    ``weights``: device tensors by C field name -- ``q`` int32 [N, K/8], ``s``,
+    ``b`` (affine: scale dtype [N, K/G]; nvfp4: uint8 [N, K/16] and fp32 [1];
+    mxfp4: uint8 [N, K/32] and None), ``gate_q``, ``gate_s``, ``gate_b`` for
+    "swiglu", ``bias`` [N].  They are copied and may be freed afterwards.
+    """
+
+    _prefix = "moe_qlinear"
+
+    def __init__(self, config: QLinearConfig, weights: Dict[str, Any], stream=None):
+        import torch
+        self._torch, self._lib, self.handle = torch, load_library(), None
+        self.config = config
+        c = config.to_c()
+        w = {n: weights.get(n) for n, _ in moe_qlinear_weights._fields_}
+        unknown = set(weights) - set(w)
+        if unknown:
+            raise MoEError(_INVALID_ARG, f"unknown weights {sorted(unknown)}")
+        cw = moe_qlinear_weights(**{n: (None if t is None else t.data_ptr()) for n, t in w.items()})
+        status = self._fn("validate")(ctypes.byref(c), ctypes.byref(cw))
+        if status != MOE_OK:
+            raise MoEError(status, self._fn("last_error")(None).decode())
+        self._check_weights(w)
+        self.device = w["q"].device
+        self._dtype = torch_act_dtype(config.act_dtype)
+        h = ctypes.c_void_p()
+        with torch.cuda.device(self.device):
+            status = self._fn("create")(ctypes.byref(c), ctypes.byref(cw), ctypes.c_void_p(self._stream(stream)[0]),
+                                        ctypes.byref(h))
+        if status != MOE_OK:
+            raise MoEError(status, self._fn("last_error")(None).decode())
+        self.handle = h.value
+
+    def _check_weights(self, w) -> None:
+        torch, c = self._torch, self.config
+        N, K, G = c.out_features, c.in_features, c.group_size
+        words = (torch.int32, torch.uint32)
+        if c.fmt == "affine":
+            sdt = (torch_act_dtype(c.scale_dtype),)
+            form = {"q": ((N, K // 8), words), "s": ((N, K // G), sdt), "b": ((N, K // G), sdt)}
+        else:
+            form = {"q": ((N, K // 8), words), "s": ((N, K // G), (torch.uint8,)),
+                    "b": ((1,), (torch.float32,)) if c.fmt == "nvfp4" else None}
+        if c.act == "swiglu":
+            form.update({"gate_" + n: f for n, f in list(form.items())})
+        if c.bias:
+            form["bias"] = ((N,), (torch_act_dtype(c.act_dtype),))
+        device = w["q"].device
+        for n, f in form.items():
+            t = w[n]
+            if f is None or t is None:
+                continue
+            if tuple(t.shape) != f[0] or t.dtype not in f[1]:
+                raise MoEError(_SHAPE, f"{n} must be {f[1][0]} {list(f[0])}, not {t.dtype} {list(t.shape)}")
+            if t.device != device or not t.is_cuda or not t.is_contiguous():
+                raise MoEError(_INVALID_ARG, f"{n} must be contiguous and on one CUDA device")
+
+    def forward(self, x, out=None, stream=None):
+        """out [T, N] of x [T, K] (rows may be strided); ``out`` may be given, rows strided too."""
+        K, N = self.config.in_features, self.config.out_features
+        px, ldx = self._rows(x, K, "x")
+        s, where = self._stream(stream)
+        if out is None:
+            with where:
+                out = self._torch.empty((x.shape[0], N), dtype=self._dtype, device=self.device)
+        elif out.shape[0] != x.shape[0]:
+            raise MoEError(_SHAPE, f"out has {out.shape[0]} rows, x {x.shape[0]}")
+        po, ldo = self._rows(out, N, "out")
+        self._check(self._lib.moe_qlinear_forward(self.handle, px, ldx, x.shape[0], po, ldo, s))
+        return out
+
+    __call__ = forward
+
+
+# ---------------------------------------------------------------------------
+# gated block with 16-bit weights
+# ---------------------------------------------------------------------------
+
+@dataclasses.dataclass
+class GatedConfig:
+    """Mirror of ``moe_gated_config``."""
+    in_features: int
+    out_features: int
+    act: str = "swiglu"          # "swiglu" or "relu2" (no gate matrix)
+    act_dtype: str = "bf16"
+    max_tokens: int = 16
+    training: bool = False
+
+    def to_c(self) -> moe_gated_config:
+        return moe_gated_config(
+            in_features=self.in_features, out_features=self.out_features, act=_name_of(ACT, self.act, "act"),
+            act_dtype=_name_of(DTYPE, self.act_dtype, "act_dtype"), max_tokens=self.max_tokens,
+            training=int(bool(self.training)))
+
+
+class GatedGrads(NamedTuple):
+    """Gradients of one backward call (None where not asked for, or no gate)."""
+    x: Any
+    gate_w: Any
+    up_w: Any
+
+
+class GatedBlock(_Handle):
+    """``silu(x Wg^T) * (x Wu^T)`` or ``max(x Wu^T, 0)^2`` over the caller's 16-bit weights, and its backward pass."""
+
+    _prefix = "moe_gated"
+
+    def __init__(self, config: GatedConfig, device=None):
+        import torch
+        self._torch, self._lib, self.handle = torch, load_library(), None
+        self.config = config
+        c = config.to_c()
+        status = self._fn("validate")(ctypes.byref(c))
+        if status != MOE_OK:
+            raise MoEError(status, self._fn("last_error")(None).decode())
+        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self._dtype = torch_act_dtype(config.act_dtype)
+        h = ctypes.c_void_p()
+        with torch.cuda.device(self.device):
+            status = self._fn("create")(ctypes.byref(c), ctypes.byref(h))
+        if status != MOE_OK:
+            raise MoEError(status, self._fn("last_error")(None).decode())
+        self.handle = h.value
+
+    def _weights(self, up_w, gate_w) -> Tuple[int, Optional[int]]:
+        c = self.config
+        pu = self._matrix(up_w, c.out_features, c.in_features, "up_w")
+        if c.act == "swiglu":
+            return pu, self._matrix(gate_w, c.out_features, c.in_features, "gate_w")
+        if gate_w is not None:
+            raise MoEError(_SHAPE, "a squared-ReLU block takes no gate matrix")
+        return pu, None
+
+    def _forward(self, x, up_w, gate_w, out, stream, save: bool):
+        c, torch = self.config, self._torch
+        px, ldx = self._rows(x, c.in_features, "x")
+        pu, pg = self._weights(up_w, gate_w)
+        s, where = self._stream(stream)
+        T, saved = x.shape[0], (None, None)
+        with where:
+            if out is None:
+                out = torch.empty((T, c.out_features), dtype=self._dtype, device=self.device)
+            elif out.shape[0] != T:
+                raise MoEError(_SHAPE, f"out has {out.shape[0]} rows, x {T}")
+            if save:
+                saved = tuple(torch.empty((T, c.out_features), dtype=torch.float32, device=self.device)
+                              if on else None for on in (pg is not None, True))
+        po, ldo = self._rows(out, c.out_features, "out")
+        ps = [t.data_ptr() if t is not None else None for t in saved]
+        self._check(self._lib.moe_gated_forward(self.handle, px, ldx, T, pg, pu, po, ldo, ps[0], ps[1], s))
+        return out, saved
+
+    def forward(self, x, up_w, gate_w=None, out=None, stream=None):
+        """out [T, N] of x [T, K] (rows may be strided) and up_w, gate_w [N, K]."""
+        return self._forward(x, up_w, gate_w, out, stream, False)[0]
+
+    __call__ = forward
+
+    def forward_train(self, x, up_w, gate_w=None, out=None, stream=None):
+        """(out, saved): ``saved`` are the fp32 pre-activations (gate, up) that ``backward`` takes."""
+        return self._forward(x, up_w, gate_w, out, stream, True)
+
+    def backward(self, d_out, saved, x, up_w, gate_w=None, need=("x", "gate_w", "up_w"), stream=None) -> GatedGrads:
+        """Gradients of the tensors named in ``need`` for the gradient ``d_out`` [T, N] of ``forward_train``'s out."""
+        c, torch = self.config, self._torch
+        if set(need) - set(GatedGrads._fields):
+            raise MoEError(_INVALID_ARG, f"need names {', '.join(GatedGrads._fields)}")
+        pd, ldd = self._rows(d_out, c.out_features, "d_out")
+        px, ldx = self._rows(x, c.in_features, "x")
+        pu, pg = self._weights(up_w, gate_w)
+        T = x.shape[0]
+        if d_out.shape[0] != T:
+            raise MoEError(_SHAPE, f"d_out has {d_out.shape[0]} rows, x {T}")
+        ps = []
+        for t, on in zip(saved, (pg is not None, True)):
+            if on and (t is None or t.dtype != torch.float32 or tuple(t.shape) != (T, c.out_features) or
+                       t.device != self.device or not t.is_contiguous()):
+                raise MoEError(_INVALID_ARG, "saved must be what forward_train returned for x")
+            ps.append(t.data_ptr() if on else None)
+        s, where = self._stream(stream)
+        with where:
+            d_x = torch.empty((T, c.in_features), dtype=self._dtype, device=self.device) if "x" in need else None
+            d_g = torch.empty_like(gate_w) if pg is not None and "gate_w" in need else None
+            d_u = torch.empty_like(up_w) if "up_w" in need else None
+        p = [t.data_ptr() if t is not None else None for t in (d_x, d_g, d_u)]
+        self._check(self._lib.moe_gated_backward(self.handle, pd, ldd, T, px, ldx, pg, pu, ps[0], ps[1], p[0],
+                                                 c.in_features, p[1], p[2], s))
+        return GatedGrads(d_x, d_g, d_u)

@@ -28,7 +28,9 @@ LIB_CHECKS = os.path.join(HERE, "libmoe_gb300_checks.so")
 VARIANTS = [(LIB, BUILD_DIR, []), (LIB_CHECKS, os.path.join(BUILD_DIR, "checks"), ["-DMOE_CHECKS=1"])]
 
 # (source, object name, extra flags)
-SOURCES = [("moe_layer.cu", "moe_layer", []), ("moe_noalloc.cu", "moe_noalloc", [])]
+SOURCES = [("moe_layer.cu", "moe_layer", []), ("moe_noalloc.cu", "moe_noalloc", []),
+           ("moe_qlinear.cu", "moe_qlinear", []), ("moe_gated.cu", "moe_gated", []),
+           ("moe_gemm16.cu", "moe_gemm16", [])]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-warn-spills"]

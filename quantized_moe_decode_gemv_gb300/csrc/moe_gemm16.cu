@@ -1,0 +1,267 @@
+// Host side of k_gemm16: tensor maps, tile and K-split choice, launches; and
+// what the operator handles share (moe_op_host.h).
+#include "moe_gemm16.cuh"
+
+#include <cudaTypedefs.h>   // PFN_cuTensorMapEncodeTiled
+
+#include <algorithm>
+#include <mutex>
+
+#include "moe_op_host.h"
+
+namespace moe_op {
+
+cudaError_t OpHandle::alloc(void** p, size_t n) {
+  *p = nullptr;
+  if (host_alloc_fails()) return cudaErrorMemoryAllocation;
+  const cudaError_t e = cudaMalloc(p, n + 256);
+  if (e == cudaSuccess) {
+    allocs.push_back(*p);
+    bytes += static_cast<int64_t>(n);
+    host_count_allocs(1);
+  }
+  return e;
+}
+
+void OpHandle::free_all() {
+  for (void* p : allocs) {
+    cudaFree(p);
+    host_count_allocs(-1);
+  }
+  allocs.clear();
+  bytes = 0;
+}
+
+moe_status OpHandle::read_status(void* stream) {
+  DeviceScope dev(device);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int v = 0;
+  cudaError_t e = dev.ok ? cudaMemcpyAsync(&v, status, sizeof(v), cudaMemcpyDeviceToHost, s) : cudaErrorInvalidDevice;
+  if (e == cudaSuccess) e = cudaMemsetAsync(status, 0, sizeof(v), s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) {
+    last_error = std::string("status read: ") + cudaGetErrorString(e);
+    return MOE_ERR_CUDA;
+  }
+  return (v & STATUS_TIMEOUT) ? MOE_ERR_TIMEOUT : MOE_OK;
+}
+
+moe_status op_device(int* device, int* num_sms, std::string* why) {
+  int dev = 0, major = 0, minor = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    *why = "no CUDA device";
+    return MOE_ERR_DEVICE;
+  }
+  if (!(major == 10 && minor == 3)) {
+    *why = "device " + std::to_string(dev) + " is not compute capability 10.3";
+    return MOE_ERR_DEVICE;
+  }
+  *device = dev;
+  *num_sms = n;
+  return MOE_OK;
+}
+
+namespace {
+
+using Encoder = PFN_cuTensorMapEncodeTiled_v12000;
+
+Encoder encoder() {
+  static std::once_flag once;
+  static Encoder fn = nullptr;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<Encoder>(p);
+  });
+  return fn;
+}
+
+// A 16-bit matrix of `rows` memory rows of `cols` elements; boxes of 64 columns
+// (128 bytes, swizzled) by box_rows rows.  Elements outside read as zero.
+bool encode(CUtensorMap* m, const void* p, int64_t cols, int64_t rows, int64_t ld, int box_rows) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t unit[2] = {1, 1};
+  return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(p), dims, strides, box, unit,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+using Kernel = void (*)(const GemmArgs);
+
+Kernel kernel_of(int cg, bool a_mn, bool b_mn) {
+  if (cg == 2) {
+    if (a_mn) return k_gemm16<2, true, true>;
+    return b_mn ? k_gemm16<2, false, true> : k_gemm16<2, false, false>;
+  }
+  if (a_mn) return k_gemm16<1, true, true>;
+  return b_mn ? k_gemm16<1, false, true> : k_gemm16<1, false, false>;
+}
+
+constexpr size_t kPartCap = 64ull << 20;   // most bytes of split-K partial sums a handle keeps
+constexpr int kMaxSplit = 16;
+
+struct Choice {
+  int cg, bn, ksplit;
+};
+
+// Tile shape and K split.  The estimate of a launch is its waves over the SMs
+// times a tile's K blocks, each the larger of its MMA time (2 BN clocks a
+// 64-wide block for 128 rows) and its copy time (64 bytes a clock and SM), plus
+// the accumulators' way out.
+Choice choose(const GemmCall& c, int sms, size_t part_bytes) {
+  Choice best{1, 64, 1};
+  double best_t = 1e30;
+  const int nkb = (c.K[0] + 63) / 64 + (c.parts > 1 ? (c.K[1] + 63) / 64 : 0);
+  for (int cg = 1; cg <= 2; ++cg) {
+    if (cg == 2 && c.M <= 128) continue;
+    for (int bn = 64; bn <= 256; bn *= 2) {
+      if (c.b_mn && bn / cg < 64) continue;   // MN-major B comes in 64-column blocks
+      const int bn_out = c.dual ? bn / 2 : bn;
+      const int64_t tiles = static_cast<int64_t>((c.M + cg * 128 - 1) / (cg * 128)) * ((c.N + bn_out - 1) / bn_out) *
+                            c.batches;
+      const int slots = sms / cg;
+      int ks = 1;
+      if (tiles * 2 <= slots) {
+        ks = static_cast<int>(std::min<int64_t>({static_cast<int64_t>(slots / tiles), kMaxSplit, std::max(1, nkb / 4)}));
+        const int64_t ldp = static_cast<int64_t>((c.N + 3) / 4 * 4) * (c.dual ? 2 : 1);
+        while (ks > 1 && static_cast<size_t>(ks) * c.batches * c.M * ldp * 4 > part_bytes) --ks;
+      }
+      const double waves = static_cast<double>((tiles * ks + slots - 1) / slots);
+      const double kb = std::max(2.0 * bn, (16384.0 + bn / cg * 128.0) / 64.0);
+      const double t = waves * ((nkb + ks - 1) / ks) * kb + bn * 8.0 + 1500.0 + (ks > 1 ? 4000.0 : 0.0);
+      if (t < best_t) {
+        best_t = t;
+        best = Choice{cg, bn, ks};
+      }
+    }
+  }
+  return best;
+}
+
+}  // namespace
+
+size_t gemm16_part_bytes(int M, int64_t ld_part) {
+  // a K split is only taken where half of the SMs would idle: at most 76 tiles
+  return std::min<size_t>(kPartCap, static_cast<size_t>(kMaxSplit) * M * ((ld_part + 7) / 4 * 4) * 4);
+}
+
+bool gemm16_setup(std::string* why) {
+  if (!encoder()) {
+    *why = "the driver has no tensor-map encoder";
+    return false;
+  }
+  for (int cg = 1; cg <= 2; ++cg)
+    for (int k = 0; k < 3; ++k) {
+      const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel_of(cg, k == 2, k >= 1)),
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, GM_SMEM_MAX);
+      if (e != cudaSuccess) {
+        *why = std::string("kernel attributes: ") + cudaGetErrorString(e);
+        return false;
+      }
+    }
+  return true;
+}
+
+cudaError_t gemm16_launch(const GemmCall& c, OpHandle& h, cudaStream_t s, int* launches, std::string* why) {
+  if (c.M < 1 || c.N < 1) return cudaSuccess;
+  const Choice ch = choose(c, h.num_sms, h.part_bytes);
+  GemmArgs a{};
+  a.M = c.M;
+  a.N = c.N;
+  a.BN = ch.bn;
+  a.dual = c.dual;
+  a.batches = c.batches;
+  a.parts = c.parts;
+  a.kb[0] = (c.K[0] + 63) / 64;
+  a.kb[1] = c.parts > 1 ? (c.K[1] + 63) / 64 : 0;
+  a.ksplit = ch.ksplit;
+  a.dt = c.dt;
+  a.act = c.act;
+  a.ldo = c.ldo;
+  a.out_vec = c.ldo % 8 == 0;
+  for (int i = 0; i < 2; ++i) {
+    a.out[i] = c.out[i];
+    if (reinterpret_cast<uintptr_t>(c.out[i]) % 16) a.out_vec = 0;
+  }
+  a.save_gate = c.save_gate;
+  a.save_up = c.save_up;
+  a.nscale_gate = c.nscale_gate;
+  a.nscale = c.nscale;
+  a.bias = c.bias;
+  a.status = h.status;
+  a.part = h.part;
+  a.ld_part = static_cast<int64_t>((c.N + 3) / 4 * 4) * (c.dual ? 2 : 1);
+
+  const int na = std::max(c.parts, c.batches), nbm = (c.parts > 1 || c.dual) ? 2 : 1;
+  bool ok = true;
+  for (int i = 0; i < na && ok; ++i) {
+    const int64_t K = c.K[c.parts > 1 ? i : 0];
+    ok = c.a_mn ? encode(&a.ta[i], c.a[i], c.M, K, c.lda, 64) : encode(&a.ta[i], c.a[i], K, c.M, c.lda, 128);
+  }
+  for (int i = 0; i < nbm && ok; ++i) {
+    const int64_t K = c.K[c.parts > 1 ? i : 0];
+    const int box = c.dual ? ch.bn / 2 : ch.bn / ch.cg;
+    ok = c.b_mn ? encode(&a.tb[i], c.b[i], c.N, K, c.ldb, 64) : encode(&a.tb[i], c.b[i], K, c.N, c.ldb, box);
+  }
+  if (!ok) {
+    *why = "tensor map refused (operands need 16-byte aligned bases and row strides)";
+    return cudaErrorInvalidValue;
+  }
+  const int nkb = (a.kb[0] + a.kb[1] + ch.ksplit - 1) / ch.ksplit;
+  a.stages = std::min(GM_MAX_STAGES, std::max(2, nkb + 1));
+  while (gm_smem_bytes(ch.bn, ch.cg, a.stages) > GM_SMEM_MAX) --a.stages;
+  const int bn_out = c.dual ? ch.bn / 2 : ch.bn;
+  const int64_t units = static_cast<int64_t>((c.M + ch.cg * 128 - 1) / (ch.cg * 128)) * ((c.N + bn_out - 1) / bn_out) *
+                        c.batches * ch.ksplit;
+  const int64_t workers = std::min<int64_t>(units, h.num_sms / ch.cg);
+
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(workers * ch.cg));
+  cfg.blockDim = dim3(GM_THREADS);
+  cfg.dynamicSmemBytes = static_cast<size_t>(gm_smem_bytes(ch.bn, ch.cg, a.stages));
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = static_cast<unsigned>(ch.cg);
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel_of(ch.cg, c.a_mn, c.b_mn), a);
+  ++*launches;
+  if (e == cudaSuccess && ch.ksplit > 1) {
+    GemmFinishArgs f{};
+    f.part = a.part;
+    f.ld_part = a.ld_part;
+    f.ksplit = a.ksplit;
+    f.batches = a.batches;
+    f.M = a.M;
+    f.N = a.N;
+    f.dual = a.dual;
+    f.act = a.act;
+    f.dt = a.dt;
+    f.out[0] = a.out[0];
+    f.out[1] = a.out[1];
+    f.ldo = a.ldo;
+    f.save_gate = a.save_gate;
+    f.save_up = a.save_up;
+    f.nscale_gate = a.nscale_gate;
+    f.nscale = a.nscale;
+    f.bias = a.bias;
+    const int64_t n = static_cast<int64_t>(a.batches) * a.M * ((a.N + 3) / 4);
+    k_gemm16_finish<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(f);
+    e = cudaGetLastError();
+    ++*launches;
+  }
+  if (e != cudaSuccess) *why = std::string("launch: ") + cudaGetErrorString(e);
+  return e;
+}
+
+}  // namespace moe_op

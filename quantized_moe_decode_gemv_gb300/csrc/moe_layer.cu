@@ -44,6 +44,12 @@ int dt_size(int dt) { return dt == DT_FP32 ? 4 : 2; }
 
 }  // namespace
 
+// the operator handles' allocations (moe_op_host.h) count and fail as the layers' do
+namespace moe_op {
+bool host_alloc_fails() { return alloc_should_fail(); }
+void host_count_allocs(int delta) { g_live_allocs.fetch_add(delta); }
+}  // namespace moe_op
+
 struct moe_layer {
   moe_layer_config cfg{};
   int device = -1;

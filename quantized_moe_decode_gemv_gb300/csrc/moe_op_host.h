@@ -1,0 +1,98 @@
+// Host side shared by the operator handles (moe_qlinear.cu, moe_gated.cu):
+// tracked allocations, the device a handle lives on, the GEMM launcher.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <string>
+#include <vector>
+
+#include "moe_layer.h"
+
+namespace moe_op {
+
+// Allocation accounting shared with the layer handles (moe_layer.cu): whether
+// the injected failure is due, and the live count of moe_debug_live_allocations.
+bool host_alloc_fails();
+void host_count_allocs(int delta);
+
+// Makes `device` current for a scope.
+struct DeviceScope {
+  int prev = -1;
+  bool ok = true;
+  explicit DeviceScope(int device) {
+    int cur = -1;
+    if (cudaGetDevice(&cur) != cudaSuccess) {
+      ok = false;
+    } else if (cur != device) {
+      prev = cur;
+      ok = cudaSetDevice(device) == cudaSuccess;
+    }
+  }
+  ~DeviceScope() {
+    if (prev >= 0) cudaSetDevice(prev);
+  }
+  DeviceScope(const DeviceScope&) = delete;
+  DeviceScope& operator=(const DeviceScope&) = delete;
+};
+
+// What every operator handle has.
+struct OpHandle {
+  int device = -1;
+  int num_sms = 0;
+  std::vector<void*> allocs;
+  int64_t bytes = 0;
+  std::string last_error;
+  int last_launches = 0;
+  int* status = nullptr;      // device word: STATUS_* bits
+  float* part = nullptr;      // partial sums of products whose K is split
+  size_t part_bytes = 0;
+
+  cudaError_t alloc(void** p, size_t n);
+  void free_all();
+  moe_status read_status(void* stream);
+};
+
+// The current device and its SM count, or MOE_ERR_DEVICE with the reason.
+moe_status op_device(int* device, int* num_sms, std::string* why);
+
+// Whether T rows of ca 16-bit elements lda apart at a meet T rows of cb elements
+// ldb apart at b.  Column ranges of one buffer (equal row strides) may interleave.
+inline bool rows_overlap(const void* a, int64_t lda, int64_t ca, const void* b, int64_t ldb, int64_t cb, int64_t T) {
+  const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
+  if (!x || !y || T < 1) return false;
+  if (x >= y + ((T - 1) * ldb + cb) * 2 || y >= x + ((T - 1) * lda + ca) * 2) return false;
+  if (lda != ldb || T == 1) return true;
+  const int64_t row = lda * 2;
+  const int64_t off = ((y - x) % row + row) % row;   // b's first column, seen from a's rows
+  return off < ca * 2 || off + cb * 2 > row;
+}
+
+struct GemmCall {
+  int M = 0, N = 0;
+  int parts = 1, batches = 1;
+  int K[2] = {0, 0};          // extent of each K part
+  bool dual = false, a_mn = false, b_mn = false;
+  const void* a[2] = {nullptr, nullptr};
+  int64_t lda = 0;            // elements between rows as they lie in memory
+  const void* b[2] = {nullptr, nullptr};
+  int64_t ldb = 0;
+  int dt = 0, act = 2;
+  void* out[2] = {nullptr, nullptr};
+  int64_t ldo = 0;
+  float *save_gate = nullptr, *save_up = nullptr;
+  const float *nscale_gate = nullptr, *nscale = nullptr;
+  const void* bias = nullptr;
+};
+
+// Launches the product on `s` (asynchronous); counts its kernel launches.
+cudaError_t gemm16_launch(const GemmCall& c, OpHandle& h, cudaStream_t s, int* launches, std::string* why);
+// Once per create, with the handle's device current: kernel attributes, the
+// tensor-map encoder; false with the reason.
+bool gemm16_setup(std::string* why);
+// Bytes of OpHandle::part that any product of at most M rows and N partial
+// columns may use.
+size_t gemm16_part_bytes(int M, int64_t ld_part);
+
+}  // namespace moe_op
