@@ -17,6 +17,7 @@ from ._capi import (ACT, DTYPE, MOE_OK, QLINEAR_ACT, WFMT, MoEError, load_librar
                     moe_qlinear_config, moe_qlinear_weights, torch_act_dtype)
 
 _INVALID_ARG, _SHAPE = 1, 5
+_HERE = contextlib.nullcontext()
 
 
 def _name_of(table: Dict[str, int], key: str, what: str) -> int:
@@ -26,49 +27,62 @@ def _name_of(table: Dict[str, int], key: str, what: str) -> int:
 
 
 class _Handle:
-    """What the operator handles share: device, streams, status, lifetime."""
+    """What the operator handles share: device, streams, status, lifetime.
+
+    A decode call's kernel takes a few microseconds, so its wrapper has to stay
+    below that: tensors are checked by plain comparisons, and the current stream
+    is read by torch's raw accessor where there is one.
+    """
 
     _prefix = ""
+
+    def _setup(self, torch, lib):
+        self._torch, self._lib, self.handle = torch, lib, None
+        self._empty = torch.empty
+        self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
     def _fn(self, name: str):
         return getattr(self._lib, f"{self._prefix}_{name}")
 
-    def _check(self, status: int) -> None:
-        if status != MOE_OK:
-            raise MoEError(status, self._fn("last_error")(self.handle).decode())
+    def _fail(self, status: int) -> None:
+        raise MoEError(status, self._fn("last_error")(self.handle).decode())
 
-    def _rows(self, x, cols: int, what: str, dtype=None) -> Tuple[int, int]:
-        """(pointer, row stride) of a [T, cols] tensor; a single row has no stride."""
-        if x.dim() != 2 or x.shape[1] != cols:
-            raise MoEError(_SHAPE, f"{what} must be [T, {cols}], not {tuple(x.shape)}")
-        if x.dtype != (dtype or self._dtype):
-            raise MoEError(_INVALID_ARG, f"{what} must be {dtype or self._dtype}, not {x.dtype}")
+    def _stride(self, x, cols: int, what: str) -> int:
+        """Row stride of a [T, cols] tensor of the handle's type on its device (a single row has none)."""
+        shape = x.shape
+        if len(shape) != 2 or shape[1] != cols:
+            raise MoEError(_SHAPE, f"{what} must be [T, {cols}], not {list(shape)}")
+        if x.dtype is not self._dtype:
+            raise MoEError(_INVALID_ARG, f"{what} must be {self._dtype}, not {x.dtype}")
         if x.device != self.device:
             raise MoEError(_INVALID_ARG, f"{what} is on {x.device}, the handle on {self.device}")
-        if x.stride(1) != 1 and x.shape[0] and cols > 1:
+        row, col = x.stride()
+        if col != 1 and cols > 1 and shape[0]:
             raise MoEError(_INVALID_ARG, f"{what} needs consecutive columns")
-        T = x.shape[0]
-        if T > 1 and x.stride(0) < cols:
+        if shape[0] <= 1:
+            return cols
+        if row < cols:
             raise MoEError(_INVALID_ARG, f"{what} has overlapping rows")
-        return x.data_ptr(), (x.stride(0) if T > 1 else cols)
+        return row
 
     def _matrix(self, w, rows: int, cols: int, what: str) -> int:
         if w is None:
             raise MoEError(_INVALID_ARG, f"{what} is missing")
-        if tuple(w.shape) != (rows, cols):
-            raise MoEError(_SHAPE, f"{what} must be [{rows}, {cols}], not {tuple(w.shape)}")
-        if w.dtype != self._dtype or w.device != self.device or not w.is_contiguous():
+        if w.shape != (rows, cols):
+            raise MoEError(_SHAPE, f"{what} must be [{rows}, {cols}], not {list(w.shape)}")
+        if w.dtype is not self._dtype or w.device != self.device or not w.is_contiguous():
             raise MoEError(_INVALID_ARG, f"{what} must be a contiguous {self._dtype} tensor on {self.device}")
         return w.data_ptr()
 
     def _stream(self, stream):
         """(stream handle, context in which outputs are allocated)."""
-        torch = self._torch
         if stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream, contextlib.nullcontext()
+            if self._raw_stream is not None:
+                return self._raw_stream(self.device.index), _HERE
+            return self._torch.cuda.current_stream(self.device).cuda_stream, _HERE
         if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
-        return int(stream.cuda_stream), torch.cuda.stream(stream)
+            stream = self._torch.cuda.ExternalStream(int(stream), device=self.device)
+        return int(stream.cuda_stream), self._torch.cuda.stream(stream)
 
     def device_status(self, stream=None) -> int:
         """Synchronises the stream and returns the status recorded by the kernels since the last call."""
@@ -130,7 +144,7 @@ class QLinear(_Handle):
 
     def __init__(self, config: QLinearConfig, weights: Dict[str, Any], stream=None):
         import torch
-        self._torch, self._lib, self.handle = torch, load_library(), None
+        self._setup(torch, load_library())
         self.config = config
         c = config.to_c()
         w = {n: weights.get(n) for n, _ in moe_qlinear_weights._fields_}
@@ -151,6 +165,7 @@ class QLinear(_Handle):
         if status != MOE_OK:
             raise MoEError(status, self._fn("last_error")(None).decode())
         self.handle = h.value
+        self._call, self._K, self._N = self._lib.moe_qlinear_forward, config.in_features, config.out_features
 
     def _check_weights(self, w) -> None:
         torch, c = self._torch, self.config
@@ -178,16 +193,23 @@ class QLinear(_Handle):
 
     def forward(self, x, out=None, stream=None):
         """out [T, N] of x [T, K] (rows may be strided); ``out`` may be given, rows strided too."""
-        K, N = self.config.in_features, self.config.out_features
-        px, ldx = self._rows(x, K, "x")
+        ldx = self._stride(x, self._K, "x")
+        T = x.shape[0]
         s, where = self._stream(stream)
         if out is None:
-            with where:
-                out = self._torch.empty((x.shape[0], N), dtype=self._dtype, device=self.device)
-        elif out.shape[0] != x.shape[0]:
-            raise MoEError(_SHAPE, f"out has {out.shape[0]} rows, x {x.shape[0]}")
-        po, ldo = self._rows(out, N, "out")
-        self._check(self._lib.moe_qlinear_forward(self.handle, px, ldx, x.shape[0], po, ldo, s))
+            if stream is None:
+                out = self._empty((T, self._N), dtype=self._dtype, device=self.device)
+            else:
+                with where:
+                    out = self._empty((T, self._N), dtype=self._dtype, device=self.device)
+            ldo = self._N
+        else:
+            ldo = self._stride(out, self._N, "out")
+            if out.shape[0] != T:
+                raise MoEError(_SHAPE, f"out has {out.shape[0]} rows, x {T}")
+        status = self._call(self.handle, x.data_ptr(), ldx, T, out.data_ptr(), ldo, s)
+        if status:
+            self._fail(status)
         return out
 
     __call__ = forward
@@ -228,7 +250,7 @@ class GatedBlock(_Handle):
 
     def __init__(self, config: GatedConfig, device=None):
         import torch
-        self._torch, self._lib, self.handle = torch, load_library(), None
+        self._setup(torch, load_library())
         self.config = config
         c = config.to_c()
         status = self._fn("validate")(ctypes.byref(c))
@@ -255,23 +277,28 @@ class GatedBlock(_Handle):
         return pu, None
 
     def _forward(self, x, up_w, gate_w, out, stream, save: bool):
-        c, torch = self.config, self._torch
-        px, ldx = self._rows(x, c.in_features, "x")
+        N = self.config.out_features
+        ldx = self._stride(x, self.config.in_features, "x")
         pu, pg = self._weights(up_w, gate_w)
         s, where = self._stream(stream)
-        T, saved = x.shape[0], (None, None)
+        T, ldo, g, u = x.shape[0], N, None, None
         with where:
             if out is None:
-                out = torch.empty((T, c.out_features), dtype=self._dtype, device=self.device)
-            elif out.shape[0] != T:
-                raise MoEError(_SHAPE, f"out has {out.shape[0]} rows, x {T}")
+                out = self._empty((T, N), dtype=self._dtype, device=self.device)
+            else:
+                ldo = self._stride(out, N, "out")
+                if out.shape[0] != T:
+                    raise MoEError(_SHAPE, f"out has {out.shape[0]} rows, x {T}")
             if save:
-                saved = tuple(torch.empty((T, c.out_features), dtype=torch.float32, device=self.device)
-                              if on else None for on in (pg is not None, True))
-        po, ldo = self._rows(out, c.out_features, "out")
-        ps = [t.data_ptr() if t is not None else None for t in saved]
-        self._check(self._lib.moe_gated_forward(self.handle, px, ldx, T, pg, pu, po, ldo, ps[0], ps[1], s))
-        return out, saved
+                u = self._empty((T, N), dtype=self._torch.float32, device=self.device)
+                if pg is not None:
+                    g = self._empty((T, N), dtype=self._torch.float32, device=self.device)
+        status = self._lib.moe_gated_forward(self.handle, x.data_ptr(), ldx, T, pg, pu, out.data_ptr(), ldo,
+                                             g.data_ptr() if g is not None else None,
+                                             u.data_ptr() if u is not None else None, s)
+        if status:
+            self._fail(status)
+        return out, (g, u)
 
     def forward(self, x, up_w, gate_w=None, out=None, stream=None):
         """out [T, N] of x [T, K] (rows may be strided) and up_w, gate_w [N, K]."""
@@ -285,27 +312,30 @@ class GatedBlock(_Handle):
 
     def backward(self, d_out, saved, x, up_w, gate_w=None, need=("x", "gate_w", "up_w"), stream=None) -> GatedGrads:
         """Gradients of the tensors named in ``need`` for the gradient ``d_out`` [T, N] of ``forward_train``'s out."""
-        c, torch = self.config, self._torch
-        if set(need) - set(GatedGrads._fields):
+        c, f32 = self.config, self._torch.float32
+        if not set(need).issubset(GatedGrads._fields):
             raise MoEError(_INVALID_ARG, f"need names {', '.join(GatedGrads._fields)}")
-        pd, ldd = self._rows(d_out, c.out_features, "d_out")
-        px, ldx = self._rows(x, c.in_features, "x")
+        K, N, T = c.in_features, c.out_features, x.shape[0]
+        ldd, ldx = self._stride(d_out, N, "d_out"), self._stride(x, K, "x")
         pu, pg = self._weights(up_w, gate_w)
-        T = x.shape[0]
         if d_out.shape[0] != T:
             raise MoEError(_SHAPE, f"d_out has {d_out.shape[0]} rows, x {T}")
-        ps = []
-        for t, on in zip(saved, (pg is not None, True)):
-            if on and (t is None or t.dtype != torch.float32 or tuple(t.shape) != (T, c.out_features) or
-                       t.device != self.device or not t.is_contiguous()):
+        ps = [None, None]
+        for i, t in enumerate(saved):
+            if i == 0 and pg is None:
+                continue
+            if (t is None or t.dtype is not f32 or t.shape != (T, N) or t.device != self.device or
+                    not t.is_contiguous()):
                 raise MoEError(_INVALID_ARG, "saved must be what forward_train returned for x")
-            ps.append(t.data_ptr() if on else None)
+            ps[i] = t.data_ptr()
         s, where = self._stream(stream)
         with where:
-            d_x = torch.empty((T, c.in_features), dtype=self._dtype, device=self.device) if "x" in need else None
-            d_g = torch.empty_like(gate_w) if pg is not None and "gate_w" in need else None
-            d_u = torch.empty_like(up_w) if "up_w" in need else None
+            d_x = self._empty((T, K), dtype=self._dtype, device=self.device) if "x" in need else None
+            d_g = self._empty((N, K), dtype=self._dtype, device=self.device) if pg is not None and "gate_w" in need else None
+            d_u = self._empty((N, K), dtype=self._dtype, device=self.device) if "up_w" in need else None
         p = [t.data_ptr() if t is not None else None for t in (d_x, d_g, d_u)]
-        self._check(self._lib.moe_gated_backward(self.handle, pd, ldd, T, px, ldx, pg, pu, ps[0], ps[1], p[0],
-                                                 c.in_features, p[1], p[2], s))
+        status = self._lib.moe_gated_backward(self.handle, d_out.data_ptr(), ldd, T, x.data_ptr(), ldx, pg, pu, ps[0],
+                                              ps[1], p[0], K, p[1], p[2], s)
+        if status:
+            self._fail(status)
         return GatedGrads(d_x, d_g, d_u)

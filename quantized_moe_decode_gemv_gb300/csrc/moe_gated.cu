@@ -18,7 +18,6 @@ struct moe_gated : OpHandle {
 
 namespace {
 
-constexpr int kSmemMax = 227 * 1024;
 thread_local std::string g_error;
 
 // Gradients of the pre-activations, eight elements a thread:
@@ -98,8 +97,6 @@ moe_status validate(const moe_gated_config* c, std::string* why) {
   return MOE_OK;
 }
 
-using StreamKernel = void (*)(const StreamArgs);
-
 StreamKernel stream_kernel(bool fp16, bool gated, int nt) {
   if (fp16) {
     if (gated) return nt == 1 ? k_stream<W_DENSE, true, true, 1, 4> : k_stream<W_DENSE, true, true, 2, 4>;
@@ -164,7 +161,7 @@ moe_status moe_gated_create(const moe_gated_config* cfg, moe_gated** out) {
   if (c.training && gated && e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->dg), grad);
   for (int nt = 1; nt <= 2 && e == cudaSuccess; ++nt)
     e = cudaFuncSetAttribute(reinterpret_cast<const void*>(stream_kernel(c.act_dtype == MOE_DTYPE_FP16, gated, nt)),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();   // the status word's clear runs on the default stream
   if (e != cudaSuccess) {
     g_error = std::string("create: ") + cudaGetErrorString(e);
@@ -210,30 +207,21 @@ moe_status moe_gated_forward(moe_gated* h, const void* x, int64_t ldx, int32_t T
     StreamArgs a{};
     a.w_gate = gate_w;
     a.w_up = up_w;
+    a.x = x;
     a.ldx = ldx;
+    a.out = out;
     a.ldo = ldo;
+    a.save_gate = save_gate;
+    a.save_up = save_up;
     a.K = K;
     a.N = N;
+    a.T = T;
     a.chunks = (K + 63) / 64;
     a.act = c.act;
-    const int tiles = (N + 15) / 16, mats = gated ? 2 : 1;
-    for (int t0 = 0; t0 < T && e == cudaSuccess;) {
-      a.T = std::min(T - t0, ST_MAX_T);
-      while (a.T > 1 && st_plan(a.chunks, a.T, a.T > 8 ? 2 : 1, mats, 0).total > kSmemMax) --a.T;
-      const int nt = a.T > 8 ? 2 : 1;
-      const StreamPlan P = st_plan(a.chunks, a.T, nt, mats, 0);
-      a.x = static_cast<const char*>(x) + static_cast<int64_t>(t0) * ldx * 2;
-      a.out = static_cast<char*>(out) + static_cast<int64_t>(t0) * ldo * 2;
-      a.save_gate = save_gate ? save_gate + static_cast<int64_t>(t0) * N : nullptr;
-      a.save_up = save_up ? save_up + static_cast<int64_t>(t0) * N : nullptr;
-      const int slots = h->num_sms * (P.total <= (kSmemMax - 2048) / 2 ? 2 : 1);
-      const int rounds = (tiles + slots - 1) / slots;
-      stream_kernel(c.act_dtype == MOE_DTYPE_FP16, gated, nt)<<<(tiles + rounds - 1) / rounds, ST_THREADS,
-                                                                static_cast<size_t>(P.total), s>>>(a);
-      e = cudaGetLastError();
-      ++h->last_launches;
-      t0 += a.T;
-    }
+    const StreamPlan P = st_plan(W_DENSE, gated, 4, T, N, h->num_sms);
+    a.depth = P.depth;
+    e = st_launch(stream_kernel(c.act_dtype == MOE_DTYPE_FP16, gated, T > 8 ? 2 : 1), a, P, s);
+    ++h->last_launches;
   } else {
     GemmCall g;
     g.M = T;

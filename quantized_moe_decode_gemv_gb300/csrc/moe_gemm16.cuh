@@ -331,21 +331,33 @@ __global__ void __launch_bounds__(GM_THREADS, 1) k_gemm16(const __grid_constant_
           for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(A.dual ? r1[j] : r0[j]);
           gm_store32(st, v, A.save_up, A.N, row0, col0, A.M, A.N, lane);
         }
+        // (each choice outside its loop: a warp is alone on its scheduler here, and 32
+        // independent elements are what hides the latency of the arithmetic)
+        if (A.nscale) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const int cc = min(col0 + j, A.N - 1);
-          float a = __uint_as_float(r0[j]), b = A.dual ? __uint_as_float(r1[j]) : 0.0f;
-          if (A.nscale) {
+          for (int j = 0; j < 32; ++j) {
+            const int cc = min(col0 + j, A.N - 1);
             if (A.dual) {
-              a *= __ldg(A.nscale_gate + cc);
-              b *= __ldg(A.nscale + cc);
+              r0[j] = __float_as_uint(__uint_as_float(r0[j]) * __ldg(A.nscale_gate + cc));
+              r1[j] = __float_as_uint(__uint_as_float(r1[j]) * __ldg(A.nscale + cc));
             } else {
-              a *= __ldg(A.nscale + cc);
+              r0[j] = __float_as_uint(__uint_as_float(r0[j]) * __ldg(A.nscale + cc));
             }
           }
-          float y = A.dual ? act_value(ACT_SWIGLU, a, b) : act_value(A.act, 0.0f, a);
-          if (A.bias) y += ld16(A.bias, cc, A.dt);
-          v[j] = y;
+        }
+        if (A.dual) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = act_value(ACT_SWIGLU, __uint_as_float(r0[j]), __uint_as_float(r1[j]));
+        } else if (A.act == ACT_RELU2) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = act_value(ACT_RELU2, 0.0f, __uint_as_float(r0[j]));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r0[j]);
+        }
+        if (A.bias) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] += ld16(A.bias, min(col0 + j, A.N - 1), A.dt);
         }
         gm_store16(st, v, A.dt, static_cast<unsigned short*>(A.out[U.z]), A.ldo, row0, col0, A.M, A.N, A.out_vec != 0,
                    lane);

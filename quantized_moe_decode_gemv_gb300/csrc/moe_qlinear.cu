@@ -13,7 +13,6 @@ using namespace moe_op;
 
 namespace {
 
-constexpr int kSmemMax = 227 * 1024;
 thread_local std::string g_error;
 
 // ---------------------------------------------------------------------------
@@ -80,6 +79,11 @@ __global__ void ql_rows(const uint8_t* s, const float* matrix_scale, int N, int 
   factor[row] = bad ? __int_as_float(0x7FC00000) : f;
 }
 
+template <int FMT>
+__device__ __forceinline__ int ql_column(int j, int t) {
+  return FMT == W_AFFINE ? 32 * (j >> 1) + 8 * t + 4 * (j & 1) : 16 * t + 4 * j;
+}
+
 // Row-major codes [N, K/8] and scales -> the streaming order of k_stream:
 //   codes  [N/16][chunks][matrices][32 lanes][4 words], rows and columns past
 //          the matrix zero
@@ -88,6 +92,8 @@ __global__ void ql_rows(const uint8_t* s, const float* matrix_scale, int N, int 
 //          nvfp4           [N/16][chunks][matrices][8][4 blocks][2] bytes
 //          mxfp4           [N/16][chunks][matrices][8][2 blocks][2] bytes
 //          (the pair: rows g and g + 8)
+// Word j of lane (g, t) holds four columns of rows g and g + 8: from 32 (j / 2)
+// + 8 t + 4 (j % 2) on in an affine chunk, from 16 t + 4 j on in an fp4 one.
 // One thread per (tile, chunk, lane) of matrix `m`.
 template <int FMT, bool FP16>
 __global__ void ql_tile(const uint32_t* q, const void* s, const void* b, const int* e0, int N, int K, int G, int chunks,
@@ -102,21 +108,20 @@ __global__ void ql_tile(const uint32_t* q, const void* s, const void* b, const i
   const int64_t tc = (tile * chunks + c) * mats + m;
   const int kb = K / G;
   uint32_t words[4];
-  uint32_t sbytes[4][2];
+  uint32_t sbytes[2] = {0u, 0u};   // fp4: the lane's 16 columns share a block
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int col = c * 64 + j * 16 + t * 4;
+    const int col = c * 64 + ql_column<FMT>(j, t);
     uint32_t half[2];   // four codes of rows g and g + 8
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int64_t row = tile * 16 + g + 8 * h;
       const bool in = row < N && col < K;
       half[h] = in ? (q[row * (K / 8) + col / 8] >> (4 * (col & 4))) & 0xFFFFu : 0u;
-      sbytes[j][h] = 0u;
       if (FMT != W_AFFINE && in) {
         const uint32_t by = static_cast<const uint8_t*>(s)[row * kb + col / G];
         bool zero = false;
-        sbytes[j][h] = scale_byte<FMT, FP16>(by, FMT == W_MXFP4 ? e0[row] : 0, &zero);
+        sbytes[h] = scale_byte<FMT, FP16>(by, FMT == W_MXFP4 ? e0[row] : 0, &zero);
         if (zero) half[h] = 0u;                                       // a zero scale: zero codes
         if (FMT == W_NVFP4 && (by & 0x80u)) half[h] ^= 0x8888u;       // a negative scale: negated codes
       }
@@ -153,15 +158,9 @@ __global__ void ql_tile(const uint32_t* q, const void* s, const void* b, const i
       const int64_t o = G == 32 ? tc * 16 + t * 8 + g : ((tile * ng + grp) * mats + m) * 8 + g;
       static_cast<uint2*>(scales)[o] = make_uint2(v[0], v[1]);
     }
-  } else if (t == 0) {
-    if (FMT == W_NVFP4) {
-      static_cast<uint2*>(scales)[tc * 8 + g] =
-          make_uint2(sbytes[0][0] | (sbytes[0][1] << 8) | (sbytes[1][0] << 16) | (sbytes[1][1] << 24),
-                     sbytes[2][0] | (sbytes[2][1] << 8) | (sbytes[3][0] << 16) | (sbytes[3][1] << 24));
-    } else {
-      static_cast<uint32_t*>(scales)[tc * 8 + g] =
-          sbytes[0][0] | (sbytes[0][1] << 8) | (sbytes[2][0] << 16) | (sbytes[2][1] << 24);
-    }
+  } else if (FMT == W_NVFP4 || t % 2 == 0) {
+    const int64_t o = FMT == W_NVFP4 ? tc * 32 + lane : tc * 16 + g * 2 + t / 2;
+    static_cast<unsigned short*>(scales)[o] = static_cast<unsigned short>(sbytes[0] | (sbytes[1] << 8));
   }
 }
 
@@ -186,41 +185,41 @@ __global__ void __launch_bounds__(256) ql_expand(const uint4* codes, const void*
   const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
   const int64_t ld = static_cast<int64_t>(chunks) * 64;
   const int64_t r0 = tile * 16 + g;
-  unsigned short* p0 = out + (static_cast<int64_t>(m) * N + r0) * ld + c * 64 + t * 4;
+  unsigned short* p0 = out + (static_cast<int64_t>(m) * N + r0) * ld + c * 64;
   unsigned short* p1 = p0 + 8 * ld;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint32_t a[4];
-    if (FMT == W_AFFINE) {
-      const int64_t grp = (static_cast<int64_t>(c) * 64 + j * 16) / G;
+  for (int jj = 0; jj < 2; ++jj) {
+    // words 2 jj and 2 jj + 1: eight consecutive columns of two rows
+    uint32_t a[2][4];
+    if constexpr (FMT == W_AFFINE) {
+      const int64_t grp = (static_cast<int64_t>(c) * 64 + jj * 32) / G;
       const int64_t ng = (static_cast<int64_t>(chunks) * 64 + G - 1) / G;
-      const int64_t o = G == 32 ? tc * 16 + (j >> 1) * 8 + g : ((tile * ng + grp) * mats + m) * 8 + g;
+      const int64_t o = G == 32 ? tc * 16 + jj * 8 + g : ((tile * ng + grp) * mats + m) * 8 + g;
       const uint2 v = __ldg(static_cast<const uint2*>(scales) + o);
-      affine_word<FP16>(ws[j], a);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const uint32_t sv = (r & 1) ? v.y : v.x;
-        const float s = lo16(sv, sdt), b = hi16(sv, sdt), off = affine_offset<FP16>();
-        a[r] = pack2(fmaf(lo16(a[r], DT) - off, s, b), fmaf(hi16(a[r], DT) - off, s, b), DT);
+      for (int j = 0; j < 2; ++j) {
+        affine_word<FP16>(ws[2 * jj + j], a[j]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t sv = (r & 1) ? v.y : v.x;
+          const float s = lo16(sv, sdt), b = hi16(sv, sdt), off = affine_offset<FP16>();
+          a[j][r] = pack2(fmaf(lo16(a[j][r], DT) - off, s, b), fmaf(hi16(a[j][r], DT) - off, s, b), DT);
+        }
       }
     } else {
-      fp4_word<FP16>(ws[j], a);
-      uint32_t sb;
-      if (FMT == W_NVFP4) {
-        const uint2 v = __ldg(static_cast<const uint2*>(scales) + tc * 8 + g);
-        sb = j < 2 ? v.x : v.y;
-      } else {
-        sb = __ldg(static_cast<const uint32_t*>(scales) + tc * 8 + g);
+      const int64_t o = FMT == W_NVFP4 ? tc * 32 + lane : tc * 16 + g * 2 + (t >> 1);
+      const uint32_t sb = __ldg(static_cast<const unsigned short*>(scales) + o);
+      const uint32_t s0 = fp4_scale<FMT, FP16>(sb, 0), s1 = fp4_scale<FMT, FP16>(sb, 1);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        fp4_word<FP16>(ws[2 * jj + j], a[j]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) a[j][r] = mul2<FP16>(a[j][r], (r & 1) ? s1 : s0);
       }
-      const int b0 = FMT == W_NVFP4 ? 2 * (j & 1) : 2 * (j >> 1);
-      const uint32_t s0 = fp4_scale<FMT, FP16>(sb, b0), s1 = fp4_scale<FMT, FP16>(sb, b0 + 1);
-      a[0] = mul2<FP16>(a[0], s0);
-      a[1] = mul2<FP16>(a[1], s1);
-      a[2] = mul2<FP16>(a[2], s0);
-      a[3] = mul2<FP16>(a[3], s1);
     }
-    if (r0 < N) *reinterpret_cast<uint2*>(p0 + j * 16) = make_uint2(a[0], a[2]);
-    if (r0 + 8 < N) *reinterpret_cast<uint2*>(p1 + j * 16) = make_uint2(a[1], a[3]);
+    const int col = ql_column<FMT>(2 * jj, t);
+    if (r0 < N) *reinterpret_cast<uint4*>(p0 + col) = make_uint4(a[0][0], a[0][2], a[1][0], a[1][2]);
+    if (r0 + 8 < N) *reinterpret_cast<uint4*>(p1 + col) = make_uint4(a[0][1], a[0][3], a[1][1], a[1][3]);
   }
 }
 
@@ -276,12 +275,6 @@ moe_status validate(const moe_qlinear_config* c, const moe_qlinear_weights* w, s
 
 // ---- k_stream launches ----
 
-int gx_of(const moe_qlinear_config& c) {
-  return c.weight_format == MOE_WFMT_AFFINE ? std::min(c.group_size, 64) : 0;
-}
-
-using StreamKernel = void (*)(const StreamArgs);
-
 template <int FMT, bool FP16, int GB>
 StreamKernel stream_kernel_g(bool gated, int nt) {
   if (gated) return nt == 1 ? k_stream<FMT, FP16, true, 1, GB> : k_stream<FMT, FP16, true, 2, GB>;
@@ -298,13 +291,6 @@ StreamKernel stream_kernel(const moe_qlinear_config& c, int nt) {
   return c.act_dtype == MOE_DTYPE_FP16 ? stream_kernel_t<true>(c, nt) : stream_kernel_t<false>(c, nt);
 }
 
-// Most token rows of one k_stream launch whose staging fits shared memory.
-int stream_rows(const moe_qlinear& h, int T) {
-  for (int t = std::min(T, ST_MAX_T); t > 1; --t)
-    if (st_plan(h.chunks, t, t > 8 ? 2 : 1, h.mats, gx_of(h.cfg)).total <= kSmemMax) return t;
-  return 1;
-}
-
 cudaError_t run_stream(moe_qlinear& h, const void* x, int64_t ldx, int T, void* out, int64_t ldo, cudaStream_t s) {
   const moe_qlinear_config& c = h.cfg;
   StreamArgs a{};
@@ -313,30 +299,22 @@ cudaError_t run_stream(moe_qlinear& h, const void* x, int64_t ldx, int T, void* 
   a.nscale_gate = h.factor[0];
   a.nscale = h.factor[1];
   a.bias = h.bias;
+  a.x = x;
   a.ldx = ldx;
+  a.out = out;
   a.ldo = ldo;
   a.K = c.in_features;
   a.N = c.out_features;
+  a.T = T;
   a.chunks = h.chunks;
   a.group = c.group_size;
   a.act = c.act;
   a.sdt = c.scale_dtype;
-  const int tiles = (a.N + 15) / 16;
-  for (int t0 = 0; t0 < T;) {
-    a.T = stream_rows(h, T - t0);
-    a.x = static_cast<const char*>(x) + static_cast<int64_t>(t0) * ldx * 2;
-    a.out = static_cast<char*>(out) + static_cast<int64_t>(t0) * ldo * 2;
-    const int nt = a.T > 8 ? 2 : 1;
-    const StreamPlan P = st_plan(h.chunks, a.T, nt, h.mats, gx_of(c));
-    const int slots = h.num_sms * (P.total <= (kSmemMax - 2048) / 2 ? 2 : 1);
-    const int rounds = (tiles + slots - 1) / slots;
-    stream_kernel(c, nt)<<<(tiles + rounds - 1) / rounds, ST_THREADS, static_cast<size_t>(P.total), s>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    ++h.last_launches;
-    t0 += a.T;
-  }
-  return cudaSuccess;
+  const int fmt = c.weight_format == MOE_WFMT_NVFP4 ? W_NVFP4 : c.weight_format == MOE_WFMT_MXFP4 ? W_MXFP4 : W_AFFINE;
+  const StreamPlan P = st_plan(fmt, h.mats == 2, c.group_size == 32 ? 2 : 4, T, a.N, h.num_sms);
+  a.depth = P.depth;
+  ++h.last_launches;
+  return st_launch(stream_kernel(c, T > 8 ? 2 : 1), a, P, s);
 }
 
 // ---- create-time launches ----
@@ -450,7 +428,7 @@ moe_status moe_qlinear_create(const moe_qlinear_config* cfg, const moe_qlinear_w
   }
   for (int nt = 1; nt <= 2 && e == cudaSuccess; ++nt)
     e = cudaFuncSetAttribute(reinterpret_cast<const void*>(stream_kernel(c, nt)),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
   if (e == cudaSuccess) e = QL_BY_FORMAT(*h, relay, *h, *w, e0, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) {

@@ -111,17 +111,15 @@ def _place(code, i, fp16):
     s, eem = code >> 3, code & 7
     if fp16:
         return s << (15, 12, 14, 13)[i] | eem << (9 - 3 * i)
-    if i < 3:
-        return s << (15 - 3 * i) | eem << (6 - 3 * i)
-    return s << 14 | (eem >> 1) << 10 | (eem & 1) << 13
+    return s << (15, 12, 14, 13)[i] | eem << (6, 3, 0, 9)[i]
 
 
 def _take(w, i, fp16):
     if fp16:
         return (w & 0x8E008E00, (w << 3) & 0x8E008E00, (w << 6) & 0x0E000E00 | (w << 1) & 0x80008000,
                 (w << 9) & 0x0E000E00 | (w << 2) & 0x80008000)[i] & 0xFFFFFFFF
-    return (w & 0x81C081C0, (w << 3) & 0x81C081C0, (w << 6) & 0x81C081C0,
-            (w >> 3) & 0x01800180 | (w >> 7) & 0x00400040 | (w << 1) & 0x80008000)[i] & 0xFFFFFFFF
+    return (w & 0x81C081C0, (w << 3) & 0x81C081C0, (w << 6) & 0x01C001C0 | (w << 1) & 0x80008000,
+            (w >> 3) & 0x01C001C0 | (w << 2) & 0x80008000)[i] & 0xFFFFFFFF
 
 
 def _value(bits, fp16):
