@@ -6,7 +6,7 @@
 #include <new>
 
 #include "moe_op_host.h"
-#include "moe_stream.cuh"
+#include "moe_stream16.cuh"
 
 using namespace moe_op;
 
@@ -32,6 +32,8 @@ __global__ void __launch_bounds__(256) k_gated_grad(const float* __restrict__ g,
                                                     const unsigned short* __restrict__ e, int64_t lde, int e_vec, int T,
                                                     int N, int dt, unsigned short* __restrict__ dg,
                                                     unsigned short* __restrict__ du) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
   const int q = N / 8;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= static_cast<int64_t>(T) * q) return;
@@ -97,13 +99,15 @@ moe_status validate(const moe_gated_config* c, std::string* why) {
   return MOE_OK;
 }
 
+using StreamKernel = void (*)(const Stream16Args);
+
+template <bool FP16>
+StreamKernel stream_kernel_t(bool gated, int nt) {
+  if (gated) return nt == 1 ? k_stream16<FP16, true, 1> : k_stream16<FP16, true, 2>;
+  return nt == 1 ? k_stream16<FP16, false, 1> : k_stream16<FP16, false, 2>;
+}
 StreamKernel stream_kernel(bool fp16, bool gated, int nt) {
-  if (fp16) {
-    if (gated) return nt == 1 ? k_stream<W_DENSE, true, true, 1, 4> : k_stream<W_DENSE, true, true, 2, 4>;
-    return nt == 1 ? k_stream<W_DENSE, true, false, 1, 4> : k_stream<W_DENSE, true, false, 2, 4>;
-  }
-  if (gated) return nt == 1 ? k_stream<W_DENSE, false, true, 1, 4> : k_stream<W_DENSE, false, true, 2, 4>;
-  return nt == 1 ? k_stream<W_DENSE, false, false, 1, 4> : k_stream<W_DENSE, false, false, 2, 4>;
+  return fp16 ? stream_kernel_t<true>(gated, nt) : stream_kernel_t<false>(gated, nt);
 }
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -161,7 +165,7 @@ moe_status moe_gated_create(const moe_gated_config* cfg, moe_gated** out) {
   if (c.training && gated && e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->dg), grad);
   for (int nt = 1; nt <= 2 && e == cudaSuccess; ++nt)
     e = cudaFuncSetAttribute(reinterpret_cast<const void*>(stream_kernel(c.act_dtype == MOE_DTYPE_FP16, gated, nt)),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, S16_SMEM_MAX);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();   // the status word's clear runs on the default stream
   if (e != cudaSuccess) {
     g_error = std::string("create: ") + cudaGetErrorString(e);
@@ -204,7 +208,7 @@ moe_status moe_gated_forward(moe_gated* h, const void* x, int64_t ldx, int32_t T
   std::string why;
   cudaError_t e = cudaSuccess;
   if (T <= ST_MAX_T) {
-    StreamArgs a{};
+    Stream16Args a{};
     a.w_gate = gate_w;
     a.w_up = up_w;
     a.x = x;
@@ -218,9 +222,10 @@ moe_status moe_gated_forward(moe_gated* h, const void* x, int64_t ldx, int32_t T
     a.T = T;
     a.chunks = (K + 63) / 64;
     a.act = c.act;
-    const StreamPlan P = st_plan(W_DENSE, gated, 4, T, N, h->num_sms);
+    const Stream16Plan P = s16_plan(gated, T, N, h->num_sms);
     a.depth = P.depth;
-    e = st_launch(stream_kernel(c.act_dtype == MOE_DTYPE_FP16, gated, T > 8 ? 2 : 1), a, P, s);
+    e = launch_chained(stream_kernel(c.act_dtype == MOE_DTYPE_FP16, gated, T > 8 ? 2 : 1), P.grid, S16_THREADS,
+                       static_cast<size_t>(P.smem), 1, s, a);
     ++h->last_launches;
   } else {
     GemmCall g;
@@ -298,14 +303,10 @@ moe_status moe_gated_backward(moe_gated* h, const void* d_out, int64_t ldd, int3
     }
     const int64_t n = static_cast<int64_t>(T) * (N / 8);
     const int e_vec = aligned16(d_out) && ldd % 8 == 0;
-    const unsigned grid = static_cast<unsigned>((n + 255) / 256);
     const unsigned short* ep = static_cast<const unsigned short*>(d_out);
     if (d_x || d_gate_w || d_up_w) {
-      if (gated)
-        k_gated_grad<true><<<grid, 256, 0, s>>>(save_gate, save_up, ep, ldd, e_vec, T, N, c.act_dtype, h->dg, h->du);
-      else
-        k_gated_grad<false><<<grid, 256, 0, s>>>(nullptr, save_up, ep, ldd, e_vec, T, N, c.act_dtype, nullptr, h->du);
-      e = cudaGetLastError();
+      e = launch_chained(gated ? k_gated_grad<true> : k_gated_grad<false>, (n + 255) / 256, 256, 0, 1, s, save_gate, save_up,
+                         ep, ldd, e_vec, T, N, c.act_dtype, h->dg, h->du);
       ++h->last_launches;
     }
     if (d_x && e == cudaSuccess) {

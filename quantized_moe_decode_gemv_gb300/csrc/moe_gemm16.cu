@@ -222,19 +222,8 @@ cudaError_t gemm16_launch(const GemmCall& c, OpHandle& h, cudaStream_t s, int* l
                         c.batches * ch.ksplit;
   const int64_t workers = std::min<int64_t>(units, h.num_sms / ch.cg);
 
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(workers * ch.cg));
-  cfg.blockDim = dim3(GM_THREADS);
-  cfg.dynamicSmemBytes = static_cast<size_t>(gm_smem_bytes(ch.bn, ch.cg, a.stages));
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = static_cast<unsigned>(ch.cg);
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel_of(ch.cg, c.a_mn, c.b_mn), a);
+  cudaError_t e = launch_chained(kernel_of(ch.cg, c.a_mn, c.b_mn), workers * ch.cg, GM_THREADS,
+                                 static_cast<size_t>(gm_smem_bytes(ch.bn, ch.cg, a.stages)), ch.cg, s, a);
   ++*launches;
   if (e == cudaSuccess && ch.ksplit > 1) {
     GemmFinishArgs f{};
@@ -247,6 +236,7 @@ cudaError_t gemm16_launch(const GemmCall& c, OpHandle& h, cudaStream_t s, int* l
     f.dual = a.dual;
     f.act = a.act;
     f.dt = a.dt;
+    f.out_vec = a.out_vec;
     f.out[0] = a.out[0];
     f.out[1] = a.out[1];
     f.ldo = a.ldo;
@@ -256,8 +246,7 @@ cudaError_t gemm16_launch(const GemmCall& c, OpHandle& h, cudaStream_t s, int* l
     f.nscale = a.nscale;
     f.bias = a.bias;
     const int64_t n = static_cast<int64_t>(a.batches) * a.M * ((a.N + 3) / 4);
-    k_gemm16_finish<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(f);
-    e = cudaGetLastError();
+    e = launch_chained(k_gemm16_finish, (n + 127) / 128, 128, 0, 1, s, f);
     ++*launches;
   }
   if (e != cudaSuccess) *why = std::string("launch: ") + cudaGetErrorString(e);

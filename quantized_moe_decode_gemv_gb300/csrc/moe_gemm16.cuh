@@ -19,10 +19,12 @@
 // for 2 x 4.2 MFLOP: 64 bytes a clock and SM beside a saturated tensor pipe;
 // with CG = 1 it would be 96, above what L2 delivers to all SMs at once.)
 //
-// Roles of a CTA's 8 warps: warp 0 issues the tensor copies into a ring of
+// Roles of a CTA's 12 warps: warp 0 issues the tensor copies into a ring of
 // shared-memory slots, warp 1 (of the pair's even CTA) issues the MMAs, warp 2
-// owns the tensor-memory allocation, warps 4-7 read finished accumulators and
-// write the epilogue.  Accumulators are double-buffered (2 x BN <= 512
+// owns the tensor-memory allocation, warps 4-11 read finished accumulators and
+// write the epilogue (two warps a quarter of the lanes, taking turns at the
+// columns: with one, a product of few K blocks and many outputs waited for its
+// epilogues).  Accumulators are double-buffered (2 x BN <= 512
 // columns), so an epilogue overlaps the next tile's MMAs.  CTAs (pairs) are
 // persistent and walk the tiles in groups of 8 tile rows, whose operands stay
 // in L2 while the columns pass.
@@ -35,9 +37,10 @@
 
 namespace moe_op {
 
-constexpr int GM_THREADS = 256;
+constexpr int GM_THREADS = 384;
+constexpr int GM_EPI_WARPS = 8;
 constexpr int GM_MAX_STAGES = 12;
-constexpr int GM_EPI_BYTES = 4 * 32 * 144;         // epilogue staging: 4 warps x 32 rows x 128 (+16) bytes
+constexpr int GM_EPI_BYTES = GM_EPI_WARPS * 32 * 80;   // epilogue staging: a warp's 32 rows x 64 (+16) bytes
 constexpr int GM_SMEM_MAX = 227 * 1024;
 
 struct GemmArgs {
@@ -105,42 +108,46 @@ __device__ __forceinline__ void gm_store16(char* st, const float (&v)[32], int d
     w[j] = make_uint4(pack2(v[8 * j], v[8 * j + 1], dt), pack2(v[8 * j + 2], v[8 * j + 3], dt),
                       pack2(v[8 * j + 4], v[8 * j + 5], dt), pack2(v[8 * j + 6], v[8 * j + 7], dt));
   __syncwarp();
-  const int c = col0 + (lane & 3) * 8;
+  if (vec && col0 + 32 <= N) {
+    unsigned short* p = out + static_cast<int64_t>(row0 + (lane >> 2)) * ld + col0 + (lane & 3) * 8;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = (lane >> 2) + 8 * i;
-    const uint4 x = *reinterpret_cast<const uint4*>(st + r * 80 + (lane & 3) * 16);
-    if (row0 + r < M) {
-      unsigned short* p = out + static_cast<int64_t>(row0 + r) * ld + c;
-      if (vec && c + 8 <= N) {
-        *reinterpret_cast<uint4*>(p) = x;
-      } else {
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (c + k < N) p[k] = static_cast<unsigned short>(xs[k >> 1] >> (16 * (k & 1)));
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int r = (lane >> 2) + 8 * i;
+      const uint4 x = *reinterpret_cast<const uint4*>(st + r * 80 + (lane & 3) * 16);
+      if (row0 + r < M) *reinterpret_cast<uint4*>(p + static_cast<int64_t>(8 * i) * ld) = x;
     }
+  } else if (col0 + lane < N) {
+    // rows that 16-byte stores do not fit: a lane a column
+    unsigned short* p = out + static_cast<int64_t>(row0) * ld + col0 + lane;
+    const int rows = min(32, M - row0);
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r)
+      p[static_cast<int64_t>(r) * ld] = *reinterpret_cast<const unsigned short*>(st + r * 80 + lane * 2);
   }
   __syncwarp();
 }
 
-// The same for fp32 values; `ld` and `out` keep 16-byte alignment (host-checked)
-// and N (the row's extent from col0's origin) is a multiple of 4.
-__device__ __forceinline__ void gm_store32(char* st, const float (&v)[32], float* out, int64_t ld, int row0, int col0,
+// The same for fp32 values, 16 columns at a time; `ld` and `out` keep 16-byte
+// alignment (host-checked) and N is a multiple of 4.
+__device__ __forceinline__ void gm_store32(char* st, const uint32_t (&v)[32], float* out, int64_t ld, int row0, int col0,
                                            int M, int N, int lane) {
-  float4* w = reinterpret_cast<float4*>(st + lane * 144);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) w[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-  __syncwarp();
-  const int c = col0 + (lane & 7) * 4;
+  for (int h = 0; h < 2; ++h) {
+    uint4* w = reinterpret_cast<uint4*>(st + lane * 80);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = (lane >> 3) + 4 * i;
-    const float4 x = *reinterpret_cast<const float4*>(st + r * 144 + (lane & 7) * 16);
-    if (row0 + r < M && c + 4 <= N) *reinterpret_cast<float4*>(out + static_cast<int64_t>(row0 + r) * ld + c) = x;
+    for (int j = 0; j < 4; ++j)
+      w[j] = make_uint4(v[16 * h + 4 * j], v[16 * h + 4 * j + 1], v[16 * h + 4 * j + 2], v[16 * h + 4 * j + 3]);
+    __syncwarp();
+    const int c = col0 + 16 * h + (lane & 3) * 4;
+    float* p = out + static_cast<int64_t>(row0 + (lane >> 2)) * ld + c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = (lane >> 2) + 8 * i;
+      const uint4 x = *reinterpret_cast<const uint4*>(st + r * 80 + (lane & 3) * 16);
+      if (row0 + r < M && c + 4 <= N) *reinterpret_cast<uint4*>(p + static_cast<int64_t>(8 * i) * ld) = x;
+    }
+    __syncwarp();
   }
-  __syncwarp();
 }
 
 template <int CG, bool AMN, bool BMN>
@@ -172,7 +179,7 @@ __global__ void __launch_bounds__(GM_THREADS, 1) k_gemm16(const __grid_constant_
     }
     for (int b = 0; b < 2; ++b) {
       bar_init(smem_u32(&accf[b]), 1);
-      bar_init(smem_u32(&acce[b]), 4 * CG);
+      bar_init(smem_u32(&acce[b]), GM_EPI_WARPS * CG);
     }
     bar_init(smem_u32(drain), 1);
     bar_fence_init();
@@ -182,6 +189,9 @@ __global__ void __launch_bounds__(GM_THREADS, 1) k_gemm16(const __grid_constant_
   if (CG == 2) cluster_sync();
   tm_fence_after();
   const uint32_t tmem = *holder;
+  // everything above may run while the kernel before this one in the stream ends
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
   bool ok = true;
   auto wait = [&](uint64_t* b, uint32_t parity) {
     if (bar_wait(smem_u32(b), parity)) return true;
@@ -281,8 +291,8 @@ __global__ void __launch_bounds__(GM_THREADS, 1) k_gemm16(const __grid_constant_
     __syncwarp();
   } else if (warp >= 4) {
     // ---------------- epilogue ----------------
-    const int ew = warp - 4;
-    char* st = epi + ew * 32 * 144;
+    const int ew = warp & 3, half = (warp - 4) >> 2;
+    char* st = epi + (warp - 4) * 32 * 80;
     uint32_t n = 0;
     for (int u = worker; ok && u < units; u += nworkers, ++n) {
       const GemmUnit U = gm_unit<CG>(A, u);
@@ -291,12 +301,20 @@ __global__ void __launch_bounds__(GM_THREADS, 1) k_gemm16(const __grid_constant_
       tm_fence_after();
       const uint32_t tcol = tmem + (static_cast<uint32_t>(ew * 32) << 16) + static_cast<uint32_t>(buf * BN);
       const int row0 = U.m0 + static_cast<int>(rank) * 128 + ew * 32;
-      for (int c = 0; c < bn_out; c += 32) {
+      const int c_last = bn_out >= 64 ? bn_out - 64 + 32 * half : 0;   // this warp's last columns
+      if (bn_out < 64 && half == 1) {   // a single piece of columns: the other warp's
+        if (lane == 0) {
+          if (CG == 2) bar_arrive_cluster(smem_u32(&acce[buf]), 0);
+          else bar_arrive(smem_u32(&acce[buf]));
+        }
+        continue;
+      }
+      for (int c = 32 * half; c < bn_out; c += 64) {
         uint32_t r0[32], r1[32];
         tm_ld32(tcol + c, r0);
         if (A.dual) tm_ld32(tcol + BN / 2 + c, r1);
         tm_wait_ld();
-        if (c + 32 >= bn_out) {
+        if (c == c_last) {
           // the accumulators are in registers: the buffer may be rewritten
           tm_fence_before();
           __syncwarp();
@@ -310,26 +328,18 @@ __global__ void __launch_bounds__(GM_THREADS, 1) k_gemm16(const __grid_constant_
         float v[32];
         if (A.ksplit > 1) {
           float* p = A.part + static_cast<int64_t>(U.split * A.batches + U.z) * A.M * A.ld_part;
-          const int half = static_cast<int>(A.dual ? A.ld_part / 2 : A.ld_part);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r0[j]);
-          gm_store32(st, v, p, A.ld_part, row0, col0, A.M, half, lane);
-          if (A.dual) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r1[j]);
-            gm_store32(st, v, p + half, A.ld_part, row0, col0, A.M, half, lane);
-          }
+          const int nh = static_cast<int>(A.dual ? A.ld_part / 2 : A.ld_part);
+          gm_store32(st, r0, p, A.ld_part, row0, col0, A.M, nh, lane);
+          if (A.dual) gm_store32(st, r1, p + nh, A.ld_part, row0, col0, A.M, nh, lane);
           continue;
         }
         if (A.save_up) {
           if (A.dual) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r0[j]);
-            gm_store32(st, v, A.save_gate, A.N, row0, col0, A.M, A.N, lane);
+            gm_store32(st, r0, A.save_gate, A.N, row0, col0, A.M, A.N, lane);
+            gm_store32(st, r1, A.save_up, A.N, row0, col0, A.M, A.N, lane);
+          } else {
+            gm_store32(st, r0, A.save_up, A.N, row0, col0, A.M, A.N, lane);
           }
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(A.dual ? r1[j] : r0[j]);
-          gm_store32(st, v, A.save_up, A.N, row0, col0, A.M, A.N, lane);
         }
         // (each choice outside its loop: a warp is alone on its scheduler here, and 32
         // independent elements are what hides the latency of the arithmetic)
@@ -359,7 +369,7 @@ __global__ void __launch_bounds__(GM_THREADS, 1) k_gemm16(const __grid_constant_
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] += ld16(A.bias, min(col0 + j, A.N - 1), A.dt);
         }
-        gm_store16(st, v, A.dt, static_cast<unsigned short*>(A.out[U.z]), A.ldo, row0, col0, A.M, A.N, A.out_vec != 0,
+        gm_store16(st, v, A.dt, static_cast<unsigned short*>(U.z ? A.out[1] : A.out[0]), A.ldo, row0, col0, A.M, A.N, A.out_vec != 0,
                    lane);
       }
     }
@@ -378,7 +388,7 @@ __global__ void __launch_bounds__(GM_THREADS, 1) k_gemm16(const __grid_constant_
 struct GemmFinishArgs {
   const float* part;
   int64_t ld_part;
-  int ksplit, batches, M, N, dual, act, dt;
+  int ksplit, batches, M, N, dual, act, dt, out_vec;
   void* out[2];
   int64_t ldo;
   float *save_gate, *save_up;
@@ -386,39 +396,52 @@ struct GemmFinishArgs {
   const void* bias;
 };
 
-__global__ void __launch_bounds__(256) k_gemm16_finish(const GemmFinishArgs A) {
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+
+__global__ void __launch_bounds__(128) k_gemm16_finish(const GemmFinishArgs A) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
   const int q = (A.N + 3) / 4;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
   if (i >= static_cast<int64_t>(A.batches) * A.M * q) return;
   const int c = static_cast<int>(i % q) * 4;
   const int64_t zr = i / q;
   const int r = static_cast<int>(zr % A.M), z = static_cast<int>(zr / A.M);
-  const int half = static_cast<int>(A.dual ? A.ld_part / 2 : A.ld_part);
-  float g[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0};
+  const int64_t half = A.dual ? A.ld_part / 2 : A.ld_part;
+  const int64_t step = static_cast<int64_t>(A.batches) * A.M * A.ld_part;
+  const float* p = A.part + (static_cast<int64_t>(z) * A.M + r) * A.ld_part + c;
+  float4 s0 = make_float4(0, 0, 0, 0), s1 = s0;
+#pragma unroll 4
   for (int s = 0; s < A.ksplit; ++s) {
-    const float* p = A.part + (static_cast<int64_t>(s * A.batches + z) * A.M + r) * A.ld_part + c;
-    const float4 a = *reinterpret_cast<const float4*>(p);
-    g[0] += a.x; g[1] += a.y; g[2] += a.z; g[3] += a.w;
-    if (A.dual) {
-      const float4 b = *reinterpret_cast<const float4*>(p + half);
-      u[0] += b.x; u[1] += b.y; u[2] += b.z; u[3] += b.w;
-    }
+    s0 = add4(s0, *reinterpret_cast<const float4*>(p + s * step));
+    if (A.dual) s1 = add4(s1, *reinterpret_cast<const float4*>(p + s * step + half));
   }
+  float g[4] = {s0.x, s0.y, s0.z, s0.w}, u[4] = {s1.x, s1.y, s1.z, s1.w};
+  if (A.save_up) {   // (N is a multiple of 8 wherever pre-activations are saved)
+    const int64_t o = static_cast<int64_t>(r) * A.N + c;
+    if (A.dual) *reinterpret_cast<float4*>(A.save_gate + o) = s0;
+    *reinterpret_cast<float4*>(A.save_up + o) = A.dual ? s1 : s0;
+  }
+  float y[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    if (c + j >= A.N) break;
-    if (A.save_up) {
-      const int64_t o = static_cast<int64_t>(r) * A.N + c + j;
-      if (A.dual) A.save_gate[o] = g[j];
-      A.save_up[o] = A.dual ? u[j] : g[j];
-    }
+    const int cc = min(c + j, A.N - 1);
     if (A.nscale) {
-      g[j] *= A.dual ? A.nscale_gate[c + j] : A.nscale[c + j];
-      if (A.dual) u[j] *= A.nscale[c + j];
+      g[j] *= A.dual ? A.nscale_gate[cc] : A.nscale[cc];
+      if (A.dual) u[j] *= A.nscale[cc];
     }
-    float y = A.dual ? act_value(ACT_SWIGLU, g[j], u[j]) : act_value(A.act, 0.0f, g[j]);
-    if (A.bias) y += ld16(A.bias, c + j, A.dt);
-    static_cast<unsigned short*>(A.out[z])[static_cast<int64_t>(r) * A.ldo + c + j] = pack1(y, A.dt);
+    y[j] = A.dual ? act_value(ACT_SWIGLU, g[j], u[j]) : act_value(A.act, 0.0f, g[j]);
+    if (A.bias) y[j] += ld16(A.bias, cc, A.dt);
+  }
+  unsigned short* o = static_cast<unsigned short*>(z ? A.out[1] : A.out[0]) + static_cast<int64_t>(r) * A.ldo + c;
+  if (A.out_vec && c + 4 <= A.N) {
+    *reinterpret_cast<uint2*>(o) = make_uint2(pack2(y[0], y[1], A.dt), pack2(y[2], y[3], A.dt));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c + j < A.N) o[j] = pack1(y[j], A.dt);
   }
 }
 

@@ -69,6 +69,28 @@ inline bool rows_overlap(const void* a, int64_t lda, int64_t ca, const void* b, 
   return off < ca * 2 || off + cb * 2 > row;
 }
 
+// A launch that may begin while the kernel before it in the stream ends
+// (programmatic dependent launch).  Every kernel launched so waits for that
+// kernel (griddepcontrol.wait) before it touches what others write or read.
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*k)(P...), int64_t grid, int threads, size_t smem, int cluster, cudaStream_t s, const A&... a) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, k, a...);
+}
+
 struct GemmCall {
   int M = 0, N = 0;
   int parts = 1, batches = 1;

@@ -173,6 +173,9 @@ __global__ void __launch_bounds__(256) ql_expand(const uint4* codes, const void*
                                                  int mats, int sdt, unsigned short* out) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int tiles = (N + 15) / 16;
+  // (the call before this one may still read `out`)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
   if (i >= static_cast<int64_t>(tiles) * chunks * mats * 32) return;
   constexpr int DT = FP16 ? DT_FP16 : DT_BF16;
   const int lane = static_cast<int>(i & 31), g = lane >> 2, t = lane & 3;
@@ -232,7 +235,7 @@ struct moe_qlinear : OpHandle {
   void* scales = nullptr;
   float* factor[2] = {nullptr, nullptr};   // fp4 per-row factors: gate, up
   void* bias = nullptr;
-  unsigned short* wide = nullptr;          // 16-bit weights of one call (T > ST_MAX_T)
+  unsigned short* wide = nullptr;          // 16-bit weights of one call that k_stream does not take
 };
 
 namespace {
@@ -275,6 +278,8 @@ moe_status validate(const moe_qlinear_config* c, const moe_qlinear_weights* w, s
 
 // ---- k_stream launches ----
 
+using StreamKernel = void (*)(const StreamArgs);
+
 template <int FMT, bool FP16, int GB>
 StreamKernel stream_kernel_g(bool gated, int nt) {
   if (gated) return nt == 1 ? k_stream<FMT, FP16, true, 1, GB> : k_stream<FMT, FP16, true, 2, GB>;
@@ -291,7 +296,20 @@ StreamKernel stream_kernel(const moe_qlinear_config& c, int nt) {
   return c.act_dtype == MOE_DTYPE_FP16 ? stream_kernel_t<true>(c, nt) : stream_kernel_t<false>(c, nt);
 }
 
-cudaError_t run_stream(moe_qlinear& h, const void* x, int64_t ldx, int T, void* out, int64_t ldo, cudaStream_t s) {
+int stream_format(const moe_qlinear_config& c) {
+  return c.weight_format == MOE_WFMT_NVFP4 ? W_NVFP4 : c.weight_format == MOE_WFMT_MXFP4 ? W_MXFP4 : W_AFFINE;
+}
+
+// k_stream's plan for T rows; false when the call goes to the tensor-core GEMM:
+// more rows than it takes, or wider ones than fit beside its rings.
+bool stream_plan(const moe_qlinear& h, int T, StreamPlan* P) {
+  const moe_qlinear_config& c = h.cfg;
+  return T <= ST_MAX_T && st_plan(stream_format(c), h.mats == 2, c.group_size == 32 ? 2 : 4, h.chunks, T, c.out_features,
+                                  h.num_sms, P);
+}
+
+cudaError_t run_stream(moe_qlinear& h, const StreamPlan& P, const void* x, int64_t ldx, int T, void* out, int64_t ldo,
+                       cudaStream_t s) {
   const moe_qlinear_config& c = h.cfg;
   StreamArgs a{};
   a.codes = h.codes;
@@ -310,11 +328,10 @@ cudaError_t run_stream(moe_qlinear& h, const void* x, int64_t ldx, int T, void* 
   a.group = c.group_size;
   a.act = c.act;
   a.sdt = c.scale_dtype;
-  const int fmt = c.weight_format == MOE_WFMT_NVFP4 ? W_NVFP4 : c.weight_format == MOE_WFMT_MXFP4 ? W_MXFP4 : W_AFFINE;
-  const StreamPlan P = st_plan(fmt, h.mats == 2, c.group_size == 32 ? 2 : 4, T, a.N, h.num_sms);
   a.depth = P.depth;
+  a.status = h.status;
   ++h.last_launches;
-  return st_launch(stream_kernel(c, T > 8 ? 2 : 1), a, P, s);
+  return launch_chained(stream_kernel(c, T > 8 ? 2 : 1), P.grid, ST_THREADS, static_cast<size_t>(P.smem), 1, s, a);
 }
 
 // ---- create-time launches ----
@@ -344,11 +361,10 @@ template <int FMT, bool FP16>
 cudaError_t expand(moe_qlinear& h, cudaStream_t s) {
   const moe_qlinear_config& c = h.cfg;
   const int64_t n = static_cast<int64_t>((c.out_features + 15) / 16) * h.chunks * h.mats * 32;
-  ql_expand<FMT, FP16><<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(h.codes, h.scales, c.out_features,
-                                                                             c.group_size, h.chunks, h.mats,
-                                                                             c.scale_dtype, h.wide);
   ++h.last_launches;
-  return cudaGetLastError();
+  return launch_chained(ql_expand<FMT, FP16>, (n + 255) / 256, 256, 0, 1, s, static_cast<const uint4*>(h.codes),
+                        static_cast<const void*>(h.scales), c.out_features, c.group_size, h.chunks, h.mats,
+                        c.scale_dtype, h.wide);
 }
 
 #define QL_BY_FORMAT(h, fn, ...)                                                              \
@@ -416,7 +432,8 @@ moe_status moe_qlinear_create(const moe_qlinear_config* cfg, const moe_qlinear_w
     if (e == cudaSuccess)
       e = cudaMemcpyAsync(h->bias, w->bias, static_cast<size_t>(c.out_features) * 2, cudaMemcpyDeviceToDevice, s);
   }
-  if (c.max_tokens > ST_MAX_T && e == cudaSuccess) {
+  StreamPlan plan;
+  if (!stream_plan(*h, c.max_tokens, &plan) && e == cudaSuccess) {
     if (!gemm16_setup(&why)) {
       st = MOE_ERR_CUDA;
       e = cudaErrorUnknown;
@@ -428,7 +445,7 @@ moe_status moe_qlinear_create(const moe_qlinear_config* cfg, const moe_qlinear_w
   }
   for (int nt = 1; nt <= 2 && e == cudaSuccess; ++nt)
     e = cudaFuncSetAttribute(reinterpret_cast<const void*>(stream_kernel(c, nt)),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, ST_SMEM_MAX);
   if (e == cudaSuccess) e = QL_BY_FORMAT(*h, relay, *h, *w, e0, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) {
@@ -469,8 +486,9 @@ moe_status moe_qlinear_forward(moe_qlinear* h, const void* x, int64_t ldx, int32
   h->last_launches = 0;
   std::string why;
   cudaError_t e;
-  if (T <= ST_MAX_T) {
-    e = run_stream(*h, x, ldx, T, out, ldo, s);
+  StreamPlan plan;
+  if (stream_plan(*h, T, &plan)) {
+    e = run_stream(*h, plan, x, ldx, T, out, ldo, s);
   } else {
     e = QL_BY_FORMAT(*h, expand, *h, s);
     if (e == cudaSuccess) {
