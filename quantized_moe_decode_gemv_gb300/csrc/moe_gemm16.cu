@@ -81,18 +81,6 @@ Encoder encoder() {
   return fn;
 }
 
-// A 16-bit matrix of `rows` memory rows of `cols` elements; boxes of 64 columns
-// (128 bytes, swizzled) by box_rows rows.  Elements outside read as zero.
-bool encode(CUtensorMap* m, const void* p, int64_t cols, int64_t rows, int64_t ld, int box_rows) {
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
-  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
-  const cuuint32_t unit[2] = {1, 1};
-  return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(p), dims, strides, box, unit,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 using Kernel = void (*)(const GemmArgs);
 
 Kernel kernel_of(int cg, bool a_mn, bool b_mn) {
@@ -146,6 +134,37 @@ Choice choose(const GemmCall& c, int sms, size_t part_bytes) {
 }
 
 }  // namespace
+
+bool encode_rows16(CUtensorMap* m, const void* p, int64_t cols, int64_t rows, int64_t ld, int box_rows) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t unit[2] = {1, 1};
+  return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(p), dims, strides, box, unit,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t gemm16_join(const JoinCall& c, cudaStream_t s) {
+  GemmFinishArgs f{};
+  f.part = c.part;
+  f.ld_part = c.ld_part;
+  f.ksplit = c.ksplit;
+  f.batches = 1;
+  f.M = c.M;
+  f.N = c.N;
+  f.dual = c.dual;
+  f.act = c.act;
+  f.dt = c.dt;
+  f.out[0] = c.out;
+  f.ldo = c.ldo;
+  f.out_vec = c.ldo % 8 == 0 && reinterpret_cast<uintptr_t>(c.out) % 16 == 0;
+  f.nscale_gate = c.nscale_gate;
+  f.nscale = c.nscale;
+  f.bias = c.bias;
+  const int64_t n = static_cast<int64_t>(c.M) * ((c.N + 3) / 4);
+  return launch_chained(k_gemm16_finish, (n + 127) / 128, 128, 0, 1, s, f);
+}
 
 size_t gemm16_part_bytes(int M, int64_t ld_part) {
   // a K split is only taken where half of the SMs would idle: at most 76 tiles
@@ -203,12 +222,12 @@ cudaError_t gemm16_launch(const GemmCall& c, OpHandle& h, cudaStream_t s, int* l
   bool ok = true;
   for (int i = 0; i < na && ok; ++i) {
     const int64_t K = c.K[c.parts > 1 ? i : 0];
-    ok = c.a_mn ? encode(&a.ta[i], c.a[i], c.M, K, c.lda, 64) : encode(&a.ta[i], c.a[i], K, c.M, c.lda, 128);
+    ok = c.a_mn ? encode_rows16(&a.ta[i], c.a[i], c.M, K, c.lda, 64) : encode_rows16(&a.ta[i], c.a[i], K, c.M, c.lda, 128);
   }
   for (int i = 0; i < nbm && ok; ++i) {
     const int64_t K = c.K[c.parts > 1 ? i : 0];
     const int box = c.dual ? ch.bn / 2 : ch.bn / ch.cg;
-    ok = c.b_mn ? encode(&a.tb[i], c.b[i], c.N, K, c.ldb, 64) : encode(&a.tb[i], c.b[i], K, c.N, c.ldb, box);
+    ok = c.b_mn ? encode_rows16(&a.tb[i], c.b[i], c.N, K, c.ldb, 64) : encode_rows16(&a.tb[i], c.b[i], K, c.N, c.ldb, box);
   }
   if (!ok) {
     *why = "tensor map refused (operands need 16-byte aligned bases and row strides)";

@@ -203,12 +203,16 @@ __global__ void __launch_bounds__(GM_THREADS, 1) k_gemm16(const __grid_constant_
   if (warp == 0) {
     // ---------------- tensor copies ----------------
     if (lane == 0) {
+      RingPos R;
+      bool again = false;   // slots have been used before
       uint32_t q = 0;
       for (int u = worker; ok && u < units; u += nworkers) {
         const GemmUnit U = gm_unit<CG>(A, u);
         for (int i = 0; i < U.nkb; ++i, ++q) {
-          const int s = q % S;
-          if (q >= static_cast<uint32_t>(S) && !wait(&empty[s], ((q / S) - 1) & 1)) break;
+          const int s = R.slot;
+          if (again && !wait(&empty[s], R.parity ^ 1u)) break;
+          R.next(S);
+          again = again || R.slot == 0;
           int kb = U.kb0 + i, p = 0;
           if (A.parts > 1 && kb >= A.kb[0]) {
             kb -= A.kb[0];
@@ -261,16 +265,18 @@ __global__ void __launch_bounds__(GM_THREADS, 1) k_gemm16(const __grid_constant_
     // ---------------- MMAs (the pair's even CTA) ----------------
     if (rank == 0 && lane == 0) {
       const uint32_t idesc = f16_idesc(CG * 128, BN, A.dt, AMN, BMN);
-      uint32_t q = 0, n = 0;
+      RingPos R;
+      uint32_t n = 0;
       for (int u = worker; ok && u < units; u += nworkers, ++n) {
         const GemmUnit U = gm_unit<CG>(A, u);
         const int buf = n & 1;
         if (n >= 2 && !wait(&acce[buf], ((n >> 1) - 1) & 1)) break;
         tm_fence_after();
         const uint32_t d = tmem + static_cast<uint32_t>(buf * BN);
-        for (int i = 0; i < U.nkb; ++i, ++q) {
-          const int s = q % S;
-          if (!wait(&full[s], (q / S) & 1)) break;
+        for (int i = 0; i < U.nkb; ++i) {
+          const int s = R.slot;
+          if (!wait(&full[s], R.parity)) break;
+          R.next(S);
           tm_fence_after();
           const uint32_t sa = smem_u32(base + s * stage_bytes), sb = sa + 128 * 128;
 #pragma unroll

@@ -2,6 +2,7 @@
 // tracked allocations, the device a handle lives on, the GEMM launcher.
 #pragma once
 
+#include <cuda.h>   // CUtensorMap
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -107,6 +108,26 @@ struct GemmCall {
   const float *nscale_gate = nullptr, *nscale = nullptr;
   const void* bias = nullptr;
 };
+
+// Partial sums of a split K ([ksplit][M][ld_part] fp32, SwiGLU: gate at 0, up at
+// ld_part / 2) added in order, and the epilogue.
+struct JoinCall {
+  const float* part = nullptr;
+  int64_t ld_part = 0;
+  int ksplit = 1, M = 0, N = 0;
+  bool dual = false;
+  int dt = 0, act = 2;
+  void* out = nullptr;
+  int64_t ldo = 0;
+  const float *nscale_gate = nullptr, *nscale = nullptr;
+  const void* bias = nullptr;
+};
+cudaError_t gemm16_join(const JoinCall& c, cudaStream_t s);
+
+// Tensor map of a 16-bit matrix of `rows` memory rows of `cols` elements, ld
+// apart; boxes of 64 columns (128 bytes, swizzled) by box_rows rows.  Elements
+// outside read as zero.  False when the driver refuses it.
+bool encode_rows16(CUtensorMap* m, const void* p, int64_t cols, int64_t rows, int64_t ld, int box_rows);
 
 // Launches the product on `s` (asynchronous); counts its kernel launches.
 cudaError_t gemm16_launch(const GemmCall& c, OpHandle& h, cudaStream_t s, int* launches, std::string* why);

@@ -1,0 +1,426 @@
+// 4-bit weights times many token rows on tcgen05 (k_qgemm): the 4-bit linear
+// operators above the few rows that k_stream takes.
+//
+//   D[n, t] = sum_k W[n, k] x[t, k]      weights as M, tokens as N
+//
+// A CTA's tile is `mt` blocks of 128 weight rows (1 or 2; SwiGLU: the gate's and
+// the up matrix's rows of the same 128 outputs) by up to 256 tokens, with fp32
+// accumulators in tensor memory.  Tokens are N because N goes in steps of 16: a
+// ragged batch pays for at most 15 rows that are not there, where as M it would
+// pay for up to 127.  Weights are never written out: each 16-bit A tile is made
+// from the codes in shared memory, once per token tile, beside the MMAs:
+//
+//   warp 0     tensor copies of the token rows' 64-column blocks into a ring of
+//              slots
+//   warps 8-23 decode, a 16-row tile of a block each: with mt = 2 eight warps a
+//              block, with mt = 1 two groups of eight that take turns at pairs
+//              of 64-column chunks.  Codes and scales come by 16-byte
+//              asynchronous copies into a private ring, are decoded as k_stream
+//              does (an affine weight is rounded once to the 16-bit type, a
+//              relative error of at most 2^-8 or 2^-11 beside the output's own;
+//              an fp4 weight times its block scale is exact) and stored to a
+//              ring of A tiles in the 128-byte swizzle
+//   warp 1     one lane issues the MMAs of a block when its A tile and its
+//              token rows are there, and commits them to their release
+//   warp 2     owns the tensor memory
+//   warps 4-7  the epilogue: a lane a weight row, so that a warp writes 32
+//              consecutive outputs of a token; while the next tile's MMAs run
+//              where two tiles' accumulators fit the 512 columns
+//
+// Per 64-wide block and mt = 2, 256 tokens: 1024 clocks of MMA beside 32 KB of
+// token rows, 9 KB of codes (41 bytes a clock, two thirds of what L2 gives an
+// SM) and 16 x 100 decode instructions (40% of the issue slots).  A warp needs
+// 1000 clocks and more from one piece's codes to its arrival at the A tile's
+// barrier, most of it latency: hence sixteen decode warps (with eight the kernel
+// took twice as long) and A tiles as a ring of their own, as deep as fits.
+// Every wait is bounded; a role whose wait runs out sets the timeout bit of the
+// status word and winds down.
+#pragma once
+
+#include "moe_stream.cuh"
+
+namespace moe_op {
+
+constexpr int QG_THREADS = 768;
+constexpr int QG_DEC_WARPS = 16;
+constexpr int QG_MAX_SLOTS = 12;
+constexpr int QG_SMEM_MAX = 227 * 1024;
+
+struct QGemmArgs {
+  CUtensorMap tx;           // token rows [T, K], boxes of 64 columns x ntok rows
+  const uint4* codes;
+  const void* scales;
+  const float *nscale_gate, *nscale;
+  const void* bias;
+  void* out;
+  int64_t ldo;
+  float* part;              // [ksplit][T][ld_part] fp32 (ksplit > 1; SwiGLU: gate at 0, up at ld_part / 2)
+  int64_t ld_part;
+  int* status;
+  int T, N, chunks, group, sdt, act;
+  int mt, ntok, ksplit;
+  int a_slots, x_slots, depth;   // A tiles, token slots, stages of a warp's code ring
+};
+
+__host__ __device__ inline int qg_region(int ntok) {   // accumulator columns of a block
+  return ntok <= 32 ? 32 : ntok <= 64 ? 64 : ntok <= 128 ? 128 : 256;
+}
+// A stage of a warp's code ring: two chunks of its tile.
+__host__ __device__ constexpr int qg_code_bytes(int fmt, int gb) { return 2 * (512 + st_scale_bytes(fmt, gb)); }
+__host__ __device__ inline int qg_x_bytes(int ntok) { return (ntok * 128 + 1023) / 1024 * 1024; }
+__host__ __device__ inline int qg_smem_bytes(int fmt, int gb, int ntok, int a_slots, int x_slots, int depth) {
+  return a_slots * 16384 + x_slots * qg_x_bytes(ntok) + QG_DEC_WARPS * depth * qg_code_bytes(fmt, gb) +
+         8 * (4 * QG_MAX_SLOTS + 8) + 1024;
+}
+
+struct QGemmUnit {
+  int split, row, t0, c0, c1;   // first 128-row block (in blocks of mt), first token, chunks [c0, c1)
+};
+__device__ __forceinline__ QGemmUnit qg_unit(const QGemmArgs& A, int q, int row_tiles, int tok_tiles, int u) {
+  QGemmUnit U;
+  U.t0 = (u % tok_tiles) * A.ntok;
+  u /= tok_tiles;
+  U.row = u % row_tiles;
+  U.split = u / row_tiles;
+  // splits at even chunks (groups of 128 and code stages stay whole)
+  const int ns = (A.chunks + 1) / 2;
+  U.c0 = static_cast<int>(static_cast<int64_t>(U.split) * ns / A.ksplit) * 2;
+  U.c1 = min(A.chunks, static_cast<int>(static_cast<int64_t>(U.split + 1) * ns / A.ksplit) * 2);
+  return U;
+}
+
+template <int FMT, bool FP16, bool GATED, int GB>
+__global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__ QGemmArgs A) {
+  constexpr int M = GATED ? 2 : 1;
+  constexpr int DT = FP16 ? DT_FP16 : DT_BF16;
+  constexpr int SCB = st_scale_bytes(FMT, GB);
+  extern __shared__ __align__(1024) char gm_smem[];
+  char* base = gm_smem + ((1024u - (smem_u32(gm_smem) & 1023u)) & 1023u);
+  const int SA = A.a_slots, SX = A.x_slots, D = A.depth, mt = A.mt, ntok = A.ntok;
+  constexpr int code_bytes = qg_code_bytes(FMT, GB);
+  const int x_bytes = qg_x_bytes(ntok);
+  char* xs = base + SA * 16384;
+  char* rings = xs + SX * x_bytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(rings + QG_DEC_WARPS * D * code_bytes);
+  uint64_t *xfull = bars, *xempty = xfull + QG_MAX_SLOTS, *afull = xempty + QG_MAX_SLOTS, *aempty = afull + QG_MAX_SLOTS,
+           *accf = aempty + QG_MAX_SLOTS, *acce = accf + 2, *drain = acce + 2;
+  uint32_t* holder = reinterpret_cast<uint32_t*>(drain + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  const int q = FMT == W_AFFINE && A.group == 128 ? 2 : 1, nu = A.chunks / q;   // chunks of a scale group
+  const int rows_tile = GATED ? 128 : 128 * mt;
+  const int row_tiles = (A.N + rows_tile - 1) / rows_tile, tok_tiles = (A.T + ntok - 1) / ntok;
+  const int units = row_tiles * tok_tiles * A.ksplit;
+  const int region = qg_region(ntok), nbuf = 2 * mt * region <= 512 ? 2 : 1;
+  const uint32_t tm_cols = static_cast<uint32_t>(nbuf * mt * region);
+
+  if (warp == 2) tm_alloc<1>(smem_u32(holder), tm_cols);
+  if (tid == 0) {
+    tma_prefetch(&A.tx);
+    for (int i = 0; i < SX; ++i) {
+      bar_init(smem_u32(&xfull[i]), 1);
+      bar_init(smem_u32(&xempty[i]), 1);
+    }
+    for (int i = 0; i < SA; ++i) {
+      bar_init(smem_u32(&afull[i]), 8);
+      bar_init(smem_u32(&aempty[i]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      bar_init(smem_u32(&accf[b]), 1);
+      bar_init(smem_u32(&acce[b]), 4);
+    }
+    bar_init(smem_u32(drain), 1);
+    bar_fence_init();
+  }
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  const uint32_t tmem = *holder;
+  bool ok = true;
+  auto wait = [&](uint32_t b, uint32_t parity) {
+    if (bar_wait(b, parity)) return true;
+    atomicOr(A.status, STATUS_TIMEOUT);
+    ok = false;
+    return false;
+  };
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  if (warp == 0) {
+    // ---------------- token rows ----------------
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (lane == 0) {
+      RingPos X;
+      bool again = false;   // slots have been used before
+      uint32_t n = 0;
+      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+        const QGemmUnit U = qg_unit(A, q, row_tiles, tok_tiles, u);
+        for (int c = U.c0; c < U.c1; ++c, ++n) {
+          const int sl = X.slot;
+          if (again && !wait(smem_u32(&xempty[sl]), X.parity ^ 1u)) break;
+          X.next(SX);
+          again = again || X.slot == 0;
+          const uint32_t bar = smem_u32(&xfull[sl]);
+          bar_expect_tx(bar, static_cast<uint32_t>(ntok * 128));
+          tma_2d<1>(smem_u32(xs + sl * x_bytes), &A.tx, c * 64, U.t0, bar);
+        }
+      }
+      if (!ok) {   // copies already issued land before the CTA ends
+        const uint32_t used = n < static_cast<uint32_t>(SX) ? n : static_cast<uint32_t>(SX);
+        for (uint32_t j = n - used; j < n; ++j) bar_wait(smem_u32(&xfull[j % SX]), (j / SX) & 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------- MMAs ----------------
+    if (lane == 0) {
+      const uint32_t idesc = f16_idesc(128, ntok, DT, 0, 0);
+      RingPos X, R;
+      uint32_t done = 0;
+      for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++done) {
+        const QGemmUnit U = qg_unit(A, q, row_tiles, tok_tiles, u);
+        const uint32_t buf = nbuf == 2 ? done & 1 : 0, use = nbuf == 2 ? done >> 1 : done;
+        if (use > 0 && !wait(smem_u32(&acce[buf]), (use - 1) & 1)) break;
+        tm_fence_after();
+        const uint32_t d = tmem + buf * static_cast<uint32_t>(mt * region);
+        for (int c = U.c0; ok && c < U.c1; ++c) {
+          const int sl = X.slot;
+          if (!wait(smem_u32(&xfull[sl]), X.parity)) break;
+          X.next(SX);
+          const uint32_t sx = smem_u32(xs + sl * x_bytes);
+          for (int a = 0; a < mt; ++a) {
+            const int as = R.slot;
+            if (!wait(smem_u32(&afull[as]), R.parity)) break;
+            R.next(SA);
+            tm_fence_after();
+            const uint32_t sa = smem_u32(base + as * 16384);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tm_mma<1>(d + static_cast<uint32_t>(a * region), sw128_desc(sa + k * 32, 16), sw128_desc(sx + k * 32, 16),
+                        idesc, (c > U.c0) | (k != 0));
+            tm_commit<1>(smem_u32(&aempty[as]));
+          }
+          tm_commit<1>(smem_u32(&xempty[sl]));
+        }
+        if (ok) tm_commit<1>(smem_u32(&accf[buf]));
+      }
+      // all MMAs end before the shared and tensor memory go
+      tm_commit<1>(smem_u32(drain));
+      bar_wait(smem_u32(drain), 0);
+    }
+    __syncwarp();
+  } else if (warp >= 8) {
+    // ---------------- decode ----------------
+    const int dw = (warp - 8) & 7, half = (warp - 8) >> 3, g = lane >> 2, t = lane & 3;
+    const int a = mt == 2 ? half : 0, m = GATED ? half : 0;   // block of the CTA's tile; matrix
+    const int step = mt == 2 ? 2 : 4;                          // chunks from one of this warp's pairs to the next
+    const int first = mt == 2 ? 0 : 2 * half;
+    const uint32_t ring = smem_u32(rings) + (warp - 8) * D * code_bytes;
+    const int tiles16 = (A.N + 15) / 16;
+    auto tile_of = [&](const QGemmUnit& U) { return GATED ? U.row * 8 + dw : (U.row * mt + a) * 8 + dw; };
+    // unit, chunk and slot of the next stage to fill: chunks fc and fc + 1 of this warp's tile
+    int fu = blockIdx.x, fc = 0, fs = 0;
+    QGemmUnit FU{};
+    auto settle = [&] {   // to a unit that has a pair for this warp
+      while (fu < units && fc >= FU.c1) {
+        fu += gridDim.x;
+        if (fu < units) {
+          FU = qg_unit(A, q, row_tiles, tok_tiles, fu);
+          fc = FU.c0 + first;
+        }
+      }
+    };
+    if (fu < units) {
+      FU = qg_unit(A, q, row_tiles, tok_tiles, fu);
+      fc = FU.c0 + first;
+    }
+    settle();
+    auto fill_next = [&] {
+      if (fu < units) {
+        const int64_t tile = tile_of(FU);
+        if (tile < tiles16) {
+          const uint32_t st = ring + fs * code_bytes + lane * 16;
+          const bool two = fc + 1 < FU.c1;
+          const uint4* src = A.codes + ((tile * A.chunks + fc) * M + m) * 32 + lane;
+          copy16(st, src, true);
+          if (two) copy16(st + 512, src + M * 32, true);
+          // (a group of 128 has one set of scales for both chunks)
+          const char* sc = static_cast<const char*>(A.scales) + ((tile * nu + fc / q) * M + m) * SCB;
+          const int per = SCB / 16, k = lane / per;   // chunk
+          if (k < (two && q == 1 ? 2 : 1)) copy16(st + 1024, sc + k * (M - 1) * SCB + lane * 16, true);
+        }
+        fc += step;
+        settle();
+      }
+      if (++fs == D) fs = 0;
+      copies_commit();
+    };
+    for (int i = 0; i < D - 1; ++i) fill_next();
+    int cs = 0;
+    // the A ring: its tiles are counted over the CTA's blocks in the MMAs' order, this
+    // warp steps over the ones that are not its own
+    RingPos R;
+    bool again = false;   // slots have been used before
+    auto skip = [&](int n) {
+      for (int i = 0; i < n; ++i) {
+        R.next(SA);
+        again = again || R.slot == 0;
+      }
+    };
+    skip(a);
+    const uint32_t row_off = static_cast<uint32_t>((dw * 16 + g) * 128);
+    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+      const QGemmUnit U = qg_unit(A, q, row_tiles, tok_tiles, u);
+      // rows past the matrix: their A rows stay what they were, their outputs are not written
+      const bool in = tile_of(U) < tiles16;
+      if (first) skip(min(first, U.c1 - U.c0));
+      for (int c = U.c0 + first; ok && c < U.c1; c += step) {
+        __syncwarp();   // every lane has read the stage that is filled now
+        fill_next();
+        copies_wait(D - 1);
+        __syncwarp();   // every lane's copies have landed
+        const uint32_t st = ring + cs * code_bytes;
+        if (++cs == D) cs = 0;
+        uint4 w[2];
+        uint2 sv[2][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          w[i] = lds16(st + i * 512 + lane * 16);
+          const uint32_t sst = st + 1024 + (q == 1 ? i * SCB : 0);
+          if constexpr (FMT == W_AFFINE) {
+            sv[i][0] = lds8(sst + g * 8);
+            sv[i][1] = GB == 2 ? lds8(sst + 64 + g * 8) : sv[i][0];
+          } else {
+            sv[i][0].x = lds2(sst + (FMT == W_NVFP4 ? lane * 2 : g * 4 + (t & 2)));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (c + i >= U.c1) break;
+          const int as = R.slot;
+          if (again && !wait(smem_u32(&aempty[as]), R.parity ^ 1u)) break;
+          skip(mt);
+          if (in) {
+            const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            const uint32_t row = smem_u32(base + as * 16384) + row_off;
+#pragma unroll
+            for (int jj = 0; jj < 2; ++jj) {
+              uint32_t v[2][4];
+              if constexpr (FMT == W_AFFINE) {
+                const uint2 x = sv[i][jj];
+                if (A.sdt == DT) {
+                  const uint32_t s0 = __byte_perm(x.x, 0, 0x1010), b0 = __byte_perm(x.x, 0, 0x3232);
+                  const uint32_t s1 = __byte_perm(x.y, 0, 0x1010), b1 = __byte_perm(x.y, 0, 0x3232);
+#pragma unroll
+                  for (int j = 0; j < 2; ++j) {
+                    affine_word<FP16>(ws[2 * jj + j], v[j]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) v[j][r] = affine16<FP16>(v[j][r], (r & 1) ? s1 : s0, (r & 1) ? b1 : b0);
+                  }
+                } else {
+#pragma unroll
+                  for (int j = 0; j < 2; ++j) {
+                    affine_word<FP16>(ws[2 * jj + j], v[j]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                      const uint32_t y = (r & 1) ? x.y : x.x;
+                      const float sc = lo16(y, A.sdt), bb = hi16(y, A.sdt), off = affine_offset<FP16>();
+                      v[j][r] = pack2(fmaf(lo16(v[j][r], DT) - off, sc, bb), fmaf(hi16(v[j][r], DT) - off, sc, bb), DT);
+                    }
+                  }
+                }
+              } else {
+                const uint32_t s0 = fp4_scale<FMT, FP16>(sv[i][0].x, 0), s1 = fp4_scale<FMT, FP16>(sv[i][0].x, 1);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  fp4_word<FP16>(ws[2 * jj + j], v[j]);
+#pragma unroll
+                  for (int r = 0; r < 4; ++r) v[j][r] = mul2<FP16>(v[j][r], (r & 1) ? s1 : s0);
+                }
+              }
+              // eight consecutive columns of rows g and g + 8, in the 128-byte swizzle
+              const int p = FMT == W_AFFINE ? 4 * jj + t : 2 * t + jj;
+              sts16(row + ((p ^ g) * 16), v[0][0], v[0][2], v[1][0], v[1][2]);
+              sts16(row + 1024 + ((p ^ g) * 16), v[0][1], v[0][3], v[1][1], v[1][3]);
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) bar_arrive(smem_u32(&afull[as]));
+        }
+        if (mt == 1) skip(max(0, min(U.c1, c + step) - (c + 2)));   // the other group's pair
+      }
+    }
+    copies_wait(0);
+  } else if (warp >= 4) {
+    // ---------------- epilogue ----------------
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int ew = warp - 4;
+    uint32_t done = 0;
+    for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++done) {
+      const QGemmUnit U = qg_unit(A, q, row_tiles, tok_tiles, u);
+      const uint32_t buf = nbuf == 2 ? done & 1 : 0, use = nbuf == 2 ? done >> 1 : done;
+      if (!wait(smem_u32(&accf[buf]), use & 1)) break;
+      tm_fence_after();
+      const uint32_t tcol = tmem + (static_cast<uint32_t>(ew * 32) << 16) + buf * static_cast<uint32_t>(mt * region);
+      const int nt = min(ntok, A.T - U.t0);
+      const int blocks = GATED ? 1 : mt;
+      for (int a = 0; a < blocks; ++a) {
+        const int row = U.row * rows_tile + a * 128 + ew * 32 + lane;
+        const bool in = row < A.N;
+        const int rc = min(row, A.N - 1);
+        float f0 = 1.0f, f1 = 1.0f, bias = 0.0f;
+        if constexpr (FMT != W_AFFINE) {
+          f0 = __ldg((GATED ? A.nscale_gate : A.nscale) + rc);
+          if (GATED) f1 = __ldg(A.nscale + rc);
+        }
+        if (A.bias) bias = ld16(A.bias, rc, DT);
+        for (int j0 = 0; j0 < nt; j0 += 16) {
+          uint32_t r0[16], r1[16];
+          tm_ld16(tcol + a * region + j0, r0);
+          if (GATED) tm_ld16(tcol + region + j0, r1);
+          tm_wait_ld();
+          if (a == blocks - 1 && j0 + 16 >= nt) {
+            // the accumulators are in registers: the buffer may be rewritten
+            tm_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(smem_u32(&acce[buf]));
+          }
+          if (A.ksplit > 1) {
+            float* p = A.part + (static_cast<int64_t>(U.split) * A.T + U.t0 + j0) * A.ld_part + row;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (in && j0 + j < nt) {
+                p[static_cast<int64_t>(j) * A.ld_part] = __uint_as_float(r0[j]);
+                if (GATED) p[static_cast<int64_t>(j) * A.ld_part + A.ld_part / 2] = __uint_as_float(r1[j]);
+              }
+            continue;
+          }
+          if (GATED) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              r0[j] = __float_as_uint(act_value(ACT_SWIGLU, __uint_as_float(r0[j]) * f0, __uint_as_float(r1[j]) * f1));
+          } else if (A.act == ACT_RELU2) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) r0[j] = __float_as_uint(act_value(ACT_RELU2, 0.0f, __uint_as_float(r0[j]) * f0));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) r0[j] = __float_as_uint(fmaf(__uint_as_float(r0[j]), f0, bias));
+          }
+          unsigned short* p =
+              static_cast<unsigned short*>(A.out) + static_cast<int64_t>(U.t0 + j0) * A.ldo + row;
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (in && j0 + j < nt) p[static_cast<int64_t>(j) * A.ldo] = pack1(__uint_as_float(r0[j]), DT);
+        }
+      }
+    }
+  }
+  tm_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tm_fence_after();
+    tm_free<1>(tmem, tm_cols);
+  }
+}
+
+}  // namespace moe_op

@@ -7,7 +7,7 @@
 #include <new>
 
 #include "moe_op_host.h"
-#include "moe_stream.cuh"
+#include "moe_qgemm.cuh"
 
 using namespace moe_op;
 
@@ -164,68 +164,6 @@ __global__ void ql_tile(const uint32_t* q, const void* s, const void* b, const i
   }
 }
 
-// The re-laid weights as 16-bit rows [matrix][N][chunks * 64] for k_gemm16: the
-// affine value rounded once to the type (a relative error of at most 2^-9 or
-// 2^-12 beside the output's own rounding of that size), the fp4 value times its
-// block scale exactly.  One thread per (tile, chunk, matrix, lane).
-template <int FMT, bool FP16>
-__global__ void __launch_bounds__(256) ql_expand(const uint4* codes, const void* scales, int N, int G, int chunks,
-                                                 int mats, int sdt, unsigned short* out) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int tiles = (N + 15) / 16;
-  // (the call before this one may still read `out`)
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
-  if (i >= static_cast<int64_t>(tiles) * chunks * mats * 32) return;
-  constexpr int DT = FP16 ? DT_FP16 : DT_BF16;
-  const int lane = static_cast<int>(i & 31), g = lane >> 2, t = lane & 3;
-  const int64_t tc = i >> 5;
-  const int m = static_cast<int>(tc % mats);
-  const int64_t tcx = tc / mats;
-  const int c = static_cast<int>(tcx % chunks);
-  const int64_t tile = tcx / chunks;
-  const uint4 w = codes[i];
-  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-  const int64_t ld = static_cast<int64_t>(chunks) * 64;
-  const int64_t r0 = tile * 16 + g;
-  unsigned short* p0 = out + (static_cast<int64_t>(m) * N + r0) * ld + c * 64;
-  unsigned short* p1 = p0 + 8 * ld;
-#pragma unroll
-  for (int jj = 0; jj < 2; ++jj) {
-    // words 2 jj and 2 jj + 1: eight consecutive columns of two rows
-    uint32_t a[2][4];
-    if constexpr (FMT == W_AFFINE) {
-      const int64_t grp = (static_cast<int64_t>(c) * 64 + jj * 32) / G;
-      const int64_t ng = (static_cast<int64_t>(chunks) * 64 + G - 1) / G;
-      const int64_t o = G == 32 ? tc * 16 + jj * 8 + g : ((tile * ng + grp) * mats + m) * 8 + g;
-      const uint2 v = __ldg(static_cast<const uint2*>(scales) + o);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        affine_word<FP16>(ws[2 * jj + j], a[j]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint32_t sv = (r & 1) ? v.y : v.x;
-          const float s = lo16(sv, sdt), b = hi16(sv, sdt), off = affine_offset<FP16>();
-          a[j][r] = pack2(fmaf(lo16(a[j][r], DT) - off, s, b), fmaf(hi16(a[j][r], DT) - off, s, b), DT);
-        }
-      }
-    } else {
-      const int64_t o = FMT == W_NVFP4 ? tc * 32 + lane : tc * 16 + g * 2 + (t >> 1);
-      const uint32_t sb = __ldg(static_cast<const unsigned short*>(scales) + o);
-      const uint32_t s0 = fp4_scale<FMT, FP16>(sb, 0), s1 = fp4_scale<FMT, FP16>(sb, 1);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        fp4_word<FP16>(ws[2 * jj + j], a[j]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) a[j][r] = mul2<FP16>(a[j][r], (r & 1) ? s1 : s0);
-      }
-    }
-    const int col = ql_column<FMT>(2 * jj, t);
-    if (r0 < N) *reinterpret_cast<uint4*>(p0 + col) = make_uint4(a[0][0], a[0][2], a[1][0], a[1][2]);
-    if (r0 + 8 < N) *reinterpret_cast<uint4*>(p1 + col) = make_uint4(a[0][1], a[0][3], a[1][1], a[1][3]);
-  }
-}
-
 }  // namespace
 
 struct moe_qlinear : OpHandle {
@@ -235,7 +173,6 @@ struct moe_qlinear : OpHandle {
   void* scales = nullptr;
   float* factor[2] = {nullptr, nullptr};   // fp4 per-row factors: gate, up
   void* bias = nullptr;
-  unsigned short* wide = nullptr;          // 16-bit weights of one call that k_stream does not take
 };
 
 namespace {
@@ -334,6 +271,135 @@ cudaError_t run_stream(moe_qlinear& h, const StreamPlan& P, const void* x, int64
   return launch_chained(stream_kernel(c, T > 8 ? 2 : 1), P.grid, ST_THREADS, static_cast<size_t>(P.smem), 1, s, a);
 }
 
+// ---- k_qgemm launches ----
+
+using QGemmKernel = void (*)(const QGemmArgs);
+
+template <bool FP16, bool GATED>
+QGemmKernel qgemm_kernel_t(const moe_qlinear_config& c) {
+  if (c.weight_format == MOE_WFMT_NVFP4) return k_qgemm<W_NVFP4, FP16, GATED, 4>;
+  if (c.weight_format == MOE_WFMT_MXFP4) return k_qgemm<W_MXFP4, FP16, GATED, 4>;
+  return c.group_size == 32 ? k_qgemm<W_AFFINE, FP16, GATED, 2> : k_qgemm<W_AFFINE, FP16, GATED, 4>;
+}
+QGemmKernel qgemm_kernel(const moe_qlinear_config& c) {
+  const bool gated = c.act == MOE_QLINEAR_SWIGLU;
+  if (c.act_dtype == MOE_DTYPE_FP16) return gated ? qgemm_kernel_t<true, true>(c) : qgemm_kernel_t<true, false>(c);
+  return gated ? qgemm_kernel_t<false, true>(c) : qgemm_kernel_t<false, false>(c);
+}
+
+// Tile and K split of a call: the least estimated time in SM clocks.  A tile's
+// 64-wide block takes the longest of its MMAs (2 mt ntok clocks), its decode
+// (230 clocks a 128-row block at the issue rate seen) and its bytes at 40 a
+// clock; a tile that does not overlap the next one adds its epilogue.
+struct QGemmPlan {
+  int mt = 0, ntok = 0, ksplit = 1, a_slots = 0, x_slots = 0, depth = 0, units = 0;
+};
+QGemmPlan qgemm_plan(const moe_qlinear& h, int T) {
+  const moe_qlinear_config& c = h.cfg;
+  const int fmt = stream_format(c), gb = c.group_size == 32 ? 2 : 4, M = h.mats;
+  const bool gated = M == 2;
+  QGemmPlan best;
+  double best_t = 1e30;
+  for (int mt = gated ? 2 : 1; mt <= 2; ++mt) {
+    const int rows = gated ? 128 : 128 * mt;
+    const int rt = (c.out_features + rows - 1) / rows;
+    for (int tt = (T + 255) / 256, last = tt + 3; tt <= last; ++tt) {
+      const int ntok = std::max(16, ((T + tt - 1) / tt + 15) / 16 * 16);
+      if (tt > 1 && (T + ntok - 1) / ntok < tt) continue;
+      for (int ks = 1; ks <= 8; ++ks) {
+        if (ks > 1) {
+          if (h.chunks / ks < 8) break;
+          if (static_cast<size_t>(ks) * T * (c.out_features + 3) / 4 * 4 * M * 4 > h.part_bytes) break;
+        }
+        const int units = rt * tt * ks;
+        const double waves = (units + h.num_sms - 1) / h.num_sms;
+        const double kb = std::max({2.0 * mt * ntok, 230.0 * mt,
+                                    (ntok * 128.0 + 8.0 * mt * (512 + st_scale_bytes(fmt, gb))) / 40.0});
+        const bool two = 2 * mt * qg_region(ntok) <= 512;
+        const double epi = 6.0 * mt * ntok;
+        const double t = waves * (static_cast<double>(h.chunks) / ks * kb + (two ? 0.0 : epi)) + epi + 4000.0 +
+                         (ks > 1 ? 5000.0 + 0.02 * ks * T * M * c.out_features / h.num_sms : 0.0);
+        if (t < best_t) {
+          best_t = t;
+          best.mt = mt;
+          best.ntok = ntok;
+          best.ksplit = ks;
+          best.units = units;
+        }
+      }
+    }
+  }
+  // shared memory: at least two code stages, six A tiles and two token slots
+  // (which fit at 256 tokens); then in turn while there is room
+  best.depth = 2;
+  best.a_slots = 6;
+  best.x_slots = 2;
+  auto fits = [&](int a, int x, int d) { return qg_smem_bytes(fmt, gb, best.ntok, a, x, d) <= QG_SMEM_MAX; };
+  for (bool more = true; more;) {
+    more = false;
+    if (best.x_slots < QG_MAX_SLOTS && fits(best.a_slots, best.x_slots + 1, best.depth)) ++best.x_slots, more = true;
+    if (best.depth < 8 && fits(best.a_slots, best.x_slots, best.depth + 1)) ++best.depth, more = true;
+    if (best.a_slots < QG_MAX_SLOTS && fits(best.a_slots + 1, best.x_slots, best.depth)) ++best.a_slots, more = true;
+  }
+  return best;
+}
+
+cudaError_t run_qgemm(moe_qlinear& h, const void* x, int64_t ldx, int T, void* out, int64_t ldo, cudaStream_t s,
+                      std::string* why) {
+  const moe_qlinear_config& c = h.cfg;
+  const QGemmPlan P = qgemm_plan(h, T);
+  QGemmArgs a{};
+  if (!encode_rows16(&a.tx, x, c.in_features, T, ldx, P.ntok)) {
+    *why = "tensor map of x refused";
+    return cudaErrorInvalidValue;
+  }
+  a.codes = h.codes;
+  a.scales = h.scales;
+  a.nscale_gate = h.factor[0];
+  a.nscale = h.factor[1];
+  a.bias = h.bias;
+  a.out = out;
+  a.ldo = ldo;
+  a.part = h.part;
+  a.ld_part = static_cast<int64_t>((c.out_features + 3) / 4 * 4) * h.mats;
+  a.status = h.status;
+  a.T = T;
+  a.N = c.out_features;
+  a.chunks = h.chunks;
+  a.group = c.group_size;
+  a.sdt = c.scale_dtype;
+  a.act = c.act;
+  a.mt = P.mt;
+  a.ntok = P.ntok;
+  a.ksplit = P.ksplit;
+  a.a_slots = P.a_slots;
+  a.x_slots = P.x_slots;
+  a.depth = P.depth;
+  const size_t smem = static_cast<size_t>(qg_smem_bytes(stream_format(c), c.group_size == 32 ? 2 : 4, P.ntok, P.a_slots,
+                                                        P.x_slots, P.depth));
+  cudaError_t e = launch_chained(qgemm_kernel(c), std::min(P.units, h.num_sms), QG_THREADS, smem, 1, s, a);
+  ++h.last_launches;
+  if (e == cudaSuccess && P.ksplit > 1) {
+    JoinCall j;
+    j.part = a.part;
+    j.ld_part = a.ld_part;
+    j.ksplit = a.ksplit;
+    j.M = T;
+    j.N = a.N;
+    j.dual = h.mats == 2;
+    j.dt = c.act_dtype;
+    j.act = c.act;
+    j.out = out;
+    j.ldo = ldo;
+    j.nscale_gate = a.nscale_gate;
+    j.nscale = a.nscale;
+    j.bias = a.bias;
+    e = gemm16_join(j, s);
+    ++h.last_launches;
+  }
+  return e;
+}
+
 // ---- create-time launches ----
 
 template <int FMT, bool FP16>
@@ -355,16 +421,6 @@ cudaError_t relay(moe_qlinear& h, const moe_qlinear_weights& w, int* e0, cudaStr
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
-}
-
-template <int FMT, bool FP16>
-cudaError_t expand(moe_qlinear& h, cudaStream_t s) {
-  const moe_qlinear_config& c = h.cfg;
-  const int64_t n = static_cast<int64_t>((c.out_features + 15) / 16) * h.chunks * h.mats * 32;
-  ++h.last_launches;
-  return launch_chained(ql_expand<FMT, FP16>, (n + 255) / 256, 256, 0, 1, s, static_cast<const uint4*>(h.codes),
-                        static_cast<const void*>(h.scales), c.out_features, c.group_size, h.chunks, h.mats,
-                        c.scale_dtype, h.wide);
 }
 
 #define QL_BY_FORMAT(h, fn, ...)                                                              \
@@ -433,13 +489,16 @@ moe_status moe_qlinear_create(const moe_qlinear_config* cfg, const moe_qlinear_w
       e = cudaMemcpyAsync(h->bias, w->bias, static_cast<size_t>(c.out_features) * 2, cudaMemcpyDeviceToDevice, s);
   }
   StreamPlan plan;
-  if (!stream_plan(*h, c.max_tokens, &plan) && e == cudaSuccess) {
+  bool streamed = true;   // whether k_stream takes every call
+  for (int t = 1; t <= c.max_tokens && streamed; ++t) streamed = stream_plan(*h, t, &plan);
+  if (!streamed && e == cudaSuccess) {
     if (!gemm16_setup(&why)) {
       st = MOE_ERR_CUDA;
       e = cudaErrorUnknown;
     }
     if (e == cudaSuccess)
-      e = h->alloc(reinterpret_cast<void**>(&h->wide), static_cast<size_t>(h->mats) * c.out_features * h->chunks * 128);
+      e = cudaFuncSetAttribute(reinterpret_cast<const void*>(qgemm_kernel(c)),
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, QG_SMEM_MAX);
     h->part_bytes = gemm16_part_bytes(c.max_tokens, static_cast<int64_t>(h->mats) * c.out_features);
     if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->part), h->part_bytes);
   }
@@ -490,28 +549,7 @@ moe_status moe_qlinear_forward(moe_qlinear* h, const void* x, int64_t ldx, int32
   if (stream_plan(*h, T, &plan)) {
     e = run_stream(*h, plan, x, ldx, T, out, ldo, s);
   } else {
-    e = QL_BY_FORMAT(*h, expand, *h, s);
-    if (e == cudaSuccess) {
-      GemmCall g;
-      const int64_t ld = static_cast<int64_t>(h->chunks) * 64;
-      g.M = T;
-      g.N = c.out_features;
-      g.K[0] = c.in_features;
-      g.dual = h->mats == 2;
-      g.a[0] = x;
-      g.lda = ldx;
-      g.b[0] = h->wide;
-      g.b[1] = h->wide + static_cast<int64_t>(c.out_features) * ld;
-      g.ldb = ld;
-      g.dt = c.act_dtype;
-      g.act = c.act;
-      g.out[0] = out;
-      g.ldo = ldo;
-      g.nscale_gate = h->factor[0];
-      g.nscale = h->factor[1];
-      g.bias = h->bias;
-      e = gemm16_launch(g, *h, s, &h->last_launches, &why);
-    }
+    e = run_qgemm(*h, x, ldx, T, out, ldo, s, &why);
   }
   if (e != cudaSuccess) {
     h->last_error = why.empty() ? std::string("launch: ") + cudaGetErrorString(e) : why;

@@ -7,12 +7,15 @@
 // stream and around the instructions a weight costs.  One CTA of 16 warps an SM
 // takes 16-row tiles of W in turn; its warps split a tile's 64-column chunks
 // among them, each a consecutive range.  A warp has a ring of stages in shared
-// memory that one lane fills by bulk copies (a stage's codes and scales are
-// consecutive in the handle's layout), over tile boundaries and a few stages ahead of the arithmetic,
-// 45 KB or more an SM under way.  The token rows lie in shared memory as they
-// are.  The warps' partial sums meet in shared memory one tile late: a warp
-// leaves its sums of a tile, goes on to the next one, and adds its share of the
-// former when it is through, so that no warp waits for the slowest.
+// memory, a stage's codes and scales consecutive in the handle's layout, filled
+// by 16-byte asynchronous copies of its lanes, over tile boundaries and a few
+// stages ahead of the arithmetic, 45 KB or more an SM under way.  (Bulk copies,
+// one for a stage's codes and one for its scales, hold the kernel up: measured,
+// an SM starts one in about 120 clocks, 22 us where the stream asks for 11.)
+// The token rows lie in shared memory as they are.  The warps' partial sums meet
+// in shared memory one tile late: a warp leaves its sums of a tile, goes on to
+// the next one, and adds its share of the former when it is through, so that no
+// warp waits for the slowest.
 //
 // The arithmetic is warp-level mma.sync m16n8k16 with the weights as A and the
 // token rows as B (columns of absent tokens are zero): at up to 16 rows that is
@@ -99,6 +102,22 @@ __device__ __forceinline__ void affine_word(uint32_t w, uint32_t (&a)[4]) {
 template <bool FP16>
 __device__ __host__ constexpr float affine_offset() { return FP16 ? 64.0f : 128.0f; }
 
+// s q + b rounded once, two codes a register: a holds M + q, so q is exact
+template <bool FP16>
+__device__ __forceinline__ uint32_t affine16(uint32_t a, uint32_t s, uint32_t b) {
+  if (FP16) {
+    const uint32_t m = 0x54005400u;
+    const __half2 r = __hfma2(__hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&m)),
+                              *reinterpret_cast<const __half2*>(&s), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  const uint32_t m = 0x43004300u;
+  const __nv_bfloat162 r =
+      __hfma2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&m)),
+              *reinterpret_cast<const __nv_bfloat162*>(&s), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 // Where the four E2M1 codes of a half word keep their bits (fp4_place) and how
 // they come out (fp4_word).
 //   fp16 (field: sign 15, eem 11..9)  code 0: 15, 11..9   1: 12, 8..6   2: 14, 5..3   3: 13, 2..0
@@ -169,14 +188,9 @@ __host__ __device__ constexpr int st_red_floats(int mats, int nt) { return ST_WA
 __host__ __device__ inline int st_smem_bytes(int fmt, int mats, int gb, int chunks, int T, int depth) {
   const int nt = T > 8 ? 2 : 1;
   return ST_WARPS * depth * st_stage_bytes(fmt, mats, nt, gb) + T * st_row_bytes(fmt, chunks) +
-         8 * st_red_floats(mats, nt) + 8 * (ST_WARPS * depth + 3);
+         8 * st_red_floats(mats, nt) + 16;
 }
 
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-               : "memory");
-}
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
@@ -187,6 +201,9 @@ __device__ __forceinline__ void lds16_if(uint32_t* r, uint32_t a, bool in) {   /
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3])
                : "r"(a), "r"(static_cast<int>(in))
                : "memory");
+}
+__device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 __device__ __forceinline__ uint2 lds8(uint32_t a) {
   uint2 v;
@@ -215,67 +232,63 @@ __global__ void __launch_bounds__(ST_THREADS, 1) k_stream(const StreamArgs A) {
   float* const red = reinterpret_cast<float*>(xs + A.T * xrow);
   uint64_t* const bars = reinterpret_cast<uint64_t*>(red + 2 * st_red_floats(M, NT));
   const uint32_t ring = smem_u32(st_smem) + warp * D * stage;
-  const uint32_t full = smem_u32(bars) + warp * D * 8;           // [D] of this warp
-  const uint32_t xbar = smem_u32(bars) + ST_WARPS * D * 8, rbar = xbar + 8;   // rbar: two tiles
+  const uint32_t rbar = smem_u32(bars);   // two: the sums of even and odd tiles
 
   // this warp's chunks (whole groups of 128)
   const int q = FMT == W_AFFINE && A.group == 128 ? 2 : 1, nu = A.chunks / q;
   const int c_lo = q * (warp * nu / ST_WARPS), c_hi = q * ((warp + 1) * nu / ST_WARPS);
 
-  // copies of chunks [c, c + n) of a tile into a slot
+  // copies of the stage's chunks from c on of a tile into a slot
   auto fill = [&](int slot, int tile, int c) {
-    if (lane == 0) {
-      const int n = min(CB, c_hi - c);
-      const uint32_t st = ring + slot * stage, bar = full + slot * 8;
-      const int64_t tc = (static_cast<int64_t>(tile) * A.chunks + c) * M;
-      const uint32_t cbytes = static_cast<uint32_t>(n * M * 512), sbytes = static_cast<uint32_t>(n / q * M * SCB);
-      bar_expect_tx(bar, cbytes + sbytes);
-      bulk_copy(st, A.codes + tc * 32, cbytes, bar);
-      const int64_t sc = (static_cast<int64_t>(tile) * nu + c / q) * M;
-      bulk_copy(st + CB * M * 512, static_cast<const char*>(A.scales) + sc * SCB, sbytes, bar);
-    }
+    const int n = min(CB, c_hi - c);
+    const uint32_t st = ring + slot * stage + lane * 16;
+    const uint4* src = A.codes + (static_cast<int64_t>(tile) * A.chunks + c) * (M * 32) + lane;
+#pragma unroll
+    for (int i = 0; i < CB; ++i)
+      if (i < n) {
+#pragma unroll
+        for (int m = 0; m < M; ++m) copy16(st + (i * M + m) * 512, src + (i * M + m) * 32, true);
+      }
+    const char* sc = static_cast<const char*>(A.scales) + (static_cast<int64_t>(tile) * nu + c / q) * (M * SCB);
+    if (lane * 16 < n / q * M * SCB) copy16(st + CB * M * 512, sc + lane * 16, true);
   };
 
-  if (lane == 0) {
-    for (int i = 0; i < D; ++i) bar_init(full + i * 8, 1);
-  }
   if (tid == 0) {
-    bar_init(xbar, 1);
     bar_init(rbar, ST_WARPS);
     bar_init(rbar + 8, ST_WARPS);
   }
   bar_fence_init();
-  __syncthreads();
 
   // The first stages.  A handle's weights do not depend on the kernel before
   // this one in the stream; the token rows may, and the outputs may be read by it.
-  int ft = c_lo < c_hi ? static_cast<int>(blockIdx.x) : tiles, fc = c_lo;   // next stage to fill
-  auto advance = [&] {
-    fc += CB;
-    if (fc >= c_hi) {
-      fc = c_lo;
-      ft += gridDim.x;
+  int ft = c_lo < c_hi ? static_cast<int>(blockIdx.x) : tiles, fc = c_lo, fs = 0;   // next stage to fill
+  auto fill_next = [&] {
+    if (ft < tiles) {
+      fill(fs, ft, fc);
+      fc += CB;
+      if (fc >= c_hi) {
+        fc = c_lo;
+        ft += gridDim.x;
+      }
     }
+    if (++fs == D) fs = 0;
+    copies_commit();
   };
-  for (int i = 0; i < D && ft < tiles; ++i) {
-    fill(i, ft, fc);
-    advance();
-  }
+  for (int i = 0; i < D - 1; ++i) fill_next();
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (tid == 0) {
-    bar_expect_tx(xbar, static_cast<uint32_t>(A.T * A.K * 2));
-    for (int r = 0; r < A.T; ++r)
-      bulk_copy(smem_u32(xs) + r * xrow, static_cast<const char*>(A.x) + static_cast<int64_t>(r) * A.ldx * 2,
-                static_cast<uint32_t>(A.K * 2), xbar);
-  }
-  // columns past K
-  for (int i = tid; i < A.T * (A.chunks * 8 - A.K / 8); i += ST_THREADS) {
-    const int w = A.chunks * 8 - A.K / 8, r = i / w;
-    *reinterpret_cast<uint4*>(xs + r * xrow + A.K * 2 + (i - r * w) * 16) = make_uint4(0, 0, 0, 0);
+  {
+    const int w = A.chunks * 8;   // 16-byte pieces of a row; past K zeros
+    for (int i = tid; i < A.T * w; i += ST_THREADS) {
+      const int r = i / w, p = i - r * w;
+      const char* src = static_cast<const char*>(A.x) + static_cast<int64_t>(r) * A.ldx * 2;
+      copy16(smem_u32(xs) + r * xrow + p * 16, p * 8 < A.K ? src + p * 16 : src, p * 8 < A.K);
+    }
+    copies_commit();
+    copies_wait(0);
   }
   __syncthreads();
-  bool ok = bar_wait(xbar, 0);
+  bool ok = true;
 
   // this lane's 16-byte pieces of a chunk's 128 bytes of token rows g (and g + 8)
   const uint32_t x0 = smem_u32(xs) + g * xrow + (FP4 ? 32 * t : 16 * t);
@@ -310,7 +323,6 @@ __global__ void __launch_bounds__(ST_THREADS, 1) k_stream(const StreamArgs A) {
   };
 
   int slot = 0, n_done = 0, prev = 0;
-  uint32_t phase = 0;
   for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, ++n_done) {
     float acc[M][NT][4];
 #pragma unroll
@@ -318,11 +330,12 @@ __global__ void __launch_bounds__(ST_THREADS, 1) k_stream(const StreamArgs A) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.0f;
     for (int cs = c_lo; cs < c_hi; cs += CB) {
-      if (!bar_wait(full + slot * 8, phase)) {
-        ok = false;
-        break;
-      }
+      __syncwarp();   // every lane has read the slot that is filled now
+      fill_next();
+      copies_wait(D - 1);
+      __syncwarp();   // every lane's copies have landed
       const uint32_t st = ring + slot * stage;
+      if (++slot == D) slot = 0;
       const int n_c = min(CB, c_hi - cs);
       const uint32_t xc = x0 + cs * 128;
 #pragma unroll
@@ -399,18 +412,7 @@ __global__ void __launch_bounds__(ST_THREADS, 1) k_stream(const StreamArgs A) {
           }
         }
       }
-      // every lane has read the slot: its next stage
-      __syncwarp();
-      if (ft < tiles) {
-        fill(slot, ft, fc);
-        advance();
-      }
-      if (++slot == D) {
-        slot = 0;
-        phase ^= 1;
-      }
     }
-    if (!ok) break;
     // The tile before this one: its sums are complete once every warp has left
     // its own.  (A warp arrives for a tile after it has added its share of the
     // one before; so when the wait is over, the buffer of the tile two back,
@@ -434,11 +436,8 @@ __global__ void __launch_bounds__(ST_THREADS, 1) k_stream(const StreamArgs A) {
     ok = bar_wait(rbar + ((n_done - 1) & 1) * 8, ((n_done - 1) >> 1) & 1);
     if (ok) join(prev, n_done - 1);
   }
-  if (!ok) {
-    // a wait ran out: report it, and let this warp's copies under way land
-    atomicOr(A.status, STATUS_TIMEOUT);
-    for (int i = 0; i < D; ++i) bar_wait(full + i * 8, i < slot ? phase ^ 1 : phase);
-  }
+  copies_wait(0);
+  if (!ok) atomicOr(A.status, STATUS_TIMEOUT);   // a wait ran out
 }
 
 // Host: the ring of a launch, two to six stages.  False when the token rows leave
