@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(GM_THREADS, 1) k_gemm16(const __grid_constant_
   uint64_t *full = bars, *empty = bars + GM_MAX_STAGES, *accf = bars + 2 * GM_MAX_STAGES, *acce = accf + 2,
            *drain = acce + 2;
   uint32_t* holder = reinterpret_cast<uint32_t*>(drain + 1);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
   const int worker = blockIdx.x / CG, nworkers = gridDim.x / CG;
 
@@ -202,28 +202,28 @@ __global__ void __launch_bounds__(GM_THREADS, 1) k_gemm16(const __grid_constant_
 
   if (warp == 0) {
     // ---------------- tensor copies ----------------
-    if (lane == 0) {
-      RingPos R;
-      bool again = false;   // slots have been used before
-      uint32_t q = 0;
-      for (int u = worker; ok && u < units; u += nworkers) {
-        const GemmUnit U = gm_unit<CG>(A, u);
-        for (int i = 0; i < U.nkb; ++i, ++q) {
-          const int s = R.slot;
-          if (again && !wait(&empty[s], R.parity ^ 1u)) break;
-          R.next(S);
-          again = again || R.slot == 0;
-          int kb = U.kb0 + i, p = 0;
-          if (A.parts > 1 && kb >= A.kb[0]) {
-            kb -= A.kb[0];
-            p = 1;
-          }
-          const CUtensorMap* ma = &A.ta[A.batches > 1 ? U.z : p];
-          // both CTAs' copies complete on the even CTA's barrier
-          const uint32_t own = smem_u32(&full[s]), fb = CG == 2 ? cluster_addr(own, 0) : own;
-          const uint32_t da = smem_u32(base + s * stage_bytes), db = da + 128 * 128;
+    RingPos R;
+    bool again = false;   // slots have been used before
+    uint32_t q = 0;
+    for (int u = worker; ok && u < units; u += nworkers) {
+      const GemmUnit U = gm_unit<CG>(A, u);
+      const int am = U.m0 + static_cast<int>(rank) * 128, bn = U.n0 + (A.dual ? 0 : static_cast<int>(rank) * b_rows);
+      for (int i = 0; i < U.nkb; ++i, ++q) {
+        const int s = R.slot;
+        if (again && !wait(&empty[s], R.parity ^ 1u)) break;
+        R.next(S);
+        again = again || R.slot == 0;
+        int kb = U.kb0 + i, p = 0;
+        if (A.parts > 1 && kb >= A.kb[0]) {
+          kb -= A.kb[0];
+          p = 1;
+        }
+        // both CTAs' copies complete on the even CTA's barrier
+        const uint32_t own = smem_u32(&full[s]), fb = CG == 2 ? cluster_addr(own, 0) : own;
+        const uint32_t da = smem_u32(base + s * stage_bytes), db = da + 128 * 128;
+        const CUtensorMap* ma = &A.ta[A.batches > 1 ? U.z : p];
+        if (elect_lane()) {
           if (rank == 0) bar_expect_tx(own, static_cast<uint32_t>(CG * stage_bytes));
-          const int am = U.m0 + static_cast<int>(rank) * 128;
           if (AMN) {
             tma_2d<CG>(da, ma, am, kb * 64, fb);
             tma_2d<CG>(da + 8192, ma, am + 64, kb * 64, fb);
@@ -232,38 +232,35 @@ __global__ void __launch_bounds__(GM_THREADS, 1) k_gemm16(const __grid_constant_
           }
           if (A.dual) {
             if (CG == 2) {
-              tma_2d<CG>(db, &A.tb[rank], kb * 64, U.n0, fb);
+              tma_2d<CG>(db, &A.tb[rank], kb * 64, bn, fb);
             } else {
-              tma_2d<CG>(db, &A.tb[0], kb * 64, U.n0, fb);
-              tma_2d<CG>(db + static_cast<uint32_t>(BN / 2 * 128), &A.tb[1], kb * 64, U.n0, fb);
+              tma_2d<CG>(db, &A.tb[0], kb * 64, bn, fb);
+              tma_2d<CG>(db + static_cast<uint32_t>(BN / 2 * 128), &A.tb[1], kb * 64, bn, fb);
             }
+          } else if (BMN) {
+            for (int j = 0; j < b_rows; j += 64)
+              tma_2d<CG>(db + static_cast<uint32_t>(j * 128), &A.tb[p], bn + j, kb * 64, fb);
           } else {
-            const CUtensorMap* mb = &A.tb[p];
-            const int bn = U.n0 + static_cast<int>(rank) * b_rows;
-            if (BMN) {
-              for (int j = 0; j < b_rows; j += 64) tma_2d<CG>(db + static_cast<uint32_t>(j * 128), mb, bn + j, kb * 64, fb);
-            } else {
-              tma_2d<CG>(db, mb, kb * 64, bn, fb);
-            }
+            tma_2d<CG>(db, &A.tb[p], kb * 64, bn, fb);
           }
         }
-      }
-      // the last use of every slot is released (so the MMAs' arrivals at this
-      // CTA's barriers have landed) before the CTA ends; after a wait that ran
-      // out, at least the copies already issued land first
-      const uint32_t used = q < static_cast<uint32_t>(S) ? q : static_cast<uint32_t>(S);
-      for (uint32_t j = q - used; j < q; ++j) {
-        if (ok) {
-          wait(&empty[j % S], (j / S) & 1);
-        } else if (rank == 0) {
-          bar_wait(smem_u32(&full[j % S]), (j / S) & 1);
-        }
+        __syncwarp();
       }
     }
-    __syncwarp();
+    // the last use of every slot is released (so the MMAs' arrivals at this
+    // CTA's barriers have landed) before the CTA ends; after a wait that ran
+    // out, at least the copies already issued land first
+    const uint32_t used = q < static_cast<uint32_t>(S) ? q : static_cast<uint32_t>(S);
+    for (uint32_t j = q - used; j < q; ++j) {
+      if (ok) {
+        wait(&empty[j % S], (j / S) & 1);
+      } else if (rank == 0) {
+        bar_wait(smem_u32(&full[j % S]), (j / S) & 1);
+      }
+    }
   } else if (warp == 1) {
     // ---------------- MMAs (the pair's even CTA) ----------------
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       const uint32_t idesc = f16_idesc(CG * 128, BN, A.dt, AMN, BMN);
       RingPos R;
       uint32_t n = 0;
@@ -279,22 +276,26 @@ __global__ void __launch_bounds__(GM_THREADS, 1) k_gemm16(const __grid_constant_
           R.next(S);
           tm_fence_after();
           const uint32_t sa = smem_u32(base + s * stage_bytes), sb = sa + 128 * 128;
+          if (elect_lane()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint64_t da = AMN ? sw128_desc(sa + k * 2048, 8192) : sw128_desc(sa + k * 32, 16);
-            const uint64_t db = BMN ? sw128_desc(sb + k * 2048, 8192) : sw128_desc(sb + k * 32, 16);
-            tm_mma<CG>(d, da, db, idesc, (i | k) != 0);
+            for (int k = 0; k < 4; ++k) {
+              const uint64_t da = AMN ? sw128_desc(sa + k * 2048, 8192) : sw128_desc(sa + k * 32, 16);
+              const uint64_t db = BMN ? sw128_desc(sb + k * 2048, 8192) : sw128_desc(sb + k * 32, 16);
+              tm_mma<CG>(d, da, db, idesc, (i | k) != 0);
+            }
+            tm_commit<CG>(smem_u32(&empty[s]));
           }
-          tm_commit<CG>(smem_u32(&empty[s]));
+          __syncwarp();
         }
-        if (ok) tm_commit<CG>(smem_u32(&accf[buf]));
+        if (ok && elect_lane()) tm_commit<CG>(smem_u32(&accf[buf]));
+        __syncwarp();
       }
       if (!ok) {   // MMAs already issued end before their tensor memory is freed
-        tm_commit<CG>(smem_u32(drain));
+        if (elect_lane()) tm_commit<CG>(smem_u32(drain));
+        __syncwarp();
         bar_wait(smem_u32(drain), 0);
       }
     }
-    __syncwarp();
   } else if (warp >= 4) {
     // ---------------- epilogue ----------------
     const int ew = warp & 3, half = (warp - 4) >> 2;

@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
   uint64_t *xfull = bars, *xempty = xfull + QG_MAX_SLOTS, *afull = xempty + QG_MAX_SLOTS, *aempty = afull + QG_MAX_SLOTS,
            *accf = aempty + QG_MAX_SLOTS, *acce = accf + 2, *drain = acce + 2;
   uint32_t* holder = reinterpret_cast<uint32_t*>(drain + 1);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
 
   const int q = FMT == W_AFFINE && A.group == 128 ? 2 : 1, nu = A.chunks / q;   // chunks of a scale group
   const int rows_tile = GATED ? 128 : 128 * mt;
@@ -148,66 +148,67 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
   if (warp == 0) {
     // ---------------- token rows ----------------
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (lane == 0) {
-      RingPos X;
-      bool again = false;   // slots have been used before
-      uint32_t n = 0;
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-        const QGemmUnit U = qg_unit(A, q, row_tiles, tok_tiles, u);
-        for (int c = U.c0; c < U.c1; ++c, ++n) {
-          const int sl = X.slot;
-          if (again && !wait(smem_u32(&xempty[sl]), X.parity ^ 1u)) break;
-          X.next(SX);
-          again = again || X.slot == 0;
-          const uint32_t bar = smem_u32(&xfull[sl]);
+    RingPos X;
+    bool again = false;   // slots have been used before
+    uint32_t n = 0;
+    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+      const QGemmUnit U = qg_unit(A, q, row_tiles, tok_tiles, u);
+      for (int c = U.c0; c < U.c1; ++c, ++n) {
+        const int sl = X.slot;
+        if (again && !wait(smem_u32(&xempty[sl]), X.parity ^ 1u)) break;
+        X.next(SX);
+        again = again || X.slot == 0;
+        const uint32_t bar = smem_u32(&xfull[sl]);
+        if (elect_lane()) {
           bar_expect_tx(bar, static_cast<uint32_t>(ntok * 128));
           tma_2d<1>(smem_u32(xs + sl * x_bytes), &A.tx, c * 64, U.t0, bar);
         }
-      }
-      if (!ok) {   // copies already issued land before the CTA ends
-        const uint32_t used = n < static_cast<uint32_t>(SX) ? n : static_cast<uint32_t>(SX);
-        for (uint32_t j = n - used; j < n; ++j) bar_wait(smem_u32(&xfull[j % SX]), (j / SX) & 1);
+        __syncwarp();
       }
     }
-    __syncwarp();
+    if (!ok) {   // copies already issued land before the CTA ends
+      const uint32_t used = n < static_cast<uint32_t>(SX) ? n : static_cast<uint32_t>(SX);
+      for (uint32_t j = n - used; j < n; ++j) bar_wait(smem_u32(&xfull[j % SX]), (j / SX) & 1);
+    }
   } else if (warp == 1) {
     // ---------------- MMAs ----------------
-    if (lane == 0) {
-      const uint32_t idesc = f16_idesc(128, ntok, DT, 0, 0);
-      RingPos X, R;
-      uint32_t done = 0;
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++done) {
-        const QGemmUnit U = qg_unit(A, q, row_tiles, tok_tiles, u);
-        const uint32_t buf = nbuf == 2 ? done & 1 : 0, use = nbuf == 2 ? done >> 1 : done;
-        if (use > 0 && !wait(smem_u32(&acce[buf]), (use - 1) & 1)) break;
-        tm_fence_after();
-        const uint32_t d = tmem + buf * static_cast<uint32_t>(mt * region);
-        for (int c = U.c0; ok && c < U.c1; ++c) {
-          const int sl = X.slot;
-          if (!wait(smem_u32(&xfull[sl]), X.parity)) break;
-          X.next(SX);
-          const uint32_t sx = smem_u32(xs + sl * x_bytes);
-          for (int a = 0; a < mt; ++a) {
-            const int as = R.slot;
-            if (!wait(smem_u32(&afull[as]), R.parity)) break;
-            R.next(SA);
-            tm_fence_after();
-            const uint32_t sa = smem_u32(base + as * 16384);
+    const uint32_t idesc = f16_idesc(128, ntok, DT, 0, 0);
+    RingPos X, R;
+    uint32_t done = 0;
+    for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++done) {
+      const QGemmUnit U = qg_unit(A, q, row_tiles, tok_tiles, u);
+      const uint32_t buf = nbuf == 2 ? done & 1 : 0, use = nbuf == 2 ? done >> 1 : done;
+      if (use > 0 && !wait(smem_u32(&acce[buf]), (use - 1) & 1)) break;
+      tm_fence_after();
+      const uint32_t d = tmem + buf * static_cast<uint32_t>(mt * region);
+      for (int c = U.c0; ok && c < U.c1; ++c) {
+        const int sl = X.slot;
+        if (!wait(smem_u32(&xfull[sl]), X.parity)) break;
+        X.next(SX);
+        const uint32_t sx = smem_u32(xs + sl * x_bytes);
+        for (int a = 0; a < mt; ++a) {
+          const int as = R.slot;
+          if (!wait(smem_u32(&afull[as]), R.parity)) break;
+          R.next(SA);
+          tm_fence_after();
+          const uint32_t sa = smem_u32(base + as * 16384), da = d + static_cast<uint32_t>(a * region);
+          if (elect_lane()) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              tm_mma<1>(d + static_cast<uint32_t>(a * region), sw128_desc(sa + k * 32, 16), sw128_desc(sx + k * 32, 16),
-                        idesc, (c > U.c0) | (k != 0));
+              tm_mma<1>(da, sw128_desc(sa + k * 32, 16), sw128_desc(sx + k * 32, 16), idesc, (c > U.c0) | (k != 0));
             tm_commit<1>(smem_u32(&aempty[as]));
+            if (a == mt - 1) tm_commit<1>(smem_u32(&xempty[sl]));
           }
-          tm_commit<1>(smem_u32(&xempty[sl]));
+          __syncwarp();
         }
-        if (ok) tm_commit<1>(smem_u32(&accf[buf]));
       }
-      // all MMAs end before the shared and tensor memory go
-      tm_commit<1>(smem_u32(drain));
-      bar_wait(smem_u32(drain), 0);
+      if (ok && elect_lane()) tm_commit<1>(smem_u32(&accf[buf]));
+      __syncwarp();
     }
+    // all MMAs end before the shared and tensor memory go
+    if (elect_lane()) tm_commit<1>(smem_u32(drain));
     __syncwarp();
+    bar_wait(smem_u32(drain), 0);
   } else if (warp >= 8) {
     // ---------------- decode ----------------
     const int dw = (warp - 8) & 7, half = (warp - 8) >> 3, g = lane >> 2, t = lane & 3;
@@ -217,45 +218,48 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
     const uint32_t ring = smem_u32(rings) + (warp - 8) * D * code_bytes;
     const int tiles16 = (A.N + 15) / 16;
     auto tile_of = [&](const QGemmUnit& U) { return GATED ? U.row * 8 + dw : (U.row * mt + a) * 8 + dw; };
-    // unit, chunk and slot of the next stage to fill: chunks fc and fc + 1 of this warp's tile
-    int fu = blockIdx.x, fc = 0, fs = 0;
-    QGemmUnit FU{};
+    // the next stage to fill: unit, chunks fc and fc + 1, their codes and scales, the slot
+    int fu = static_cast<int>(blockIdx.x) - static_cast<int>(gridDim.x), fc = 0, fend = 0;
+    bool fin = false;   // the unit's tile is inside the matrix
+    const char *fsrc = nullptr, *fsc = nullptr;
+    uint32_t fst = ring + lane * 16;
+    const uint32_t ring_end = fst + D * code_bytes;
+    // this lane's piece of the scales: chunk and bytes (a group of 128 has one set for both chunks)
+    const int sk = lane / (SCB / 16);
+    const int s_off = sk * (M - 1) * SCB + lane * 16;
     auto settle = [&] {   // to a unit that has a pair for this warp
-      while (fu < units && fc >= FU.c1) {
+      while (fu < units && fc >= fend) {
         fu += gridDim.x;
-        if (fu < units) {
-          FU = qg_unit(A, q, row_tiles, tok_tiles, fu);
-          fc = FU.c0 + first;
-        }
+        if (fu >= units) break;
+        const QGemmUnit FU = qg_unit(A, q, row_tiles, tok_tiles, fu);
+        fc = FU.c0 + first;
+        fend = FU.c1;
+        const int64_t tile = tile_of(FU);
+        fin = tile < tiles16;
+        fsrc = reinterpret_cast<const char*>(A.codes + ((tile * A.chunks + fc) * M + m) * 32 + lane);
+        fsc = static_cast<const char*>(A.scales) + ((tile * nu + fc / q) * M + m) * SCB + s_off;
       }
     };
-    if (fu < units) {
-      FU = qg_unit(A, q, row_tiles, tok_tiles, fu);
-      fc = FU.c0 + first;
-    }
     settle();
     auto fill_next = [&] {
       if (fu < units) {
-        const int64_t tile = tile_of(FU);
-        if (tile < tiles16) {
-          const uint32_t st = ring + fs * code_bytes + lane * 16;
-          const bool two = fc + 1 < FU.c1;
-          const uint4* src = A.codes + ((tile * A.chunks + fc) * M + m) * 32 + lane;
-          copy16(st, src, true);
-          if (two) copy16(st + 512, src + M * 32, true);
-          // (a group of 128 has one set of scales for both chunks)
-          const char* sc = static_cast<const char*>(A.scales) + ((tile * nu + fc / q) * M + m) * SCB;
-          const int per = SCB / 16, k = lane / per;   // chunk
-          if (k < (two && q == 1 ? 2 : 1)) copy16(st + 1024, sc + k * (M - 1) * SCB + lane * 16, true);
+        if (fin) {
+          const bool two = fc + 1 < fend;
+          copy16(fst, fsrc, true);
+          if (two) copy16(fst + 512, fsrc + M * 512, true);
+          if (sk < (two && q == 1 ? 2 : 1)) copy16(fst + 1024, fsc, true);
+          fsrc += step * (M * 512);
+          fsc += (q == 1 ? step : step / 2) * (M * SCB);
         }
         fc += step;
-        settle();
+        if (fc >= fend) settle();
       }
-      if (++fs == D) fs = 0;
+      fst += code_bytes;
+      if (fst == ring_end) fst = ring + lane * 16;
       copies_commit();
     };
     for (int i = 0; i < D - 1; ++i) fill_next();
-    int cs = 0;
+    uint32_t cst = ring;
     // the A ring: its tiles are counted over the CTA's blocks in the MMAs' order, this
     // warp steps over the ones that are not its own
     RingPos R;
@@ -276,10 +280,12 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
       for (int c = U.c0 + first; ok && c < U.c1; c += step) {
         __syncwarp();   // every lane has read the stage that is filled now
         fill_next();
-        copies_wait(D - 1);
+        if (D == 3) copies_wait_n<2>();
+        else copies_wait_n<1>();
         __syncwarp();   // every lane's copies have landed
-        const uint32_t st = ring + cs * code_bytes;
-        if (++cs == D) cs = 0;
+        const uint32_t st = cst;
+        cst += code_bytes;
+        if (cst == ring + D * code_bytes) cst = ring;
         uint4 w[2];
         uint2 sv[2][2];
 #pragma unroll
@@ -293,12 +299,17 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
             sv[i][0].x = lds2(sst + (FMT == W_NVFP4 ? lane * 2 : g * 4 + (t & 2)));
           }
         }
+        // the pair's A tiles; they are released in order, so the later one's release is both's
+        const bool two = c + 1 < U.c1;
+        const int as0 = R.slot;
+        if (two) skip(mt);
+        const int as1 = R.slot;
+        if (again && !wait(smem_u32(&aempty[as1]), R.parity ^ 1u)) break;
+        skip(mt);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          if (c + i >= U.c1) break;
-          const int as = R.slot;
-          if (again && !wait(smem_u32(&aempty[as]), R.parity ^ 1u)) break;
-          skip(mt);
+          if (i == 1 && !two) break;
+          const int as = i == 0 ? as0 : as1;
           if (in) {
             const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
             const uint32_t row = smem_u32(base + as * 16384) + row_off;
@@ -343,9 +354,12 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
               sts16(row + 1024 + ((p ^ g) * 16), v[0][1], v[0][3], v[1][1], v[1][3]);
             }
           }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) bar_arrive(smem_u32(&afull[as]));
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(smem_u32(&afull[as0]));
+          if (two) bar_arrive(smem_u32(&afull[as1]));
         }
         if (mt == 1) skip(max(0, min(U.c1, c + step) - (c + 2)));   // the other group's pair
       }

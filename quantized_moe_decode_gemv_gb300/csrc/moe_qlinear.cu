@@ -338,7 +338,7 @@ QGemmPlan qgemm_plan(const moe_qlinear& h, int T) {
   for (bool more = true; more;) {
     more = false;
     if (best.x_slots < QG_MAX_SLOTS && fits(best.a_slots, best.x_slots + 1, best.depth)) ++best.x_slots, more = true;
-    if (best.depth < 8 && fits(best.a_slots, best.x_slots, best.depth + 1)) ++best.depth, more = true;
+    if (best.depth < 3 && fits(best.a_slots, best.x_slots, best.depth + 1)) ++best.depth, more = true;
     if (best.a_slots < QG_MAX_SLOTS && fits(best.a_slots + 1, best.x_slots, best.depth)) ++best.a_slots, more = true;
   }
   return best;
