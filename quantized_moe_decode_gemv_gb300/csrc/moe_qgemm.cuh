@@ -10,31 +10,32 @@
 // pay for up to 127.  Weights are never written out: each 16-bit A tile is made
 // from the codes in shared memory, once per token tile, beside the MMAs:
 //
-//   warp 0     tensor copies of the token rows' 64-column blocks into a ring of
-//              slots
+// A slot of the ring holds a 64-wide K block: the tile's A blocks and its token
+// rows.  One barrier says that both are there and one that the MMAs are done with
+// them -- a wait or a commit is some 250 clocks in the warp that issues the MMAs,
+// and with barriers for each A block and for the token rows it could not keep the
+// tensor pipe fed.
+//
+//   warp 0     tensor copies of the token rows
 //   warps 8-23 decode, a 16-row tile of a block each: with mt = 2 eight warps a
 //              block, with mt = 1 two groups of eight that take turns at pairs
-//              of 64-column chunks.  Codes and scales come by 16-byte
-//              asynchronous copies into a private ring, are decoded as k_stream
-//              does (an affine weight is rounded once to the 16-bit type, a
-//              relative error of at most 2^-8 or 2^-11 beside the output's own;
-//              an fp4 weight times its block scale is exact) and stored to a
-//              ring of A tiles in the 128-byte swizzle
-//   warp 1     one lane issues the MMAs of a block when its A tile and its
-//              token rows are there, and commits them to their release
+//              of K blocks.  Codes and scales come by 16-byte asynchronous copies
+//              into a private ring, are decoded as k_stream does (an affine weight
+//              is rounded once to the 16-bit type, a relative error of at most
+//              2^-8 or 2^-11 beside the output's own; an fp4 weight times its
+//              block scale is exact) and stored in the 128-byte swizzle
+//   warp 1     issues the MMAs of a slot and commits them to its release
 //   warp 2     owns the tensor memory
-//   warps 4-7  the epilogue: a lane a weight row, so that a warp writes 32
-//              consecutive outputs of a token; while the next tile's MMAs run
-//              where two tiles' accumulators fit the 512 columns
+//   warps 4-7  the epilogue: a lane a weight row; four lanes exchange four tokens'
+//              values so that each stores four consecutive outputs of one.  It
+//              overlaps the next tile's MMAs where two tiles' accumulators fit
+//              the 512 columns
 //
-// Per 64-wide block and mt = 2, 256 tokens: 1024 clocks of MMA beside 32 KB of
-// token rows, 9 KB of codes (41 bytes a clock, two thirds of what L2 gives an
-// SM) and 16 x 100 decode instructions (40% of the issue slots).  A warp needs
-// 1000 clocks and more from one piece's codes to its arrival at the A tile's
-// barrier, most of it latency: hence sixteen decode warps (with eight the kernel
-// took twice as long) and A tiles as a ring of their own, as deep as fits.
-// Every wait is bounded; a role whose wait runs out sets the timeout bit of the
-// status word and winds down.
+// Per K block and mt = 2, 256 tokens: 1024 clocks of MMA beside 32 KB of token
+// rows, 9 KB of codes (41 bytes a clock, two thirds of what L2 gives an SM) and
+// 16 x 100 decode instructions (40% of the issue slots).  Every wait is bounded;
+// a role whose wait runs out sets the timeout bit of the status word and winds
+// down.
 #pragma once
 
 #include "moe_stream.cuh"
@@ -43,7 +44,7 @@ namespace moe_op {
 
 constexpr int QG_THREADS = 768;
 constexpr int QG_DEC_WARPS = 16;
-constexpr int QG_MAX_SLOTS = 12;
+constexpr int QG_MAX_SLOTS = 8;
 constexpr int QG_SMEM_MAX = 227 * 1024;
 
 struct QGemmArgs {
@@ -54,12 +55,13 @@ struct QGemmArgs {
   const void* bias;
   void* out;
   int64_t ldo;
+  int out_vec;              // out and ldo allow 8-byte stores
   float* part;              // [ksplit][T][ld_part] fp32 (ksplit > 1; SwiGLU: gate at 0, up at ld_part / 2)
   int64_t ld_part;
   int* status;
   int T, N, chunks, group, sdt, act;
   int mt, ntok, ksplit;
-  int a_slots, x_slots, depth;   // A tiles, token slots, stages of a warp's code ring
+  int slots, depth;         // of the ring, and stages of a warp's code ring (2 or 3)
 };
 
 __host__ __device__ inline int qg_region(int ntok) {   // accumulator columns of a block
@@ -67,10 +69,9 @@ __host__ __device__ inline int qg_region(int ntok) {   // accumulator columns of
 }
 // A stage of a warp's code ring: two chunks of its tile.
 __host__ __device__ constexpr int qg_code_bytes(int fmt, int gb) { return 2 * (512 + st_scale_bytes(fmt, gb)); }
-__host__ __device__ inline int qg_x_bytes(int ntok) { return (ntok * 128 + 1023) / 1024 * 1024; }
-__host__ __device__ inline int qg_smem_bytes(int fmt, int gb, int ntok, int a_slots, int x_slots, int depth) {
-  return a_slots * 16384 + x_slots * qg_x_bytes(ntok) + QG_DEC_WARPS * depth * qg_code_bytes(fmt, gb) +
-         8 * (4 * QG_MAX_SLOTS + 8) + 1024;
+__host__ __device__ inline int qg_slot_bytes(int mt, int ntok) { return mt * 16384 + (ntok * 128 + 1023) / 1024 * 1024; }
+__host__ __device__ inline int qg_smem_bytes(int fmt, int gb, int mt, int ntok, int slots, int depth) {
+  return slots * qg_slot_bytes(mt, ntok) + QG_DEC_WARPS * depth * qg_code_bytes(fmt, gb) + 8 * (2 * QG_MAX_SLOTS + 8) + 1024;
 }
 
 struct QGemmUnit {
@@ -96,14 +97,12 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
   constexpr int SCB = st_scale_bytes(FMT, GB);
   extern __shared__ __align__(1024) char gm_smem[];
   char* base = gm_smem + ((1024u - (smem_u32(gm_smem) & 1023u)) & 1023u);
-  const int SA = A.a_slots, SX = A.x_slots, D = A.depth, mt = A.mt, ntok = A.ntok;
+  const int S = A.slots, D = A.depth, mt = A.mt, ntok = A.ntok;
   constexpr int code_bytes = qg_code_bytes(FMT, GB);
-  const int x_bytes = qg_x_bytes(ntok);
-  char* xs = base + SA * 16384;
-  char* rings = xs + SX * x_bytes;
+  const int slot_bytes = qg_slot_bytes(mt, ntok);
+  char* rings = base + S * slot_bytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(rings + QG_DEC_WARPS * D * code_bytes);
-  uint64_t *xfull = bars, *xempty = xfull + QG_MAX_SLOTS, *afull = xempty + QG_MAX_SLOTS, *aempty = afull + QG_MAX_SLOTS,
-           *accf = aempty + QG_MAX_SLOTS, *acce = accf + 2, *drain = acce + 2;
+  uint64_t *full = bars, *empty = full + QG_MAX_SLOTS, *accf = empty + QG_MAX_SLOTS, *acce = accf + 2, *drain = acce + 2;
   uint32_t* holder = reinterpret_cast<uint32_t*>(drain + 1);
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
 
@@ -117,13 +116,9 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
   if (warp == 2) tm_alloc<1>(smem_u32(holder), tm_cols);
   if (tid == 0) {
     tma_prefetch(&A.tx);
-    for (int i = 0; i < SX; ++i) {
-      bar_init(smem_u32(&xfull[i]), 1);
-      bar_init(smem_u32(&xempty[i]), 1);
-    }
-    for (int i = 0; i < SA; ++i) {
-      bar_init(smem_u32(&afull[i]), 8);
-      bar_init(smem_u32(&aempty[i]), 1);
+    for (int i = 0; i < S; ++i) {
+      bar_init(smem_u32(&full[i]), 8 * mt + 1);   // eight decode warps a block, and the token rows' copy
+      bar_init(smem_u32(&empty[i]), 1);
     }
     for (int b = 0; b < 2; ++b) {
       bar_init(smem_u32(&accf[b]), 1);
@@ -148,32 +143,32 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
   if (warp == 0) {
     // ---------------- token rows ----------------
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    RingPos X;
+    RingPos R;
     bool again = false;   // slots have been used before
     uint32_t n = 0;
     for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
       const QGemmUnit U = qg_unit(A, q, row_tiles, tok_tiles, u);
       for (int c = U.c0; c < U.c1; ++c, ++n) {
-        const int sl = X.slot;
-        if (again && !wait(smem_u32(&xempty[sl]), X.parity ^ 1u)) break;
-        X.next(SX);
-        again = again || X.slot == 0;
-        const uint32_t bar = smem_u32(&xfull[sl]);
+        const int sl = R.slot;
+        if (again && !wait(smem_u32(&empty[sl]), R.parity ^ 1u)) break;
+        R.next(S);
+        again = again || R.slot == 0;
+        const uint32_t bar = smem_u32(&full[sl]);
         if (elect_lane()) {
           bar_expect_tx(bar, static_cast<uint32_t>(ntok * 128));
-          tma_2d<1>(smem_u32(xs + sl * x_bytes), &A.tx, c * 64, U.t0, bar);
+          tma_2d<1>(smem_u32(base + sl * slot_bytes + mt * 16384), &A.tx, c * 64, U.t0, bar);
         }
         __syncwarp();
       }
     }
     if (!ok) {   // copies already issued land before the CTA ends
-      const uint32_t used = n < static_cast<uint32_t>(SX) ? n : static_cast<uint32_t>(SX);
-      for (uint32_t j = n - used; j < n; ++j) bar_wait(smem_u32(&xfull[j % SX]), (j / SX) & 1);
+      const uint32_t used = n < static_cast<uint32_t>(S) ? n : static_cast<uint32_t>(S);
+      for (uint32_t j = n - used; j < n; ++j) bar_wait(smem_u32(&full[j % S]), (j / S) & 1);
     }
   } else if (warp == 1) {
     // ---------------- MMAs ----------------
     const uint32_t idesc = f16_idesc(128, ntok, DT, 0, 0);
-    RingPos X, R;
+    RingPos R;
     uint32_t done = 0;
     for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++done) {
       const QGemmUnit U = qg_unit(A, q, row_tiles, tok_tiles, u);
@@ -181,26 +176,25 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
       if (use > 0 && !wait(smem_u32(&acce[buf]), (use - 1) & 1)) break;
       tm_fence_after();
       const uint32_t d = tmem + buf * static_cast<uint32_t>(mt * region);
-      for (int c = U.c0; ok && c < U.c1; ++c) {
-        const int sl = X.slot;
-        if (!wait(smem_u32(&xfull[sl]), X.parity)) break;
-        X.next(SX);
-        const uint32_t sx = smem_u32(xs + sl * x_bytes);
-        for (int a = 0; a < mt; ++a) {
-          const int as = R.slot;
-          if (!wait(smem_u32(&afull[as]), R.parity)) break;
-          R.next(SA);
-          tm_fence_after();
-          const uint32_t sa = smem_u32(base + as * 16384), da = d + static_cast<uint32_t>(a * region);
-          if (elect_lane()) {
+      for (int c = U.c0; c < U.c1; ++c) {
+        const int sl = R.slot;
+        if (!wait(smem_u32(&full[sl]), R.parity)) break;
+        R.next(S);
+        tm_fence_after();
+        const uint32_t sa = smem_u32(base + sl * slot_bytes), sx = sa + static_cast<uint32_t>(mt) * 16384;
+        if (elect_lane()) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tm_mma<1>(d, sw128_desc(sa + k * 32, 16), sw128_desc(sx + k * 32, 16), idesc, (c > U.c0) | (k != 0));
+          if (mt == 2) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              tm_mma<1>(da, sw128_desc(sa + k * 32, 16), sw128_desc(sx + k * 32, 16), idesc, (c > U.c0) | (k != 0));
-            tm_commit<1>(smem_u32(&aempty[as]));
-            if (a == mt - 1) tm_commit<1>(smem_u32(&xempty[sl]));
+              tm_mma<1>(d + static_cast<uint32_t>(region), sw128_desc(sa + 16384 + k * 32, 16),
+                        sw128_desc(sx + k * 32, 16), idesc, (c > U.c0) | (k != 0));
           }
-          __syncwarp();
+          tm_commit<1>(smem_u32(&empty[sl]));
         }
+        __syncwarp();
       }
       if (ok && elect_lane()) tm_commit<1>(smem_u32(&accf[buf]));
       __syncwarp();
@@ -260,17 +254,17 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
     };
     for (int i = 0; i < D - 1; ++i) fill_next();
     uint32_t cst = ring;
-    // the A ring: its tiles are counted over the CTA's blocks in the MMAs' order, this
-    // warp steps over the ones that are not its own
     RingPos R;
     bool again = false;   // slots have been used before
     auto skip = [&](int n) {
       for (int i = 0; i < n; ++i) {
-        R.next(SA);
+        R.next(S);
         again = again || R.slot == 0;
       }
     };
-    skip(a);
+    // With four slots or more a pair of K blocks is taken at once: the slots are
+    // released in order, so the later one's release is both's.
+    const bool pairs = S >= 4;
     const uint32_t row_off = static_cast<uint32_t>((dw * 16 + g) * 128);
     for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
       const QGemmUnit U = qg_unit(A, q, row_tiles, tok_tiles, u);
@@ -299,20 +293,19 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
             sv[i][0].x = lds2(sst + (FMT == W_NVFP4 ? lane * 2 : g * 4 + (t & 2)));
           }
         }
-        // the pair's A tiles; they are released in order, so the later one's release is both's
         const bool two = c + 1 < U.c1;
-        const int as0 = R.slot;
-        if (two) skip(mt);
-        const int as1 = R.slot;
-        if (again && !wait(smem_u32(&aempty[as1]), R.parity ^ 1u)) break;
-        skip(mt);
+        const int sl0 = R.slot;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (i == 1 && !two) break;
-          const int as = i == 0 ? as0 : as1;
+          if (pairs && i == 0 && two) skip(1);
+          const int sl = pairs && i == 0 ? sl0 : R.slot;
+          if (!(pairs && i == 1)) {
+            if (again && !wait(smem_u32(&empty[R.slot]), R.parity ^ 1u)) break;
+          }
           if (in) {
             const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-            const uint32_t row = smem_u32(base + as * 16384) + row_off;
+            const uint32_t row = smem_u32(base + sl * slot_bytes + a * 16384) + row_off;
 #pragma unroll
             for (int jj = 0; jj < 2; ++jj) {
               uint32_t v[2][4];
@@ -354,14 +347,18 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
               sts16(row + 1024 + ((p ^ g) * 16), v[0][1], v[0][3], v[1][1], v[1][3]);
             }
           }
+          if (!pairs || i == 1 || !two) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+              if (pairs && i == 1) bar_arrive(smem_u32(&full[sl0]));
+              bar_arrive(smem_u32(&full[sl]));
+            }
+            skip(1);
+          }
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-          bar_arrive(smem_u32(&afull[as0]));
-          if (two) bar_arrive(smem_u32(&afull[as1]));
-        }
-        if (mt == 1) skip(max(0, min(U.c1, c + step) - (c + 2)));   // the other group's pair
+        if (!ok) break;
+        if (mt == 1) skip(max(0, min(U.c1, c + step) - (c + 2)));   // the other group's K blocks
       }
     }
     copies_wait(0);
@@ -420,11 +417,28 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
 #pragma unroll
             for (int j = 0; j < 16; ++j) r0[j] = __float_as_uint(fmaf(__uint_as_float(r0[j]), f0, bias));
           }
-          unsigned short* p =
-              static_cast<unsigned short*>(A.out) + static_cast<int64_t>(U.t0 + j0) * A.ldo + row;
+          unsigned short* p = static_cast<unsigned short*>(A.out) + static_cast<int64_t>(U.t0 + j0) * A.ldo;
+          if (A.out_vec && row - lane + 32 <= A.N) {
+            // tokens j..j+3: after two exchanges lane l has token j + l % 4 of rows l / 4 * 4 on
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (in && j0 + j < nt) p[static_cast<int64_t>(j) * A.ldo] = pack1(__uint_as_float(r0[j]), DT);
+            for (int j = 0; j < 16; j += 4) {
+              uint32_t v0 = pack2(__uint_as_float(r0[j]), __uint_as_float(r0[j + 1]), DT);
+              uint32_t v1 = pack2(__uint_as_float(r0[j + 2]), __uint_as_float(r0[j + 3]), DT);
+              const uint32_t x0 = __shfl_xor_sync(0xFFFFFFFFu, v0, 1), x1 = __shfl_xor_sync(0xFFFFFFFFu, v1, 1);
+              const uint32_t sel = lane & 1 ? 0x3276u : 0x5410u;
+              v0 = __byte_perm(v0, x0, sel);
+              v1 = __byte_perm(v1, x1, sel);
+              const uint32_t y = __shfl_xor_sync(0xFFFFFFFFu, lane & 2 ? v0 : v1, 2);
+              const uint2 w = lane & 2 ? make_uint2(y, v1) : make_uint2(v0, y);
+              const int tk = j + (lane & 3);
+              if (j0 + tk < nt)
+                *reinterpret_cast<uint2*>(p + static_cast<int64_t>(tk) * A.ldo + (row - (lane & 3))) = w;
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (in && j0 + j < nt) p[static_cast<int64_t>(j) * A.ldo + row] = pack1(__uint_as_float(r0[j]), DT);
+          }
         }
       }
     }

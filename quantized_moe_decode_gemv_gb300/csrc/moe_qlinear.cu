@@ -292,7 +292,7 @@ QGemmKernel qgemm_kernel(const moe_qlinear_config& c) {
 // (230 clocks a 128-row block at the issue rate seen) and its bytes at 40 a
 // clock; a tile that does not overlap the next one adds its epilogue.
 struct QGemmPlan {
-  int mt = 0, ntok = 0, ksplit = 1, a_slots = 0, x_slots = 0, depth = 0, units = 0;
+  int mt = 0, ntok = 0, ksplit = 1, slots = 0, depth = 0, units = 0;
 };
 QGemmPlan qgemm_plan(const moe_qlinear& h, int T) {
   const moe_qlinear_config& c = h.cfg;
@@ -329,18 +329,14 @@ QGemmPlan qgemm_plan(const moe_qlinear& h, int T) {
       }
     }
   }
-  // shared memory: at least two code stages, six A tiles and two token slots
-  // (which fit at 256 tokens); then in turn while there is room
+  // shared memory: slots first, then a third code stage (two slots and two stages
+  // fit at 256 tokens)
   best.depth = 2;
-  best.a_slots = 6;
-  best.x_slots = 2;
-  auto fits = [&](int a, int x, int d) { return qg_smem_bytes(fmt, gb, best.ntok, a, x, d) <= QG_SMEM_MAX; };
-  for (bool more = true; more;) {
-    more = false;
-    if (best.x_slots < QG_MAX_SLOTS && fits(best.a_slots, best.x_slots + 1, best.depth)) ++best.x_slots, more = true;
-    if (best.depth < 3 && fits(best.a_slots, best.x_slots, best.depth + 1)) ++best.depth, more = true;
-    if (best.a_slots < QG_MAX_SLOTS && fits(best.a_slots + 1, best.x_slots, best.depth)) ++best.a_slots, more = true;
-  }
+  best.slots = 2;
+  auto fits = [&](int n, int d) { return qg_smem_bytes(fmt, gb, best.mt, best.ntok, n, d) <= QG_SMEM_MAX; };
+  while (best.slots < 4 && fits(best.slots + 1, 2)) ++best.slots;
+  if (fits(best.slots, 3)) best.depth = 3;
+  while (best.slots < QG_MAX_SLOTS && fits(best.slots + 1, best.depth)) ++best.slots;
   return best;
 }
 
@@ -360,6 +356,7 @@ cudaError_t run_qgemm(moe_qlinear& h, const void* x, int64_t ldx, int T, void* o
   a.bias = h.bias;
   a.out = out;
   a.ldo = ldo;
+  a.out_vec = ldo % 4 == 0 && reinterpret_cast<uintptr_t>(out) % 8 == 0;
   a.part = h.part;
   a.ld_part = static_cast<int64_t>((c.out_features + 3) / 4 * 4) * h.mats;
   a.status = h.status;
@@ -372,11 +369,10 @@ cudaError_t run_qgemm(moe_qlinear& h, const void* x, int64_t ldx, int T, void* o
   a.mt = P.mt;
   a.ntok = P.ntok;
   a.ksplit = P.ksplit;
-  a.a_slots = P.a_slots;
-  a.x_slots = P.x_slots;
+  a.slots = P.slots;
   a.depth = P.depth;
-  const size_t smem = static_cast<size_t>(qg_smem_bytes(stream_format(c), c.group_size == 32 ? 2 : 4, P.ntok, P.a_slots,
-                                                        P.x_slots, P.depth));
+  const size_t smem = static_cast<size_t>(qg_smem_bytes(stream_format(c), c.group_size == 32 ? 2 : 4, P.mt, P.ntok,
+                                                        P.slots, P.depth));
   cudaError_t e = launch_chained(qgemm_kernel(c), std::min(P.units, h.num_sms), QG_THREADS, smem, 1, s, a);
   ++h.last_launches;
   if (e == cudaSuccess && P.ksplit > 1) {

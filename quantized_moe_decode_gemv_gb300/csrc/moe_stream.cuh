@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(ST_THREADS, 1) k_stream(const StreamArgs A) {
   const uint32_t rbar = smem_u32(bars);   // two: the sums of even and odd tiles
 
   // this warp's chunks (whole groups of 128)
-  const int q = FMT == W_AFFINE && A.group == 128 ? 2 : 1, nu = A.chunks / q;
+  const int qs = FMT == W_AFFINE && A.group == 128 ? 1 : 0, q = 1 << qs, nu = A.chunks >> qs;
   const int c_lo = q * (warp * nu / ST_WARPS), c_hi = q * ((warp + 1) * nu / ST_WARPS);
 
   // copies of the stage's chunks from c on of a tile into a slot
@@ -249,8 +249,8 @@ __global__ void __launch_bounds__(ST_THREADS, 1) k_stream(const StreamArgs A) {
 #pragma unroll
         for (int m = 0; m < M; ++m) copy16(st + (i * M + m) * 512, src + (i * M + m) * 32, true);
       }
-    const char* sc = static_cast<const char*>(A.scales) + (static_cast<int64_t>(tile) * nu + c / q) * (M * SCB);
-    if (lane * 16 < n / q * M * SCB) copy16(st + CB * M * 512, sc + lane * 16, true);
+    const char* sc = static_cast<const char*>(A.scales) + (static_cast<int64_t>(tile) * nu + (c >> qs)) * (M * SCB);
+    if (lane * 16 < (n >> qs) * (M * SCB)) copy16(st + CB * M * 512, sc + lane * 16, true);
   };
 
   if (tid == 0) {
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(ST_THREADS, 1) k_stream(const StreamArgs A) {
 #pragma unroll
             for (int m = 0; m < M; ++m) {
               const uint4 w = lds16(st + (i * M + m) * 512 + lane * 16);
-              const uint2 v = lds8(st + CB * M * 512 + (i / q * M + m) * SCB + f * 64 + g * 8);
+              const uint2 v = lds8(st + CB * M * 512 + ((i >> qs) * M + m) * SCB + f * 64 + g * 8);
               const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
               float d[NT][4];
 #pragma unroll
