@@ -304,6 +304,13 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
             if (again && !wait(smem_u32(&empty[R.slot]), R.parity ^ 1u)) break;
           }
           if (in) {
+            // (groups of 32: odd rows store their halves in the other order, so that eight lanes' stores touch all banks)
+            if (!st_wide(FMT, GB) && (g & 1)) {
+              w[i] = make_uint4(w[i].z, w[i].w, w[i].x, w[i].y);
+              const uint2 x = sv[i][0];
+              sv[i][0] = sv[i][1];
+              sv[i][1] = x;
+            }
             const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
             const uint32_t row = smem_u32(base + sl * slot_bytes + a * 16384) + row_off;
 #pragma unroll
@@ -342,7 +349,7 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
                 }
               }
               // eight consecutive columns of rows g and g + 8, in the 128-byte swizzle
-              const int p = FMT == W_AFFINE ? 4 * jj + t : 2 * t + jj;
+              const int p = st_wide(FMT, GB) ? 2 * t + jj : 4 * (jj ^ (g & 1)) + t;
               sts16(row + ((p ^ g) * 16), v[0][0], v[0][2], v[1][0], v[1][2]);
               sts16(row + 1024 + ((p ^ g) * 16), v[0][1], v[0][3], v[1][1], v[1][3]);
             }

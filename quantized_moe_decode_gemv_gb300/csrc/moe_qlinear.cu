@@ -79,11 +79,6 @@ __global__ void ql_rows(const uint8_t* s, const float* matrix_scale, int N, int 
   factor[row] = bad ? __int_as_float(0x7FC00000) : f;
 }
 
-template <int FMT>
-__device__ __forceinline__ int ql_column(int j, int t) {
-  return FMT == W_AFFINE ? 32 * (j >> 1) + 8 * t + 4 * (j & 1) : 16 * t + 4 * j;
-}
-
 // Row-major codes [N, K/8] and scales -> the streaming order of k_stream:
 //   codes  [N/16][chunks][matrices][32 lanes][4 words], rows and columns past
 //          the matrix zero
@@ -92,8 +87,8 @@ __device__ __forceinline__ int ql_column(int j, int t) {
 //          nvfp4           [N/16][chunks][matrices][8][4 blocks][2] bytes
 //          mxfp4           [N/16][chunks][matrices][8][2 blocks][2] bytes
 //          (the pair: rows g and g + 8)
-// Word j of lane (g, t) holds four columns of rows g and g + 8: from 32 (j / 2)
-// + 8 t + 4 (j % 2) on in an affine chunk, from 16 t + 4 j on in an fp4 one.
+// Word j of lane (g, t) holds four columns of rows g and g + 8: from 16 t + 4 j on,
+// or, of affine codes in groups of 32, from 32 (j / 2) + 8 t + 4 (j % 2) on.
 // One thread per (tile, chunk, lane) of matrix `m`.
 template <int FMT, bool FP16>
 __global__ void ql_tile(const uint32_t* q, const void* s, const void* b, const int* e0, int N, int K, int G, int chunks,
@@ -111,7 +106,7 @@ __global__ void ql_tile(const uint32_t* q, const void* s, const void* b, const i
   uint32_t sbytes[2] = {0u, 0u};   // fp4: the lane's 16 columns share a block
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int col = c * 64 + ql_column<FMT>(j, t);
+    const int col = c * 64 + (FMT == W_AFFINE && G == 32 ? 32 * (j >> 1) + 8 * t + 4 * (j & 1) : 16 * t + 4 * j);
     uint32_t half[2];   // four codes of rows g and g + 8
 #pragma unroll
     for (int h = 0; h < 2; ++h) {

@@ -25,22 +25,21 @@
 // The MMA's k index may run through a chunk's 64 columns in any order that A
 // and B share; each format takes the one that makes its loads wide and its
 // scales few (lane (g, t) of a warp: rows g and g + 8, four lanes t a row):
-//   affine   columns 8 t and 32 + 8 t on; codes re-laid at create time (ql_tile) so that a
-//            16-byte load holds the lane's codes of the chunk, and a shift and a
-//            mask-and-or make M + q (M = 128 in bf16, 64 in fp16: the code in
-//            the low mantissa bits of M).  The MMAs of a group accumulate apart
-//            and fold in fp32:  y += s d + (b - M s) X,  X the group's sum of x,
-//            which one more MMA with ones for A delivers in the same lanes.
-//            (M is small so that the cancellation costs at most 7 bits of the
-//            fp32 accumulator.)
-//   fp4      columns 16 t .. 16 t + 15, one scale block (or half of one): a lane
-//            needs two scales a chunk.  Codes are re-laid so that sign, exponent
-//            and mantissa bits land in a 16-bit float's fields by shifts and
-//            masks: the E2M1 value times 2^-126 (bf16) or 2^-14 (fp16),
-//            subnormals included.  One packed multiply applies the block scale;
-//            the product of an E2M1 value (2 significant bits) and an E4M3 (4
-//            bits) or E8M0 scale is exact in both types, so the accumulators run
-//            through all of K and a per-row fp32 factor closes the sum (ql_rows).
+//   all but groups of 32: columns 16 t .. 16 t + 15 of the chunk, a scale group
+//            or part of one, so that a lane needs two scales a chunk
+//   affine in groups of 32: columns 8 t and 32 + 8 t on, eight of each group
+// Affine codes are re-laid at create time (ql_tile) so that a 16-byte load holds
+// the lane's codes of the chunk, and a shift and a mask-and-or make M + q (M = 128
+// in bf16, 64 in fp16: the code in the low mantissa bits of M).  The MMAs of a
+// group accumulate apart and fold in fp32:  y += s d + (b - M s) X,  X the group's
+// sum of x, which one more MMA with ones for A delivers in the same lanes.  (M is
+// small so that the cancellation costs at most 7 bits of the fp32 accumulator.)
+// fp4 codes are re-laid so that sign, exponent and mantissa bits land in a 16-bit
+// float's fields by shifts and masks: the E2M1 value times 2^-126 (bf16) or 2^-14
+// (fp16), subnormals included.  One packed multiply applies the block scale; the
+// product of an E2M1 value (2 significant bits) and an E4M3 (4 bits) or E8M0 scale
+// is exact in both types, so the accumulators run through all of K and a per-row
+// fp32 factor closes the sum (ql_rows).
 #pragma once
 
 #include "moe_sm103.cuh"
@@ -66,7 +65,7 @@ struct StreamArgs {
   int chunks;               // ceil(K / 64)
   int group;                // affine: group size
   int act, sdt;             // activation; affine: type of the scales
-  int depth;                // stages of a warp's ring
+  int depth;                // stages of a warp's ring, 2..4
   int* status;
 };
 
@@ -168,26 +167,26 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t s) {
 // Shared memory of a launch:
 //   [ST_WARPS rings of `depth` stages][token rows][partial sums, two tiles][barriers]
 // A stage holds st_chunks() chunks: their matrices x 512 bytes of codes, then the
-// scales.  Token rows are 16 (fp4) or 64 bytes longer than K, so that the
-// fragment reads of eight lanes (two rows of four lanes) touch all banks once.
+// scales.  Token rows are 16 bytes longer than K (64 with groups of 32), so that
+// the fragment reads of eight lanes (two rows of four lanes) touch all banks once.
 __host__ __device__ constexpr int st_scale_bytes(int fmt, int gb) {   // a chunk and matrix (affine: a group)
   return fmt == W_AFFINE ? (gb == 2 ? 128 : 64) : fmt == W_NVFP4 ? 64 : 32;
 }
-// Chunks of a stage: 2 KB of codes, or half with two token tiles, whose rows and
+// Whether a lane's columns of a chunk are consecutive (else eight of each half).
+__host__ __device__ constexpr bool st_wide(int fmt, int gb) { return fmt != W_AFFINE || gb == 4; }
+// Chunks of a stage: 4 KB of codes, or 1 KB with two token tiles, whose rows and
 // sums need the room (affine: at least the two chunks of a group of 128).
 __host__ __device__ constexpr int st_chunks(int fmt, int mats, int nt, int gb) {
-  return nt == 1 ? 4 / mats : (fmt == W_AFFINE && gb == 4) ? 2 : 2 / mats;
+  return nt == 1 ? 8 / mats : (fmt == W_AFFINE && gb == 4) ? 2 : 2 / mats;
 }
 __host__ __device__ constexpr int st_stage_bytes(int fmt, int mats, int nt, int gb) {
   return mats * st_chunks(fmt, mats, nt, gb) * (512 + st_scale_bytes(fmt, gb));
 }
-__host__ __device__ inline int st_row_bytes(int fmt, int chunks) {
-  return chunks * 128 + (fmt == W_NVFP4 || fmt == W_MXFP4 ? 16 : 64);
-}
+__host__ __device__ inline int st_row_bytes(int fmt, int gb, int chunks) { return chunks * 128 + (st_wide(fmt, gb) ? 16 : 64); }
 __host__ __device__ constexpr int st_red_floats(int mats, int nt) { return ST_WARPS * mats * nt * 128; }
 __host__ __device__ inline int st_smem_bytes(int fmt, int mats, int gb, int chunks, int T, int depth) {
   const int nt = T > 8 ? 2 : 1;
-  return ST_WARPS * depth * st_stage_bytes(fmt, mats, nt, gb) + T * st_row_bytes(fmt, chunks) +
+  return ST_WARPS * depth * st_stage_bytes(fmt, mats, nt, gb) + T * st_row_bytes(fmt, gb, chunks) +
          8 * st_red_floats(mats, nt) + 16;
 }
 
@@ -221,13 +220,13 @@ template <int FMT, bool FP16, bool GATED, int NT, int GB>
 __global__ void __launch_bounds__(ST_THREADS, 1) k_stream(const StreamArgs A) {
   constexpr int M = GATED ? 2 : 1;
   constexpr int DT = FP16 ? DT_FP16 : DT_BF16;
-  constexpr bool FP4 = FMT == W_NVFP4 || FMT == W_MXFP4;
+  constexpr bool FP4 = FMT == W_NVFP4 || FMT == W_MXFP4, WIDE = st_wide(FMT, GB);
   constexpr int SCB = st_scale_bytes(FMT, GB);
   extern __shared__ __align__(128) char st_smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   constexpr int CB = st_chunks(FMT, M, NT, GB), stage = st_stage_bytes(FMT, M, NT, GB);
   const int tiles = (A.N + 15) / 16, D = A.depth;
-  const int xrow = st_row_bytes(FMT, A.chunks);
+  const int xrow = st_row_bytes(FMT, GB, A.chunks);
   char* const xs = st_smem + ST_WARPS * D * stage;
   float* const red = reinterpret_cast<float*>(xs + A.T * xrow);
   uint64_t* const bars = reinterpret_cast<uint64_t*>(red + 2 * st_red_floats(M, NT));
@@ -238,19 +237,45 @@ __global__ void __launch_bounds__(ST_THREADS, 1) k_stream(const StreamArgs A) {
   const int qs = FMT == W_AFFINE && A.group == 128 ? 1 : 0, q = 1 << qs, nu = A.chunks >> qs;
   const int c_lo = q * (warp * nu / ST_WARPS), c_hi = q * ((warp + 1) * nu / ST_WARPS);
 
-  // copies of the stage's chunks from c on of a tile into a slot
-  auto fill = [&](int slot, int tile, int c) {
-    const int n = min(CB, c_hi - c);
-    const uint32_t st = ring + slot * stage + lane * 16;
-    const uint4* src = A.codes + (static_cast<int64_t>(tile) * A.chunks + c) * (M * 32) + lane;
+  // the next stage to fill: tile, chunk, their codes and scales, the slot
+  int ft = c_lo < c_hi ? static_cast<int>(blockIdx.x) : tiles, fc = c_lo;
+  const char *fsrc = nullptr, *fsc = nullptr;
+  uint32_t fst = ring + lane * 16;
+  const uint32_t ring_end = fst + D * stage;
+  auto settle = [&] {   // to the start of this warp's chunks of tile ft
+    fc = c_lo;
+    fsrc = reinterpret_cast<const char*>(A.codes) + (static_cast<int64_t>(ft) * A.chunks + c_lo) * (M * 512) + lane * 16;
+    fsc = static_cast<const char*>(A.scales) + (static_cast<int64_t>(ft) * nu + (c_lo >> qs)) * (M * SCB) + lane * 16;
+  };
+  auto fill_next = [&] {
+    if (ft < tiles) {
+      const int n = min(CB, c_hi - fc);
 #pragma unroll
-    for (int i = 0; i < CB; ++i)
-      if (i < n) {
+      for (int i = 0; i < CB; ++i)
+        if (i < n) {
 #pragma unroll
-        for (int m = 0; m < M; ++m) copy16(st + (i * M + m) * 512, src + (i * M + m) * 32, true);
+          for (int m = 0; m < M; ++m) copy16(fst + (i * M + m) * 512, fsrc + (i * M + m) * 512, true);
+        }
+      const int sbytes = (n >> qs) * (M * SCB);
+#pragma unroll
+      for (int i = 0; i < (CB * M * SCB + 511) / 512; ++i)
+        if (lane * 16 + i * 512 < sbytes) copy16(fst + CB * M * 512 + i * 512, fsc + i * 512, true);
+      fsrc += CB * M * 512;
+      fsc += (CB >> qs) * (M * SCB);
+      fc += CB;
+      if (fc >= c_hi) {
+        ft += gridDim.x;
+        settle();
       }
-    const char* sc = static_cast<const char*>(A.scales) + (static_cast<int64_t>(tile) * nu + (c >> qs)) * (M * SCB);
-    if (lane * 16 < (n >> qs) * (M * SCB)) copy16(st + CB * M * 512, sc + lane * 16, true);
+    }
+    fst += stage;
+    if (fst == ring_end) fst = ring + lane * 16;
+    copies_commit();
+  };
+  auto stage_here = [&] {   // until the oldest stage has landed
+    if (D == 2) copies_wait_n<1>();
+    else if (D == 3) copies_wait_n<2>();
+    else copies_wait_n<3>();
   };
 
   if (tid == 0) {
@@ -261,19 +286,7 @@ __global__ void __launch_bounds__(ST_THREADS, 1) k_stream(const StreamArgs A) {
 
   // The first stages.  A handle's weights do not depend on the kernel before
   // this one in the stream; the token rows may, and the outputs may be read by it.
-  int ft = c_lo < c_hi ? static_cast<int>(blockIdx.x) : tiles, fc = c_lo, fs = 0;   // next stage to fill
-  auto fill_next = [&] {
-    if (ft < tiles) {
-      fill(fs, ft, fc);
-      fc += CB;
-      if (fc >= c_hi) {
-        fc = c_lo;
-        ft += gridDim.x;
-      }
-    }
-    if (++fs == D) fs = 0;
-    copies_commit();
-  };
+  settle();
   for (int i = 0; i < D - 1; ++i) fill_next();
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -291,7 +304,7 @@ __global__ void __launch_bounds__(ST_THREADS, 1) k_stream(const StreamArgs A) {
   bool ok = true;
 
   // this lane's 16-byte pieces of a chunk's 128 bytes of token rows g (and g + 8)
-  const uint32_t x0 = smem_u32(xs) + g * xrow + (FP4 ? 32 * t : 16 * t);
+  const uint32_t x0 = smem_u32(xs) + g * xrow + (WIDE ? 32 * t : 16 * t);
   uint32_t bf[NT][8];
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -322,7 +335,8 @@ __global__ void __launch_bounds__(ST_THREADS, 1) k_stream(const StreamArgs A) {
     static_cast<unsigned short*>(A.out)[static_cast<int64_t>(tok) * A.ldo + row] = pack1(y, DT);
   };
 
-  int slot = 0, n_done = 0, prev = 0;
+  uint32_t cst = ring;
+  int n_done = 0, prev = 0;
   for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, ++n_done) {
     float acc[M][NT][4];
 #pragma unroll
@@ -332,10 +346,11 @@ __global__ void __launch_bounds__(ST_THREADS, 1) k_stream(const StreamArgs A) {
     for (int cs = c_lo; cs < c_hi; cs += CB) {
       __syncwarp();   // every lane has read the slot that is filled now
       fill_next();
-      copies_wait(D - 1);
+      stage_here();
       __syncwarp();   // every lane's copies have landed
-      const uint32_t st = ring + slot * stage;
-      if (++slot == D) slot = 0;
+      const uint32_t st = cst;
+      cst += stage;
+      if (cst == ring + D * stage) cst = ring;
       const int n_c = min(CB, c_hi - cs);
       const uint32_t xc = x0 + cs * 128;
 #pragma unroll
@@ -346,7 +361,7 @@ __global__ void __launch_bounds__(ST_THREADS, 1) k_stream(const StreamArgs A) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           lds16_if(bf[n], xc + n * 8 * xrow + i * 128, n * 8 + g < A.T);
-          lds16_if(bf[n] + 4, xc + n * 8 * xrow + i * 128 + (FP4 ? 16 : 64), n * 8 + g < A.T);
+          lds16_if(bf[n] + 4, xc + n * 8 * xrow + i * 128 + (WIDE ? 16 : 64), n * 8 + g < A.T);
         }
         if constexpr (FMT == W_AFFINE) {
           constexpr uint32_t one = FP16 ? 0x3C003C00u : 0x3F803F80u;
@@ -440,7 +455,7 @@ __global__ void __launch_bounds__(ST_THREADS, 1) k_stream(const StreamArgs A) {
   if (!ok) atomicOr(A.status, STATUS_TIMEOUT);   // a wait ran out
 }
 
-// Host: the ring of a launch, two to six stages.  False when the token rows leave
+// Host: the ring of a launch, two to four stages.  False when the token rows leave
 // no room for it.
 struct StreamPlan {
   int depth = 0, grid = 0, smem = 0;
@@ -448,7 +463,7 @@ struct StreamPlan {
 constexpr int ST_SMEM_MAX = 226 * 1024;
 inline bool st_plan(int fmt, bool gated, int gb, int chunks, int T, int N, int sms, StreamPlan* P) {
   const int mats = gated ? 2 : 1;
-  int d = 6;
+  int d = 4;
   while (d >= 2 && st_smem_bytes(fmt, mats, gb, chunks, T, d) > ST_SMEM_MAX) --d;
   if (d < 2) return false;
   const int tiles = (N + 15) / 16, rounds = (tiles + sms - 1) / sms;
