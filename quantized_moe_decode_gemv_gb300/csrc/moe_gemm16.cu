@@ -96,37 +96,42 @@ constexpr size_t kPartCap = 64ull << 20;   // most bytes of split-K partial sums
 constexpr int kMaxSplit = 16;
 
 struct Choice {
-  int cg, bn, ksplit;
+  int cg, bn, ksplit, sub;
 };
 
-// Tile shape and K split.  The estimate of a launch is its waves over the SMs
-// times a tile's K blocks, each the larger of its MMA time (2 BN clocks a
-// 64-wide block for 128 rows) and its copy time (64 bytes a clock and SM), plus
-// the accumulators' way out.
+// Tile shape and K split: the least estimated time in SM clocks.  A launch takes
+// its waves over the SMs times a tile's K blocks, each the longest of its MMAs
+// (2 BN clocks for 128 rows), its bytes (48 a clock and SM; rows past M are not
+// fetched) and the issuing warp's wait and commit (400 clocks a slot), then the last
+// accumulators' way out.  A K split adds the partial sums' way through memory and
+// a launch: on 333 x 4096 x 3712, two splits of 256-column tiles took 22.0 us where
+// one pass of 128-column tiles takes 16.5; on 9 x 11008 x 2048, one pass took 33 us
+// where four splits take 12.
 Choice choose(const GemmCall& c, int sms, size_t part_bytes) {
-  Choice best{1, 64, 1};
+  Choice best{1, 64, 1, 2};
   double best_t = 1e30;
   const int nkb = (c.K[0] + 63) / 64 + (c.parts > 1 ? (c.K[1] + 63) / 64 : 0);
   for (int cg = 1; cg <= 2; ++cg) {
     if (cg == 2 && c.M <= 128) continue;
     for (int bn = 64; bn <= 256; bn *= 2) {
       if (c.b_mn && bn / cg < 64) continue;   // MN-major B comes in 64-column blocks
-      const int bn_out = c.dual ? bn / 2 : bn;
+      const int bn_out = c.dual ? bn / 2 : bn, sub = bn == 256 ? 1 : 2;
       const int64_t tiles = static_cast<int64_t>((c.M + cg * 128 - 1) / (cg * 128)) * ((c.N + bn_out - 1) / bn_out) *
                             c.batches;
       const int slots = sms / cg;
-      int ks = 1;
-      if (tiles * 2 <= slots) {
-        ks = static_cast<int>(std::min<int64_t>({static_cast<int64_t>(slots / tiles), kMaxSplit, std::max(1, nkb / 4)}));
+      const double bytes = std::min(128, c.M) * 128.0 + bn / cg * 128.0;
+      const double kb = std::max({2.0 * bn, bytes / 48.0, 400.0 / sub});
+      for (int ks = 1; ks <= kMaxSplit; ++ks) {
         const int64_t ldp = static_cast<int64_t>((c.N + 3) / 4 * 4) * (c.dual ? 2 : 1);
-        while (ks > 1 && static_cast<size_t>(ks) * c.batches * c.M * ldp * 4 > part_bytes) --ks;
-      }
-      const double waves = static_cast<double>((tiles * ks + slots - 1) / slots);
-      const double kb = std::max(2.0 * bn, (16384.0 + bn / cg * 128.0) / 64.0);
-      const double t = waves * ((nkb + ks - 1) / ks) * kb + bn * 8.0 + 1500.0 + (ks > 1 ? 4000.0 : 0.0);
-      if (t < best_t) {
-        best_t = t;
-        best = Choice{cg, bn, ks};
+        const double part = static_cast<double>(ks) * c.batches * c.M * ldp * 4;
+        if (ks > 1 && (tiles * ks > slots || nkb / ks < 4 || part > static_cast<double>(part_bytes))) break;
+        const double waves = static_cast<double>((tiles * ks + slots - 1) / slots);
+        const double t = waves * ((nkb + ks - 1) / ks) * kb + bn * 12.0 + (waves - 1) * 1500.0 +
+                         (ks > 1 ? 7000.0 + part * 2 / (sms * 30.0) : 0.0);
+        if (t < best_t) {
+          best_t = t;
+          best = Choice{cg, bn, ks, sub};
+        }
       }
     }
   }
@@ -233,16 +238,16 @@ cudaError_t gemm16_launch(const GemmCall& c, OpHandle& h, cudaStream_t s, int* l
     *why = "tensor map refused (operands need 16-byte aligned bases and row strides)";
     return cudaErrorInvalidValue;
   }
-  const int nkb = (a.kb[0] + a.kb[1] + ch.ksplit - 1) / ch.ksplit;
-  a.stages = std::min(GM_MAX_STAGES, std::max(2, nkb + 1));
-  while (gm_smem_bytes(ch.bn, ch.cg, a.stages) > GM_SMEM_MAX) --a.stages;
+  a.sub = ch.sub;
+  a.stages = GM_MAX_STAGES;
+  while (gm_smem_bytes(ch.bn, ch.cg, a.stages, a.sub) > GM_SMEM_MAX) --a.stages;
   const int bn_out = c.dual ? ch.bn / 2 : ch.bn;
   const int64_t units = static_cast<int64_t>((c.M + ch.cg * 128 - 1) / (ch.cg * 128)) * ((c.N + bn_out - 1) / bn_out) *
                         c.batches * ch.ksplit;
   const int64_t workers = std::min<int64_t>(units, h.num_sms / ch.cg);
 
   cudaError_t e = launch_chained(kernel_of(ch.cg, c.a_mn, c.b_mn), workers * ch.cg, GM_THREADS,
-                                 static_cast<size_t>(gm_smem_bytes(ch.bn, ch.cg, a.stages)), ch.cg, s, a);
+                                 static_cast<size_t>(gm_smem_bytes(ch.bn, ch.cg, a.stages, a.sub)), ch.cg, s, a);
   ++*launches;
   if (e == cudaSuccess && ch.ksplit > 1) {
     GemmFinishArgs f{};

@@ -29,6 +29,9 @@
 // persistent and walk the tiles in groups of 8 tile rows, whose operands stay
 // in L2 while the columns pass.
 //
+// A slot of the ring holds one 64-wide K block, or two where a block's MMAs are
+// short: a wait and a commit cost the issuing warp some 400 clocks.
+//
 // Every wait is bounded; a role whose wait runs out sets the timeout bit of
 // the status word and winds down.
 #pragma once
@@ -51,7 +54,7 @@ struct GemmArgs {
   int batches;          // batch z: ta[z], tb[0], out[z]
   int parts, kb[2];     // K parts (part p: ta[p], tb[p]) and their 64-wide K blocks
   int ksplit;           // K blocks divided over this many units; partial sums to `part`
-  int stages;
+  int stages, sub;      // slots of the ring and K blocks a slot
   int dt;               // 16-bit type of A, B and the output
   int act;
   void* out[2];
@@ -66,8 +69,8 @@ struct GemmArgs {
 };
 
 __host__ __device__ inline int gm_stage_bytes(int BN, int CG) { return 128 * 128 + BN / CG * 128; }
-__host__ __device__ inline int gm_smem_bytes(int BN, int CG, int stages) {
-  return stages * gm_stage_bytes(BN, CG) + GM_EPI_BYTES + 8 * (2 * GM_MAX_STAGES + 6) + 1024;
+__host__ __device__ inline int gm_smem_bytes(int BN, int CG, int stages, int sub) {
+  return stages * sub * gm_stage_bytes(BN, CG) + GM_EPI_BYTES + 8 * (2 * GM_MAX_STAGES + 6) + 1024;
 }
 
 struct GemmUnit {
@@ -157,7 +160,8 @@ __global__ void __launch_bounds__(GM_THREADS, 1) k_gemm16(const __grid_constant_
   const int S = A.stages, BN = A.BN;
   const int b_rows = BN / CG;                       // B rows this CTA holds
   const int stage_bytes = gm_stage_bytes(BN, CG);
-  char* epi = base + S * stage_bytes;
+  const int slot_bytes = A.sub * stage_bytes;
+  char* epi = base + S * slot_bytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(epi + GM_EPI_BYTES);
   uint64_t *full = bars, *empty = bars + GM_MAX_STAGES, *accf = bars + 2 * GM_MAX_STAGES, *acce = accf + 2,
            *drain = acce + 2;
@@ -208,40 +212,42 @@ __global__ void __launch_bounds__(GM_THREADS, 1) k_gemm16(const __grid_constant_
     for (int u = worker; ok && u < units; u += nworkers) {
       const GemmUnit U = gm_unit<CG>(A, u);
       const int am = U.m0 + static_cast<int>(rank) * 128, bn = U.n0 + (A.dual ? 0 : static_cast<int>(rank) * b_rows);
-      for (int i = 0; i < U.nkb; ++i, ++q) {
-        const int s = R.slot;
+      for (int i = 0; i < U.nkb; i += A.sub, ++q) {
+        const int s = R.slot, nk = min(A.sub, U.nkb - i);
         if (again && !wait(&empty[s], R.parity ^ 1u)) break;
         R.next(S);
         again = again || R.slot == 0;
-        int kb = U.kb0 + i, p = 0;
-        if (A.parts > 1 && kb >= A.kb[0]) {
-          kb -= A.kb[0];
-          p = 1;
-        }
         // both CTAs' copies complete on the even CTA's barrier
         const uint32_t own = smem_u32(&full[s]), fb = CG == 2 ? cluster_addr(own, 0) : own;
-        const uint32_t da = smem_u32(base + s * stage_bytes), db = da + 128 * 128;
-        const CUtensorMap* ma = &A.ta[A.batches > 1 ? U.z : p];
         if (elect_lane()) {
-          if (rank == 0) bar_expect_tx(own, static_cast<uint32_t>(CG * stage_bytes));
-          if (AMN) {
-            tma_2d<CG>(da, ma, am, kb * 64, fb);
-            tma_2d<CG>(da + 8192, ma, am + 64, kb * 64, fb);
-          } else {
-            tma_2d<CG>(da, ma, kb * 64, am, fb);
-          }
-          if (A.dual) {
-            if (CG == 2) {
-              tma_2d<CG>(db, &A.tb[rank], kb * 64, bn, fb);
-            } else {
-              tma_2d<CG>(db, &A.tb[0], kb * 64, bn, fb);
-              tma_2d<CG>(db + static_cast<uint32_t>(BN / 2 * 128), &A.tb[1], kb * 64, bn, fb);
+          if (rank == 0) bar_expect_tx(own, static_cast<uint32_t>(CG * stage_bytes * nk));
+          for (int j = 0; j < nk; ++j) {
+            int kb = U.kb0 + i + j, p = 0;
+            if (A.parts > 1 && kb >= A.kb[0]) {
+              kb -= A.kb[0];
+              p = 1;
             }
-          } else if (BMN) {
-            for (int j = 0; j < b_rows; j += 64)
-              tma_2d<CG>(db + static_cast<uint32_t>(j * 128), &A.tb[p], bn + j, kb * 64, fb);
-          } else {
-            tma_2d<CG>(db, &A.tb[p], kb * 64, bn, fb);
+            const uint32_t da = smem_u32(base + s * slot_bytes + j * stage_bytes), db = da + 128 * 128;
+            const CUtensorMap* ma = &A.ta[A.batches > 1 ? U.z : p];
+            if (AMN) {
+              tma_2d<CG>(da, ma, am, kb * 64, fb);
+              tma_2d<CG>(da + 8192, ma, am + 64, kb * 64, fb);
+            } else {
+              tma_2d<CG>(da, ma, kb * 64, am, fb);
+            }
+            if (A.dual) {
+              if (CG == 2) {
+                tma_2d<CG>(db, &A.tb[rank], kb * 64, bn, fb);
+              } else {
+                tma_2d<CG>(db, &A.tb[0], kb * 64, bn, fb);
+                tma_2d<CG>(db + static_cast<uint32_t>(BN / 2 * 128), &A.tb[1], kb * 64, bn, fb);
+              }
+            } else if (BMN) {
+              for (int r = 0; r < b_rows; r += 64)
+                tma_2d<CG>(db + static_cast<uint32_t>(r * 128), &A.tb[p], bn + r, kb * 64, fb);
+            } else {
+              tma_2d<CG>(db, &A.tb[p], kb * 64, bn, fb);
+            }
           }
         }
         __syncwarp();
@@ -270,18 +276,20 @@ __global__ void __launch_bounds__(GM_THREADS, 1) k_gemm16(const __grid_constant_
         if (n >= 2 && !wait(&acce[buf], ((n >> 1) - 1) & 1)) break;
         tm_fence_after();
         const uint32_t d = tmem + static_cast<uint32_t>(buf * BN);
-        for (int i = 0; i < U.nkb; ++i) {
-          const int s = R.slot;
+        for (int i = 0; i < U.nkb; i += A.sub) {
+          const int s = R.slot, nk = min(A.sub, U.nkb - i);
           if (!wait(&full[s], R.parity)) break;
           R.next(S);
           tm_fence_after();
-          const uint32_t sa = smem_u32(base + s * stage_bytes), sb = sa + 128 * 128;
           if (elect_lane()) {
+            for (int j = 0; j < nk; ++j) {
+              const uint32_t sa = smem_u32(base + s * slot_bytes + j * stage_bytes), sb = sa + 128 * 128;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint64_t da = AMN ? sw128_desc(sa + k * 2048, 8192) : sw128_desc(sa + k * 32, 16);
-              const uint64_t db = BMN ? sw128_desc(sb + k * 2048, 8192) : sw128_desc(sb + k * 32, 16);
-              tm_mma<CG>(d, da, db, idesc, (i | k) != 0);
+              for (int k = 0; k < 4; ++k) {
+                const uint64_t da = AMN ? sw128_desc(sa + k * 2048, 8192) : sw128_desc(sa + k * 32, 16);
+                const uint64_t db = BMN ? sw128_desc(sb + k * 2048, 8192) : sw128_desc(sb + k * 32, 16);
+                tm_mma<CG>(d, da, db, idesc, (i | j | k) != 0);
+              }
             }
             tm_commit<CG>(smem_u32(&empty[s]));
           }

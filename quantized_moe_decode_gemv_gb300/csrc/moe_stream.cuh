@@ -174,10 +174,10 @@ __host__ __device__ constexpr int st_scale_bytes(int fmt, int gb) {   // a chunk
 }
 // Whether a lane's columns of a chunk are consecutive (else eight of each half).
 __host__ __device__ constexpr bool st_wide(int fmt, int gb) { return fmt != W_AFFINE || gb == 4; }
-// Chunks of a stage: 4 KB of codes, or 1 KB with two token tiles, whose rows and
+// Chunks of a stage: 2 KB of codes, or 1 KB with two token tiles, whose rows and
 // sums need the room (affine: at least the two chunks of a group of 128).
 __host__ __device__ constexpr int st_chunks(int fmt, int mats, int nt, int gb) {
-  return nt == 1 ? 8 / mats : (fmt == W_AFFINE && gb == 4) ? 2 : 2 / mats;
+  return nt == 1 ? 4 / mats : (fmt == W_AFFINE && gb == 4) ? 2 : 2 / mats;
 }
 __host__ __device__ constexpr int st_stage_bytes(int fmt, int mats, int nt, int gb) {
   return mats * st_chunks(fmt, mats, nt, gb) * (512 + st_scale_bytes(fmt, gb));
