@@ -209,10 +209,12 @@ cudaError_t gemm16_launch(const GemmCall& c, OpHandle& h, cudaStream_t s, int* l
   a.dt = c.dt;
   a.act = c.act;
   a.ldo = c.ldo;
-  a.out_vec = c.ldo % 8 == 0;
+  a.out_vec = c.ldo % 16 == 0 ? 2 : c.ldo % 8 == 0 ? 1 : 0;
   for (int i = 0; i < 2; ++i) {
     a.out[i] = c.out[i];
-    if (reinterpret_cast<uintptr_t>(c.out[i]) % 16) a.out_vec = 0;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(c.out[i]);
+    if (at % 16) a.out_vec = 0;
+    else if (at % 32 && a.out_vec == 2) a.out_vec = 1;
   }
   a.save_gate = c.save_gate;
   a.save_up = c.save_up;

@@ -59,7 +59,7 @@ struct GemmArgs {
   int act;
   void* out[2];
   int64_t ldo;
-  int out_vec;          // out and ldo allow 16-byte stores
+  int out_vec;          // out and ldo allow 16-byte (1) or 32-byte (2) stores
   float *save_gate, *save_up;   // pre-activations [M, N] fp32, or null
   const float *nscale_gate, *nscale;   // per-column factors of the accumulators, or null
   const void* bias;     // [N] dt, or null
@@ -100,11 +100,23 @@ __device__ __forceinline__ GemmUnit gm_unit(const GemmArgs& A, int u) {
   return U;
 }
 
-// A warp's 32 rows x 32 columns of 16-bit values (lane = row) to global memory
-// through its staging rows, so that four lanes write 64 consecutive bytes of a
-// row instead of every lane a piece of another one.
+// A warp's 32 rows x 32 columns of 16-bit values (lane = row) to global memory: a
+// lane writes its row's 64 bytes as two whole sectors.  Rows that are not 32-byte
+// aligned, or end inside the piece, go through the warp's staging rows instead,
+// four lanes to 64 bytes of a row, or a lane to a column.
 __device__ __forceinline__ void gm_store16(char* st, const float (&v)[32], int dt, unsigned short* out, int64_t ld,
-                                           int row0, int col0, int M, int N, bool vec, int lane) {
+                                           int row0, int col0, int M, int N, int vec, int lane) {
+  if (vec == 2 && col0 + 32 <= N) {
+    if (row0 + lane < M) {
+      unsigned short* p = out + static_cast<int64_t>(row0 + lane) * ld + col0;
+#pragma unroll
+      for (int j = 0; j < 32; j += 16)
+        stg32(p + j, pack2(v[j], v[j + 1], dt), pack2(v[j + 2], v[j + 3], dt), pack2(v[j + 4], v[j + 5], dt),
+              pack2(v[j + 6], v[j + 7], dt), pack2(v[j + 8], v[j + 9], dt), pack2(v[j + 10], v[j + 11], dt),
+              pack2(v[j + 12], v[j + 13], dt), pack2(v[j + 14], v[j + 15], dt));
+    }
+    return;
+  }
   uint4* w = reinterpret_cast<uint4*>(st + lane * 80);
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -130,10 +142,18 @@ __device__ __forceinline__ void gm_store16(char* st, const float (&v)[32], int d
   __syncwarp();
 }
 
-// The same for fp32 values, 16 columns at a time; `ld` and `out` keep 16-byte
-// alignment (host-checked) and N is a multiple of 4.
+// The same for fp32 values, staged 16 columns at a time; `ld` and `out` keep
+// 16-byte alignment (host-checked) and N is a multiple of 4.
 __device__ __forceinline__ void gm_store32(char* st, const uint32_t (&v)[32], float* out, int64_t ld, int row0, int col0,
                                            int M, int N, int lane) {
+  if (ld % 8 == 0 && (reinterpret_cast<uintptr_t>(out) & 31) == 0 && col0 + 32 <= N) {
+    if (row0 + lane < M) {
+      float* p = out + static_cast<int64_t>(row0 + lane) * ld + col0;
+#pragma unroll
+      for (int j = 0; j < 32; j += 8) stg32(p + j, v[j], v[j + 1], v[j + 2], v[j + 3], v[j + 4], v[j + 5], v[j + 6], v[j + 7]);
+    }
+    return;
+  }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint4* w = reinterpret_cast<uint4*>(st + lane * 80);
@@ -384,7 +404,7 @@ __global__ void __launch_bounds__(GM_THREADS, 1) k_gemm16(const __grid_constant_
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] += ld16(A.bias, min(col0 + j, A.N - 1), A.dt);
         }
-        gm_store16(st, v, A.dt, static_cast<unsigned short*>(U.z ? A.out[1] : A.out[0]), A.ldo, row0, col0, A.M, A.N, A.out_vec != 0,
+        gm_store16(st, v, A.dt, static_cast<unsigned short*>(U.z ? A.out[1] : A.out[0]), A.ldo, row0, col0, A.M, A.N, A.out_vec,
                    lane);
       }
     }

@@ -261,6 +261,14 @@ __device__ __forceinline__ float ld16(const void* p, int64_t i, int dt) {
   return lo16(static_cast<const unsigned short*>(p)[i], dt);
 }
 
+// 32 bytes (a whole sector) of a lane; p 32-byte aligned
+__device__ __forceinline__ void stg32(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f,
+                                      uint32_t g, uint32_t h) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e),
+               "r"(f), "r"(g), "r"(h)
+               : "memory");
+}
+
 // ---- activations (moe_act) ----
 __device__ __forceinline__ float sigmoid_f(float g) { return 1.0f / (1.0f + __expf(-g)); }
 // silu(g) u, or max(u, 0)^2, or u.  A NaN passes through every form (fmaxf
