@@ -266,36 +266,36 @@ class GatedBlock(_Handle):
         if status != MOE_OK:
             raise MoEError(status, self._fn("last_error")(None).decode())
         self.handle = h.value
+        self._call_forward, self._call_backward = self._lib.moe_gated_forward, self._lib.moe_gated_backward
+        self._K, self._N, self._gated, self._f32 = config.in_features, config.out_features, config.act == "swiglu", torch.float32
 
     def _weights(self, up_w, gate_w) -> Tuple[int, Optional[int]]:
-        c = self.config
-        pu = self._matrix(up_w, c.out_features, c.in_features, "up_w")
-        if c.act == "swiglu":
-            return pu, self._matrix(gate_w, c.out_features, c.in_features, "gate_w")
+        pu = self._matrix(up_w, self._N, self._K, "up_w")
+        if self._gated:
+            return pu, self._matrix(gate_w, self._N, self._K, "gate_w")
         if gate_w is not None:
             raise MoEError(_SHAPE, "a squared-ReLU block takes no gate matrix")
         return pu, None
 
     def _forward(self, x, up_w, gate_w, out, stream, save: bool):
-        N = self.config.out_features
-        ldx = self._stride(x, self.config.in_features, "x")
+        N, device, empty = self._N, self.device, self._empty
+        ldx = self._stride(x, self._K, "x")
         pu, pg = self._weights(up_w, gate_w)
         s, where = self._stream(stream)
         T, ldo, g, u = x.shape[0], N, None, None
+        if out is not None:
+            ldo = self._stride(out, N, "out")
+            if out.shape[0] != T:
+                raise MoEError(_SHAPE, f"out has {out.shape[0]} rows, x {T}")
         with where:
             if out is None:
-                out = self._empty((T, N), dtype=self._dtype, device=self.device)
-            else:
-                ldo = self._stride(out, N, "out")
-                if out.shape[0] != T:
-                    raise MoEError(_SHAPE, f"out has {out.shape[0]} rows, x {T}")
+                out = empty((T, N), dtype=self._dtype, device=device)
             if save:
-                u = self._empty((T, N), dtype=self._torch.float32, device=self.device)
+                u = empty((T, N), dtype=self._f32, device=device)
                 if pg is not None:
-                    g = self._empty((T, N), dtype=self._torch.float32, device=self.device)
-        status = self._lib.moe_gated_forward(self.handle, x.data_ptr(), ldx, T, pg, pu, out.data_ptr(), ldo,
-                                             g.data_ptr() if g is not None else None,
-                                             u.data_ptr() if u is not None else None, s)
+                    g = empty((T, N), dtype=self._f32, device=device)
+        status = self._call_forward(self.handle, x.data_ptr(), ldx, T, pg, pu, out.data_ptr(), ldo,
+                                    None if g is None else g.data_ptr(), None if u is None else u.data_ptr(), s)
         if status:
             self._fail(status)
         return out, (g, u)
@@ -312,10 +312,11 @@ class GatedBlock(_Handle):
 
     def backward(self, d_out, saved, x, up_w, gate_w=None, need=("x", "gate_w", "up_w"), stream=None) -> GatedGrads:
         """Gradients of the tensors named in ``need`` for the gradient ``d_out`` [T, N] of ``forward_train``'s out."""
-        c, f32 = self.config, self._torch.float32
-        if not set(need).issubset(GatedGrads._fields):
-            raise MoEError(_INVALID_ARG, f"need names {', '.join(GatedGrads._fields)}")
-        K, N, T = c.in_features, c.out_features, x.shape[0]
+        f32, device, dtype, empty = self._f32, self.device, self._dtype, self._empty
+        for n in need:
+            if n not in GatedGrads._fields:
+                raise MoEError(_INVALID_ARG, f"need names {', '.join(GatedGrads._fields)}")
+        K, N, T = self._K, self._N, x.shape[0]
         ldd, ldx = self._stride(d_out, N, "d_out"), self._stride(x, K, "x")
         pu, pg = self._weights(up_w, gate_w)
         if d_out.shape[0] != T:
@@ -324,18 +325,18 @@ class GatedBlock(_Handle):
         for i, t in enumerate(saved):
             if i == 0 and pg is None:
                 continue
-            if (t is None or t.dtype is not f32 or t.shape != (T, N) or t.device != self.device or
+            if (t is None or t.dtype is not f32 or t.shape != (T, N) or t.device != device or
                     not t.is_contiguous()):
                 raise MoEError(_INVALID_ARG, "saved must be what forward_train returned for x")
             ps[i] = t.data_ptr()
         s, where = self._stream(stream)
         with where:
-            d_x = self._empty((T, K), dtype=self._dtype, device=self.device) if "x" in need else None
-            d_g = self._empty((N, K), dtype=self._dtype, device=self.device) if pg is not None and "gate_w" in need else None
-            d_u = self._empty((N, K), dtype=self._dtype, device=self.device) if "up_w" in need else None
-        p = [t.data_ptr() if t is not None else None for t in (d_x, d_g, d_u)]
-        status = self._lib.moe_gated_backward(self.handle, d_out.data_ptr(), ldd, T, x.data_ptr(), ldx, pg, pu, ps[0],
-                                              ps[1], p[0], K, p[1], p[2], s)
+            d_x = empty((T, K), dtype=dtype, device=device) if "x" in need else None
+            d_g = empty((N, K), dtype=dtype, device=device) if pg is not None and "gate_w" in need else None
+            d_u = empty((N, K), dtype=dtype, device=device) if "up_w" in need else None
+        p = [None if t is None else t.data_ptr() for t in (d_x, d_g, d_u)]
+        status = self._call_backward(self.handle, d_out.data_ptr(), ldd, T, x.data_ptr(), ldx, pg, pu, ps[0], ps[1],
+                                     p[0], K, p[1], p[2], s)
         if status:
             self._fail(status)
         return GatedGrads(d_x, d_g, d_u)

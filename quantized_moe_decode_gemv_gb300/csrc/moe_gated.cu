@@ -6,6 +6,7 @@
 #include <new>
 
 #include "moe_op_host.h"
+#include "moe_outer.cuh"
 #include "moe_stream16.cuh"
 
 using namespace moe_op;
@@ -108,6 +109,14 @@ StreamKernel stream_kernel_t(bool gated, int nt) {
 }
 StreamKernel stream_kernel(bool fp16, bool gated, int nt) {
   return fp16 ? stream_kernel_t<true>(gated, nt) : stream_kernel_t<false>(gated, nt);
+}
+
+using OuterKernel = void (*)(const OuterArgs);
+
+template <bool FP16>
+OuterKernel outer_kernel(int T) {
+  const int ks = (T + 15) / 16;
+  return ks == 1 ? k_outer<FP16, 1> : ks == 2 ? k_outer<FP16, 2> : k_outer<FP16, 3>;
 }
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -327,7 +336,23 @@ moe_status moe_gated_backward(moe_gated* h, const void* d_out, int64_t ldd, int3
       g.ldo = lddx;
       e = gemm16_launch(g, *h, s, &h->last_launches, &why);
     }
-    if ((d_gate_w || d_up_w) && e == cudaSuccess) {
+    if ((d_gate_w || d_up_w) && e == cudaSuccess && T <= OUT_MAX_T) {
+      OuterArgs a{};
+      a.d[0] = d_gate_w ? h->dg : h->du;
+      a.d[1] = h->du;
+      a.out[0] = static_cast<unsigned short*>(d_gate_w ? d_gate_w : d_up_w);
+      a.out[1] = static_cast<unsigned short*>(d_up_w);
+      a.x = static_cast<const unsigned short*>(x);
+      a.ldx = ldx;
+      a.T = T;
+      a.N = N;
+      a.K = K;
+      e = launch_chained(c.act_dtype == MOE_DTYPE_FP16 ? outer_kernel<true>(T) : outer_kernel<false>(T),
+                         dim3(static_cast<unsigned>((K + OUT_COLS - 1) / OUT_COLS),
+                              static_cast<unsigned>((N + OUT_ROWS - 1) / OUT_ROWS), d_gate_w && d_up_w ? 2u : 1u),
+                         256, 0, 1, s, a);
+      ++h->last_launches;
+    } else if ((d_gate_w || d_up_w) && e == cudaSuccess) {
       GemmCall g;
       g.M = N;
       g.N = K;

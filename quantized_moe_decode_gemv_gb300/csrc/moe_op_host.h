@@ -74,9 +74,9 @@ inline bool rows_overlap(const void* a, int64_t lda, int64_t ca, const void* b, 
 // (programmatic dependent launch).  Every kernel launched so waits for that
 // kernel (griddepcontrol.wait) before it touches what others write or read.
 template <typename... P, typename... A>
-cudaError_t launch_chained(void (*k)(P...), int64_t grid, int threads, size_t smem, int cluster, cudaStream_t s, const A&... a) {
+cudaError_t launch_chained(void (*k)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s, const A&... a) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -90,6 +90,11 @@ cudaError_t launch_chained(void (*k)(P...), int64_t grid, int threads, size_t sm
   cfg.attrs = at;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k, a...);
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*k)(P...), int64_t grid, int threads, size_t smem, int cluster, cudaStream_t s, const A&... a) {
+  return launch_chained(k, dim3(static_cast<unsigned>(grid)), threads, smem, cluster, s, a...);
 }
 
 struct GemmCall {

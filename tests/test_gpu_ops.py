@@ -245,8 +245,8 @@ def test_block_forward(pkg, T, K, N, act, dtype):
     assert op.device_status() == 0
 
 
-@pytest.mark.parametrize("T,K,N", [(1, 64, 32), (2, 2048, 264), (16, 512, 256), (33, 520, 1000), (200, 320, 200),
-                                   (257, 136, 72), (515, 1032, 776)])
+@pytest.mark.parametrize("T,K,N", [(1, 64, 32), (2, 2048, 264), (16, 512, 256), (24, 264, 520), (33, 520, 1000), (48, 72, 136),
+                                   (49, 72, 136), (200, 320, 200), (257, 136, 72), (515, 1032, 776)])
 @pytest.mark.parametrize("act", ["swiglu", "relu2"])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_block_backward(pkg, T, K, N, act, dtype):
