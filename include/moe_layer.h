@@ -348,7 +348,15 @@ moe_status moe_router_topk_noalloc(const void *x, int32_t T, int32_t hidden, int
  *   act SWIGLU  out = silu(x Wg^T) * (x Wu^T)     (both products, the activation
  *   act RELU2   out = max(x Wu^T, 0)^2             and the product in one pass)
  *
- * Sums, pre-activations and activations are fp32; out is rounded once.
+ * Sums, pre-activations and activations are fp32; out is rounded once.  Up to 16
+ * rows (fewer when rows of x are very wide: 16 rows of 4096 columns fit, 8 of 8192)
+ * a streaming kernel multiplies by the codes themselves.  Above that the weights
+ * are decoded to act_dtype on their way into the tensor cores: exactly for the fp4
+ * formats, rounded once for affine ones (with fp16 activations an affine weight
+ * has to stay below 65504).  A row of W with a NaN scale gives NaN, a NaN in a row
+ * of x reaches that row of out only, an infinity in x gives infinity or NaN.
+ * MXFP4: a block scale more than 2^24 (fp16) or 2^250 (bf16) below the largest of
+ * its row of W counts with fewer bits or as zero.
  * ------------------------------------------------------------------------- */
 typedef enum moe_qlinear_act {
   MOE_QLINEAR_SWIGLU = 0,   /* the values of moe_act */
@@ -395,16 +403,17 @@ typedef struct moe_qlinear moe_qlinear;
 moe_status moe_qlinear_validate(const moe_qlinear_config *cfg, const moe_qlinear_weights *w);
 
 /* Create on the current CUDA device: validates, re-lays the weights out on
- * `stream` and synchronises it.  On failure everything is freed and *out is
- * NULL. */
+ * `stream` and synchronises it (so not inside a stream capture).  On failure
+ * everything is freed and *out is NULL. */
 moe_status moe_qlinear_create(const moe_qlinear_config *cfg, const moe_qlinear_weights *w, void *stream,
                               moe_qlinear **out);
 
 /* out[T, N] = the operator of x[T, K].  DEVICE pointers on the handle's
  * device (the call makes it current and restores the caller's); rows of x are
  * ldx elements apart (ldx >= K, a multiple of 8, x 16-byte aligned), rows of
- * out ldo elements apart (ldo >= N); x and out must not overlap.  0 <= T <=
- * max_tokens; T = 0 does nothing.  Asynchronous on `stream`, and may be
+ * out ldo elements apart (ldo >= N); x and out must not overlap (as column ranges
+ * of one buffer, ldx = ldo, they may interleave).  0 <= T <= max_tokens; T = 0
+ * does nothing; rows of out from T on and what lies between rows stay as they are.  Asynchronous on `stream`, and may be
  * captured into a CUDA graph.  Like a layer, a handle has one workspace: its
  * calls (and replays of graphs that hold them) must not overlap on the GPU. */
 moe_status moe_qlinear_forward(moe_qlinear *h, const void *x, int64_t ldx, int32_t T, void *out, int64_t ldo,
@@ -450,7 +459,8 @@ typedef struct moe_gated moe_gated;
 /* MOE_ERR_INVALID_ARG: null cfg, sizes < 1, bad enum values.  MOE_ERR_SHAPE: K
  * or N not a multiple of 8.  MOE_ERR_UNSUPPORTED: fp32, K > 65536, N > 2^24. */
 moe_status moe_gated_validate(const moe_gated_config *cfg);
-/* Create on the current CUDA device (workspace only: a handle holds no weights). */
+/* Create on the current CUDA device (workspace only: a handle holds no weights).
+ * Synchronises the device, so not inside a stream capture. */
 moe_status moe_gated_create(const moe_gated_config *cfg, moe_gated **out);
 
 /* out[T, N] from x[T, K] and gate_w, up_w [N, K] (row-major, contiguous; gate_w

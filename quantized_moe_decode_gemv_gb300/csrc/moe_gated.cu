@@ -130,16 +130,15 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
 
 }  // namespace
 
-extern "C" {
-
-moe_status moe_gated_validate(const moe_gated_config* cfg) {
+static moe_status validate_entry(const moe_gated_config* cfg) {
   std::string why;
   const moe_status st = validate(cfg, &why);
   if (st != MOE_OK) g_error = why;
   return st;
 }
 
-moe_status moe_gated_create(const moe_gated_config* cfg, moe_gated** out) {
+// (h: the handle while it is not the caller's, for the entry point to free when an exception ends this)
+static moe_status create(const moe_gated_config* cfg, moe_gated** out, moe_gated*& h) {
   if (out) *out = nullptr;
   std::string why;
   moe_status st = validate(cfg, &why);
@@ -154,7 +153,7 @@ moe_status moe_gated_create(const moe_gated_config* cfg, moe_gated** out) {
     g_error = why;
     return st;
   }
-  moe_gated* h = new (std::nothrow) moe_gated();
+  h = new (std::nothrow) moe_gated();
   if (!h) {
     g_error = "host memory";
     return MOE_ERR_OOM;
@@ -180,13 +179,15 @@ moe_status moe_gated_create(const moe_gated_config* cfg, moe_gated** out) {
     g_error = std::string("create: ") + cudaGetErrorString(e);
     h->free_all();
     delete h;
+    h = nullptr;
     return e == cudaErrorMemoryAllocation ? MOE_ERR_OOM : MOE_ERR_CUDA;
   }
   *out = h;
+  h = nullptr;
   return MOE_OK;
 }
 
-moe_status moe_gated_forward(moe_gated* h, const void* x, int64_t ldx, int32_t T, const void* gate_w, const void* up_w,
+static moe_status forward(moe_gated* h, const void* x, int64_t ldx, int32_t T, const void* gate_w, const void* up_w,
                              void* out, int64_t ldo, float* save_gate, float* save_up, void* stream) {
   if (!h) return MOE_ERR_INVALID_ARG;
   const moe_gated_config& c = h->cfg;
@@ -262,7 +263,7 @@ moe_status moe_gated_forward(moe_gated* h, const void* x, int64_t ldx, int32_t T
   return MOE_OK;
 }
 
-moe_status moe_gated_backward(moe_gated* h, const void* d_out, int64_t ldd, int32_t T, const void* x, int64_t ldx,
+static moe_status backward(moe_gated* h, const void* d_out, int64_t ldd, int32_t T, const void* x, int64_t ldx,
                               const void* gate_w, const void* up_w, const float* save_gate, const float* save_up,
                               void* d_x, int64_t lddx, void* d_gate_w, void* d_up_w, void* stream) {
   if (!h) return MOE_ERR_INVALID_ARG;
@@ -348,8 +349,8 @@ moe_status moe_gated_backward(moe_gated* h, const void* d_out, int64_t ldd, int3
       a.N = N;
       a.K = K;
       e = launch_chained(c.act_dtype == MOE_DTYPE_FP16 ? outer_kernel<true>(T) : outer_kernel<false>(T),
-                         dim3(static_cast<unsigned>((K + OUT_COLS - 1) / OUT_COLS),
-                              static_cast<unsigned>((N + OUT_ROWS - 1) / OUT_ROWS), d_gate_w && d_up_w ? 2u : 1u),
+                         dim3(static_cast<unsigned>((N + OUT_ROWS - 1) / OUT_ROWS),
+                              static_cast<unsigned>((K + OUT_COLS - 1) / OUT_COLS), d_gate_w && d_up_w ? 2u : 1u),
                          256, 0, 1, s, a);
       ++h->last_launches;
     } else if ((d_gate_w || d_up_w) && e == cudaSuccess) {
@@ -378,7 +379,36 @@ moe_status moe_gated_backward(moe_gated* h, const void* d_out, int64_t ldd, int3
   return MOE_OK;
 }
 
-moe_status moe_gated_device_status(moe_gated* h, void* stream) { return h ? h->read_status(stream) : MOE_ERR_INVALID_ARG; }
+extern "C" {
+
+moe_status moe_gated_validate(const moe_gated_config* cfg) {
+  return op_entry([&] { return validate_entry(cfg); });
+}
+
+moe_status moe_gated_create(const moe_gated_config* cfg, moe_gated** out) {
+  moe_gated* h = nullptr;
+  const moe_status st = op_entry([&] { return create(cfg, out, h); });
+  if (h) {
+    h->free_all();
+    delete h;
+  }
+  return st;
+}
+
+moe_status moe_gated_forward(moe_gated* h, const void* x, int64_t ldx, int32_t T, const void* gate_w, const void* up_w,
+                             void* out, int64_t ldo, float* save_gate, float* save_up, void* stream) {
+  return op_entry([&] { return forward(h, x, ldx, T, gate_w, up_w, out, ldo, save_gate, save_up, stream); });
+}
+
+moe_status moe_gated_backward(moe_gated* h, const void* d_out, int64_t ldd, int32_t T, const void* x, int64_t ldx,
+                              const void* gate_w, const void* up_w, const float* save_gate, const float* save_up,
+                              void* d_x, int64_t lddx, void* d_gate_w, void* d_up_w, void* stream) {
+  return op_entry([&] { return backward(h, d_out, ldd, T, x, ldx, gate_w, up_w, save_gate, save_up, d_x, lddx, d_gate_w, d_up_w, stream); });
+}
+
+moe_status moe_gated_device_status(moe_gated* h, void* stream) {
+  return op_entry([&] { return h ? h->read_status(stream) : MOE_ERR_INVALID_ARG; });
+}
 
 int64_t moe_gated_device_bytes(const moe_gated* h) { return h ? h->bytes : 0; }
 

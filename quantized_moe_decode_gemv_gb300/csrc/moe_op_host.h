@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <new>
 #include <string>
 #include <vector>
 
@@ -38,6 +39,18 @@ struct DeviceScope {
   DeviceScope& operator=(const DeviceScope&) = delete;
 };
 
+// Runs the body of a C entry point: no C++ exception leaves it.
+template <typename F>
+moe_status op_entry(F&& body) noexcept {
+  try {
+    return body();
+  } catch (const std::bad_alloc&) {
+    return MOE_ERR_OOM;   // host memory
+  } catch (...) {
+    return MOE_ERR_CUDA;
+  }
+}
+
 // What every operator handle has.
 struct OpHandle {
   int device = -1;
@@ -50,6 +63,7 @@ struct OpHandle {
   float* part = nullptr;      // partial sums of products whose K is split
   size_t part_bytes = 0;
 
+  OpHandle() { allocs.reserve(16); }
   cudaError_t alloc(void** p, size_t n);
   void free_all();
   moe_status read_status(void* stream);

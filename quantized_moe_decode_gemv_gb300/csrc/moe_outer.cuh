@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(256) k_outer(const OuterArgs A) {
   __shared__ __align__(16) unsigned short ds[KS * 16][OUT_ROWS + 8];
   __shared__ __align__(16) unsigned short xs[KS * 16][OUT_COLS + 8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int n0 = blockIdx.y * OUT_ROWS, k0 = blockIdx.x * OUT_COLS, z = blockIdx.z;
+  const int n0 = blockIdx.x * OUT_ROWS, k0 = blockIdx.y * OUT_COLS, z = blockIdx.z;   // (N has up to 2^17 row blocks)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   const unsigned short* d = z ? A.d[1] : A.d[0];

@@ -425,17 +425,16 @@ cudaError_t relay(moe_qlinear& h, const moe_qlinear_weights& w, int* e0, cudaStr
 
 }  // namespace
 
-extern "C" {
-
-moe_status moe_qlinear_validate(const moe_qlinear_config* cfg, const moe_qlinear_weights* w) {
+static moe_status validate_entry(const moe_qlinear_config* cfg, const moe_qlinear_weights* w) {
   std::string why;
   const moe_status st = validate(cfg, w, &why);
   if (st != MOE_OK) g_error = why;
   return st;
 }
 
-moe_status moe_qlinear_create(const moe_qlinear_config* cfg, const moe_qlinear_weights* w, void* stream,
-                              moe_qlinear** out) {
+// (h: the handle while it is not the caller's, for the entry point to free when an exception ends this)
+static moe_status create(const moe_qlinear_config* cfg, const moe_qlinear_weights* w, void* stream,
+                              moe_qlinear** out, moe_qlinear*& h) {
   if (out) *out = nullptr;
   std::string why;
   moe_status st = validate(cfg, w, &why);
@@ -449,7 +448,7 @@ moe_status moe_qlinear_create(const moe_qlinear_config* cfg, const moe_qlinear_w
     g_error = why;
     return st;
   }
-  moe_qlinear* h = new (std::nothrow) moe_qlinear();
+  h = new (std::nothrow) moe_qlinear();
   if (!h) {
     g_error = "host memory";
     return MOE_ERR_OOM;
@@ -503,14 +502,16 @@ moe_status moe_qlinear_create(const moe_qlinear_config* cfg, const moe_qlinear_w
     cudaStreamSynchronize(s);
     h->free_all();
     delete h;
+    h = nullptr;
     g_error = why;
     return st != MOE_OK ? st : e == cudaErrorMemoryAllocation ? MOE_ERR_OOM : MOE_ERR_CUDA;
   }
   *out = h;
+  h = nullptr;
   return MOE_OK;
 }
 
-moe_status moe_qlinear_forward(moe_qlinear* h, const void* x, int64_t ldx, int32_t T, void* out, int64_t ldo,
+static moe_status forward(moe_qlinear* h, const void* x, int64_t ldx, int32_t T, void* out, int64_t ldo,
                                void* stream) {
   if (!h) return MOE_ERR_INVALID_ARG;
   const moe_qlinear_config& c = h->cfg;
@@ -549,8 +550,30 @@ moe_status moe_qlinear_forward(moe_qlinear* h, const void* x, int64_t ldx, int32
   return MOE_OK;
 }
 
+extern "C" {
+
+moe_status moe_qlinear_validate(const moe_qlinear_config* cfg, const moe_qlinear_weights* w) {
+  return op_entry([&] { return validate_entry(cfg, w); });
+}
+
+moe_status moe_qlinear_create(const moe_qlinear_config* cfg, const moe_qlinear_weights* w, void* stream,
+                              moe_qlinear** out) {
+  moe_qlinear* h = nullptr;
+  const moe_status st = op_entry([&] { return create(cfg, w, stream, out, h); });
+  if (h) {
+    h->free_all();
+    delete h;
+  }
+  return st;
+}
+
+moe_status moe_qlinear_forward(moe_qlinear* h, const void* x, int64_t ldx, int32_t T, void* out, int64_t ldo,
+                               void* stream) {
+  return op_entry([&] { return forward(h, x, ldx, T, out, ldo, stream); });
+}
+
 moe_status moe_qlinear_device_status(moe_qlinear* h, void* stream) {
-  return h ? h->read_status(stream) : MOE_ERR_INVALID_ARG;
+  return op_entry([&] { return h ? h->read_status(stream) : MOE_ERR_INVALID_ARG; });
 }
 
 int64_t moe_qlinear_device_bytes(const moe_qlinear* h) { return h ? h->bytes : 0; }
