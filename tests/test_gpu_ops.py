@@ -488,3 +488,85 @@ def test_refusals_with_tensors(pkg):
     relu = make_block(pkg, 20, 128, 64, "bf16", "relu2", False)[0]
     with pytest.raises(pkg.MoEError):
         relu(x, up, gate)
+
+
+def test_calls_between_other_kernels(pkg):
+    """Inputs rewritten right before each call and outputs read right after, with
+    nothing waited for: the chained launches start early but may not run ahead."""
+    T = 7
+    lin, _, _, _ = make_linear(pkg, 264, 512, "nvfp4", 16, "bf16", "none", False, 64, seed=2)
+    many, _, _, _ = make_linear(pkg, 264, 512, "affine", 64, "bf16", "relu2", False, 64, seed=3)
+    block, x, up, gate, e = make_block(pkg, T, 264, 512, "bf16", "swiglu", True)
+    inputs = [(rows(T, 264, "bf16", 50 + i), torch.randn_like(up) * 0.05) for i in range(12)]
+
+    def step(xi, wi):
+        x.copy_(xi)
+        up.copy_(wi)
+        h, saved = block.forward_train(x, up, gate)
+        d = block.backward(e, saved, x, up, gate)
+        y = lin(h)
+        wide = h.repeat(6, 1)
+        z = many(wide)
+        wide.zero_()      # after the call read it
+        return [t.clone() for t in (h, *d, y, z)]
+
+    x = x.contiguous()
+    torch.cuda.synchronize()
+    fast = [step(*i) for i in inputs]
+    torch.cuda.synchronize()
+    for i, got in zip(inputs, fast):
+        want = step(*i)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("T", [5, 70])
+def test_block_rows_and_columns_beyond_are_left(pkg, T):
+    block, x, up, gate, _ = make_block(pkg, T, 128, 72, "bf16", "swiglu", False)
+    for pad in (4, 13):   # rows aligned to 8 bytes, and odd ones
+        buf = torch.full((T + 3, 72 + 2 * pad), 7.0, dtype=torch.bfloat16, device="cuda")
+        block(x, up, gate, out=buf[:T, pad:pad + 72])
+        want, e, *_ = want_block(x, up, gate, "bf16", "swiglu")
+        ref.check(buf[:T, pad:pad + 72], want, e, "bf16", "strided out")
+        buf[:T, pad:pad + 72] = 7.0
+        assert (buf == 7.0).all()
+
+
+def test_strided_gradient_of_the_output(pkg):
+    """d_out as a column range, aligned and not."""
+    for pad in (0, 8, 3):
+        block, x, up, gate, e = make_block(pkg, 30, 128, 72, "bf16", "swiglu", True, seed=4)
+        _, saved = block.forward_train(x, up, gate)
+        want = block.backward(e, saved, x, up, gate)
+        wide = torch.zeros(30, 72 + pad, dtype=torch.bfloat16, device="cuda")
+        wide[:, pad:] = e
+        got = block.backward(wide[:, pad:], saved, x, up, gate)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_offsets_past_32_bits(pkg):
+    """70000 rows of 32768 outputs: 2.3 billion elements."""
+    T, N = 70000, 32768
+    some = torch.tensor([0, 1, 65535, 65536, T - 2, T - 1], device="cuda")
+    op, _, w, _ = make_linear(pkg, N, 64, "affine", 64, "bf16", "none", False, T)
+    x = torch.randn(T, 64, device="cuda", dtype=torch.bfloat16)
+    out = op(x)
+    xd = x[some].double()
+    want = xd @ w.T
+    ref.check(out[some], want, ref.product_bound(xd, w, 1, "bf16"), "bf16", "linear")
+    del out, op
+    block, _, up, _, _ = make_block(pkg, T, 64, N, "bf16", "relu2", True)
+    out, saved = block.forward_train(x, up)
+    wantb, err, g, u, eg, eu = want_block(x[some], up, None, "bf16", "relu2")
+    ref.check(out[some], wantb, err, "bf16", "out")
+    e = torch.randn(T, N, device="cuda", dtype=torch.bfloat16) * 0.1
+    d = block.backward(e, saved, x, up)
+    grads = want_grads(x[some], up, None, e[some], g, u, eg, eu, "bf16", "relu2")
+    ref.check(d.x[some], *grads["x"], "bf16", "d_x")
+    # the weights' gradient over all rows, for some of them
+    ns = torch.tensor([0, 5, 32760, N - 1], device="cuda")
+    uu = x.double() @ up[ns].double().T
+    du = 2 * e[:, ns].double() * torch.clamp(uu, min=0)
+    edu = 2 * e[:, ns].double().abs() * ref.product_bound(x.double(), up[ns].double(), 0, "bf16") + 2.0 ** -22 * du.abs()
+    bound = ref.product_bound(du.T.contiguous(), x.double().T.contiguous(), 1, "bf16") + edu.T @ x.double().abs()
+    ref.check(d.up_w[ns], du.T @ x.double(), bound, "bf16", "d_up_w")
