@@ -150,8 +150,9 @@ template <int FMT, bool FP16>
 __device__ __forceinline__ uint32_t fp4_scale(uint32_t bytes, int sel) {
   const uint32_t bb = __byte_perm(bytes, 0u, 0x4040u | static_cast<uint32_t>(sel) | (static_cast<uint32_t>(sel) << 8));
   // bb = the byte in the low 8 bits of both halves
-  if (FMT == W_NVFP4) return FP16 ? bb << 7 : (bb << 4) | 0x70007000u;
-  return FP16 ? bb << 10 : bb << 7;
+  // (multiplications: they run beside the shifts and masks of the codes)
+  if (FMT == W_NVFP4) return FP16 ? bb * 128u : bb * 16u + 0x70007000u;
+  return FP16 ? bb * 1024u : bb * 128u;
 }
 template <bool FP16>
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t s) {
@@ -165,7 +166,8 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t s) {
 }
 
 // Shared memory of a launch:
-//   [ST_WARPS rings of `depth` stages][token rows][partial sums, two tiles][barriers]
+//   [ST_WARPS rings of `depth` stages][token rows][a stage's width of zeros][partial
+//   sums, two tiles][barriers]
 // A stage holds st_chunks() chunks: their matrices x 512 bytes of codes, then the
 // scales.  Token rows are 16 bytes longer than K (64 with groups of 32), so that
 // the fragment reads of eight lanes (two rows of four lanes) touch all banks once.
@@ -187,6 +189,7 @@ __host__ __device__ constexpr int st_red_floats(int mats, int nt) { return ST_WA
 __host__ __device__ inline int st_smem_bytes(int fmt, int mats, int gb, int chunks, int T, int depth) {
   const int nt = T > 8 ? 2 : 1;
   return ST_WARPS * depth * st_stage_bytes(fmt, mats, nt, gb) + T * st_row_bytes(fmt, gb, chunks) +
+         st_chunks(fmt, mats, nt, gb) * 128 +
          8 * st_red_floats(mats, nt) + 16;
 }
 
@@ -194,12 +197,6 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
   return v;
-}
-__device__ __forceinline__ void lds16_if(uint32_t* r, uint32_t a, bool in) {   // else left as they are
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3])
-               : "r"(a), "r"(static_cast<int>(in))
-               : "memory");
 }
 __device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
@@ -228,7 +225,8 @@ __global__ void __launch_bounds__(ST_THREADS, 1) k_stream(const StreamArgs A) {
   const int tiles = (A.N + 15) / 16, D = A.depth;
   const int xrow = st_row_bytes(FMT, GB, A.chunks);
   char* const xs = st_smem + ST_WARPS * D * stage;
-  float* const red = reinterpret_cast<float*>(xs + A.T * xrow);
+  char* const zeros = xs + A.T * xrow;   // what lanes of absent tokens read
+  float* const red = reinterpret_cast<float*>(zeros + CB * 128);
   uint64_t* const bars = reinterpret_cast<uint64_t*>(red + 2 * st_red_floats(M, NT));
   const uint32_t ring = smem_u32(st_smem) + warp * D * stage;
   const uint32_t rbar = smem_u32(bars);   // two: the sums of even and odd tiles
@@ -298,18 +296,21 @@ __global__ void __launch_bounds__(ST_THREADS, 1) k_stream(const StreamArgs A) {
       copy16(smem_u32(xs) + r * xrow + p * 16, p * 8 < A.K ? src + p * 16 : src, p * 8 < A.K);
     }
     copies_commit();
+    for (int i = tid; i < CB * 8; i += ST_THREADS) *reinterpret_cast<uint4*>(zeros + i * 16) = make_uint4(0, 0, 0, 0);
     copies_wait(0);
   }
   __syncthreads();
   bool ok = true;
 
   // this lane's 16-byte pieces of a chunk's 128 bytes of token rows g (and g + 8)
-  const uint32_t x0 = smem_u32(xs) + g * xrow + (WIDE ? 32 * t : 16 * t);
-  uint32_t bf[NT][8];
+  uint32_t xat[NT];
+  int xstep[NT];   // bytes from a chunk to the next
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) bf[n][k] = 0u;
+  for (int n = 0; n < NT; ++n) {
+    const bool in = n * 8 + g < A.T;
+    xat[n] = smem_u32(in ? xs + (n * 8 + g) * xrow : zeros) + (WIDE ? 32 * t : 16 * t);
+    xstep[n] = in ? 128 : 0;
+  }
 
   // adds the warps' sums of a tile: one thread an output, a quarter (or half) of the CTA
   auto join = [&](int tile, int n_done) {
@@ -352,16 +353,17 @@ __global__ void __launch_bounds__(ST_THREADS, 1) k_stream(const StreamArgs A) {
       cst += stage;
       if (cst == ring + D * stage) cst = ring;
       const int n_c = min(CB, c_hi - cs);
-      const uint32_t xc = x0 + cs * 128;
 #pragma unroll
       for (int i = 0; i < CB; ++i) {
         if (i >= n_c) break;
         // B fragments: 16-column steps j = 0..3, two registers each
-        // (absent tokens' registers stay zero)
+        uint32_t bf[NT][8];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          lds16_if(bf[n], xc + n * 8 * xrow + i * 128, n * 8 + g < A.T);
-          lds16_if(bf[n] + 4, xc + n * 8 * xrow + i * 128 + (WIDE ? 16 : 64), n * 8 + g < A.T);
+          const uint32_t at = xat[n] + cs * xstep[n] + i * 128;
+          const uint4 v0 = lds16(at), v1 = lds16(at + (WIDE ? 16 : 64));
+          bf[n][0] = v0.x; bf[n][1] = v0.y; bf[n][2] = v0.z; bf[n][3] = v0.w;
+          bf[n][4] = v1.x; bf[n][5] = v1.y; bf[n][6] = v1.z; bf[n][7] = v1.w;
         }
         if constexpr (FMT == W_AFFINE) {
           constexpr uint32_t one = FP16 ? 0x3C003C00u : 0x3F803F80u;
