@@ -349,8 +349,8 @@ moe_status moe_router_topk_noalloc(const void *x, int32_t T, int32_t hidden, int
  *   act RELU2   out = max(x Wu^T, 0)^2             and the product in one pass)
  *
  * Sums, pre-activations and activations are fp32; out is rounded once.  Up to 16
- * rows (fewer when rows of x are very wide: 16 rows of 4096 columns fit, 8 of 8192)
- * a streaming kernel multiplies by the codes themselves.  Above that the weights
+ * rows (fewer where rows of x several thousand columns wide leave it no shared
+ * memory) a streaming kernel multiplies by the codes themselves.  Above that the weights
  * are decoded to act_dtype on their way into the tensor cores: exactly for the fp4
  * formats, rounded once for affine ones (with fp16 activations an affine weight
  * has to stay below 65504).  A row of W with a NaN scale gives NaN, a NaN in a row

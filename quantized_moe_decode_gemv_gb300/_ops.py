@@ -257,7 +257,9 @@ class GatedBlock(_Handle):
         if status != MOE_OK:
             raise MoEError(status, self._fn("last_error")(None).decode())
         self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-        if self.device.type == "cuda" and self.device.index is None:
+        if self.device.type != "cuda":
+            raise MoEError(_INVALID_ARG, f"a gated block runs on a CUDA device, not on {self.device}")
+        if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
         self._dtype = torch_act_dtype(config.act_dtype)
         h = ctypes.c_void_p()

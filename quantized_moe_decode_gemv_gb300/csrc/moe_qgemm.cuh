@@ -3,9 +3,11 @@
 //
 //   D[n, t] = sum_k W[n, k] x[t, k]      weights as M, tokens as N
 //
-// A CTA's tile is `mt` blocks of 128 weight rows (1 or 2; SwiGLU: the gate's and
-// the up matrix's rows of the same 128 outputs) by up to 256 tokens, with fp32
-// accumulators in tensor memory.  Tokens are N because N goes in steps of 16: a
+// A CTA's tile is 128 weight rows (SwiGLU: two blocks, the gate's and the up
+// matrix's rows of the same 128 outputs) by up to 256 tokens, with fp32
+// accumulators in tensor memory.  (Two blocks of one matrix a CTA, which read the
+// token rows once for both, were slower at every size: 41 us against 28 at 160
+// rows, 206 against 188 at 2048, because two tiles' accumulators no longer fit.)  Tokens are N because N goes in steps of 16: a
 // ragged batch pays for at most 15 rows that are not there, where as M it would
 // pay for up to 127.  Weights are never written out: each 16-bit A tile is made
 // from the codes in shared memory, once per token tile, beside the MMAs:
@@ -17,9 +19,9 @@
 // tensor pipe fed.
 //
 //   warp 0     tensor copies of the token rows
-//   warps 8-23 decode, a 16-row tile of a block each: with mt = 2 eight warps a
-//              block, with mt = 1 two groups of eight that take turns at pairs
-//              of K blocks.  Codes and scales come by 16-byte asynchronous copies
+//   warps 8-23 decode, a 16-row tile of a block each: with two blocks eight warps a
+//              block, with one two groups of eight that take turns at pairs of K
+//              blocks.  Codes and scales come by 16-byte asynchronous copies
 //              into a private ring, are decoded as k_stream does (an affine weight
 //              is rounded once to the 16-bit type, a relative error of at most
 //              2^-8 or 2^-11 beside the output's own; an fp4 weight times its
@@ -31,9 +33,9 @@
 //              overlaps the next tile's MMAs where two tiles' accumulators fit
 //              the 512 columns
 //
-// Per K block and mt = 2, 256 tokens: 1024 clocks of MMA beside 32 KB of token
-// rows, 9 KB of codes (41 bytes a clock, two thirds of what L2 gives an SM) and
-// 16 x 100 decode instructions (40% of the issue slots).  Every wait is bounded;
+// Per K block of two matrices and 256 tokens: 1024 clocks of MMA beside 32 KB of
+// token rows, 9 KB of codes (41 bytes a clock, two thirds of what L2 gives an SM)
+// and 16 x 100 decode instructions (40% of the issue slots).  Every wait is bounded;
 // a role whose wait runs out sets the timeout bit of the status word and winds
 // down.
 #pragma once
@@ -60,7 +62,7 @@ struct QGemmArgs {
   int64_t ld_part;
   int* status;
   int T, N, chunks, group, sdt, act;
-  int mt, ntok, ksplit;
+  int ntok, ksplit;
   int slots, depth;         // of the ring, and stages of a warp's code ring (2 or 3)
 };
 
@@ -75,7 +77,7 @@ __host__ __device__ inline int qg_smem_bytes(int fmt, int gb, int mt, int ntok, 
 }
 
 struct QGemmUnit {
-  int split, row, t0, c0, c1;   // first 128-row block (in blocks of mt), first token, chunks [c0, c1)
+  int split, row, t0, c0, c1;   // 128-row block, first token, chunks [c0, c1)
 };
 __device__ __forceinline__ QGemmUnit qg_unit(const QGemmArgs& A, int q, int row_tiles, int tok_tiles, int u) {
   QGemmUnit U;
@@ -97,7 +99,8 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
   constexpr int SCB = st_scale_bytes(FMT, GB);
   extern __shared__ __align__(1024) char gm_smem[];
   char* base = gm_smem + ((1024u - (smem_u32(gm_smem) & 1023u)) & 1023u);
-  const int S = A.slots, D = A.depth, mt = A.mt, ntok = A.ntok;
+  constexpr int mt = M;   // A blocks of a tile
+  const int S = A.slots, D = A.depth, ntok = A.ntok;
   constexpr int code_bytes = qg_code_bytes(FMT, GB);
   const int slot_bytes = qg_slot_bytes(mt, ntok);
   char* rings = base + S * slot_bytes;
@@ -107,8 +110,7 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
 
   const int q = FMT == W_AFFINE && A.group == 128 ? 2 : 1, nu = A.chunks / q;   // chunks of a scale group
-  const int rows_tile = GATED ? 128 : 128 * mt;
-  const int row_tiles = (A.N + rows_tile - 1) / rows_tile, tok_tiles = (A.T + ntok - 1) / ntok;
+  const int row_tiles = (A.N + 127) / 128, tok_tiles = (A.T + ntok - 1) / ntok;
   const int units = row_tiles * tok_tiles * A.ksplit;
   const int region = qg_region(ntok), nbuf = 2 * mt * region <= 512 ? 2 : 1;
   const uint32_t tm_cols = static_cast<uint32_t>(nbuf * mt * region);
@@ -206,12 +208,12 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
   } else if (warp >= 8) {
     // ---------------- decode ----------------
     const int dw = (warp - 8) & 7, half = (warp - 8) >> 3, g = lane >> 2, t = lane & 3;
-    const int a = mt == 2 ? half : 0, m = GATED ? half : 0;   // block of the CTA's tile; matrix
-    const int step = mt == 2 ? 2 : 4;                          // chunks from one of this warp's pairs to the next
-    const int first = mt == 2 ? 0 : 2 * half;
+    const int m = GATED ? half : 0;         // matrix, and its A block
+    const int step = GATED ? 2 : 4;         // chunks from one of this warp's pairs to the next
+    const int first = GATED ? 0 : 2 * half;
     const uint32_t ring = smem_u32(rings) + (warp - 8) * D * code_bytes;
     const int tiles16 = (A.N + 15) / 16;
-    auto tile_of = [&](const QGemmUnit& U) { return GATED ? U.row * 8 + dw : (U.row * mt + a) * 8 + dw; };
+    auto tile_of = [&](const QGemmUnit& U) { return U.row * 8 + dw; };
     // the next stage to fill: unit, chunks fc and fc + 1, their codes and scales, the slot
     int fu = static_cast<int>(blockIdx.x) - static_cast<int>(gridDim.x), fc = 0, fend = 0;
     bool fin = false;   // the unit's tile is inside the matrix
@@ -312,7 +314,7 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
               sv[i][1] = x;
             }
             const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-            const uint32_t row = smem_u32(base + sl * slot_bytes + a * 16384) + row_off;
+            const uint32_t row = smem_u32(base + sl * slot_bytes + m * 16384) + row_off;
 #pragma unroll
             for (int jj = 0; jj < 2; ++jj) {
               uint32_t v[2][4];
@@ -365,7 +367,7 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
           }
         }
         if (!ok) break;
-        if (mt == 1) skip(max(0, min(U.c1, c + step) - (c + 2)));   // the other group's K blocks
+        if (!GATED) skip(max(0, min(U.c1, c + step) - (c + 2)));   // the other group's K blocks
       }
     }
     copies_wait(0);
@@ -381,9 +383,8 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
       tm_fence_after();
       const uint32_t tcol = tmem + (static_cast<uint32_t>(ew * 32) << 16) + buf * static_cast<uint32_t>(mt * region);
       const int nt = min(ntok, A.T - U.t0);
-      const int blocks = GATED ? 1 : mt;
-      for (int a = 0; a < blocks; ++a) {
-        const int row = U.row * rows_tile + a * 128 + ew * 32 + lane;
+      {
+        const int row = U.row * 128 + ew * 32 + lane;
         const bool in = row < A.N;
         const int rc = min(row, A.N - 1);
         float f0 = 1.0f, f1 = 1.0f, bias = 0.0f;
@@ -394,10 +395,10 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
         if (A.bias) bias = ld16(A.bias, rc, DT);
         for (int j0 = 0; j0 < nt; j0 += 16) {
           uint32_t r0[16], r1[16];
-          tm_ld16(tcol + a * region + j0, r0);
+          tm_ld16(tcol + j0, r0);
           if (GATED) tm_ld16(tcol + region + j0, r1);
           tm_wait_ld();
-          if (a == blocks - 1 && j0 + 16 >= nt) {
+          if (j0 + 16 >= nt) {
             // the accumulators are in registers: the buffer may be rewritten
             tm_fence_before();
             __syncwarp();

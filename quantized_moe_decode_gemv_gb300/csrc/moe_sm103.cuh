@@ -13,7 +13,6 @@ namespace moe_op {
 
 enum : int { DT_BF16 = 0, DT_FP16 = 1 };       // moe_dtype
 enum : int { ACT_SWIGLU = 0, ACT_RELU2 = 1, ACT_NONE = 2 };
-enum : int { FMT_AFFINE = 0, FMT_NVFP4 = 1, FMT_MXFP4 = 2 };
 
 constexpr int STATUS_TIMEOUT = 2;               // bits of a handle's status word
 constexpr long long WAIT_CLOCKS = 4ll << 30;    // a wait gives up after about two seconds
@@ -270,7 +269,6 @@ __device__ __forceinline__ void stg32(void* p, uint32_t a, uint32_t b, uint32_t 
 }
 
 // ---- activations (moe_act) ----
-__device__ __forceinline__ float sigmoid_f(float g) { return 1.0f / (1.0f + __expf(-g)); }
 // silu(g) u, or max(u, 0)^2, or u.  A NaN passes through every form (fmaxf
 // would drop it).
 __device__ __forceinline__ float act_value(int act, float g, float u) {

@@ -145,7 +145,7 @@ __device__ __forceinline__ void fp4_word(uint32_t w, uint32_t (&a)[4]) {
   }
 }
 // A stored scale byte as a pair of 16-bit floats (the byte's value, made by
-// ql_scale_byte, sits in the exponent and mantissa fields).
+// scale_byte at create time, sits in the exponent and mantissa fields).
 template <int FMT, bool FP16>
 __device__ __forceinline__ uint32_t fp4_scale(uint32_t bytes, int sel) {
   const uint32_t bb = __byte_perm(bytes, 0u, 0x4040u | static_cast<uint32_t>(sel) | (static_cast<uint32_t>(sel) << 8));
