@@ -34,10 +34,12 @@
 //              the 512 columns
 //
 // Per K block of two matrices and 256 tokens: 1024 clocks of MMA beside 32 KB of
-// token rows, 9 KB of codes (41 bytes a clock, two thirds of what L2 gives an SM)
-// and 16 x 100 decode instructions (40% of the issue slots).  Every wait is bounded;
-// a role whose wait runs out sets the timeout bit of the status word and winds
-// down.
+// token rows, 9 KB of codes (41 bytes a clock) and 16 x 100 decode instructions
+// (40% of the issue slots).  Measured: 2048 rows of 4096 against 16384, affine,
+// 185 us (1.49 PFLOP/s), 300 rows against 2 x 8192, MXFP4, 38.6 us (1.04).
+//
+// Every wait is bounded; a role whose wait runs out sets the timeout bit of the
+// status word and winds down.
 #pragma once
 
 #include "moe_stream.cuh"

@@ -570,3 +570,33 @@ def test_offsets_past_32_bits(pkg):
     edu = 2 * e[:, ns].double().abs() * ref.product_bound(x.double(), up[ns].double(), 0, "bf16") + 2.0 ** -22 * du.abs()
     bound = ref.product_bound(du.T.contiguous(), x.double().T.contiguous(), 1, "bf16") + edu.T @ x.double().abs()
     ref.check(d.up_w[ns], du.T @ x.double(), bound, "bf16", "d_up_w")
+
+
+def test_two_threads(pkg):
+    """Handles of their own, streams of their own, calls at the same time."""
+    import threading
+    made = [make_block(pkg, 60, 256, 264, "bf16", "swiglu", True, seed=s) for s in (0, 1)]
+    want = []
+    for op, x, up, gate, e in made:
+        out, saved = op.forward_train(x, up, gate)
+        want.append((out, *op.backward(e, saved, x, up, gate)))
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        op, x, up, gate, e = made[i]
+        stream = torch.cuda.Stream()
+        for _ in range(20):
+            with torch.cuda.stream(stream):
+                out, saved = op.forward_train(x, up, gate)
+                got = (out, *op.backward(e, saved, x, up, gate))
+            stream.synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
