@@ -218,9 +218,6 @@ cudaError_t gemm16_launch(const GemmCall& c, OpHandle& h, cudaStream_t s, int* l
   }
   a.save_gate = c.save_gate;
   a.save_up = c.save_up;
-  a.nscale_gate = c.nscale_gate;
-  a.nscale = c.nscale;
-  a.bias = c.bias;
   a.status = h.status;
   a.part = h.part;
   a.ld_part = static_cast<int64_t>((c.N + 3) / 4 * 4) * (c.dual ? 2 : 1);
@@ -268,9 +265,6 @@ cudaError_t gemm16_launch(const GemmCall& c, OpHandle& h, cudaStream_t s, int* l
     f.ldo = a.ldo;
     f.save_gate = a.save_gate;
     f.save_up = a.save_up;
-    f.nscale_gate = a.nscale_gate;
-    f.nscale = a.nscale;
-    f.bias = a.bias;
     const int64_t n = static_cast<int64_t>(a.batches) * a.M * ((a.N + 3) / 4);
     e = launch_chained(k_gemm16_finish, (n + 127) / 128, 128, 0, 1, s, f);
     ++*launches;

@@ -1,6 +1,5 @@
 // 16-bit GEMM on tcgen05 with warp-specialised roles (k_gemm16): the products
-// of the gated block's forward and backward pass, and of the 4-bit linear
-// operators once their weights are expanded.
+// of the gated block's forward and backward pass.
 //
 //   D[m, n] = sum_k A[m, k] B[n, k]        fp32 accumulators in tensor memory
 //
@@ -15,9 +14,9 @@
 // A tile is CG * 128 rows by BN columns.  With CG = 2 a pair of CTAs shares
 // it: each holds 128 rows of A and half of B's rows, one tcgen05.mma reads both
 // CTAs' shared memory, and B's tile is read from L2 once for 256 rows instead
-// of once per 128.  (At 256 x 256
-// a 64-wide K step moves 64 KB into the pair for 8.4 million multiply-adds: 64
-// bytes a clock and SM beside a saturated tensor pipe; with CG = 1, 96.)
+// of once per 128.  (At 256 x 256 a 64-wide K step moves 64 KB into the pair for
+// 4.2 million multiply-adds: 64 bytes a clock and SM beside a saturated tensor
+// pipe; with CG = 1, 96.)
 // Measured on 4096 rows of 4096 against 2 x 8192: 280 us, 1.97 PFLOP/s; with the
 // pre-activations saved 320 us.
 //
@@ -63,8 +62,6 @@ struct GemmArgs {
   int64_t ldo;
   int out_vec;          // out and ldo allow 16-byte (1) or 32-byte (2) stores
   float *save_gate, *save_up;   // pre-activations [M, N] fp32, or null
-  const float *nscale_gate, *nscale;   // per-column factors of the accumulators, or null
-  const void* bias;     // [N] dt, or null
   float* part;          // [ksplit][batch][M][ld_part] fp32
   int64_t ld_part;      // columns of a partial row (dual: gate at 0, up at ld_part / 2)
   int* status;
@@ -380,18 +377,6 @@ __global__ void __launch_bounds__(GM_THREADS, 1) k_gemm16(const __grid_constant_
         }
         // (each choice outside its loop: a warp is alone on its scheduler here, and 32
         // independent elements are what hides the latency of the arithmetic)
-        if (A.nscale) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const int cc = min(col0 + j, A.N - 1);
-            if (A.dual) {
-              r0[j] = __float_as_uint(__uint_as_float(r0[j]) * __ldg(A.nscale_gate + cc));
-              r1[j] = __float_as_uint(__uint_as_float(r1[j]) * __ldg(A.nscale + cc));
-            } else {
-              r0[j] = __float_as_uint(__uint_as_float(r0[j]) * __ldg(A.nscale + cc));
-            }
-          }
-        }
         if (A.dual) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = act_value(ACT_SWIGLU, __uint_as_float(r0[j]), __uint_as_float(r1[j]));
@@ -401,10 +386,6 @@ __global__ void __launch_bounds__(GM_THREADS, 1) k_gemm16(const __grid_constant_
         } else {
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r0[j]);
-        }
-        if (A.bias) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] += ld16(A.bias, min(col0 + j, A.N - 1), A.dt);
         }
         gm_store16(st, v, A.dt, static_cast<unsigned short*>(U.z ? A.out[1] : A.out[0]), A.ldo, row0, col0, A.M, A.N, A.out_vec,
                    lane);
@@ -420,8 +401,9 @@ __global__ void __launch_bounds__(GM_THREADS, 1) k_gemm16(const __grid_constant_
   }
 }
 
-// Sums the K splits' partials in order and applies the epilogue: one thread per
-// output row and four columns.
+// Sums the K splits' partials in order and applies the epilogue (k_qgemm's too,
+// with its per-column factors and bias): one thread per output row and four
+// columns.
 struct GemmFinishArgs {
   const float* part;
   int64_t ld_part;

@@ -124,8 +124,6 @@ struct GemmCall {
   void* out[2] = {nullptr, nullptr};
   int64_t ldo = 0;
   float *save_gate = nullptr, *save_up = nullptr;
-  const float *nscale_gate = nullptr, *nscale = nullptr;
-  const void* bias = nullptr;
 };
 
 // Partial sums of a split K ([ksplit][M][ld_part] fp32, SwiGLU: gate at 0, up at
