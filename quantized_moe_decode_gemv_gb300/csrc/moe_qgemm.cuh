@@ -42,6 +42,8 @@
 // status word and winds down.
 #pragma once
 
+#include <algorithm>
+
 #include "moe_stream.cuh"
 
 namespace moe_op {
@@ -81,7 +83,7 @@ __host__ __device__ inline int qg_smem_bytes(int fmt, int gb, int mt, int ntok, 
 struct QGemmUnit {
   int split, row, t0, c0, c1;   // 128-row block, first token, chunks [c0, c1)
 };
-__device__ __forceinline__ QGemmUnit qg_unit(const QGemmArgs& A, int q, int row_tiles, int tok_tiles, int u) {
+__host__ __device__ __forceinline__ QGemmUnit qg_unit(const QGemmArgs& A, int q, int row_tiles, int tok_tiles, int u) {
   QGemmUnit U;
   U.t0 = (u % tok_tiles) * A.ntok;
   u /= tok_tiles;
@@ -90,8 +92,64 @@ __device__ __forceinline__ QGemmUnit qg_unit(const QGemmArgs& A, int q, int row_
   // splits at even chunks (groups of 128 and code stages stay whole)
   const int ns = (A.chunks + 1) / 2;
   U.c0 = static_cast<int>(static_cast<int64_t>(U.split) * ns / A.ksplit) * 2;
-  U.c1 = min(A.chunks, static_cast<int>(static_cast<int64_t>(U.split + 1) * ns / A.ksplit) * 2);
+  U.c1 = static_cast<int>(static_cast<int64_t>(U.split + 1) * ns / A.ksplit) * 2;
+  if (U.c1 > A.chunks) U.c1 = A.chunks;
   return U;
+}
+
+// A decode warp's place in the ring.  Before it fills a block's slot it waits for
+// the release of the block S before it, and a barrier tells only the parity of its
+// releases: a slot one release further behind looks the same.  So the wait at block
+// n is right only if the warp knows that block n - 2 S was released, that is, if
+// its last wait (releases come in order) was at block n - S or later.
+struct QGemmRing {
+  int S = 0;            // slots
+  RingPos R;
+  bool again = false;   // slots have been used before
+  int block = 0;        // blocks of this CTA so far
+  __host__ __device__ __forceinline__ void skip(int n) {
+    for (int i = 0; i < n; ++i) {
+      R.next(S);
+      again = again || R.slot == 0;
+      ++block;
+    }
+  }
+  // wait(block, slot, parity): until the slot of the next block is free
+  template <typename W>
+  __host__ __device__ __forceinline__ bool free_slot(W&& wait) const {
+    return !again || wait(block, R.slot, R.parity ^ 1u);
+  }
+  // n blocks of the other group go by; their slots' releases are seen
+  template <typename W>
+  __host__ __device__ __forceinline__ bool pass(int n, W&& wait) {
+    if (n < 1) return true;
+    skip(n - 1);
+    if (!free_slot(wait)) return false;
+    skip(1);
+    return true;
+  }
+};
+
+// The K blocks [c0, c1) of a unit as a decode group takes them: pair(c) for blocks c
+// and c + 1, all pairs of a gated product, every other one where two groups take
+// turns.  Inside a unit three blocks lie between a group's waits (four where it
+// waits at the later block of a pair, with S >= 4), which the ring's three or more
+// slots allow (qg_plan).  Where units meet there may be more, so the blocks passed
+// over there are waited for like the group's own.
+template <bool GATED, typename P, typename W>
+__host__ __device__ __forceinline__ bool qg_walk(QGemmRing& Q, int c0, int c1, int half, P&& pair, W&& wait) {
+  constexpr int step = GATED ? 2 : 4;
+  const int first = GATED ? 0 : 2 * half;
+  if (!GATED && half && !Q.pass(first < c1 - c0 ? first : c1 - c0, wait)) return false;
+  for (int c = c0 + first; c < c1; c += step) {
+    if (!pair(c)) return false;
+    if (!GATED) {
+      const int end = c + step < c1 ? c + step : c1, n = end > c + 2 ? end - (c + 2) : 0;
+      if (c + step < c1) Q.skip(n);
+      else if (!Q.pass(n, wait)) return false;
+    }
+  }
+  return true;
 }
 
 template <int FMT, bool FP16, bool GATED, int GB>
@@ -258,14 +316,9 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
     };
     for (int i = 0; i < D - 1; ++i) fill_next();
     uint32_t cst = ring;
-    RingPos R;
-    bool again = false;   // slots have been used before
-    auto skip = [&](int n) {
-      for (int i = 0; i < n; ++i) {
-        R.next(S);
-        again = again || R.slot == 0;
-      }
-    };
+    QGemmRing Q;
+    Q.S = S;
+    auto slot_free = [&](int, int sl, uint32_t parity) { return wait(smem_u32(&empty[sl]), parity); };
     // With four slots or more a pair of K blocks is taken at once: the slots are
     // released in order, so the later one's release is both's.
     const bool pairs = S >= 4;
@@ -274,8 +327,7 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
       const QGemmUnit U = qg_unit(A, q, row_tiles, tok_tiles, u);
       // rows past the matrix: their A rows stay what they were, their outputs are not written
       const bool in = tile_of(U) < tiles16;
-      if (first) skip(min(first, U.c1 - U.c0));
-      for (int c = U.c0 + first; ok && c < U.c1; c += step) {
+      qg_walk<GATED>(Q, U.c0, U.c1, half, [&](int c) {
         __syncwarp();   // every lane has read the stage that is filled now
         fill_next();
         if (D == 3) copies_wait_n<2>();
@@ -298,15 +350,13 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
           }
         }
         const bool two = c + 1 < U.c1;
-        const int sl0 = R.slot;
+        const int sl0 = Q.R.slot;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (i == 1 && !two) break;
-          if (pairs && i == 0 && two) skip(1);
-          const int sl = pairs && i == 0 ? sl0 : R.slot;
-          if (!(pairs && i == 1)) {
-            if (again && !wait(smem_u32(&empty[R.slot]), R.parity ^ 1u)) break;
-          }
+          if (pairs && i == 0 && two) Q.skip(1);
+          const int sl = pairs && i == 0 ? sl0 : Q.R.slot;
+          if (!(pairs && i == 1) && !Q.free_slot(slot_free)) break;
           if (in) {
             // (groups of 32: odd rows store their halves in the other order, so that eight lanes' stores touch all banks)
             if (!st_wide(FMT, GB) && (g & 1)) {
@@ -365,12 +415,11 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
               if (pairs && i == 1) bar_arrive(smem_u32(&full[sl0]));
               bar_arrive(smem_u32(&full[sl]));
             }
-            skip(1);
+            Q.skip(1);
           }
         }
-        if (!ok) break;
-        if (!GATED) skip(max(0, min(U.c1, c + step) - (c + 2)));   // the other group's K blocks
-      }
+        return ok;
+      }, slot_free);
     }
     copies_wait(0);
   } else if (warp >= 4) {
@@ -459,6 +508,54 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
     tm_fence_after();
     tm_free<1>(tmem, tm_cols);
   }
+}
+
+// Host: token tile and K split of a call: the least estimated time in SM clocks.  A
+// tile's 64-wide block takes the longest of its MMAs (2 ntok clocks a matrix), its
+// decode (700 clocks at the rate seen, both matrices of a pair at once, two groups
+// of warps taking turns with one) and its bytes at 40 a clock; a tile that does not
+// overlap the next one adds its epilogue.
+struct QGemmPlan {
+  int ntok = 0, ksplit = 1, slots = 0, depth = 0, units = 0;
+};
+inline QGemmPlan qg_plan(int fmt, int gb, int M, int chunks, int T, int N, int sms, size_t part_bytes) {
+  QGemmPlan best;
+  double best_t = 1e30;
+  const int rt = (N + 127) / 128;
+  for (int tt = (T + 255) / 256, last = tt + 3; tt <= last; ++tt) {
+    const int ntok = std::max(16, ((T + tt - 1) / tt + 15) / 16 * 16);
+    if ((T + ntok - 1) / ntok < tt) continue;
+    for (int ks = 1; ks <= 8; ++ks) {
+      if (ks > 1) {
+        if (chunks / ks < 8) break;
+        if (static_cast<size_t>(ks) * T * (N + 3) / 4 * 4 * M * 4 > part_bytes) break;
+      }
+      const int units = rt * tt * ks;
+      const double waves = (units + sms - 1) / sms;
+      const double kb = std::max({2.0 * M * ntok, M == 2 ? 700.0 : 350.0,
+                                  (ntok * 128.0 + 8.0 * M * (512 + st_scale_bytes(fmt, gb))) / 40.0});
+      const bool two = 2 * M * qg_region(ntok) <= 512;
+      const double epi = 6.0 * M * ntok;
+      const double t = waves * (static_cast<double>(chunks) / ks * kb + (two ? 0.0 : epi)) + epi + 4000.0 +
+                       (ks > 1 ? 7000.0 + 0.25 * ks * T * M * N / sms : 0.0);
+      if (t < best_t) {
+        best_t = t;
+        best.ntok = ntok;
+        best.ksplit = ks;
+        best.units = units;
+      }
+    }
+  }
+  // shared memory: slots first, then a third code stage.  Two slots of a pair of
+  // matrices and two stages fit at 256 tokens; with one matrix three do, which its
+  // decode groups need (qg_walk).
+  best.depth = 2;
+  best.slots = 2;
+  auto fits = [&](int n, int d) { return qg_smem_bytes(fmt, gb, M, best.ntok, n, d) <= QG_SMEM_MAX; };
+  while (best.slots < 4 && fits(best.slots + 1, 2)) ++best.slots;
+  if (fits(best.slots, 3)) best.depth = 3;
+  while (best.slots < QG_MAX_SLOTS && fits(best.slots + 1, best.depth)) ++best.slots;
+  return best;
 }
 
 }  // namespace moe_op

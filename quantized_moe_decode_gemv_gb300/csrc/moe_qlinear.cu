@@ -282,53 +282,9 @@ QGemmKernel qgemm_kernel(const moe_qlinear_config& c) {
   return gated ? qgemm_kernel_t<false, true>(c) : qgemm_kernel_t<false, false>(c);
 }
 
-// Token tile and K split of a call: the least estimated time in SM clocks.  A
-// tile's 64-wide block takes the longest of its MMAs (2 ntok clocks a matrix), its
-// decode (700 clocks at the rate seen, both matrices of a pair at once, two groups
-// of warps taking turns with one) and its bytes at 40 a clock; a tile that does not
-// overlap the next one adds its epilogue.
-struct QGemmPlan {
-  int ntok = 0, ksplit = 1, slots = 0, depth = 0, units = 0;
-};
 QGemmPlan qgemm_plan(const moe_qlinear& h, int T) {
   const moe_qlinear_config& c = h.cfg;
-  const int fmt = stream_format(c), gb = c.group_size == 32 ? 2 : 4, M = h.mats;
-  QGemmPlan best;
-  double best_t = 1e30;
-  const int rt = (c.out_features + 127) / 128;
-  for (int tt = (T + 255) / 256, last = tt + 3; tt <= last; ++tt) {
-    const int ntok = std::max(16, ((T + tt - 1) / tt + 15) / 16 * 16);
-    if ((T + ntok - 1) / ntok < tt) continue;
-    for (int ks = 1; ks <= 8; ++ks) {
-      if (ks > 1) {
-        if (h.chunks / ks < 8) break;
-        if (static_cast<size_t>(ks) * T * (c.out_features + 3) / 4 * 4 * M * 4 > h.part_bytes) break;
-      }
-      const int units = rt * tt * ks;
-      const double waves = (units + h.num_sms - 1) / h.num_sms;
-      const double kb = std::max({2.0 * M * ntok, M == 2 ? 700.0 : 350.0,
-                                  (ntok * 128.0 + 8.0 * M * (512 + st_scale_bytes(fmt, gb))) / 40.0});
-      const bool two = 2 * M * qg_region(ntok) <= 512;
-      const double epi = 6.0 * M * ntok;
-      const double t = waves * (static_cast<double>(h.chunks) / ks * kb + (two ? 0.0 : epi)) + epi + 4000.0 +
-                       (ks > 1 ? 7000.0 + 0.25 * ks * T * M * c.out_features / h.num_sms : 0.0);
-      if (t < best_t) {
-        best_t = t;
-        best.ntok = ntok;
-        best.ksplit = ks;
-        best.units = units;
-      }
-    }
-  }
-  // shared memory: slots first, then a third code stage (two slots and two stages
-  // fit at 256 tokens)
-  best.depth = 2;
-  best.slots = 2;
-  auto fits = [&](int n, int d) { return qg_smem_bytes(fmt, gb, M, best.ntok, n, d) <= QG_SMEM_MAX; };
-  while (best.slots < 4 && fits(best.slots + 1, 2)) ++best.slots;
-  if (fits(best.slots, 3)) best.depth = 3;
-  while (best.slots < QG_MAX_SLOTS && fits(best.slots + 1, best.depth)) ++best.slots;
-  return best;
+  return qg_plan(stream_format(c), c.group_size == 32 ? 2 : 4, h.mats, h.chunks, T, c.out_features, h.num_sms, h.part_bytes);
 }
 
 cudaError_t run_qgemm(moe_qlinear& h, const void* x, int64_t ldx, int T, void* out, int64_t ldo, cudaStream_t s,

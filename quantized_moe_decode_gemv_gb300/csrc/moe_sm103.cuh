@@ -74,7 +74,7 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
 struct RingPos {
   int slot = 0;
   uint32_t parity = 0;
-  __device__ __forceinline__ void next(int n) {
+  __host__ __device__ __forceinline__ void next(int n) {
     if (++slot == n) {
       slot = 0;
       parity ^= 1u;
