@@ -230,6 +230,7 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
   } else if (warp == 1) {
     // ---------------- MMAs ----------------
     const uint32_t idesc = f16_idesc(128, ntok, DT, 0, 0);
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // no token rows come before: the waits are bounded
     RingPos R;
     uint32_t done = 0;
     for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++done) {
@@ -318,7 +319,14 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
     uint32_t cst = ring;
     QGemmRing Q;
     Q.S = S;
-    auto slot_free = [&](int, int sl, uint32_t parity) { return wait(smem_u32(&empty[sl]), parity); };
+    // The first slots are filled while the kernel before this one in the stream
+    // ends; a bounded wait begins after it, or its time would count.
+    bool after = false;
+    auto slot_free = [&](int, int sl, uint32_t parity) {
+      if (!after) asm volatile("griddepcontrol.wait;" ::: "memory");
+      after = true;
+      return wait(smem_u32(&empty[sl]), parity);
+    };
     // With four slots or more a pair of K blocks is taken at once: the slots are
     // released in order, so the later one's release is both's.
     const bool pairs = S >= 4;
