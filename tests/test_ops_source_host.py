@@ -20,3 +20,14 @@ def test_bounded_waits_begin_after_the_kernel_before(role):
     text = source("moe_qgemm.cuh")
     part = text[text.index(f"// ---------------- {role} ----------------"):]
     assert "griddepcontrol.wait" in part and part.index("griddepcontrol.wait") < part.index("wait(smem_u32")
+
+
+@pytest.mark.parametrize("name", ["moe_gated.cu", "moe_gemm16.cuh", "moe_outer.cuh", "moe_qgemm.cuh", "moe_stream.cuh",
+                                  "moe_stream16.cuh"])
+def test_chained_kernels_promise_no_constant_inputs(name):
+    """A chained kernel's inputs may be written while it already runs, until its wait:
+    none is declared const __restrict__, which allows reads ahead of the wait."""
+    for kernel in re.split(r"__global__", source(name))[1:]:
+        head, body = kernel.split("{", 1)
+        if "griddepcontrol.wait" in body.split("__global__")[0]:
+            assert "__restrict__" not in head, head
