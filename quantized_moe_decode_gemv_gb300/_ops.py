@@ -4,7 +4,9 @@ the linear operators with 4-bit weights and the 16-bit gated block.
 Argument checks and marshalling; the arithmetic runs in the CUDA library.
 Outputs are allocated on the stream of the call: with ``stream=None`` the
 current one, otherwise the given one, where a consumer on another stream has to
-order itself after the call as after any kernel.
+order itself after the call as after any kernel.  The caller orders a given stream
+after what writes the inputs; tensors handed to such a call are marked as used on
+it (``Tensor.record_stream``), so they may be dropped right after the call.
 """
 from __future__ import annotations
 
@@ -74,14 +76,17 @@ class _Handle:
             raise MoEError(_INVALID_ARG, f"{what} must be a contiguous {self._dtype} tensor on {self.device}")
         return w.data_ptr()
 
-    def _stream(self, stream):
-        """(stream handle, context in which outputs are allocated)."""
+    def _stream(self, stream, *tensors):
+        """(stream handle, context in which outputs are allocated) of a call that uses ``tensors``."""
         if stream is None:
             if self._raw_stream is not None:
                 return self._raw_stream(self.device.index), _HERE
             return self._torch.cuda.current_stream(self.device).cuda_stream, _HERE
         if not hasattr(stream, "cuda_stream"):
             stream = self._torch.cuda.ExternalStream(int(stream), device=self.device)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)   # not the allocation's own: freed memory waits for it
         return int(stream.cuda_stream), self._torch.cuda.stream(stream)
 
     def device_status(self, stream=None) -> int:
@@ -195,7 +200,7 @@ class QLinear(_Handle):
         """out [T, N] of x [T, K] (rows may be strided); ``out`` may be given, rows strided too."""
         ldx = self._stride(x, self._K, "x")
         T = x.shape[0]
-        s, where = self._stream(stream)
+        s, where = self._stream(stream, x, out)
         if out is None:
             if stream is None:
                 out = self._empty((T, self._N), dtype=self._dtype, device=self.device)
@@ -283,7 +288,7 @@ class GatedBlock(_Handle):
         N, device, empty = self._N, self.device, self._empty
         ldx = self._stride(x, self._K, "x")
         pu, pg = self._weights(up_w, gate_w)
-        s, where = self._stream(stream)
+        s, where = self._stream(stream, x, up_w, gate_w, out)
         T, ldo, g, u = x.shape[0], N, None, None
         if out is not None:
             ldo = self._stride(out, N, "out")
@@ -331,7 +336,7 @@ class GatedBlock(_Handle):
                     not t.is_contiguous()):
                 raise MoEError(_INVALID_ARG, "saved must be what forward_train returned for x")
             ps[i] = t.data_ptr()
-        s, where = self._stream(stream)
+        s, where = self._stream(stream, d_out, x, up_w, gate_w, *(saved if pg is not None else saved[1:]))
         with where:
             d_x = empty((T, K), dtype=dtype, device=device) if "x" in need else None
             d_g = empty((N, K), dtype=dtype, device=device) if pg is not None and "gate_w" in need else None
