@@ -168,9 +168,11 @@ static moe_status create(const moe_gated_config* cfg, moe_gated** out, moe_gated
   const bool gated = c.act == MOE_ACT_SWIGLU;
   cudaError_t e = h->alloc(reinterpret_cast<void**>(&h->status), 64);
   if (e == cudaSuccess) e = cudaMemset(h->status, 0, 64);
-  h->part_bytes = gemm16_part_bytes(c.max_tokens, std::max<int64_t>(c.out_features * (gated ? 2ll : 1ll),
-                                                                    c.training ? c.in_features : 0));
-  if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->part), h->part_bytes);
+  if (c.training || c.max_tokens > ST_MAX_T) {   // else every call streams and splits nothing
+    h->part_bytes = gemm16_part_bytes(c.max_tokens, std::max<int64_t>(c.out_features * (gated ? 2ll : 1ll),
+                                                                      c.training ? c.in_features : 0), sms);
+    if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->part), h->part_bytes);
+  }
   const size_t grad = static_cast<size_t>(c.max_tokens) * c.out_features * 2;
   if (c.training && e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->du), grad);
   if (c.training && gated && e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->dg), grad);

@@ -151,8 +151,8 @@ cudaError_t gemm16_launch(const GemmCall& c, OpHandle& h, cudaStream_t s, int* l
 // Once per create, with the handle's device current: kernel attributes, the
 // tensor-map encoder; false with the reason.
 bool gemm16_setup(std::string* why);
-// Bytes of OpHandle::part that any product of at most M rows and N partial
-// columns may use.
-size_t gemm16_part_bytes(int M, int64_t ld_part);
+// Bytes of OpHandle::part for the K splits of gemm16_launch with at most M rows
+// and ld_part partial columns.
+size_t gemm16_part_bytes(int M, int64_t ld_part, int sms);
 
 }  // namespace moe_op

@@ -526,6 +526,10 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
 struct QGemmPlan {
   int ntok = 0, ksplit = 1, slots = 0, depth = 0, units = 0;
 };
+// Bytes of partial sums of a K split (rounded up from [ks][T][M] rows of (N + 3) / 4 * 4).
+inline size_t qg_split_bytes(int M, int N, int T, int ks) {
+  return static_cast<size_t>(ks) * T * (N + 3) / 4 * 4 * M * 4;
+}
 inline QGemmPlan qg_plan(int fmt, int gb, int M, int chunks, int T, int N, int sms, size_t part_bytes) {
   QGemmPlan best;
   double best_t = 1e30;
@@ -536,7 +540,7 @@ inline QGemmPlan qg_plan(int fmt, int gb, int M, int chunks, int T, int N, int s
     for (int ks = 1; ks <= 8; ++ks) {
       if (ks > 1) {
         if (chunks / ks < 8) break;
-        if (static_cast<size_t>(ks) * T * (N + 3) / 4 * 4 * M * 4 > part_bytes) break;
+        if (qg_split_bytes(M, N, T, ks) > part_bytes) break;
       }
       const int units = rt * tt * ks;
       const double waves = (units + sms - 1) / sms;
@@ -564,6 +568,18 @@ inline QGemmPlan qg_plan(int fmt, int gb, int M, int chunks, int T, int N, int s
   if (fits(best.slots, 3)) best.depth = 3;
   while (best.slots < QG_MAX_SLOTS && fits(best.slots + 1, best.depth)) ++best.slots;
   return best;
+}
+
+// Host: bytes of partial sums that the plans of 1 to max_tokens rows use, of 64 MB
+// that they may ask for.  (4096 x 4096, 4096 rows: 9 MB.)
+inline size_t qg_part_bytes(int fmt, int gb, int M, int chunks, int max_tokens, int N, int sms) {
+  constexpr size_t cap = 64ull << 20;
+  size_t most = 0;
+  for (int T = 1; T <= max_tokens && chunks >= 16 && qg_split_bytes(M, N, T, 2) <= cap; ++T) {
+    const QGemmPlan P = qg_plan(fmt, gb, M, chunks, T, N, sms, cap);
+    if (P.ksplit > 1) most = std::max(most, qg_split_bytes(M, N, T, P.ksplit));
+  }
+  return most;
 }
 
 }  // namespace moe_op

@@ -440,8 +440,9 @@ static moe_status create(const moe_qlinear_config* cfg, const moe_qlinear_weight
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(reinterpret_cast<const void*>(qgemm_kernel(c)),
                                cudaFuncAttributeMaxDynamicSharedMemorySize, QG_SMEM_MAX);
-    h->part_bytes = gemm16_part_bytes(c.max_tokens, static_cast<int64_t>(h->mats) * c.out_features);
-    if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->part), h->part_bytes);
+    h->part_bytes = qg_part_bytes(stream_format(c), c.group_size == 32 ? 2 : 4, h->mats, h->chunks, c.max_tokens,
+                                  c.out_features, sms);
+    if (e == cudaSuccess && h->part_bytes) e = h->alloc(reinterpret_cast<void**>(&h->part), h->part_bytes);
   }
   for (int nt = 1; nt <= 2 && e == cudaSuccess; ++nt)
     e = cudaFuncSetAttribute(reinterpret_cast<const void*>(stream_kernel(c, nt)),
