@@ -466,8 +466,9 @@ moe_status moe_gated_create(const moe_gated_config *cfg, moe_gated **out);
 /* out[T, N] from x[T, K] and gate_w, up_w [N, K] (row-major, contiguous; gate_w
  * NULL for RELU2).  save_gate, save_up: NULL, or [T, N] fp32 buffers that
  * receive the pre-activations g and u for the backward pass (both for SWIGLU,
- * save_up alone for RELU2).  All pointers 16-byte aligned except out; ldx and
- * ldo as in moe_qlinear_forward.  T = 0 does nothing.  Streams, devices, graphs
+ * save_up alone for RELU2); they overlap neither each other nor x, out or the
+ * weights.  All pointers 16-byte aligned except out; ldx and ldo as in
+ * moe_qlinear_forward.  T = 0 does nothing.  Streams, devices, graphs
  * and overlap as moe_qlinear_forward. */
 moe_status moe_gated_forward(moe_gated *h, const void *x, int64_t ldx, int32_t T, const void *gate_w, const void *up_w,
                              void *out, int64_t ldo, float *save_gate, float *save_up, void *stream);

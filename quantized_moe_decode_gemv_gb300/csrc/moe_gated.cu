@@ -217,6 +217,11 @@ static moe_status forward(moe_gated* h, const void* x, int64_t ldx, int32_t T, c
   const int64_t no = span(T, ldo, N), nw = static_cast<int64_t>(K) * N * 2;
   if (rows_overlap(x, ldx, K, out, ldo, N, T) || overlap(out, no, up_w, nw) || overlap(out, no, gate_w, nw))
     return fail(MOE_ERR_INVALID_ARG, "out overlaps an input");
+  const int64_t nx = span(T, ldx, K), ns = 4ll * T * N;
+  for (const float* p : {save_gate, save_up})
+    if (overlap(p, ns, x, nx) || overlap(p, ns, out, no) || overlap(p, ns, up_w, nw) || overlap(p, ns, gate_w, nw))
+      return fail(MOE_ERR_INVALID_ARG, "a saved buffer overlaps an input or out");
+  if (overlap(save_gate, ns, save_up, ns)) return fail(MOE_ERR_INVALID_ARG, "the saved buffers overlap");
   DeviceScope dev(h->device);
   if (!dev.ok) return fail(MOE_ERR_DEVICE, "the handle's device cannot be made current");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
