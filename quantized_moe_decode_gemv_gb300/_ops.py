@@ -13,6 +13,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import dataclasses
+import operator
 from typing import Any, Dict, NamedTuple, Optional, Tuple
 
 from ._capi import (ACT, DTYPE, MOE_OK, QLINEAR_ACT, WFMT, MoEError, load_library, moe_gated_config,
@@ -26,6 +27,14 @@ def _name_of(table: Dict[str, int], key: str, what: str) -> int:
     if key not in table:
         raise MoEError(_INVALID_ARG, f"unknown {what} {key!r} (one of {', '.join(table)})")
     return table[key]
+
+
+def _int32(value, what: str) -> int:
+    """``value`` for a C int32 field (ctypes would keep its low 32 bits)."""
+    v = operator.index(value)
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise MoEError(_INVALID_ARG, f"{what} {v} does not fit 32 bits")
+    return v
 
 
 class _Handle:
@@ -63,6 +72,8 @@ class _Handle:
             raise MoEError(_INVALID_ARG, f"{what} needs consecutive columns")
         if shape[0] <= 1:
             return cols
+        if shape[0] >= 2 ** 31:   # (the C entry refuses more rows than max_tokens)
+            raise MoEError(_INVALID_ARG, f"{what} has {shape[0]} rows")
         if row < cols:
             raise MoEError(_INVALID_ARG, f"{what} has overlapping rows")
         return row
@@ -130,10 +141,11 @@ class QLinearConfig:
 
     def to_c(self) -> moe_qlinear_config:
         return moe_qlinear_config(
-            in_features=self.in_features, out_features=self.out_features, group_size=self.group_size,
+            in_features=_int32(self.in_features, "in_features"),
+            out_features=_int32(self.out_features, "out_features"), group_size=_int32(self.group_size, "group_size"),
             weight_format=_name_of(WFMT, self.fmt, "fmt"), act_dtype=_name_of(DTYPE, self.act_dtype, "act_dtype"),
             scale_dtype=_name_of(DTYPE, self.scale_dtype, "scale_dtype"), act=_name_of(QLINEAR_ACT, self.act, "act"),
-            has_bias=int(bool(self.bias)), max_tokens=self.max_tokens)
+            has_bias=int(bool(self.bias)), max_tokens=_int32(self.max_tokens, "max_tokens"))
 
 
 class QLinear(_Handle):
@@ -236,9 +248,10 @@ class GatedConfig:
 
     def to_c(self) -> moe_gated_config:
         return moe_gated_config(
-            in_features=self.in_features, out_features=self.out_features, act=_name_of(ACT, self.act, "act"),
-            act_dtype=_name_of(DTYPE, self.act_dtype, "act_dtype"), max_tokens=self.max_tokens,
-            training=int(bool(self.training)))
+            in_features=_int32(self.in_features, "in_features"),
+            out_features=_int32(self.out_features, "out_features"), act=_name_of(ACT, self.act, "act"),
+            act_dtype=_name_of(DTYPE, self.act_dtype, "act_dtype"),
+            max_tokens=_int32(self.max_tokens, "max_tokens"), training=int(bool(self.training)))
 
 
 class GatedGrads(NamedTuple):
