@@ -352,11 +352,15 @@ moe_status moe_router_topk_noalloc(const void *x, int32_t T, int32_t hidden, int
  * rows (fewer where rows of x several thousand columns wide leave it no shared
  * memory) a streaming kernel multiplies by the codes themselves.  Above that the weights
  * are decoded to act_dtype on their way into the tensor cores: exactly for the fp4
- * formats, rounded once for affine ones (with fp16 activations an affine weight
- * has to stay below 65504).  A row of W with a NaN scale gives NaN, a NaN in a row
- * of x reaches that row of out only, an infinity in x gives infinity or NaN.
- * MXFP4: a block scale more than 2^24 (fp16) or 2^250 (bf16) below the largest of
- * its row of W counts with fewer bits or as zero.
+ * formats, rounded once for affine ones, so that the same row of x may come out
+ * differently, within that rounding, in a larger batch.  (With fp16 activations a
+ * decoded affine weight has fp16's range there: it has to stay below 65504, and one
+ * below 2^-14 keeps fewer bits, down to none at 2^-25.)  A row of W with a NaN scale
+ * gives NaN, a NaN in a row of x reaches that row of out only, an infinity in x gives
+ * infinity or NaN.  Finite bf16 rows of x should stay below 2^110 (the affine codes
+ * are multiplied with an offset of 128 that cancels) and above 2^-100 (NVFP4 sums run
+ * 2^20 lower).  MXFP4: a block scale more than 2^24 (fp16) or 2^110 (bf16) below the
+ * largest of its row of W counts with fewer bits or as zero, whatever x is.
  * ------------------------------------------------------------------------- */
 typedef enum moe_qlinear_act {
   MOE_QLINEAR_SWIGLU = 0,   /* the values of moe_act */
@@ -442,8 +446,10 @@ const char *moe_qlinear_last_error(const moe_qlinear *h);
  *   d_x = dg Wg + du Wu,  d_gate_w = dg^T x,  d_up_w = du^T x
  *
  * Sums and pre-activations are fp32; outputs and gradients are rounded once
- * from fp32.  (dg and du are rounded to act_dtype on their way into the
- * tensor-core products.)
+ * from fp32.  dg and du are rounded to act_dtype on their way into the
+ * tensor-core products.  In fp16 they have its range there: above 65504 they are
+ * infinite, below 2^-14 they keep fewer bits, down to none at 2^-25.  Scale the
+ * loss so that they lie between.
  * ------------------------------------------------------------------------- */
 typedef struct moe_gated_config {
   int32_t in_features;    /* K: a multiple of 8, 8..65536 */

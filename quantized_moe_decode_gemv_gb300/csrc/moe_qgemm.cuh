@@ -24,8 +24,9 @@
 //              blocks.  Codes and scales come by 16-byte asynchronous copies
 //              into a private ring, are decoded as k_stream does (an affine weight
 //              is rounded once to the 16-bit type, a relative error of at most
-//              2^-8 or 2^-11 beside the output's own; an fp4 weight times its
-//              block scale is exact) and stored in the 128-byte swizzle
+//              2^-8 or 2^-11 beside the output's own, in fp16 more below 2^-14,
+//              where its steps stay 2^-24; an fp4 weight times its block scale is
+//              exact) and stored in the 128-byte swizzle
 //   warp 1     issues the MMAs of a slot and commits them to its release
 //   warp 2     owns the tensor memory
 //   warps 4-7  the epilogue: a lane a weight row; four lanes exchange four tokens'

@@ -36,7 +36,8 @@ __device__ uint32_t e4m3_fields(uint32_t byte, bool* zero) {
 // times 2^106 (bf16) or 2^7 (fp16); MXFP4 keeps the exponent relative to the
 // row's largest e0, as the float 2^(byte - e0 + 126) (bf16) or 2^(byte - e0 +
 // 15) (fp16).  A scale below the type's range (2^-252, or 2^-29 of the row's
-// largest) counts as zero.
+// largest) counts as zero; the weights themselves, v times it, are whole down to
+// 2^-132 (bf16) or 2^-24 (fp16) of the largest scale.
 template <int FMT, bool FP16>
 __device__ uint32_t scale_byte(uint32_t byte, int e0, bool* zero) {
   if (FMT == W_NVFP4) {
