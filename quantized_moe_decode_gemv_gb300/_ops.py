@@ -155,6 +155,8 @@ class QLinear(_Handle):
     ``b`` (affine: scale dtype [N, K/G]; nvfp4: uint8 [N, K/16] and fp32 [1];
     mxfp4: uint8 [N, K/32] and None), ``gate_q``, ``gate_s``, ``gate_b`` for
     "swiglu", ``bias`` [N].  They are copied and may be freed afterwards.
+
+    No autograd function: ``requires_grad`` is not looked at, and ``out`` carries no graph.
     """
 
     _prefix = "moe_qlinear"
@@ -262,7 +264,12 @@ class GatedGrads(NamedTuple):
 
 
 class GatedBlock(_Handle):
-    """``silu(x Wg^T) * (x Wu^T)`` or ``max(x Wu^T, 0)^2`` over the caller's 16-bit weights, and its backward pass."""
+    """``silu(x Wg^T) * (x Wu^T)`` or ``max(x Wu^T, 0)^2`` over the caller's 16-bit weights, and its backward pass.
+
+    No autograd function: ``requires_grad`` is not looked at, outputs carry no graph
+    and no ``.grad`` is written; a training loop calls ``backward`` and hands its
+    results on.
+    """
 
     _prefix = "moe_gated"
 

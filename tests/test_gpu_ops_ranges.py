@@ -3,7 +3,7 @@ import pytest
 import torch
 
 from tests import ops_reference as ref
-from tests.test_gpu_ops import FORMATS, make_linear, rows, want_linear
+from tests.test_gpu_ops import FORMATS, make_block, make_linear, rows, want_linear
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +43,19 @@ def test_large_and_small_rows(pkg, fmt, G, T, scale):
     x = rows(T, 512, "bf16", 4, scale=scale)
     want, e = want_linear(x, None, w, None, fmt, G, "bf16", "none")
     ref.check(op(x), want, e, "bf16", "range")
+
+
+def test_no_graph_is_recorded(pkg):
+    """The operators are no autograd functions: inputs that require gradients are taken
+    as they are, outputs carry no graph, and nobody's .grad is touched."""
+    op, _, _, _ = make_linear(pkg, 64, 128, "affine", 64, "bf16", "none", False, 32)
+    block, x, up, gate, e = make_block(pkg, 20, 128, 64, "bf16", "swiglu", True)
+    plain = block.forward_train(x, up, gate)
+    x, up, gate = (t.detach().clone().requires_grad_() for t in (x, up, gate))
+    out, saved = block.forward_train(x, up, gate)
+    d = block.backward(e, saved, x, up, gate)
+    y = op(x)
+    for t in (out, *saved, *d, y):
+        assert not t.requires_grad and t.grad_fn is None
+    assert x.grad is None and up.grad is None and gate.grad is None
+    assert torch.equal(out, plain[0])
