@@ -177,11 +177,14 @@ size_t gemm16_part_bytes(int M, int64_t ld_part, int sms) {
                           static_cast<size_t>(kMaxSplit) * M * ((ld_part + 7) / 4 * 4) * 4);
 }
 
+bool encoder_found(std::string* why) {
+  if (encoder()) return true;
+  *why = "the driver has no tensor-map encoder";
+  return false;
+}
+
 bool gemm16_setup(std::string* why) {
-  if (!encoder()) {
-    *why = "the driver has no tensor-map encoder";
-    return false;
-  }
+  if (!encoder_found(why)) return false;
   for (int cg = 1; cg <= 2; ++cg)
     for (int k = 0; k < 3; ++k) {
       const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel_of(cg, k == 2, k >= 1)),

@@ -143,8 +143,11 @@ cudaError_t gemm16_join(const JoinCall& c, cudaStream_t s);
 
 // Tensor map of a 16-bit matrix of `rows` memory rows of `cols` elements, ld
 // apart; boxes of 64 columns (128 bytes, swizzled) by box_rows rows.  Elements
-// outside read as zero.  False when the driver refuses it.
+// outside read as zero.  False when the driver refuses it.  Needs encoder_found().
 bool encode_rows16(CUtensorMap* m, const void* p, int64_t cols, int64_t rows, int64_t ld, int box_rows);
+
+// Whether the driver has a tensor-map encoder (looked up once); false with the reason.
+bool encoder_found(std::string* why);
 
 // Launches the product on `s` (asynchronous); counts its kernel launches.
 cudaError_t gemm16_launch(const GemmCall& c, OpHandle& h, cudaStream_t s, int* launches, std::string* why);

@@ -84,7 +84,7 @@ __host__ __device__ inline int qg_smem_bytes(int fmt, int gb, int mt, int ntok, 
 struct QGemmUnit {
   int split, row, t0, c0, c1;   // 128-row block, first token, chunks [c0, c1)
 };
-__host__ __device__ __forceinline__ QGemmUnit qg_unit(const QGemmArgs& A, int q, int row_tiles, int tok_tiles, int u) {
+__host__ __device__ __forceinline__ QGemmUnit qg_unit(const QGemmArgs& A, int row_tiles, int tok_tiles, int u) {
   QGemmUnit U;
   U.t0 = (u % tok_tiles) * A.ntok;
   u /= tok_tiles;
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
     bool again = false;   // slots have been used before
     uint32_t n = 0;
     for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-      const QGemmUnit U = qg_unit(A, q, row_tiles, tok_tiles, u);
+      const QGemmUnit U = qg_unit(A, row_tiles, tok_tiles, u);
       for (int c = U.c0; c < U.c1; ++c, ++n) {
         const int sl = R.slot;
         if (again && !wait(smem_u32(&empty[sl]), R.parity ^ 1u)) break;
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
     RingPos R;
     uint32_t done = 0;
     for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++done) {
-      const QGemmUnit U = qg_unit(A, q, row_tiles, tok_tiles, u);
+      const QGemmUnit U = qg_unit(A, row_tiles, tok_tiles, u);
       const uint32_t buf = nbuf == 2 ? done & 1 : 0, use = nbuf == 2 ? done >> 1 : done;
       if (use > 0 && !wait(smem_u32(&acce[buf]), (use - 1) & 1)) break;
       tm_fence_after();
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
       while (fu < units && fc >= fend) {
         fu += gridDim.x;
         if (fu >= units) break;
-        const QGemmUnit FU = qg_unit(A, q, row_tiles, tok_tiles, fu);
+        const QGemmUnit FU = qg_unit(A, row_tiles, tok_tiles, fu);
         fc = FU.c0 + first;
         fend = FU.c1;
         const int64_t tile = tile_of(FU);
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
     const bool pairs = S >= 4;
     const uint32_t row_off = static_cast<uint32_t>((dw * 16 + g) * 128);
     for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-      const QGemmUnit U = qg_unit(A, q, row_tiles, tok_tiles, u);
+      const QGemmUnit U = qg_unit(A, row_tiles, tok_tiles, u);
       // rows past the matrix: their A rows stay what they were, their outputs are not written
       const bool in = tile_of(U) < tiles16;
       qg_walk<GATED>(Q, U.c0, U.c1, half, [&](int c) {
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
     const int ew = warp - 4;
     uint32_t done = 0;
     for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++done) {
-      const QGemmUnit U = qg_unit(A, q, row_tiles, tok_tiles, u);
+      const QGemmUnit U = qg_unit(A, row_tiles, tok_tiles, u);
       const uint32_t buf = nbuf == 2 ? done & 1 : 0, use = nbuf == 2 ? done >> 1 : done;
       if (!wait(smem_u32(&accf[buf]), use & 1)) break;
       tm_fence_after();

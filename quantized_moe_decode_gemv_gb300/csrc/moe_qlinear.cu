@@ -434,7 +434,7 @@ static moe_status create(const moe_qlinear_config* cfg, const moe_qlinear_weight
   bool streamed = true;   // whether k_stream takes every call
   for (int t = 1; t <= c.max_tokens && streamed; ++t) streamed = stream_plan(*h, t, &plan);
   if (!streamed && e == cudaSuccess) {
-    if (!gemm16_setup(&why)) {
+    if (!encoder_found(&why)) {
       st = MOE_ERR_CUDA;
       e = cudaErrorUnknown;
     }
