@@ -2,8 +2,8 @@
 
 ``python -m quantized_moe_decode_gemv_gb300.build`` (or ``build()``) compiles
 each translation unit in parallel and links ``libmoe_gb300.so`` next to this
-file, and beside it the debug build ``libmoe_gb300_checks.so`` (the same
-sources compiled with ``-DMOE_CHECKS=1``: kernels check the indices they read
+file, and beside it the debug build ``libmoe_gb300_checks.so`` (the layer's
+sources compiled with ``-DMOE_CHECKS=1``, the others' objects shared: kernels check the indices they read
 from data and record violations in the status word; NVTX ranges on).  The
 binding loads the debug build when ``MOE_CHECKS=1`` is set in the environment.
 Only nvcc and the host C++ compiler are needed (no cmake, no torch extension
@@ -31,6 +31,8 @@ VARIANTS = [(LIB, BUILD_DIR, []), (LIB_CHECKS, os.path.join(BUILD_DIR, "checks")
 SOURCES = [("moe_layer.cu", "moe_layer", []), ("moe_noalloc.cu", "moe_noalloc", []),
            ("moe_qlinear.cu", "moe_qlinear", []), ("moe_gated.cu", "moe_gated", []),
            ("moe_gemm16.cu", "moe_gemm16", [])]
+# units without a check: every variant links the default build's object
+NO_CHECKS = {"moe_qlinear", "moe_gated", "moe_gemm16"}
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-warn-spills"]
@@ -59,6 +61,9 @@ def build(verbose: bool = False, checks: bool = True) -> str:
         os.makedirs(odir, exist_ok=True)
         objs = []
         for src, name, extra in SOURCES:
+            if name in NO_CHECKS and odir != BUILD_DIR:
+                objs.append(os.path.join(BUILD_DIR, name + ".o"))
+                continue
             obj = os.path.join(odir, name + ".o")
             objs.append(obj)
             cmds.append([nvcc, *ARCH, *FLAGS, *vflags, *extra, "-I", INCLUDE, "-I", CSRC, "-c",
