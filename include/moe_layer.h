@@ -419,7 +419,8 @@ moe_status moe_qlinear_create(const moe_qlinear_config *cfg, const moe_qlinear_w
  * of one buffer, ldx = ldo, they may interleave).  0 <= T <= max_tokens; T = 0
  * does nothing; rows of out from T on and what lies between rows stay as they are.  Asynchronous on `stream`, and may be
  * captured into a CUDA graph.  Like a layer, a handle has one workspace: its
- * calls (and replays of graphs that hold them) must not overlap on the GPU. */
+ * calls (and replays of graphs that hold them) must not overlap on the GPU.  It
+ * has one error message too: host threads that share a handle take turns. */
 moe_status moe_qlinear_forward(moe_qlinear *h, const void *x, int64_t ldx, int32_t T, void *out, int64_t ldo,
                                void *stream);
 
@@ -428,7 +429,9 @@ moe_status moe_qlinear_forward(moe_qlinear *h, const void *x, int64_t ldx, int32
 moe_status moe_qlinear_device_status(moe_qlinear *h, void *stream);
 int64_t moe_qlinear_device_bytes(const moe_qlinear *h);          /* weights and workspace */
 int32_t moe_qlinear_last_launch_count(const moe_qlinear *h);     /* kernels of the last forward */
-moe_status moe_qlinear_destroy(moe_qlinear *h);                  /* NULL is a no-op */
+/* Synchronises the device (so not while a stream is captured; a graph that holds
+ * the handle's calls is not replayed afterwards).  NULL is a no-op. */
+moe_status moe_qlinear_destroy(moe_qlinear *h);
 /* Last error of a handle; NULL: of the last failed create or validate on this thread. */
 const char *moe_qlinear_last_error(const moe_qlinear *h);
 
@@ -492,7 +495,7 @@ moe_status moe_gated_backward(moe_gated *h, const void *d_out, int64_t ldd, int3
 moe_status moe_gated_device_status(moe_gated *h, void *stream);
 int64_t moe_gated_device_bytes(const moe_gated *h);
 int32_t moe_gated_last_launch_count(const moe_gated *h);
-moe_status moe_gated_destroy(moe_gated *h);
+moe_status moe_gated_destroy(moe_gated *h);   /* as moe_qlinear_destroy */
 const char *moe_gated_last_error(const moe_gated *h);
 
 /* Device allocations currently held by all handles of this process (for leak

@@ -111,6 +111,7 @@ class _Handle:
         return int(self._fn("last_launch_count")(self.handle))
 
     def close(self) -> None:
+        """Frees the handle (also when it is collected); waits for the device, so not during a graph capture."""
         if getattr(self, "handle", None):
             handle, self.handle = self.handle, None
             self._fn("destroy")(handle)
