@@ -17,8 +17,8 @@
 // of once per 128.  (At 256 x 256 a 64-wide K step moves 64 KB into the pair for
 // 4.2 million multiply-adds: 64 bytes a clock and SM beside a saturated tensor
 // pipe; with CG = 1, 96.)
-// Measured on 4096 rows of 4096 against 2 x 8192: 280 us, 1.97 PFLOP/s; with the
-// pre-activations saved 320 us.
+// Measured on 4096 rows of 4096 against 2 x 8192, passes back to back: 280 to 288 us,
+// 1.97 to 1.91 PFLOP/s; with the pre-activations saved 306 to 320 us.
 //
 // Roles of a CTA's 12 warps: warp 0 issues the tensor copies into a ring of
 // shared-memory slots, warp 1 (of the pair's even CTA) issues the MMAs, warp 2

@@ -3,14 +3,17 @@
 //
 // Writing dW is all the time there is: with T = 9 the products are 18 flops for
 // each 2 bytes written.  A GEMM tile spends longer filling its pipeline and
-// handing its accumulators over than on its one or two K blocks (23 us for
+// handing its accumulators over than on its one or two K blocks (19 us for
 // 2 x 5504 x 2048 at T = 9, 45 MB written); here a CTA stages 128 columns of d and
 // 256 of x once, and each of its 8 warps keeps the x fragments of 32 columns in
 // registers and walks the 128 rows with warp-level MMAs (m16n8k16, T as k), whose
 // results go straight out.  The MMA's columns are dealt so that a lane's results
 // of four MMAs are eight consecutive columns of a row: 16-byte stores, four lanes
-// to 64 bytes.  d comes transposed through ldmatrix.  Measured on the same: 8 us,
-// 5.6 TB/s (15 us at 48 rows, where the GEMM takes 20).
+// to 64 bytes.  d comes transposed through ldmatrix.  Measured as what the
+// weights' gradients add to a backward pass that writes d_x, passes back to back in a
+// graph, this kernel and the GEMM: 2 x 5504 x 2048 at 9, 32 and 48 rows 8.7, 14.0 and
+// 19.7 us (5.2 TB/s at 9) against 18.7, 20.3 and 20.4; at 48 rows 2 x 8192 x 4096 44.7
+// against 52.8 and 3712 x 4096 14.3 against 17.4.  From 49 rows on the GEMM.
 #pragma once
 
 #include "moe_stream.cuh"   // mma_16816

@@ -36,8 +36,11 @@
 //
 // Per K block of two matrices and 256 tokens: 1024 clocks of MMA beside 32 KB of
 // token rows, 9 KB of codes (41 bytes a clock) and 16 x 100 decode instructions
-// (40% of the issue slots).  Measured: 2048 rows of 4096 against 16384, affine,
-// 185 us (1.49 PFLOP/s), 300 rows against 2 x 8192, MXFP4, 38.6 us (1.04).
+// (40% of the issue slots).  Measured, passes back to back in a graph: 2048 rows of
+// 4096 against 16384, affine, 191 us (1.44 PFLOP/s; 203 in a run of seconds, where
+// power bounds the clock), NVFP4 180 us; 300 rows against 2 x 8192, MXFP4, 39.5 us
+// (1.02).  With few rows a K block takes what its decode takes: 0.30 us with one
+// affine matrix, 0.26 NVFP4, 0.49 with an affine pair (32 rows of 8192 less 32 of 4096).
 //
 // Every wait is bounded; a role whose wait runs out sets the timeout bit of the
 // status word and winds down.
@@ -521,9 +524,9 @@ __global__ void __launch_bounds__(QG_THREADS, 1) k_qgemm(const __grid_constant__
 
 // Host: token tile and K split of a call: the least estimated time in SM clocks.  A
 // tile's 64-wide block takes the longest of its MMAs (2 ntok clocks a matrix), its
-// decode (700 clocks at the rate seen, both matrices of a pair at once, two groups
-// of warps taking turns with one) and its bytes at 40 a clock; a tile that does not
-// overlap the next one adds its epilogue.
+// decode (taken as 700 clocks for a pair, half of that for one matrix, whose two
+// groups of warps take turns; measured: about 950 and 600) and its bytes at 40 a
+// clock; a tile that does not overlap the next one adds its epilogue.
 struct QGemmPlan {
   int ntok = 0, ksplit = 1, slots = 0, depth = 0, units = 0;
 };

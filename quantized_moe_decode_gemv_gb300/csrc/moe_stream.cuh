@@ -11,7 +11,7 @@
 // by 16-byte asynchronous copies of its lanes, over tile boundaries and a few
 // stages ahead of the arithmetic, 45 KB or more an SM under way.  (Bulk copies,
 // one for a stage's codes and one for its scales, took 22.1 us where these take
-// 19.9: 75.6 MB of NVFP4 weights at one token; now 18.9, 4.0 TB/s.)
+// 19.9: 75.6 MB of NVFP4 weights at one token; now 18.8 to 19.3, 4.0 TB/s.)
 // The token rows lie in shared memory as they are.  The warps' partial sums meet
 // in shared memory one tile late: a warp leaves its sums of a tile, goes on to
 // the next one, and adds its share of the former when it is through, so that no

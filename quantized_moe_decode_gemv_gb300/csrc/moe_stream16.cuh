@@ -11,7 +11,7 @@
 // A lane reads only what it copied itself, so the ring needs no barrier; one
 // barrier a tile joins the warps' partial sums, while the copies of the next
 // tiles are under way.  (Bulk copies, one a row and stage, took 12.2 us where
-// this takes 5.9 (5.2 TB/s): 30.4 MB at one token; they are 256 bytes each.)
+// this takes 5.9 to 6.6 (5.2 to 4.6 TB/s): 30.4 MB at one token; they are 256 bytes each.)
 //
 // The arithmetic is warp-level mma.sync m16n8k16 with the weights as A and the
 // token rows as B (columns of absent tokens are zero).  The MMA's k index runs
