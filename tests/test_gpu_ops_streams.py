@@ -79,3 +79,36 @@ def test_a_call_after_a_join_waits_for_both_streams(pkg):
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(got[0], wy) and torch.equal(got[1], wy) and torch.equal(got[2], wz)
+
+
+def test_captured_on_a_given_stream(pkg):
+    """The capture's own stream and one forked from it, by object and by number; inputs made
+    inside and outside the capture."""
+    T = 40
+    op, _, _, _ = make_linear(pkg, 320, 512, "mxfp4", 32, "bf16", "none", False, 64)
+    block, x, up, gate, e = make_block(pkg, T, 512, 320, "bf16", "swiglu", True)
+    x = x.contiguous()
+
+    def want_of():
+        h, saved = block.forward_train(x, up, gate)
+        return op(x), h, *block.backward(e, saved, x, up, gate)
+
+    want = want_of()
+    torch.cuda.synchronize()
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        inside = x + 0
+        side.wait_stream(main)
+        y = op.forward(inside, stream=side.cuda_stream)
+        h, saved = block.forward_train(x, up, gate, stream=main)
+        d = block.backward(e, saved, x, up, gate, stream=main.cuda_stream)
+        main.wait_stream(side)
+        del inside
+    for seed in (1, 2):
+        x.copy_(rows(T, 512, "bf16", seed))
+        torch.cuda.synchronize()
+        want = want_of()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, (y, h, *d)))
