@@ -76,7 +76,8 @@ typedef enum moe_status {
   MOE_ERR_CUDA = 8,         /* a CUDA runtime call failed */
   MOE_ERR_TIMEOUT = 9,      /* a bounded device-side wait ran out */
   MOE_ERR_NONFINITE = 10,   /* a router selection key was NaN or infinite */
-  MOE_ERR_INDEX = 11        /* MOE_CHECKS builds: a kernel's index check failed */
+  MOE_ERR_INDEX = 11        /* an index read from data was out of range (layers: MOE_CHECKS
+                               builds; moe_rows: every build) */
 } moe_status;
 
 typedef enum moe_act {
@@ -497,6 +498,85 @@ int64_t moe_gated_device_bytes(const moe_gated *h);
 int32_t moe_gated_last_launch_count(const moe_gated *h);
 moe_status moe_gated_destroy(moe_gated *h);   /* as moe_qlinear_destroy */
 const char *moe_gated_last_error(const moe_gated *h);
+
+/* ---------------------------------------------------------------------------
+ * Tokens sorted by expert and back
+ *
+ * What stands on both sides of the experts' own products when a batch is routed,
+ * for serving and for training.  A pick i = t k + j is token t's j-th expert
+ * (ids[T, k], as moe_layer_forward_ex gives them); a pick of -1 has no expert.
+ *
+ *   plan      offsets[E + 1]: expert e has the sorted rows offsets[e] ..
+ *             offsets[e + 1] - 1 (offsets[E]: the picks with an expert);
+ *             order[T k]: the pick of every sorted row, an expert's in the order of
+ *             the picks, -1 from offsets[E] on;
+ *             place[T, k]: the sorted row of every pick, -1 without an expert
+ *   dispatch  rows[r] = x[order[r] / k], zero from offsets[E] on
+ *             its gradient: d_x[t] = sum_j d_rows[place[t, j]] (combine without w)
+ *   combine   out[t] = sum_j w[t, j] y[place[t, j]]
+ *             its gradient: d_y[r] = w[order[r]] d_out[order[r] / k] (zero from
+ *             offsets[E] on), d_w[t, j] = <d_out[t], y[place[t, j]]>
+ *
+ * Rows are 16-bit, of any width; sums are fp32, in the order of j, and rounded once.  A
+ * pick without an expert adds nothing, whatever its weight, and has d_w = 0; the same
+ * expert may be picked twice.  The plan's three arrays are the caller's: a training
+ * loop keeps them until its backward pass.
+ * ------------------------------------------------------------------------- */
+typedef struct moe_rows_config {
+  int32_t n_experts;      /* E: 1..1024 */
+  int32_t top_k;          /* k: 1..min(E, 16) */
+  int32_t act_dtype;      /* BF16|FP16: every row */
+  int32_t max_tokens;     /* largest T of a call, >= 1; max_tokens * top_k <= 2^24 */
+} moe_rows_config;
+
+typedef struct moe_rows moe_rows;
+
+/* MOE_ERR_INVALID_ARG: null cfg, sizes < 1, unknown dtype.  MOE_ERR_TOPK_GT_E:
+ * top_k not in 1..E.  MOE_ERR_UNSUPPORTED: E > 1024, top_k > 16, fp32,
+ * max_tokens * top_k > 2^24. */
+moe_status moe_rows_validate(const moe_rows_config *cfg);
+/* Create on the current CUDA device (workspace only).  Synchronises the device, so
+ * not inside a stream capture. */
+moe_status moe_rows_create(const moe_rows_config *cfg, moe_rows **out);
+
+/* The plan of ids[T, k] (int32: id_bytes 4, int64: 8; contiguous).  An id that is
+ * neither -1 nor an expert counts as -1 and is reported by moe_rows_device_status
+ * (MOE_ERR_INDEX).  T = 0 writes offsets (zeros) alone.  DEVICE pointers, aligned to
+ * their elements; outputs overlap neither inputs nor each other, in every call here.
+ * Streams, devices, graphs and overlap as moe_qlinear_forward. */
+moe_status moe_rows_plan(moe_rows *h, const void *ids, int32_t id_bytes, int32_t T, int32_t *offsets, int32_t *order,
+                         int32_t *place, void *stream);
+
+/* The plan, and rows[T k, width] of x[T, width] in its order.  Rows of x are ldx
+ * elements apart, those of `rows` ld_rows (each >= width; column ranges of one buffer
+ * may interleave).  All T k rows are written.  1 <= width <= 65536, any row stride:
+ * rows whose addresses and width allow 16-byte accesses are moved fastest. */
+moe_status moe_rows_dispatch(moe_rows *h, const void *x, int64_t ldx, int32_t T, int32_t width, const void *ids,
+                             int32_t id_bytes, int32_t *offsets, int32_t *order, int32_t *place, void *rows,
+                             int64_t ld_rows, void *stream);
+
+/* The rows alone, by a plan that an earlier call wrote for T tokens.  Here and below a
+ * place past the T k rows counts as -1 and is reported as above. */
+moe_status moe_rows_take(moe_rows *h, const void *x, int64_t ldx, int32_t T, int32_t width, const int32_t *offsets,
+                         const int32_t *place, void *rows, int64_t ld_rows, void *stream);
+
+/* out[T, width] from y[T k, width] and w[T, k] (w_dtype: a moe_dtype; contiguous), or
+ * with w NULL the plain sum of a token's rows: the gradient of dispatch. */
+moe_status moe_rows_combine(moe_rows *h, const void *y, int64_t ldy, int32_t T, int32_t width, const void *w,
+                            int32_t w_dtype, const int32_t *place, void *out, int64_t ldo, void *stream);
+
+/* d_y[T k, width] and d_w[T, k] (w's type) for d_out[T, width]; either may be NULL
+ * when it is not wanted (y is read for d_w alone, w and offsets for d_y alone). */
+moe_status moe_rows_combine_backward(moe_rows *h, const void *d_out, int64_t ldd, int32_t T, int32_t width, const void *y,
+                                     int64_t ldy, const void *w, int32_t w_dtype, const int32_t *offsets,
+                                     const int32_t *place, void *d_y, int64_t lddy, void *d_w, void *stream);
+
+/* Synchronises `stream`, reads and clears the status word: MOE_OK or MOE_ERR_INDEX. */
+moe_status moe_rows_device_status(moe_rows *h, void *stream);
+int64_t moe_rows_device_bytes(const moe_rows *h);
+int32_t moe_rows_last_launch_count(const moe_rows *h);
+moe_status moe_rows_destroy(moe_rows *h);   /* as moe_qlinear_destroy */
+const char *moe_rows_last_error(const moe_rows *h);
 
 /* Device allocations currently held by all handles of this process (for leak
  * checks around refused creates). */

@@ -12,3 +12,6 @@ from ._capi import (  # noqa: F401
 from ._ops import (  # noqa: F401
     GatedBlock, GatedConfig, GatedGrads, QLinear, QLinearConfig,
 )
+from ._train_ops import (  # noqa: F401
+    ExpertRows, ExpertRowsConfig, RowGrads, RowPlan,
+)

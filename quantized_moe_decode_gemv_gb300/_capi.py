@@ -76,6 +76,12 @@ class moe_gated_config(ctypes.Structure):
                 ("in_features", "out_features", "act", "act_dtype", "max_tokens", "training")]
 
 
+class moe_rows_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_experts", "top_k", "act_dtype", "max_tokens")]
+
+
+_I32, _I64, _PTR = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
+
 # symbol -> (restype, argtypes)
 SIGNATURES = {
     "moe_abi_version": (ctypes.c_int32, []),
@@ -135,6 +141,19 @@ SIGNATURES = {
     "moe_gated_last_launch_count": (ctypes.c_int32, [ctypes.c_void_p]),
     "moe_gated_destroy": (ctypes.c_int, [ctypes.c_void_p]),
     "moe_gated_last_error": (ctypes.c_char_p, [ctypes.c_void_p]),
+    "moe_rows_validate": (ctypes.c_int, [ctypes.POINTER(moe_rows_config)]),
+    "moe_rows_create": (ctypes.c_int, [ctypes.POINTER(moe_rows_config), ctypes.POINTER(_PTR)]),
+    "moe_rows_plan": (ctypes.c_int, [_PTR, _PTR, _I32, _I32, _PTR, _PTR, _PTR, _PTR]),
+    "moe_rows_dispatch": (ctypes.c_int, [_PTR, _PTR, _I64, _I32, _I32, _PTR, _I32, _PTR, _PTR, _PTR, _PTR, _I64, _PTR]),
+    "moe_rows_take": (ctypes.c_int, [_PTR, _PTR, _I64, _I32, _I32, _PTR, _PTR, _PTR, _I64, _PTR]),
+    "moe_rows_combine": (ctypes.c_int, [_PTR, _PTR, _I64, _I32, _I32, _PTR, _I32, _PTR, _PTR, _I64, _PTR]),
+    "moe_rows_combine_backward": (ctypes.c_int, [_PTR, _PTR, _I64, _I32, _I32, _PTR, _I64, _PTR, _I32, _PTR, _PTR, _PTR, _I64,
+                                                 _PTR, _PTR]),
+    "moe_rows_device_status": (ctypes.c_int, [_PTR, _PTR]),
+    "moe_rows_device_bytes": (ctypes.c_int64, [_PTR]),
+    "moe_rows_last_launch_count": (ctypes.c_int32, [_PTR]),
+    "moe_rows_destroy": (ctypes.c_int, [_PTR]),
+    "moe_rows_last_error": (ctypes.c_char_p, [_PTR]),
     "moe_debug_live_allocations": (ctypes.c_int64, []),
     "moe_debug_fail_allocation": (None, [ctypes.c_int32]),
 }

@@ -1,0 +1,226 @@
+"""Python handles of the operators around the training of routed experts
+(include/moe_layer.h): tokens sorted by expert and back.
+
+Argument checks and marshalling, as in ``_ops``; the arithmetic runs in the CUDA
+library.
+"""
+from __future__ import annotations
+
+import ctypes
+import dataclasses
+from typing import Any, NamedTuple
+
+from ._capi import DTYPE, MOE_OK, MoEError, load_library, moe_rows_config, torch_act_dtype
+from ._ops import _INVALID_ARG, _SHAPE, _Handle, _int32, _name_of
+
+
+def _device_of(torch, device):
+    """A CUDA device with its index; the current one for None."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    if device.type != "cuda":
+        raise MoEError(_INVALID_ARG, f"the operator runs on a CUDA device, not on {device}")
+    return torch.device("cuda", torch.cuda.current_device()) if device.index is None else device
+
+
+def _create(handle, torch, c) -> None:
+    """Validates the C config and creates the handle on its device."""
+    status = handle._fn("validate")(ctypes.byref(c))
+    if status == MOE_OK:
+        h = ctypes.c_void_p()
+        with torch.cuda.device(handle.device):
+            status = handle._fn("create")(ctypes.byref(c), ctypes.byref(h))
+    if status != MOE_OK:
+        raise MoEError(status, handle._fn("last_error")(None).decode())
+    handle.handle = h.value
+
+
+# ---------------------------------------------------------------------------
+# tokens sorted by expert and back
+# ---------------------------------------------------------------------------
+
+@dataclasses.dataclass
+class ExpertRowsConfig:
+    """Mirror of ``moe_rows_config``."""
+    n_experts: int
+    top_k: int
+    act_dtype: str = "bf16"
+    max_tokens: int = 16
+
+    def to_c(self) -> moe_rows_config:
+        return moe_rows_config(
+            n_experts=_int32(self.n_experts, "n_experts"), top_k=_int32(self.top_k, "top_k"),
+            act_dtype=_name_of(DTYPE, self.act_dtype, "act_dtype"), max_tokens=_int32(self.max_tokens, "max_tokens"))
+
+
+class RowPlan(NamedTuple):
+    """Where every pick's row is: int32 tensors offsets [E + 1], order [T k], place [T, k]."""
+    offsets: Any
+    order: Any
+    place: Any
+
+
+class RowGrads(NamedTuple):
+    """Gradients of ``combine`` (None where not asked for)."""
+    y: Any
+    w: Any
+
+
+class ExpertRows(_Handle):
+    """A batch's tokens as rows sorted by expert, the experts' rows back to the tokens with
+    weights, and the gradients of both.
+
+    ``ids`` [T, k] (int32 or int64, -1: no expert) name each token's experts.  Sorted rows
+    come as [T k, H]: expert e's are ``offsets[e] : offsets[e + 1]``, rows from
+    ``offsets[E]`` on are zero.
+
+    No autograd function: ``requires_grad`` is not looked at, outputs carry no graph; a
+    training loop keeps the plan and calls the backward methods.
+    """
+
+    _prefix = "moe_rows"
+
+    def __init__(self, config: ExpertRowsConfig, device=None):
+        import torch
+        self._setup(torch, load_library())
+        self.config = config
+        c = config.to_c()
+        status = self._fn("validate")(ctypes.byref(c))
+        if status != MOE_OK:
+            raise MoEError(status, self._fn("last_error")(None).decode())
+        self.device = _device_of(torch, device)
+        _create(self, torch, c)
+        self._dtype, self._k, self._E = torch_act_dtype(config.act_dtype), config.top_k, config.n_experts
+        self._i32, self._id_bytes = torch.int32, {torch.int32: 4, torch.int64: 8}
+        self._w_types = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+    def _rows_of(self, x, what: str, rows=None):
+        """(row stride, width) of a 2-D tensor of ``rows`` rows."""
+        shape = x.shape
+        if len(shape) != 2 or (rows is not None and shape[0] != rows):
+            raise MoEError(_SHAPE, f"{what} must be [{'T' if rows is None else rows}, H], not {list(shape)}")
+        return self._stride(x, shape[1], what), shape[1]
+
+    def _ids(self, ids):
+        if len(ids.shape) != 2 or ids.shape[1] != self._k:
+            raise MoEError(_SHAPE, f"ids must be [T, {self._k}], not {list(ids.shape)}")
+        if ids.dtype not in self._id_bytes or ids.device != self.device or not ids.is_contiguous():
+            raise MoEError(_INVALID_ARG, f"ids must be a contiguous int32 or int64 tensor on {self.device}")
+        if ids.shape[0] > self.config.max_tokens:
+            raise MoEError(_INVALID_ARG, f"{ids.shape[0]} tokens, max_tokens is {self.config.max_tokens}")
+        return ids.shape[0]
+
+    def _plan(self, plan, T=None):
+        """T of a plan, its tensors checked."""
+        offsets, order, place = plan
+        if T is None:
+            T = place.shape[0]
+        for t, shape, what in ((offsets, (self._E + 1,), "offsets"), (order, (T * self._k,), "order"),
+                               (place, (T, self._k), "place")):
+            if t.shape != shape:
+                raise MoEError(_SHAPE, f"the plan's {what} must be {list(shape)}, not {list(t.shape)}")
+            if t.dtype is not self._i32 or t.device != self.device or not t.is_contiguous():
+                raise MoEError(_INVALID_ARG, f"the plan's {what} must be a contiguous int32 tensor on {self.device}")
+        return T
+
+    def _weights(self, w, T):
+        if w.shape != (T, self._k):
+            raise MoEError(_SHAPE, f"w must be [{T}, {self._k}], not {list(w.shape)}")
+        if w.dtype not in self._w_types or w.device != self.device or not w.is_contiguous():
+            raise MoEError(_INVALID_ARG, f"w must be a contiguous fp32, bf16 or fp16 tensor on {self.device}")
+        return self._w_types[w.dtype]
+
+    def _out(self, out, rows, H, what, where):
+        """(tensor, row stride) of an output that may be given."""
+        if out is None:
+            with where:
+                return self._empty((rows, H), dtype=self._dtype, device=self.device), H
+        ld = self._stride(out, H, what)
+        if out.shape[0] != rows:
+            raise MoEError(_SHAPE, f"{what} has {out.shape[0]} rows, not {rows}")
+        return out, ld
+
+    def _new_plan(self, T, where) -> RowPlan:
+        empty, device, i32 = self._empty, self.device, self._i32
+        with where:
+            return RowPlan(empty((self._E + 1,), dtype=i32, device=device),
+                           empty((T * self._k,), dtype=i32, device=device), empty((T, self._k), dtype=i32, device=device))
+
+    def plan(self, ids, stream=None) -> RowPlan:
+        """The plan of ids [T, k] alone."""
+        T = self._ids(ids)
+        s, where = self._stream(stream, ids)
+        p = self._new_plan(T, where)
+        status = self._lib.moe_rows_plan(self.handle, ids.data_ptr(), self._id_bytes[ids.dtype], T, p[0].data_ptr(),
+                                         p[1].data_ptr(), p[2].data_ptr(), s)
+        if status:
+            self._fail(status)
+        return p
+
+    def dispatch(self, x, ids, out=None, stream=None):
+        """(rows [T k, H], plan) of x [T, H] (rows may be strided) and ids [T, k]."""
+        T = self._ids(ids)
+        ldx, H = self._rows_of(x, "x", T)
+        s, where = self._stream(stream, x, ids, out)
+        out, ldo = self._out(out, T * self._k, H, "out", where)
+        p = self._new_plan(T, where)
+        status = self._lib.moe_rows_dispatch(self.handle, x.data_ptr(), ldx, T, H, ids.data_ptr(), self._id_bytes[ids.dtype],
+                                             p[0].data_ptr(), p[1].data_ptr(), p[2].data_ptr(), out.data_ptr(), ldo, s)
+        if status:
+            self._fail(status)
+        return out, p
+
+    def take(self, x, plan, out=None, stream=None):
+        """rows [T k, H] of x [T, H] by a plan that is there already."""
+        T = self._plan(plan)
+        ldx, H = self._rows_of(x, "x", T)
+        s, where = self._stream(stream, x, out, *plan)
+        out, ldo = self._out(out, T * self._k, H, "out", where)
+        status = self._lib.moe_rows_take(self.handle, x.data_ptr(), ldx, T, H, plan[0].data_ptr(), plan[2].data_ptr(),
+                                         out.data_ptr(), ldo, s)
+        if status:
+            self._fail(status)
+        return out
+
+    def _combine(self, y, w, plan, out, stream, what):
+        T = self._plan(plan)
+        ldy, H = self._rows_of(y, what, T * self._k)
+        wt = 2 if w is None else self._weights(w, T)
+        s, where = self._stream(stream, y, w, out, *plan)
+        out, ldo = self._out(out, T, H, "out", where)
+        status = self._lib.moe_rows_combine(self.handle, y.data_ptr(), ldy, T, H, None if w is None else w.data_ptr(), wt,
+                                            plan[2].data_ptr(), out.data_ptr(), ldo, s)
+        if status:
+            self._fail(status)
+        return out
+
+    def combine(self, y, w, plan, out=None, stream=None):
+        """out [T, H]: a token's rows of y [T k, H], weighted by w [T, k] (fp32 or 16-bit) and summed."""
+        if w is None:
+            raise MoEError(_INVALID_ARG, "w is missing")
+        return self._combine(y, w, plan, out, stream, "y")
+
+    def dispatch_backward(self, d_rows, plan, out=None, stream=None):
+        """d_x [T, H] for the gradient d_rows [T k, H] of ``dispatch``'s (or ``take``'s) rows."""
+        return self._combine(d_rows, None, plan, out, stream, "d_rows")
+
+    def combine_backward(self, d_out, y, w, plan, need=("y", "w"), stream=None) -> RowGrads:
+        """Gradients of the tensors named in ``need`` for the gradient d_out [T, H] of ``combine``'s out."""
+        for n in need:
+            if n not in RowGrads._fields:
+                raise MoEError(_INVALID_ARG, f"need names {', '.join(RowGrads._fields)}")
+        T = self._plan(plan)
+        ldd, H = self._rows_of(d_out, "d_out", T)
+        ldy, Hy = self._rows_of(y, "y", T * self._k)
+        if Hy != H:
+            raise MoEError(_SHAPE, f"y is {Hy} wide, d_out {H}")
+        wt = self._weights(w, T)
+        s, where = self._stream(stream, d_out, y, w, *plan)
+        with where:
+            d_y = self._empty((T * self._k, H), dtype=self._dtype, device=self.device) if "y" in need else None
+            d_w = self._empty((T, self._k), dtype=w.dtype, device=self.device) if "w" in need else None
+        status = self._lib.moe_rows_combine_backward(
+            self.handle, d_out.data_ptr(), ldd, T, H, y.data_ptr(), ldy, w.data_ptr(), wt, plan[0].data_ptr(),
+            plan[2].data_ptr(), None if d_y is None else d_y.data_ptr(), H, None if d_w is None else d_w.data_ptr(), s)
+        if status:
+            self._fail(status)
+        return RowGrads(d_y, d_w)

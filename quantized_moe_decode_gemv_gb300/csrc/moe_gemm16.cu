@@ -43,6 +43,10 @@ moe_status OpHandle::read_status(void* stream) {
     last_error = std::string("status read: ") + cudaGetErrorString(e);
     return MOE_ERR_CUDA;
   }
+  if (v & STATUS_INDEX) {
+    last_error = "an index read from data was out of range";
+    return MOE_ERR_INDEX;
+  }
   return (v & STATUS_TIMEOUT) ? MOE_ERR_TIMEOUT : MOE_OK;
 }
 

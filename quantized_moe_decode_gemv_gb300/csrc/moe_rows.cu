@@ -1,0 +1,443 @@
+// Tokens sorted by expert and back (moe_rows_* in include/moe_layer.h): host side
+// and C ABI.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <new>
+
+#include "moe_op_host.h"
+#include "moe_rows.cuh"
+
+using namespace moe_op;
+
+struct moe_rows : OpHandle {
+  moe_rows_config cfg{};
+  int* totals = nullptr;   // picks of every expert in every chunk of the plan
+};
+
+namespace {
+
+thread_local std::string g_error;
+
+constexpr int64_t kMaxPicks = 1 << 24;
+
+moe_status validate(const moe_rows_config* c, std::string* why) {
+  auto fail = [&](moe_status s, const char* msg) {
+    *why = msg;
+    return s;
+  };
+  if (!c) return fail(MOE_ERR_INVALID_ARG, "config is NULL");
+  if (c->n_experts < 1 || c->max_tokens < 1) return fail(MOE_ERR_INVALID_ARG, "n_experts and max_tokens must be positive");
+  if (c->act_dtype < 0 || c->act_dtype > 2) return fail(MOE_ERR_INVALID_ARG, "unknown dtype");
+  if (c->top_k < 1 || c->top_k > c->n_experts) return fail(MOE_ERR_TOPK_GT_E, "top_k must be in 1..n_experts");
+  if (c->n_experts > RW_MAX_E) return fail(MOE_ERR_UNSUPPORTED, "n_experts above 1024");
+  if (c->top_k > RW_MAX_K) return fail(MOE_ERR_UNSUPPORTED, "top_k above 16");
+  if (c->act_dtype == MOE_DTYPE_FP32) return fail(MOE_ERR_UNSUPPORTED, "fp32 activations");
+  if (static_cast<int64_t>(c->max_tokens) * c->top_k > kMaxPicks)
+    return fail(MOE_ERR_UNSUPPORTED, "max_tokens * top_k above 2^24");
+  return MOE_OK;
+}
+
+// Rows of 16-bit elements: n of them, `cols` wide, ld apart.  (p NULL: none)
+struct Rows {
+  const void* p;
+  int64_t ld, n, cols;
+  int64_t bytes() const { return n > 0 ? ((n - 1) * ld + cols) * 2 : 0; }
+};
+
+struct Range {
+  const void* p;
+  int64_t bytes;
+  Range(const void* q, int64_t n) : p(q), bytes(n) {}
+  Range(const Rows& r) : p(r.p), bytes(r.bytes()) {}
+};
+
+bool overlap(const Range& a, const Range& b) {
+  const char *x = static_cast<const char*>(a.p), *y = static_cast<const char*>(b.p);
+  return x && y && x < y + b.bytes && y < x + a.bytes;
+}
+
+// Whether an output meets an input or another output.
+bool clash(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
+  for (const Range* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Range& i : ins)
+      if (overlap(*o, i)) return true;
+    for (const Range* p = outs.begin(); p != o; ++p)
+      if (overlap(*o, *p)) return true;
+  }
+  return false;
+}
+
+// Whether rows meet rows in memory.  Column ranges of one buffer may interleave.
+bool meet(const Rows& a, const Rows& b) {
+  if (!overlap(a, b)) return false;
+  return a.ld != b.ld || rows_overlap(a.p, a.ld, a.cols, b.p, b.ld, b.cols, std::max(a.n, b.n));
+}
+
+// As many elements a lane as all rows' addresses allow: 8, 2 or 1.
+int vector_of(std::initializer_list<Rows> all) {
+  int64_t bits = all.begin()->cols * 2;
+  for (const Rows& r : all)
+    if (r.p) bits |= static_cast<int64_t>(reinterpret_cast<uintptr_t>(r.p)) | (r.n > 1 ? r.ld * 2 : 0);
+  return bits % 16 == 0 ? 8 : bits % 4 == 0 ? 2 : 1;
+}
+
+// A warp for each piece of a row, up to 8; up to 16 where tokens alone do not fill the SMs.
+int row_threads(int T, int H, int vec, int sms) {
+  const int pieces = (H + 32 * vec - 1) / (32 * vec);
+  return 32 * std::min(pieces, T < 2 * sms ? 16 : 8);
+}
+
+using RowKernel = void (*)(const RowArgs);
+
+RowKernel take_kernel(int vec) { return vec == 8 ? k_rows_take<8> : vec == 2 ? k_rows_take<2> : k_rows_take<1>; }
+RowKernel combine_kernel(int vec) {
+  return vec == 8 ? k_rows_combine<8> : vec == 2 ? k_rows_combine<2> : k_rows_combine<1>;
+}
+template <bool Y, bool W>
+RowKernel grad_kernel_t(int vec) {
+  return vec == 8 ? k_rows_grad<8, Y, W> : vec == 2 ? k_rows_grad<2, Y, W> : k_rows_grad<1, Y, W>;
+}
+RowKernel grad_kernel(int vec, bool y, bool w) {
+  return y ? (w ? grad_kernel_t<true, true>(vec) : grad_kernel_t<true, false>(vec)) : grad_kernel_t<false, true>(vec);
+}
+
+bool misaligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
+
+moe_status fail(moe_rows* h, moe_status st, const char* msg) {
+  h->last_error = msg;
+  return st;
+}
+
+moe_status launched(moe_rows* h, cudaError_t e) {
+  if (e == cudaSuccess) return MOE_OK;
+  h->last_error = std::string("launch: ") + cudaGetErrorString(e);
+  return MOE_ERR_CUDA;
+}
+
+// What every call checks of its sizes; MOE_OK with nothing to do when T is 0.
+moe_status check_sizes(moe_rows* h, int32_t T, int32_t width) {
+  if (T < 0 || T > h->cfg.max_tokens) return fail(h, MOE_ERR_INVALID_ARG, "T must be in 0..max_tokens");
+  if (width < 1 || width > 65536) return fail(h, MOE_ERR_INVALID_ARG, "width must be in 1..65536");
+  return MOE_OK;
+}
+
+moe_status check_rows(moe_rows* h, const Rows& r, const char* what) {
+  if (!r.p || misaligned(r.p, 2) || (r.n > 1 && r.ld < r.cols)) {
+    h->last_error = std::string(what) + " must not be NULL, and its rows must be at least width elements apart";
+    return MOE_ERR_INVALID_ARG;
+  }
+  return MOE_OK;
+}
+
+moe_status check_ids(moe_rows* h, const void* ids, int32_t id_bytes, const int32_t* offsets, const int32_t* order,
+                     const int32_t* place, int32_t T) {
+  if (id_bytes != 4 && id_bytes != 8) return fail(h, MOE_ERR_INVALID_ARG, "ids have 4 or 8 bytes");
+  if (!offsets || misaligned(offsets, 4) || misaligned(order, 4) || misaligned(place, 4) ||
+      misaligned(ids, static_cast<uintptr_t>(id_bytes)) || (T > 0 && (!ids || !order || !place)))
+    return fail(h, MOE_ERR_INVALID_ARG, "ids, offsets, order and place must be aligned and not NULL");
+  return MOE_OK;
+}
+
+cudaError_t launch_plan(moe_rows* h, const void* ids, int32_t id_bytes, int32_t T, int32_t* offsets, int32_t* order,
+                        int32_t* place, cudaStream_t s) {
+  const int E = h->cfg.n_experts;
+  if (T == 0) return cudaMemsetAsync(offsets, 0, static_cast<size_t>(E + 1) * 4, s);
+  PlanArgs a{};
+  a.ids = ids;
+  a.id64 = id_bytes == 8;
+  a.P = T * h->cfg.top_k;
+  a.E = E;
+  a.chunks = (a.P + RW_CHUNK - 1) / RW_CHUNK;
+  a.totals = h->totals;
+  a.offsets = offsets;
+  a.order = order;
+  a.place = place;
+  a.status = h->status;
+  const size_t smem = static_cast<size_t>(rw_plan_smem(E));
+  cudaError_t e = cudaSuccess;
+  if (a.chunks > 1) {
+    e = launch_chained(k_rows_plan<true>, a.chunks, RW_PLAN_THREADS, smem, 1, s, a);
+    ++h->last_launches;
+  }
+  if (e == cudaSuccess) {
+    e = launch_chained(k_rows_plan<false>, a.chunks, RW_PLAN_THREADS, smem, 1, s, a);
+    ++h->last_launches;
+  }
+  return e;
+}
+
+cudaError_t launch_take(moe_rows* h, const Rows& x, const Rows& rows, int32_t T, int32_t width, const int32_t* offsets,
+                        const int32_t* place, cudaStream_t s) {
+  RowArgs a{};
+  a.tok = static_cast<const unsigned short*>(x.p);
+  a.ld_tok = x.ld;
+  a.row_out = static_cast<unsigned short*>(const_cast<void*>(rows.p));
+  a.ld_row_out = rows.ld;
+  a.offsets = offsets;
+  a.place = place;
+  a.T = T;
+  a.k = h->cfg.top_k;
+  a.H = width;
+  a.E = h->cfg.n_experts;
+  a.dt = h->cfg.act_dtype;
+  a.status = h->status;
+  const int vec = vector_of({x, rows});
+  ++h->last_launches;
+  return launch_chained(take_kernel(vec), T, row_threads(T, width, vec, h->num_sms), 0, 1, s, a);
+}
+
+moe_status plan(moe_rows* h, const void* ids, int32_t id_bytes, int32_t T, int32_t* offsets, int32_t* order, int32_t* place,
+                void* stream) {
+  if (!h) return MOE_ERR_INVALID_ARG;
+  moe_status st = check_sizes(h, T, 1);
+  if (st == MOE_OK) st = check_ids(h, ids, id_bytes, offsets, order, place, T);
+  if (st != MOE_OK) return st;
+  const int64_t P = static_cast<int64_t>(T) * h->cfg.top_k;
+  if (clash({{offsets, 4ll * (h->cfg.n_experts + 1)}, {order, 4 * P}, {place, 4 * P}}, {{ids, id_bytes * P}}))
+    return fail(h, MOE_ERR_INVALID_ARG, "the plan overlaps the ids or itself");
+  DeviceScope dev(h->device);
+  if (!dev.ok) return fail(h, MOE_ERR_DEVICE, "the handle's device cannot be made current");
+  h->last_launches = 0;
+  return launched(h, launch_plan(h, ids, id_bytes, T, offsets, order, place, static_cast<cudaStream_t>(stream)));
+}
+
+// The rows alone (ids NULL), or the plan and the rows.
+moe_status take(moe_rows* h, bool with_plan, const void* x, int64_t ldx, int32_t T, int32_t width, const void* ids,
+                int32_t id_bytes, int32_t* offsets, int32_t* order, int32_t* place, void* rows, int64_t ld_rows,
+                void* stream) {
+  if (!h) return MOE_ERR_INVALID_ARG;
+  moe_status st = check_sizes(h, T, width);
+  if (st == MOE_OK && with_plan) st = check_ids(h, ids, id_bytes, offsets, order, place, T);
+  if (st != MOE_OK) return st;
+  h->last_launches = 0;
+  if (T == 0 && !with_plan) return MOE_OK;
+  const int64_t P = static_cast<int64_t>(T) * h->cfg.top_k, nb = 4ll * (h->cfg.n_experts + 1);
+  const Rows in{x, ldx, T, width}, out{rows, ld_rows, P, width};
+  if (T > 0) {
+    if (st == MOE_OK) st = check_rows(h, in, "x");
+    if (st == MOE_OK) st = check_rows(h, out, "rows");
+    if (st != MOE_OK) return st;
+    if (!offsets || !place || misaligned(offsets, 4) || misaligned(place, 4))
+      return fail(h, MOE_ERR_INVALID_ARG, "offsets and place must be aligned and not NULL");
+    if (meet(in, out)) return fail(h, MOE_ERR_INVALID_ARG, "rows overlaps x");
+    if (with_plan ? clash({{offsets, nb}, {order, 4 * P}, {place, 4 * P}, out}, {{ids, id_bytes * P}}) ||
+                        clash({{offsets, nb}, {order, 4 * P}, {place, 4 * P}}, {in})
+                  : clash({out}, {{offsets, nb}, {place, 4 * P}}))
+      return fail(h, MOE_ERR_INVALID_ARG, "the rows, the plan and the inputs overlap");
+  }
+  DeviceScope dev(h->device);
+  if (!dev.ok) return fail(h, MOE_ERR_DEVICE, "the handle's device cannot be made current");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = with_plan ? launch_plan(h, ids, id_bytes, T, offsets, order, place, s) : cudaSuccess;
+  if (e == cudaSuccess && T > 0) e = launch_take(h, in, out, T, width, offsets, place, s);
+  return launched(h, e);
+}
+
+moe_status combine(moe_rows* h, const void* y, int64_t ldy, int32_t T, int32_t width, const void* w, int32_t w_dtype,
+                   const int32_t* place, void* out, int64_t ldo, void* stream) {
+  if (!h) return MOE_ERR_INVALID_ARG;
+  moe_status st = check_sizes(h, T, width);
+  if (st != MOE_OK) return st;
+  if (w && (w_dtype < 0 || w_dtype > 2)) return fail(h, MOE_ERR_INVALID_ARG, "unknown type of w");
+  h->last_launches = 0;
+  if (T == 0) return MOE_OK;
+  const int64_t P = static_cast<int64_t>(T) * h->cfg.top_k;
+  const Rows in{y, ldy, P, width}, to{out, ldo, T, width};
+  st = check_rows(h, in, "y");
+  if (st == MOE_OK) st = check_rows(h, to, "out");
+  if (st != MOE_OK) return st;
+  if (!place || misaligned(place, 4) || misaligned(w, w_dtype == 2 ? 4 : 2))
+    return fail(h, MOE_ERR_INVALID_ARG, "place must be aligned and not NULL, w aligned");
+  if (meet(in, to) || clash({to}, {{w, P * (w_dtype == 2 ? 4 : 2)}, {place, 4 * P}}))
+    return fail(h, MOE_ERR_INVALID_ARG, "out overlaps an input");
+  DeviceScope dev(h->device);
+  if (!dev.ok) return fail(h, MOE_ERR_DEVICE, "the handle's device cannot be made current");
+  RowArgs a{};
+  a.row = static_cast<const unsigned short*>(y);
+  a.ld_row = ldy;
+  a.tok_out = static_cast<unsigned short*>(out);
+  a.ld_tok = ldo;
+  a.w = w;
+  a.w_dt = w_dtype;
+  a.place = place;
+  a.T = T;
+  a.k = h->cfg.top_k;
+  a.H = width;
+  a.E = h->cfg.n_experts;
+  a.dt = h->cfg.act_dtype;
+  a.status = h->status;
+  const int vec = vector_of({in, to});
+  ++h->last_launches;
+  return launched(h, launch_chained(combine_kernel(vec), T, row_threads(T, width, vec, h->num_sms), 0, 1,
+                                    static_cast<cudaStream_t>(stream), a));
+}
+
+moe_status combine_backward(moe_rows* h, const void* d_out, int64_t ldd, int32_t T, int32_t width, const void* y, int64_t ldy,
+                            const void* w, int32_t w_dtype, const int32_t* offsets, const int32_t* place, void* d_y,
+                            int64_t lddy, void* d_w, void* stream) {
+  if (!h) return MOE_ERR_INVALID_ARG;
+  moe_status st = check_sizes(h, T, width);
+  if (st != MOE_OK) return st;
+  if (w_dtype < 0 || w_dtype > 2) return fail(h, MOE_ERR_INVALID_ARG, "unknown type of w");
+  h->last_launches = 0;
+  if (T == 0 || (!d_y && !d_w)) return MOE_OK;
+  const int64_t P = static_cast<int64_t>(T) * h->cfg.top_k;
+  const Rows e{d_out, ldd, T, width}, in{d_w ? y : nullptr, ldy, P, width}, to{d_y, lddy, P, width};
+  st = check_rows(h, e, "d_out");
+  if (st == MOE_OK && d_w) st = check_rows(h, in, "y");
+  if (st == MOE_OK && d_y) st = check_rows(h, to, "d_y");
+  if (st != MOE_OK) return st;
+  const uintptr_t wb = w_dtype == 2 ? 4 : 2;
+  if (!place || misaligned(place, 4) || (d_y && (!w || !offsets)) || misaligned(offsets, 4) || misaligned(w, wb) ||
+      misaligned(d_w, wb))
+    return fail(h, MOE_ERR_INVALID_ARG, "w, offsets and place must be aligned and not NULL");
+  const int64_t nw = P * static_cast<int64_t>(wb), nb = 4ll * (h->cfg.n_experts + 1);
+  if (meet(e, to) || meet(in, to) || clash({{d_w, nw}}, {e, in, {w, nw}, {offsets, nb}, {place, 4 * P}}) ||
+      clash({to, {d_w, nw}}, {{w, nw}, {offsets, nb}, {place, 4 * P}}))
+    return fail(h, MOE_ERR_INVALID_ARG, "a gradient overlaps an input or the other gradient");
+  DeviceScope dev(h->device);
+  if (!dev.ok) return fail(h, MOE_ERR_DEVICE, "the handle's device cannot be made current");
+  RowArgs a{};
+  a.tok = static_cast<const unsigned short*>(d_out);
+  a.ld_tok = ldd;
+  a.row = static_cast<const unsigned short*>(in.p);
+  a.ld_row = ldy;
+  a.row_out = static_cast<unsigned short*>(d_y);
+  a.ld_row_out = lddy;
+  a.w = w;
+  a.d_w = d_w;
+  a.w_dt = w_dtype;
+  a.offsets = offsets;
+  a.place = place;
+  a.T = T;
+  a.k = h->cfg.top_k;
+  a.H = width;
+  a.E = h->cfg.n_experts;
+  a.dt = h->cfg.act_dtype;
+  a.status = h->status;
+  const int vec = vector_of({e, in, to});
+  ++h->last_launches;
+  return launched(h, launch_chained(grad_kernel(vec, d_y != nullptr, d_w != nullptr), T,
+                                    row_threads(T, width, vec, h->num_sms), 0, 1, static_cast<cudaStream_t>(stream), a));
+}
+
+// (h: the handle while it is not the caller's, for the entry point to free when an exception ends this)
+moe_status create(const moe_rows_config* cfg, moe_rows** out, moe_rows*& h) {
+  if (out) *out = nullptr;
+  std::string why;
+  moe_status st = validate(cfg, &why);
+  if (st == MOE_OK && !out) {
+    st = MOE_ERR_INVALID_ARG;
+    why = "out must not be NULL";
+  }
+  int device = 0, sms = 0;
+  if (st == MOE_OK) st = op_device(&device, &sms, &why);
+  if (st != MOE_OK) {
+    g_error = why;
+    return st;
+  }
+  h = new (std::nothrow) moe_rows();
+  if (!h) {
+    g_error = "host memory";
+    return MOE_ERR_OOM;
+  }
+  h->device = device;
+  h->num_sms = sms;
+  h->cfg = *cfg;
+  cudaError_t e = h->alloc(reinterpret_cast<void**>(&h->status), 64);
+  if (e == cudaSuccess) e = cudaMemset(h->status, 0, 64);
+  const int64_t chunks = (static_cast<int64_t>(cfg->max_tokens) * cfg->top_k + RW_CHUNK - 1) / RW_CHUNK;
+  if (e == cudaSuccess && chunks > 1)
+    e = h->alloc(reinterpret_cast<void**>(&h->totals), static_cast<size_t>(chunks) * (cfg->n_experts + 1) * 4);
+  for (const void* k : {reinterpret_cast<const void*>(k_rows_plan<true>), reinterpret_cast<const void*>(k_rows_plan<false>)})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, rw_plan_smem(RW_MAX_E));
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();   // the status word's clear runs on the default stream
+  if (e != cudaSuccess) {
+    g_error = std::string("create: ") + cudaGetErrorString(e);
+    h->free_all();
+    delete h;
+    h = nullptr;
+    return e == cudaErrorMemoryAllocation ? MOE_ERR_OOM : MOE_ERR_CUDA;
+  }
+  *out = h;
+  h = nullptr;
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_rows_validate(const moe_rows_config* cfg) {
+  return op_entry([&] {
+    std::string why;
+    const moe_status st = validate(cfg, &why);
+    if (st != MOE_OK) g_error = why;
+    return st;
+  });
+}
+
+moe_status moe_rows_create(const moe_rows_config* cfg, moe_rows** out) {
+  moe_rows* h = nullptr;
+  const moe_status st = op_entry([&] { return create(cfg, out, h); });
+  if (h) {
+    h->free_all();
+    delete h;
+  }
+  return st;
+}
+
+moe_status moe_rows_plan(moe_rows* h, const void* ids, int32_t id_bytes, int32_t T, int32_t* offsets, int32_t* order,
+                         int32_t* place, void* stream) {
+  return op_entry([&] { return plan(h, ids, id_bytes, T, offsets, order, place, stream); });
+}
+
+moe_status moe_rows_dispatch(moe_rows* h, const void* x, int64_t ldx, int32_t T, int32_t width, const void* ids,
+                             int32_t id_bytes, int32_t* offsets, int32_t* order, int32_t* place, void* rows, int64_t ld_rows,
+                             void* stream) {
+  return op_entry([&] { return take(h, true, x, ldx, T, width, ids, id_bytes, offsets, order, place, rows, ld_rows, stream); });
+}
+
+moe_status moe_rows_take(moe_rows* h, const void* x, int64_t ldx, int32_t T, int32_t width, const int32_t* offsets,
+                         const int32_t* place, void* rows, int64_t ld_rows, void* stream) {
+  return op_entry([&] {
+    return take(h, false, x, ldx, T, width, nullptr, 4, const_cast<int32_t*>(offsets), nullptr, const_cast<int32_t*>(place),
+                rows, ld_rows, stream);
+  });
+}
+
+moe_status moe_rows_combine(moe_rows* h, const void* y, int64_t ldy, int32_t T, int32_t width, const void* w, int32_t w_dtype,
+                            const int32_t* place, void* out, int64_t ldo, void* stream) {
+  return op_entry([&] { return combine(h, y, ldy, T, width, w, w_dtype, place, out, ldo, stream); });
+}
+
+moe_status moe_rows_combine_backward(moe_rows* h, const void* d_out, int64_t ldd, int32_t T, int32_t width, const void* y,
+                                     int64_t ldy, const void* w, int32_t w_dtype, const int32_t* offsets,
+                                     const int32_t* place, void* d_y, int64_t lddy, void* d_w, void* stream) {
+  return op_entry(
+      [&] { return combine_backward(h, d_out, ldd, T, width, y, ldy, w, w_dtype, offsets, place, d_y, lddy, d_w, stream); });
+}
+
+moe_status moe_rows_device_status(moe_rows* h, void* stream) {
+  return op_entry([&] { return h ? h->read_status(stream) : MOE_ERR_INVALID_ARG; });
+}
+
+int64_t moe_rows_device_bytes(const moe_rows* h) { return h ? h->bytes : 0; }
+
+int32_t moe_rows_last_launch_count(const moe_rows* h) { return h ? h->last_launches : 0; }
+
+moe_status moe_rows_destroy(moe_rows* h) {
+  if (!h) return MOE_OK;
+  {
+    DeviceScope dev(h->device);
+    cudaDeviceSynchronize();
+    h->free_all();
+  }
+  delete h;
+  return MOE_OK;
+}
+
+const char* moe_rows_last_error(const moe_rows* h) { return h ? h->last_error.c_str() : g_error.c_str(); }
+
+}  // extern "C"

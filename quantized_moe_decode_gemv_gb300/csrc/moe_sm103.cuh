@@ -15,6 +15,7 @@ enum : int { DT_BF16 = 0, DT_FP16 = 1 };       // moe_dtype
 enum : int { ACT_SWIGLU = 0, ACT_RELU2 = 1, ACT_NONE = 2 };
 
 constexpr int STATUS_TIMEOUT = 2;               // bits of a handle's status word
+constexpr int STATUS_INDEX = 4;                 // an index read from data was out of range
 constexpr long long WAIT_CLOCKS = 4ll << 30;    // a wait gives up after about two seconds
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
