@@ -578,6 +578,59 @@ int32_t moe_rows_last_launch_count(const moe_rows *h);
 moe_status moe_rows_destroy(moe_rows *h);   /* as moe_qlinear_destroy */
 const char *moe_rows_last_error(const moe_rows *h);
 
+/* ---------------------------------------------------------------------------
+ * Orthogonalised updates
+ *
+ * A stack of matrices G[n, rows, cols] (weight gradients, or momentum), each brought
+ * near the orthogonal matrix of its singular vectors by Newton-Schulz products:
+ *
+ *   X = G / (|G| + eps)                        |G| the Frobenius norm
+ *   steps times:  X <- a X + b (X X^T) X + c (X X^T)^2 X
+ *
+ * so that every singular value s of X becomes a s + b s^3 + c s^5, step by step; with
+ * (a, b, c) = (3.4445, -4.775, 2.0315) those above some 0.002 come to 0.7 .. 1.2 in five.
+ * out is bf16.  Products have fp16 operands (scaled by powers of two, the diagonals of
+ * X X^T and of its polynomial apart in fp32, X in two terms where it is multiplied by a
+ * alone) and fp32 sums: the error is below that of out's own rounding, some 1e-3 of
+ * out's norm for each matrix.  Any finite G: its norm is taken without overflow.  A
+ * matrix with a NaN or an infinity becomes NaN, the others of the stack do not.  G = 0
+ * gives 0 (with eps = 0: NaN).
+ * ------------------------------------------------------------------------- */
+typedef struct moe_ortho_config {
+  int32_t rows, cols;     /* of every matrix: 1..32768 */
+  int32_t dtype;          /* BF16|FP16|FP32: G */
+  int32_t steps;          /* 1..64 */
+  int32_t max_matrices;   /* largest n of a call, >= 1 */
+  float a, b, c;          /* finite, such that no singular value of 0..1 grows above 4 */
+  float eps;              /* >= 0 */
+} moe_ortho_config;
+
+typedef struct moe_ortho moe_ortho;
+
+/* MOE_ERR_INVALID_ARG: null cfg, sizes or steps < 1, unknown dtype, coefficients or
+ * eps not finite, eps < 0.  MOE_ERR_UNSUPPORTED: rows or cols > 32768, steps > 64, more
+ * than 2^24 tiles of 128 x 128 in all matrices, coefficients that let a singular value
+ * of 0..1 grow above 4 (or |b l + c l^2|, l its square, above 64). */
+moe_status moe_ortho_validate(const moe_ortho_config *cfg);
+/* Create on the current CUDA device: a workspace of about 6 bytes an element of X and
+ * 4 a min(rows, cols)^2, for max_matrices of them.  Synchronises the device, so not
+ * inside a stream capture. */
+moe_status moe_ortho_create(const moe_ortho_config *cfg, moe_ortho **out);
+
+/* out[n, rows, cols] (bf16) of g[n, rows, cols]; 0 <= n <= max_matrices, n = 0 does
+ * nothing.  DEVICE pointers; rows are ldg and ldo elements apart (>= cols), matrices
+ * step_g and step_o (step_g >= 0; out's matrices must not reach into each other); out
+ * and g must not overlap.  What lies between rows and matrices of out stays.  Streams,
+ * devices, graphs and overlap as moe_qlinear_forward. */
+moe_status moe_ortho_forward(moe_ortho *h, const void *g, int64_t ldg, int64_t step_g, int32_t n, void *out, int64_t ldo,
+                             int64_t step_o, void *stream);
+
+moe_status moe_ortho_device_status(moe_ortho *h, void *stream);   /* as moe_qlinear_device_status */
+int64_t moe_ortho_device_bytes(const moe_ortho *h);
+int32_t moe_ortho_last_launch_count(const moe_ortho *h);
+moe_status moe_ortho_destroy(moe_ortho *h);   /* as moe_qlinear_destroy */
+const char *moe_ortho_last_error(const moe_ortho *h);
+
 /* Device allocations currently held by all handles of this process (for leak
  * checks around refused creates). */
 int64_t moe_debug_live_allocations(void);

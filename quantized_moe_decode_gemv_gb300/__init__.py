@@ -13,5 +13,5 @@ from ._ops import (  # noqa: F401
     GatedBlock, GatedConfig, GatedGrads, QLinear, QLinearConfig,
 )
 from ._train_ops import (  # noqa: F401
-    ExpertRows, ExpertRowsConfig, RowGrads, RowPlan,
+    ExpertRows, ExpertRowsConfig, OrthoConfig, Orthogonalizer, RowGrads, RowPlan,
 )

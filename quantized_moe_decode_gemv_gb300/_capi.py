@@ -80,6 +80,11 @@ class moe_rows_config(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("n_experts", "top_k", "act_dtype", "max_tokens")]
 
 
+class moe_ortho_config(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("rows", "cols", "dtype", "steps", "max_matrices")] +
+                [(n, ctypes.c_float) for n in ("a", "b", "c", "eps")])
+
+
 _I32, _I64, _PTR = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
 
 # symbol -> (restype, argtypes)
@@ -154,6 +159,14 @@ SIGNATURES = {
     "moe_rows_last_launch_count": (ctypes.c_int32, [_PTR]),
     "moe_rows_destroy": (ctypes.c_int, [_PTR]),
     "moe_rows_last_error": (ctypes.c_char_p, [_PTR]),
+    "moe_ortho_validate": (ctypes.c_int, [ctypes.POINTER(moe_ortho_config)]),
+    "moe_ortho_create": (ctypes.c_int, [ctypes.POINTER(moe_ortho_config), ctypes.POINTER(_PTR)]),
+    "moe_ortho_forward": (ctypes.c_int, [_PTR, _PTR, _I64, _I64, _I32, _PTR, _I64, _I64, _PTR]),
+    "moe_ortho_device_status": (ctypes.c_int, [_PTR, _PTR]),
+    "moe_ortho_device_bytes": (ctypes.c_int64, [_PTR]),
+    "moe_ortho_last_launch_count": (ctypes.c_int32, [_PTR]),
+    "moe_ortho_destroy": (ctypes.c_int, [_PTR]),
+    "moe_ortho_last_error": (ctypes.c_char_p, [_PTR]),
     "moe_debug_live_allocations": (ctypes.c_int64, []),
     "moe_debug_fail_allocation": (None, [ctypes.c_int32]),
 }

@@ -1,5 +1,5 @@
 """Python handles of the operators around the training of routed experts
-(include/moe_layer.h): tokens sorted by expert and back.
+(include/moe_layer.h): tokens sorted by expert and back, orthogonalised updates.
 
 Argument checks and marshalling, as in ``_ops``; the arithmetic runs in the CUDA
 library.
@@ -8,9 +8,9 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
-from typing import Any, NamedTuple
+from typing import Any, NamedTuple, Tuple
 
-from ._capi import DTYPE, MOE_OK, MoEError, load_library, moe_rows_config, torch_act_dtype
+from ._capi import DTYPE, MOE_OK, MoEError, load_library, moe_ortho_config, moe_rows_config, torch_act_dtype
 from ._ops import _INVALID_ARG, _SHAPE, _Handle, _int32, _name_of
 
 
@@ -224,3 +224,86 @@ class ExpertRows(_Handle):
         if status:
             self._fail(status)
         return RowGrads(d_y, d_w)
+
+
+# ---------------------------------------------------------------------------
+# orthogonalised updates
+# ---------------------------------------------------------------------------
+
+@dataclasses.dataclass
+class OrthoConfig:
+    """Mirror of ``moe_ortho_config``."""
+    rows: int
+    cols: int
+    max_matrices: int = 1
+    dtype: str = "bf16"          # of the matrices: "bf16", "fp16" or "fp32"
+    steps: int = 5
+    coefficients: Tuple[float, float, float] = (3.4445, -4.7750, 2.0315)
+    eps: float = 1e-7
+
+    def to_c(self) -> moe_ortho_config:
+        if len(self.coefficients) != 3:
+            raise MoEError(_INVALID_ARG, f"three coefficients (of X, X^3 and X^5), not {len(self.coefficients)}")
+        a, b, c = (float(v) for v in self.coefficients)
+        return moe_ortho_config(
+            rows=_int32(self.rows, "rows"), cols=_int32(self.cols, "cols"), dtype=_name_of(DTYPE, self.dtype, "dtype"),
+            steps=_int32(self.steps, "steps"), max_matrices=_int32(self.max_matrices, "max_matrices"), a=a, b=b, c=c,
+            eps=float(self.eps))
+
+
+class Orthogonalizer(_Handle):
+    """Matrices [rows, cols], alone or stacked as [n, rows, cols], each brought near the
+    orthogonal matrix of its singular vectors (all singular values to about 1), as bf16.
+
+    For weight gradients or momentum of any of the three types; a tall matrix is taken
+    from its other side, nothing is transposed in memory.
+    """
+
+    _prefix = "moe_ortho"
+
+    def __init__(self, config: OrthoConfig, device=None):
+        import torch
+        self._setup(torch, load_library())
+        self.config = config
+        c = config.to_c()
+        status = self._fn("validate")(ctypes.byref(c))
+        if status != MOE_OK:
+            raise MoEError(status, self._fn("last_error")(None).decode())
+        self.device = _device_of(torch, device)
+        _create(self, torch, c)
+        self._dtype = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}[config.dtype]
+        self._bf16, self._R, self._C, self._call = torch.bfloat16, config.rows, config.cols, self._lib.moe_ortho_forward
+
+    def _stack(self, t, dtype, what: str):
+        """(number, row stride, matrix stride) of a matrix or a stack of them."""
+        shape = t.shape
+        if len(shape) not in (2, 3) or shape[-2] != self._R or shape[-1] != self._C:
+            raise MoEError(_SHAPE, f"{what} must be [{self._R}, {self._C}] or a stack of them, not {list(shape)}")
+        if t.dtype is not dtype:
+            raise MoEError(_INVALID_ARG, f"{what} must be {dtype}, not {t.dtype}")
+        if t.device != self.device:
+            raise MoEError(_INVALID_ARG, f"{what} is on {t.device}, the handle on {self.device}")
+        n = shape[0] if len(shape) == 3 else 1
+        stride = t.stride()
+        if stride[-1] != 1 and self._C > 1 and n:
+            raise MoEError(_INVALID_ARG, f"{what} needs consecutive columns")
+        if n > self.config.max_matrices:
+            raise MoEError(_INVALID_ARG, f"{what} has {n} matrices, max_matrices is {self.config.max_matrices}")
+        return n, stride[-2], stride[0] if len(shape) == 3 else 0
+
+    def forward(self, g, out=None, stream=None):
+        """out (bf16, g's shape) of g; rows and matrices of both may be strided."""
+        n, ldg, step_g = self._stack(g, self._dtype, "g")
+        s, where = self._stream(stream, g, out)
+        if out is None:
+            with where:
+                out = self._empty(g.shape, dtype=self._bf16, device=self.device)
+        elif out.shape != g.shape:
+            raise MoEError(_SHAPE, f"out must be {list(g.shape)}, not {list(out.shape)}")
+        _, ldo, step_o = self._stack(out, self._bf16, "out")
+        status = self._call(self.handle, g.data_ptr(), ldg, step_g, n, out.data_ptr(), ldo, step_o, s)
+        if status:
+            self._fail(status)
+        return out
+
+    __call__ = forward

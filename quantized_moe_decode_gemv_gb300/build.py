@@ -30,9 +30,10 @@ VARIANTS = [(LIB, BUILD_DIR, []), (LIB_CHECKS, os.path.join(BUILD_DIR, "checks")
 # (source, object name, extra flags)
 SOURCES = [("moe_layer.cu", "moe_layer", []), ("moe_noalloc.cu", "moe_noalloc", []),
            ("moe_qlinear.cu", "moe_qlinear", []), ("moe_gated.cu", "moe_gated", []),
-           ("moe_gemm16.cu", "moe_gemm16", []), ("moe_rows.cu", "moe_rows", [])]
+           ("moe_gemm16.cu", "moe_gemm16", []), ("moe_rows.cu", "moe_rows", []),
+           ("moe_ortho.cu", "moe_ortho", [])]
 # units without a check: every variant links the default build's object
-NO_CHECKS = {"moe_qlinear", "moe_gated", "moe_gemm16", "moe_rows"}
+NO_CHECKS = {"moe_qlinear", "moe_gated", "moe_gemm16", "moe_rows", "moe_ortho"}
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-warn-spills"]

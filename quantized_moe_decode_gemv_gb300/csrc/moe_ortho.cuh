@@ -1,0 +1,541 @@
+// Newton-Schulz products (moe_ortho_* in include/moe_layer.h) on tcgen05: a matrix X
+// with small side m becomes p(X) = a X + b (X X^T) X + c (X X^T)^2 X, step by step.
+//
+//   GRAM   A = X X^T                     [m, m], symmetric
+//   POLY   B = b A + c A A               [m, m], symmetric
+//   APPLY  X <- a X + B X                (tall matrices: X^T X, and X B)
+//
+// What is held in which precision.  Operands are fp16: at the rate of bf16 with three
+// more bits.  X is scaled by s = 2^q and A, B by s^2, 4^q about m, so that neither the
+// entries of X (about 1 / sqrt(m n) of its norm at the start) nor the largest value of
+// A and B (2.8 s^2) leave fp16's range; powers of two, so exact.  Two things keep the
+// result's error below the rounding of its bf16 output (1.66e-3 of its norm; with it
+// measured 1.8e-3 on 1024 x 4096 and 8192 x 4096, 1.9e-3 on 64 x 256):
+//   - The diagonals d of A and e of B are kept apart in fp32 and the fp16 matrices have
+//     zeros there: A = O + diag(d), and
+//       (A A)_ij = (O O)_ij + O_ij (d_i + d_j) + [i = j] d_i^2
+//     in the epilogue.  Near the fixed point A is close to a multiple of 1, so the
+//     diagonal is most of A's norm, and of its rounding: with it in fp16 the error of a
+//     full-rank matrix was 1.5 to 1.7e-3, without 1.0 to 1.2e-3.
+//   - X is kept as two fp16 terms, hi + lo.  Products take hi, the linear term a X both:
+//     what rounding leaves of X lies in directions that X itself may not have, where p
+//     multiplies by a = 3.4 a step; without lo a gradient of 9 tokens was off by 4e-2.
+//
+// Roles of a CTA's 12 warps, as in k_gemm16: tensor copies, MMAs, tensor memory, and
+// eight epilogue warps; accumulators double-buffered, CTAs (pairs) persistent.  Tiles are
+// square, CG * 128 on a side; a symmetric product computes those on and below the
+// diagonal and stores the others as their transposes.
+//
+// Every wait is bounded; a role whose wait runs out sets the timeout bit of the status
+// word and winds down.
+#pragma once
+
+#include "moe_sm103.cuh"
+
+namespace moe_op {
+
+constexpr int OR_THREADS = 384;
+constexpr int OR_EPI_WARPS = 8;
+constexpr int OR_MAX_STAGES = 8;
+constexpr int OR_EPI_BYTES = OR_EPI_WARPS * 32 * 80;   // a warp's 32 rows x 64 (+16) bytes
+constexpr int OR_SMEM_MAX = 227 * 1024;
+enum : int { OR_GRAM = 0, OR_POLY = 1, OR_APPLY = 2 };
+
+struct OrthoArgs {
+  CUtensorMap ta, tb;       // 3-D: columns, rows, matrix
+  int M, N, kb;             // output rows and columns, 64-wide K blocks
+  int batches;
+  int stages, sub;          // slots of the ring and K blocks a slot
+  const unsigned short *hi, *lo;   // APPLY: X; POLY: hi = O
+  int64_t ld_x, step_x;
+  const float* diag;        // POLY: d; APPLY: e
+  int64_t step_diag;
+  unsigned short *out_hi, *out_lo;   // GRAM: O; POLY: P (B without its diagonal); APPLY: X
+  int64_t ld_out, step_out;
+  float* diag_out;          // GRAM: d; POLY: e
+  unsigned short* last;     // APPLY, last step: the caller's bf16 matrices, else null
+  int64_t ld_last, step_last;
+  int vec_last;             // rows of `last` allow 32-byte stores
+  int e_by_row;             // APPLY: e belongs to rows (wide) or columns (tall)
+  float ka, kb_, kc, inv_s2;   // a, b, c / s^2, 1 / s^2
+  float inv_s;
+  int* status;
+};
+
+__host__ __device__ inline int or_stage_bytes() { return 2 * 128 * 128; }   // 128 rows of A and of B (CG 2: a half of it)
+__host__ __device__ inline int or_smem_bytes(int stages, int sub) {
+  return stages * sub * or_stage_bytes() + OR_EPI_BYTES + 8 * (2 * OR_MAX_STAGES + 6) + 1024;
+}
+
+struct OrthoUnit {
+  int z, m0, n0;
+  bool mirror;
+};
+
+// Unit u: matrices, then tiles.  Symmetric: tile rows one after the other, each up to
+// the diagonal; else in groups of 8 tile rows, rows fastest.
+template <int CG, bool SYM>
+__device__ __forceinline__ OrthoUnit or_unit(const OrthoArgs& A, int u) {
+  constexpr int TS = CG * 128;
+  const int tm = (A.M + TS - 1) / TS, tn = (A.N + TS - 1) / TS;
+  const int tiles = SYM ? tm * (tm + 1) / 2 : tm * tn;
+  OrthoUnit U;
+  U.z = u / tiles;
+  int t = u - U.z * tiles;
+  if (SYM) {
+    int i = static_cast<int>((sqrtf(8.0f * t + 1.0f) - 1.0f) * 0.5f);
+    while (i * (i + 1) / 2 > t) --i;
+    while ((i + 1) * (i + 2) / 2 <= t) ++i;
+    const int j = t - i * (i + 1) / 2;
+    U.m0 = i * TS;
+    U.n0 = j * TS;
+    U.mirror = i != j;
+  } else {
+    const int g = t / (8 * tn), rows = min(8, tm - 8 * g);
+    t -= g * 8 * tn;
+    U.m0 = (8 * g + t % rows) * TS;
+    U.n0 = (t / rows) * TS;
+    U.mirror = false;
+  }
+  return U;
+}
+
+template <int CG, bool SYM>
+__host__ __device__ inline int64_t or_units(int M, int N, int batches) {
+  const int64_t tm = (M + CG * 128 - 1) / (CG * 128), tn = (N + CG * 128 - 1) / (CG * 128);
+  return batches * (SYM ? tm * (tm + 1) / 2 : tm * tn);
+}
+
+// A lane's 32 values as fp16 at p (64 bytes, 32-byte aligned).
+__device__ __forceinline__ void or_store(unsigned short* p, const float (&v)[32], int dt) {
+#pragma unroll
+  for (int j = 0; j < 32; j += 16)
+    stg32(p + j, pack2(v[j], v[j + 1], dt), pack2(v[j + 2], v[j + 3], dt), pack2(v[j + 4], v[j + 5], dt),
+          pack2(v[j + 6], v[j + 7], dt), pack2(v[j + 8], v[j + 9], dt), pack2(v[j + 10], v[j + 11], dt),
+          pack2(v[j + 12], v[j + 13], dt), pack2(v[j + 14], v[j + 15], dt));
+}
+
+// The transpose of a warp's 32 x 32 values (lane = row): p is the place of row 0, column
+// 0 of it, `cols` of its rows exist.  Neighbouring lanes trade one of two columns, so
+// that a lane stores two rows' values of a column at once.
+__device__ __forceinline__ void or_store_mirror(unsigned short* p, int64_t ld, const float (&v)[32], int cols, int lane) {
+  const int odd = lane & 1;
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) {
+    const float give = odd ? v[j] : v[j + 1];
+    const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 1);
+    const uint32_t w = odd ? pack2(got, v[j + 1], DT_FP16) : pack2(v[j], got, DT_FP16);
+    if (j + odd < cols) *reinterpret_cast<uint32_t*>(p + (j + odd) * ld + (lane & ~1)) = w;
+  }
+}
+
+// 32 fp16 values (64 bytes, 16-byte aligned) as four words of eight.
+__device__ __forceinline__ void or_load(const unsigned short* p, uint4 (&w)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = reinterpret_cast<const uint4*>(p)[j];
+}
+__device__ __forceinline__ float or_value(const uint4 (&w)[4], int j) {
+  const uint4& u = w[j / 8];
+  const uint32_t x = j % 8 < 2 ? u.x : j % 8 < 4 ? u.y : j % 8 < 6 ? u.z : u.w;
+  return j & 1 ? hi16(x, DT_FP16) : lo16(x, DT_FP16);
+}
+
+template <int CG, bool AMN, bool BMN, int MODE>
+__global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__ OrthoArgs A) {
+  constexpr bool SYM = MODE != OR_APPLY;
+  constexpr int BN = CG * 128;
+  extern __shared__ __align__(1024) char or_smem[];
+  char* base = or_smem + ((1024u - (smem_u32(or_smem) & 1023u)) & 1023u);
+  const int S = A.stages;
+  const int stage_bytes = or_stage_bytes(), slot_bytes = A.sub * stage_bytes;
+  char* epi = base + S * slot_bytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(epi + OR_EPI_BYTES);
+  uint64_t *full = bars, *empty = bars + OR_MAX_STAGES, *accf = bars + 2 * OR_MAX_STAGES, *acce = accf + 2, *drain = acce + 2;
+  uint32_t* holder = reinterpret_cast<uint32_t*>(drain + 1);
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+  const int worker = blockIdx.x / CG, nworkers = gridDim.x / CG;
+  const int units = static_cast<int>(or_units<CG, SYM>(A.M, A.N, A.batches));
+  constexpr uint32_t tm_cols = 2 * BN;
+
+  if (warp == 2) tm_alloc<CG>(smem_u32(holder), tm_cols);
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      bar_init(smem_u32(&full[s]), 1);
+      bar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      bar_init(smem_u32(&accf[b]), 1);
+      bar_init(smem_u32(&acce[b]), OR_EPI_WARPS * CG);
+    }
+    bar_init(smem_u32(drain), 1);
+    bar_fence_init();
+  }
+  tm_fence_before();
+  __syncthreads();
+  if (CG == 2) cluster_sync();
+  tm_fence_after();
+  const uint32_t tmem = *holder;
+  // everything above may run while the kernel before this one in the stream ends
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  bool ok = true;
+  auto wait = [&](uint64_t* b, uint32_t parity) {
+    if (bar_wait(smem_u32(b), parity)) return true;
+    atomicOr(A.status, STATUS_TIMEOUT);
+    ok = false;
+    return false;
+  };
+
+  if (warp == 0) {
+    // ---------------- tensor copies ----------------
+    RingPos R;
+    bool again = false;   // slots have been used before
+    uint32_t q = 0;
+    for (int u = worker; ok && u < units; u += nworkers) {
+      const OrthoUnit U = or_unit<CG, SYM>(A, u);
+      const int am = U.m0 + static_cast<int>(rank) * 128, bn = U.n0 + static_cast<int>(rank) * 128;
+      for (int i = 0; i < A.kb; i += A.sub, ++q) {
+        const int s = R.slot, nk = min(A.sub, A.kb - i);
+        if (again && !wait(&empty[s], R.parity ^ 1u)) break;
+        R.next(S);
+        again = again || R.slot == 0;
+        // both CTAs' copies complete on the even CTA's barrier
+        const uint32_t own = smem_u32(&full[s]), fb = CG == 2 ? cluster_addr(own, 0) : own;
+        if (elect_lane()) {
+          if (rank == 0) bar_expect_tx(own, static_cast<uint32_t>(CG * stage_bytes * nk));
+          for (int j = 0; j < nk; ++j) {
+            const int k0 = (i + j) * 64;
+            const uint32_t da = smem_u32(base + s * slot_bytes + j * stage_bytes), db = da + 128 * 128;
+            if (AMN) {
+              tma_3d<CG>(da, &A.ta, am, k0, U.z, fb);
+              tma_3d<CG>(da + 8192, &A.ta, am + 64, k0, U.z, fb);
+            } else {
+              tma_3d<CG>(da, &A.ta, k0, am, U.z, fb);
+            }
+            if (BMN) {
+              tma_3d<CG>(db, &A.tb, bn, k0, U.z, fb);
+              tma_3d<CG>(db + 8192, &A.tb, bn + 64, k0, U.z, fb);
+            } else {
+              tma_3d<CG>(db, &A.tb, k0, bn, U.z, fb);
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+    // the last use of every slot is released (so the MMAs' arrivals at this
+    // CTA's barriers have landed) before the CTA ends; after a wait that ran
+    // out, at least the copies already issued land first
+    const uint32_t used = q < static_cast<uint32_t>(S) ? q : static_cast<uint32_t>(S);
+    for (uint32_t j = q - used; j < q; ++j) {
+      if (ok) {
+        wait(&empty[j % S], (j / S) & 1);
+      } else if (rank == 0) {
+        bar_wait(smem_u32(&full[j % S]), (j / S) & 1);
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------- MMAs (the pair's even CTA) ----------------
+    if (rank == 0) {
+      const uint32_t idesc = f16_idesc(CG * 128, BN, DT_FP16, AMN, BMN);
+      RingPos R;
+      uint32_t n = 0;
+      for (int u = worker; ok && u < units; u += nworkers, ++n) {
+        const int buf = n & 1;
+        if (n >= 2 && !wait(&acce[buf], ((n >> 1) - 1) & 1)) break;
+        tm_fence_after();
+        const uint32_t d = tmem + static_cast<uint32_t>(buf * BN);
+        for (int i = 0; i < A.kb; i += A.sub) {
+          const int s = R.slot, nk = min(A.sub, A.kb - i);
+          if (!wait(&full[s], R.parity)) break;
+          R.next(S);
+          tm_fence_after();
+          if (elect_lane()) {
+            for (int j = 0; j < nk; ++j) {
+              const uint32_t sa = smem_u32(base + s * slot_bytes + j * stage_bytes), sb = sa + 128 * 128;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint64_t da = AMN ? sw128_desc(sa + k * 2048, 8192) : sw128_desc(sa + k * 32, 16);
+                const uint64_t db = BMN ? sw128_desc(sb + k * 2048, 8192) : sw128_desc(sb + k * 32, 16);
+                tm_mma<CG>(d, da, db, idesc, (i | j | k) != 0);
+              }
+            }
+            tm_commit<CG>(smem_u32(&empty[s]));
+          }
+          __syncwarp();
+        }
+        if (ok && elect_lane()) tm_commit<CG>(smem_u32(&accf[buf]));
+        __syncwarp();
+      }
+      if (!ok) {   // MMAs already issued end before their tensor memory is freed
+        if (elect_lane()) tm_commit<CG>(smem_u32(drain));
+        __syncwarp();
+        bar_wait(smem_u32(drain), 0);
+      }
+    }
+  } else if (warp >= 4) {
+    // ---------------- epilogue ----------------
+    const int ew = warp & 3, half = (warp - 4) >> 2;
+    char* st = epi + (warp - 4) * 32 * 80;
+    uint32_t n = 0;
+    for (int u = worker; ok && u < units; u += nworkers, ++n) {
+      const OrthoUnit U = or_unit<CG, SYM>(A, u);
+      const int buf = n & 1;
+      if (!wait(&accf[buf], (n >> 1) & 1)) break;
+      tm_fence_after();
+      const uint32_t tcol = tmem + (static_cast<uint32_t>(ew * 32) << 16) + static_cast<uint32_t>(buf * BN);
+      const int row0 = U.m0 + static_cast<int>(rank) * 128 + ew * 32, row = row0 + lane;
+      const float* diag = A.diag + U.z * A.step_diag;
+      const bool in = row < A.M;
+      const float d_row = (MODE == OR_POLY || (MODE == OR_APPLY && A.e_by_row)) && in ? diag[row] : 0.0f;
+      for (int c = 32 * half; c < BN; c += 64) {
+        const int col0 = U.n0 + c;
+        const bool live = row0 < A.M && col0 < A.N;   // (a piece reaches past the last column only into its row's padding)
+        // what the piece needs of memory is under way while the accumulators are read
+        uint4 hi[4], lo[4];
+        float dc[32];
+        if (MODE != OR_GRAM && live && in) {
+          const int64_t o = U.z * A.step_x + row * A.ld_x + col0;
+          or_load(A.hi + o, hi);
+          if (MODE == OR_APPLY) or_load(A.lo + o, lo);
+        }
+        if ((MODE == OR_POLY || (MODE == OR_APPLY && !A.e_by_row)) && live) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(dc + j) = *reinterpret_cast<const float4*>(diag + col0 + j);
+        }
+        uint32_t r[32];
+        tm_ld32(tcol + c, r);
+        tm_wait_ld();
+        if (c + 64 >= BN) {
+          // the accumulators are in registers: the buffer may be rewritten
+          tm_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (CG == 2) bar_arrive_cluster(smem_u32(&acce[buf]), 0);
+            else bar_arrive(smem_u32(&acce[buf]));
+          }
+        }
+        if (!live) continue;
+        float v[32];
+        if (MODE == OR_GRAM) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+        } else if (MODE == OR_POLY) {
+          if (in) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float o = or_value(hi, j);
+              v[j] = fmaf(A.kb_, o, A.kc * fmaf(o, d_row + dc[j], __uint_as_float(r[j])));
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+          }
+        } else {
+          if (in) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float e = A.e_by_row ? d_row : dc[j];
+              v[j] = fmaf(A.ka + e, or_value(hi, j), fmaf(A.ka, or_value(lo, j), A.inv_s2 * __uint_as_float(r[j])));
+            }
+          }
+        }
+        if (SYM) {
+          if (row0 == col0) {   // the diagonal: kept apart, in fp32
+            float own = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j == lane) {
+                own = __uint_as_float(r[j]);
+                v[j] = 0.0f;
+              }
+            if (in) {
+              if (MODE == OR_POLY) own = (A.kb_ * d_row + A.kc * fmaf(d_row, d_row, own)) * A.inv_s2;
+              A.diag_out[U.z * A.step_diag + row] = own;
+            }
+          }
+          unsigned short* out = A.out_hi + U.z * A.step_out;
+          if (in) or_store(out + row * A.ld_out + col0, v, DT_FP16);
+          if (U.mirror) or_store_mirror(out + col0 * A.ld_out + row0, A.ld_out, v, A.N - col0, lane);
+        } else if (!A.last) {
+          if (in) {
+            const int64_t o = U.z * A.step_out + row * A.ld_out + col0;
+            or_store(A.out_hi + o, v, DT_FP16);
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const uint32_t h = pack2(v[j], v[j + 1], DT_FP16);
+              v[j] -= lo16(h, DT_FP16);
+              v[j + 1] -= hi16(h, DT_FP16);
+            }
+            or_store(A.out_lo + o, v, DT_FP16);
+          }
+        } else {
+          unsigned short* out = A.last + U.z * A.step_last + col0;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] *= A.inv_s;
+          if (A.vec_last && col0 + 32 <= A.N) {
+            if (in) or_store(out + row * A.ld_last, v, DT_BF16);
+          } else {
+            // rows that 32-byte stores do not fit: a lane a column, by way of shared memory
+            uint4* w = reinterpret_cast<uint4*>(st + lane * 80);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              w[j] = make_uint4(pack2(v[8 * j], v[8 * j + 1], DT_BF16), pack2(v[8 * j + 2], v[8 * j + 3], DT_BF16),
+                                pack2(v[8 * j + 4], v[8 * j + 5], DT_BF16), pack2(v[8 * j + 6], v[8 * j + 7], DT_BF16));
+            __syncwarp();
+            if (col0 + lane < A.N) {
+              const int rows = min(32, A.M - row0);
+#pragma unroll 8
+              for (int i = 0; i < rows; ++i)
+                out[(row0 + i) * A.ld_last + lane] = *reinterpret_cast<const unsigned short*>(st + i * 80 + lane * 2);
+            }
+            __syncwarp();
+          }
+        }
+      }
+    }
+  }
+  tm_fence_before();
+  __syncthreads();
+  if (CG == 2) cluster_sync();
+  if (warp == 2) {
+    tm_fence_after();
+    tm_free<CG>(tmem, tm_cols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the start: X = s G / (|G| + eps)
+// ---------------------------------------------------------------------------
+
+constexpr int OR_NORM_CTAS = 128;   // partial sums of a matrix at most
+
+struct OrthoStart {
+  const void* g;
+  int dt;                   // moe_dtype of g
+  int64_t ldg, step_g;
+  int M, N, ctas;           // CTAs a matrix
+  float* part;              // [matrix][OR_NORM_CTAS][3]
+  unsigned short *hi, *lo;
+  int64_t ld_x, step_x;
+  int vec;                  // elements of a row come eight at a time
+  double s, eps;
+};
+
+// Up to eight elements from column c of a row (zeros past the last one).
+__device__ __forceinline__ void or_read(const OrthoStart& A, int64_t at, int left, float (&v)[8]) {
+  if (A.vec && left >= 8) {
+    if (A.dt == 2) {
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(A.g) + at);
+      *reinterpret_cast<float4*>(v) = p[0];
+      *reinterpret_cast<float4*>(v + 4) = p[1];
+    } else {
+      const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const unsigned short*>(A.g) + at);
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = lo16(u[j], A.dt);
+        v[2 * j + 1] = hi16(u[j], A.dt);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    v[j] = j >= left ? 0.0f : A.dt == 2 ? static_cast<const float*>(A.g)[at + j] : ld16(A.g, at + j, A.dt);
+}
+
+// Squares summed in fp32 in three ranges (of 2^-40 and 2^40), each scaled into the
+// middle: a square of any fp32 value neither overflows nor vanishes.
+__global__ void __launch_bounds__(256) k_ortho_norm(const OrthoStart A) {
+  __shared__ float sums[8][3];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int z = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float s[3] = {0.0f, 0.0f, 0.0f};
+  const int q = (A.N + 7) / 8;
+  const int64_t n = static_cast<int64_t>(A.M) * q;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t r = i / q;
+    const int c = static_cast<int>(i - r * q) * 8;
+    float v[8];
+    or_read(A, z * A.step_g + r * A.ldg + c, A.N - c, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float x = fabsf(v[j]);
+      if (x > 0x1p40f) {
+        s[2] = fmaf(x * 0x1p-60f, x * 0x1p-60f, s[2]);
+      } else if (x < 0x1p-40f) {
+        s[0] = fmaf(x * 0x1p60f, x * 0x1p60f, s[0]);
+      } else {
+        s[1] = fmaf(x, x, s[1]);   // (NaN too)
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) s[k] += __shfl_xor_sync(0xFFFFFFFFu, s[k], d);
+    if (lane == 0) sums[warp][k] = s[k];
+  }
+  __syncthreads();
+  if (threadIdx.x < 3) {
+    float t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) t += sums[w][threadIdx.x];
+    A.part[(static_cast<int64_t>(z) * OR_NORM_CTAS + blockIdx.x) * 3 + threadIdx.x] = t;
+  }
+}
+
+// X = hi + lo in fp16.  Every CTA adds the matrix's partial sums in order; the factor
+// s / (|G| + eps) is applied as two, so that it has 64-bit numbers' range.
+__global__ void __launch_bounds__(256) k_ortho_start(const OrthoStart A) {
+  __shared__ float factor[2];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int z = blockIdx.y;
+  if (threadIdx.x < 32) {
+    double t[3] = {0.0, 0.0, 0.0};
+    for (int i = threadIdx.x; i < A.ctas; i += 32)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) t[k] += A.part[(static_cast<int64_t>(z) * OR_NORM_CTAS + i) * 3 + k];
+    double sum = t[0] * 0x1p-120 + t[1] + t[2] * 0x1p120;
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    if (threadIdx.x == 0) {
+      const double r = A.s / (sqrt(sum) + A.eps);
+      int ex = 0;
+      if (r > 0.0 && r < 1e300) {
+        frexp(r, &ex);
+        factor[0] = static_cast<float>(ldexp(1.0, ex / 2));
+        factor[1] = static_cast<float>(ldexp(r, -(ex / 2)));
+      } else {
+        factor[0] = 1.0f;
+        factor[1] = static_cast<float>(r);
+      }
+    }
+  }
+  __syncthreads();
+  const float f0 = factor[0], f1 = factor[1];
+  const int q = (A.N + 7) / 8;
+  const int64_t n = static_cast<int64_t>(A.M) * q;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t r = i / q;
+    const int c = static_cast<int>(i - r * q) * 8;
+    float v[8];
+    or_read(A, z * A.step_g + r * A.ldg + c, A.N - c, v);
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float a = v[2 * j] * f0 * f1, b = v[2 * j + 1] * f0 * f1;
+      h[j] = pack2(a, b, DT_FP16);
+      l[j] = pack2(a - lo16(h[j], DT_FP16), b - hi16(h[j], DT_FP16), DT_FP16);
+    }
+    const int64_t o = z * A.step_x + r * A.ld_x + c;   // (rows are padded to 32 elements)
+    *reinterpret_cast<uint4*>(A.hi + o) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(A.lo + o) = make_uint4(l[0], l[1], l[2], l[3]);
+  }
+}
+
+}  // namespace moe_op
