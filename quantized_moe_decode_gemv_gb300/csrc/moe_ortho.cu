@@ -12,11 +12,14 @@
 using namespace moe_op;
 
 struct moe_ortho : OpHandle {
+  int64_t own_step_x() const { return (cfg.rows + 31) / 32 * (ld_x / 32) * 2048; }
+  int64_t own_step_a() const { return (m + 31) / 32 * (ld_a / 32) * 1024; }
   moe_ortho_config cfg{};
   int m = 0;                        // the smaller side: A and B are [m, m]
   int64_t ld_x = 0, ld_a = 0;       // row strides of X and of A, B
   int q = 0;                        // scale of X: 2^q
-  unsigned short *hi[2] = {nullptr, nullptr}, *lo = nullptr, *a = nullptr, *b = nullptr;
+  unsigned short *hi[2] = {nullptr, nullptr}, *a = nullptr, *b = nullptr;   // rows, as tensor copies read them
+  unsigned short *own_x = nullptr, *own_a = nullptr;   // 32 x 32 pieces, as epilogues do
   float *d = nullptr, *e = nullptr, *sums = nullptr;
 };
 
@@ -111,10 +114,10 @@ cudaError_t launch(moe_ortho* h, int mode, bool tall, OrthoArgs a, int k, const 
   a.stages = OR_MAX_STAGES;
   while (or_smem_bytes(a.stages, a.sub) > OR_SMEM_MAX) --a.stages;
   const int64_t xs = h->cfg.rows * h->ld_x, as = h->m * h->ld_a;
-  const bool ok = (amn ? encode_stack16(&a.ta, pa, a.M, k, lda, a.batches, xs, 64)
-                       : encode_stack16(&a.ta, pa, k, a.M, lda, a.batches, mode == OR_GRAM || (mode == OR_APPLY && tall) ? xs : as, 128)) &&
-                  (bmn ? encode_stack16(&a.tb, pb, a.N, k, ldb, a.batches, xs, 64)
-                       : encode_stack16(&a.tb, pb, k, a.N, ldb, a.batches, mode == OR_GRAM ? xs : as, 128));
+  const bool ok = (amn ? encode_stack16(&a.ta, pa, a.M, k, lda, a.batches, xs, 64, 64)
+                       : encode_stack16(&a.ta, pa, k, a.M, lda, a.batches, mode == OR_GRAM || (mode == OR_APPLY && tall) ? xs : as, 64, 128)) &&
+                  (bmn ? encode_stack16(&a.tb, pb, a.N, k, ldb, a.batches, xs, 64, 64)
+                       : encode_stack16(&a.tb, pb, k, a.N, ldb, a.batches, mode == OR_GRAM ? xs : as, 64, 128));
   if (!ok) {
     *why = "tensor map refused";
     return cudaErrorInvalidValue;
@@ -167,10 +170,12 @@ moe_status forward(moe_ortho* h, const void* g, int64_t ldg, int64_t step_g, int
   t.M = c.rows;
   t.N = c.cols;
   const int64_t pieces = R * ((C + 7) / 8);
-  t.ctas = static_cast<int>(std::min<int64_t>(OR_NORM_CTAS, (pieces + 1023) / 1024));
+  t.ctas = static_cast<int>(std::min<int64_t>({OR_NORM_CTAS, (pieces + 1023) / 1024, tiles(8ll * h->num_sms, n)}));
   t.part = h->sums;
   t.hi = h->hi[0];
-  t.lo = h->lo;
+  t.own = h->own_x;
+  t.step_own = h->own_step_x();
+  t.own_cols = static_cast<int>(h->ld_x / 32);
   t.ld_x = h->ld_x;
   t.step_x = xs;
   t.vec = reinterpret_cast<uintptr_t>(g) % 16 == 0 && (R == 1 || ldg * gb % 16 == 0) && step_g * gb % 16 == 0;
@@ -184,7 +189,7 @@ moe_status forward(moe_ortho* h, const void* g, int64_t ldg, int64_t step_g, int
     p.g = gp + z * step_g * gb;
     p.part += static_cast<int64_t>(z) * OR_NORM_CTAS * 3;
     p.hi += z * xs;
-    p.lo += z * xs;
+    p.own += z * t.step_own;
     const dim3 grid(static_cast<unsigned>(t.ctas), static_cast<unsigned>(nz));
     e = launch_chained(k_ortho_norm, grid, 256, 0, 1, s, p);
     if (e == cudaSuccess) e = launch_chained(k_ortho_start, grid, 256, 0, 1, s, p);
@@ -200,42 +205,46 @@ moe_status forward(moe_ortho* h, const void* g, int64_t ldg, int64_t step_g, int
   base.inv_s2 = static_cast<float>(1.0 / (scale * scale));
   base.step_diag = ds;
   base.status = h->status;
+  // where the epilogues' tensor copies write: pieces of 32 x 32
+  auto rows_of = [&](CUtensorMap* map, const void* p, int64_t cols, int64_t rows, int64_t ld, int64_t step) {
+    if (encode_stack16(map, p, cols, rows, ld, n, step, 32, 32)) return true;
+    why = "tensor map refused";
+    e = cudaErrorInvalidValue;
+    return false;
+  };
   for (int i = 0; i < c.steps && e == cudaSuccess; ++i) {
     const unsigned short* x = h->hi[i & 1];
     OrthoArgs a = base;      // O = X X^T without its diagonal
     a.M = a.N = m;
-    a.out_hi = h->a;
-    a.ld_out = h->ld_a;
-    a.step_out = as;
+    a.own = h->own_a;
+    a.step_own = h->own_step_a();
+    a.own_cols = static_cast<int>(h->ld_a / 32);
     a.diag_out = h->d;
+    if (!rows_of(&a.to, h->a, m, m, h->ld_a, as)) break;
     e = launch(h, OR_GRAM, tall, a, tall ? c.rows : c.cols, x, h->ld_x, x, h->ld_x, s, &why);
     if (e != cudaSuccess) break;
-    a.hi = h->a;             // P = b A + c A A without its diagonal
-    a.ld_x = h->ld_a;
-    a.step_x = as;
-    a.diag = h->d;
-    a.out_hi = h->b;
+    a.diag = h->d;           // P = b A + c A A without its diagonal
     a.diag_out = h->e;
+    if (!rows_of(&a.to, h->b, m, m, h->ld_a, as)) break;
     e = launch(h, OR_POLY, tall, a, m, h->a, h->ld_a, h->a, h->ld_a, s, &why);
     if (e != cudaSuccess) break;
     a = base;
     a.M = c.rows;
     a.N = c.cols;
-    a.hi = x;
-    a.lo = h->lo;
-    a.ld_x = h->ld_x;
-    a.step_x = xs;
+    a.own = h->own_x;
+    a.step_own = t.step_own;
+    a.own_cols = t.own_cols;
     a.diag = h->e;
     a.e_by_row = !tall;
-    a.out_hi = h->hi[(i + 1) & 1];
-    a.out_lo = h->lo;
-    a.ld_out = h->ld_x;
-    a.step_out = xs;
-    if (i + 1 == c.steps) {
+    a.final = i + 1 == c.steps;
+    if (!a.final) {
+      if (!rows_of(&a.to, h->hi[(i + 1) & 1], C, R, h->ld_x, xs)) break;
+    } else if (reinterpret_cast<uintptr_t>(out) % 16 == 0 && ldo % 8 == 0 && step_o % 8 == 0) {
+      if (!rows_of(&a.to, out, C, R, ldo, n > 1 ? step_o : (R * ldo + 7) / 8 * 8)) break;
+    } else {
       a.last = static_cast<unsigned short*>(out);
       a.ld_last = ldo;
       a.step_last = step_o;
-      a.vec_last = reinterpret_cast<uintptr_t>(out) % 32 == 0 && ldo % 16 == 0 && step_o % 16 == 0;
     }
     e = tall ? launch(h, OR_APPLY, true, a, m, x, h->ld_x, h->b, h->ld_a, s, &why)
              : launch(h, OR_APPLY, false, a, m, h->b, h->ld_a, x, h->ld_x, s, &why);
@@ -279,8 +288,10 @@ moe_status create(const moe_ortho_config* cfg, moe_ortho** out, moe_ortho*& h) {
   const size_t n = static_cast<size_t>(c.max_matrices), x = n * c.rows * h->ld_x * 2, a = n * h->m * h->ld_a * 2;
   cudaError_t e = h->alloc(reinterpret_cast<void**>(&h->status), 64);
   if (e == cudaSuccess) e = cudaMemset(h->status, 0, 64);
-  for (unsigned short** p : {&h->hi[0], &h->hi[1], &h->lo})
+  for (unsigned short** p : {&h->hi[0], &h->hi[1]})
     if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(p), x);
+  if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->own_x), n * h->own_step_x() * 2);
+  if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->own_a), n * h->own_step_a() * 2);
   for (unsigned short** p : {&h->a, &h->b})
     if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(p), a);
   for (float** p : {&h->d, &h->e})

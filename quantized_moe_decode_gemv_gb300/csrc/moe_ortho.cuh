@@ -26,6 +26,13 @@
 // square, CG * 128 on a side; a symmetric product computes those on and below the
 // diagonal and stores the others as their transposes.
 //
+// An epilogue warp's piece is 32 x 32 values, a row a lane.  Memory that lanes address by
+// their rows is 32 lines an instruction, and that paced the epilogues (17 thousand clocks
+// for a 256 x 256 tile, more than the MMAs of K = 1024).  So what an epilogue reads of its
+// own element, X for the linear term and O for b A, lies a second time in pieces as lanes
+// read them (16 bytes of 32 lanes side by side), and rows are written by tensor copies
+// from shared memory.
+//
 // Every wait is bounded; a role whose wait runs out sets the timeout bit of the status
 // word and winds down.
 #pragma once
@@ -37,7 +44,7 @@ namespace moe_op {
 constexpr int OR_THREADS = 384;
 constexpr int OR_EPI_WARPS = 8;
 constexpr int OR_MAX_STAGES = 8;
-constexpr int OR_EPI_BYTES = OR_EPI_WARPS * 32 * 80;   // a warp's 32 rows x 64 (+16) bytes
+constexpr int OR_EPI_BYTES = OR_EPI_WARPS * 4096;   // a warp's 32 x 32 values and their transpose
 constexpr int OR_SMEM_MAX = 227 * 1024;
 enum : int { OR_GRAM = 0, OR_POLY = 1, OR_APPLY = 2 };
 
@@ -46,16 +53,16 @@ struct OrthoArgs {
   int M, N, kb;             // output rows and columns, 64-wide K blocks
   int batches;
   int stages, sub;          // slots of the ring and K blocks a slot
-  const unsigned short *hi, *lo;   // APPLY: X; POLY: hi = O
-  int64_t ld_x, step_x;
+  CUtensorMap to;           // GRAM: O; POLY: P (B without its diagonal); APPLY: X's hi, or the caller's matrices
+  unsigned short* own;      // pieces of 32 x 32 values: O (GRAM writes, POLY reads), X as hi and lo (APPLY)
+  int64_t step_own;
+  int own_cols;             // pieces in a row of them
   const float* diag;        // POLY: d; APPLY: e
   int64_t step_diag;
-  unsigned short *out_hi, *out_lo;   // GRAM: O; POLY: P (B without its diagonal); APPLY: X
-  int64_t ld_out, step_out;
   float* diag_out;          // GRAM: d; POLY: e
-  unsigned short* last;     // APPLY, last step: the caller's bf16 matrices, else null
+  int final;                // APPLY: the last step, whose result is the caller's
+  unsigned short* last;     // the caller's bf16 matrices where tensor copies cannot write them, else null
   int64_t ld_last, step_last;
-  int vec_last;             // rows of `last` allow 32-byte stores
   int e_by_row;             // APPLY: e belongs to rows (wide) or columns (tall)
   float ka, kb_, kc, inv_s2;   // a, b, c / s^2, 1 / s^2
   float inv_s;
@@ -106,33 +113,44 @@ __host__ __device__ inline int64_t or_units(int M, int N, int batches) {
   return batches * (SYM ? tm * (tm + 1) / 2 : tm * tn);
 }
 
-// A lane's 32 values as fp16 at p (64 bytes, 32-byte aligned).
-__device__ __forceinline__ void or_store(unsigned short* p, const float (&v)[32], int dt) {
-#pragma unroll
-  for (int j = 0; j < 32; j += 16)
-    stg32(p + j, pack2(v[j], v[j + 1], dt), pack2(v[j + 2], v[j + 3], dt), pack2(v[j + 4], v[j + 5], dt),
-          pack2(v[j + 6], v[j + 7], dt), pack2(v[j + 8], v[j + 9], dt), pack2(v[j + 10], v[j + 11], dt),
-          pack2(v[j + 12], v[j + 13], dt), pack2(v[j + 14], v[j + 15], dt));
+// A warp's piece in shared memory as a tensor copy of 32 columns reads it: rows of 64
+// bytes, their 16-byte words exchanged by the row (64-byte swizzle).
+__device__ __forceinline__ uint32_t or_at(uint32_t st, int row, int word) {
+  return st + static_cast<uint32_t>(row * 64 + ((word ^ (row >> 1 & 3)) << 4));
 }
-
-// The transpose of a warp's 32 x 32 values (lane = row): p is the place of row 0, column
-// 0 of it, `cols` of its rows exist.  Neighbouring lanes trade one of two columns, so
-// that a lane stores two rows' values of a column at once.
-__device__ __forceinline__ void or_store_mirror(unsigned short* p, int64_t ld, const float (&v)[32], int cols, int lane) {
+__device__ __forceinline__ void or_stage(uint32_t st, const uint4 (&w)[4], int lane) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(or_at(st, lane, j)), "r"(w[j].x), "r"(w[j].y), "r"(w[j].z), "r"(w[j].w)
+                 : "memory");
+}
+// Its transpose.  Neighbouring lanes trade one of two columns, so that a lane writes two
+// rows' values of a column at once.
+__device__ __forceinline__ void or_stage_mirror(uint32_t st, const float (&v)[32], int lane) {
   const int odd = lane & 1;
 #pragma unroll
   for (int j = 0; j < 32; j += 2) {
     const float give = odd ? v[j] : v[j + 1];
     const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 1);
     const uint32_t w = odd ? pack2(got, v[j + 1], DT_FP16) : pack2(v[j], got, DT_FP16);
-    if (j + odd < cols) *reinterpret_cast<uint32_t*>(p + (j + odd) * ld + (lane & ~1)) = w;
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(or_at(st, j + odd, lane >> 3) + static_cast<uint32_t>(lane & 6) * 2), "r"(w) : "memory");
   }
 }
 
-// 32 fp16 values (64 bytes, 16-byte aligned) as four words of eight.
-__device__ __forceinline__ void or_load(const unsigned short* p, uint4 (&w)[4]) {
+__device__ __forceinline__ void or_pack(const float (&v)[32], int dt, uint4 (&w)[4]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) w[j] = reinterpret_cast<const uint4*>(p)[j];
+  for (int j = 0; j < 4; ++j)
+    w[j] = make_uint4(pack2(v[8 * j], v[8 * j + 1], dt), pack2(v[8 * j + 2], v[8 * j + 3], dt),
+                      pack2(v[8 * j + 4], v[8 * j + 5], dt), pack2(v[8 * j + 6], v[8 * j + 7], dt));
+}
+// Half of a piece (hi or lo): a lane's row as four words, those of the lanes side by side.
+__device__ __forceinline__ void or_load(const unsigned short* p, uint4 (&w)[4], int lane) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const uint4*>(p + j * 256 + lane * 8);
+}
+__device__ __forceinline__ void or_save(unsigned short* p, const uint4 (&w)[4], int lane) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(p + j * 256 + lane * 8) = w[j];
 }
 __device__ __forceinline__ float or_value(const uint4 (&w)[4], int j) {
   const uint4& u = w[j / 8];
@@ -277,29 +295,33 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
   } else if (warp >= 4) {
     // ---------------- epilogue ----------------
     const int ew = warp & 3, half = (warp - 4) >> 2;
-    char* st = epi + (warp - 4) * 32 * 80;
+    const uint32_t st = smem_u32(epi + (warp - 4) * 4096);
     uint32_t n = 0;
     for (int u = worker; ok && u < units; u += nworkers, ++n) {
       const OrthoUnit U = or_unit<CG, SYM>(A, u);
       const int buf = n & 1;
-      if (!wait(&accf[buf], (n >> 1) & 1)) break;
-      tm_fence_after();
       const uint32_t tcol = tmem + (static_cast<uint32_t>(ew * 32) << 16) + static_cast<uint32_t>(buf * BN);
       const int row0 = U.m0 + static_cast<int>(rank) * 128 + ew * 32, row = row0 + lane;
       const float* diag = A.diag + U.z * A.step_diag;
       const bool in = row < A.M;
       const float d_row = (MODE == OR_POLY || (MODE == OR_APPLY && A.e_by_row)) && in ? diag[row] : 0.0f;
+      // what a piece needs of its own elements is under way before its accumulators are
+      unsigned short* own = A.own + U.z * A.step_own + (static_cast<int64_t>(row0 >> 5) * A.own_cols + (U.n0 >> 5)) *
+                                                           (MODE == OR_APPLY ? 2048 : 1024);
+      uint4 hi[4], lo[4];
+      auto fetch = [&](int c) {
+        if (MODE == OR_GRAM || row0 >= A.M || U.n0 + c >= A.N) return;
+        const unsigned short* p = own + (c >> 5) * (MODE == OR_APPLY ? 2048 : 1024);
+        or_load(p, hi, lane);
+        if (MODE == OR_APPLY) or_load(p + 1024, lo, lane);
+      };
+      fetch(32 * half);
+      if (!wait(&accf[buf], (n >> 1) & 1)) break;
+      tm_fence_after();
       for (int c = 32 * half; c < BN; c += 64) {
         const int col0 = U.n0 + c;
-        const bool live = row0 < A.M && col0 < A.N;   // (a piece reaches past the last column only into its row's padding)
-        // what the piece needs of memory is under way while the accumulators are read
-        uint4 hi[4], lo[4];
+        const bool live = row0 < A.M && col0 < A.N;
         float dc[32];
-        if (MODE != OR_GRAM && live && in) {
-          const int64_t o = U.z * A.step_x + row * A.ld_x + col0;
-          or_load(A.hi + o, hi);
-          if (MODE == OR_APPLY) or_load(A.lo + o, lo);
-        }
         if ((MODE == OR_POLY || (MODE == OR_APPLY && !A.e_by_row)) && live) {
 #pragma unroll
           for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(dc + j) = *reinterpret_cast<const float4*>(diag + col0 + j);
@@ -318,83 +340,80 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
         }
         if (!live) continue;
         float v[32];
-        if (MODE == OR_GRAM) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-        } else if (MODE == OR_POLY) {
-          if (in) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float o = or_value(hi, j);
-              v[j] = fmaf(A.kb_, o, A.kc * fmaf(o, d_row + dc[j], __uint_as_float(r[j])));
-            }
+        for (int j = 0; j < 32; ++j) {
+          const float acc = __uint_as_float(r[j]);
+          if (MODE == OR_GRAM) {
+            v[j] = acc;
+          } else if (MODE == OR_POLY) {
+            const float o = or_value(hi, j);
+            v[j] = fmaf(A.kb_, o, A.kc * fmaf(o, d_row + dc[j], acc));
           } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-          }
-        } else {
-          if (in) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float e = A.e_by_row ? d_row : dc[j];
-              v[j] = fmaf(A.ka + e, or_value(hi, j), fmaf(A.ka, or_value(lo, j), A.inv_s2 * __uint_as_float(r[j])));
-            }
+            const float e = A.e_by_row ? d_row : dc[j];
+            v[j] = fmaf(A.ka + e, or_value(hi, j), fmaf(A.ka, or_value(lo, j), A.inv_s2 * acc));
           }
         }
-        if (SYM) {
-          if (row0 == col0) {   // the diagonal: kept apart, in fp32
-            float own = 0.0f;
+        if (c + 64 < BN) fetch(c + 64);
+        if (SYM && row0 == col0) {   // the diagonal: kept apart, in fp32
+          float mine = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j == lane) {
-                own = __uint_as_float(r[j]);
-                v[j] = 0.0f;
-              }
-            if (in) {
-              if (MODE == OR_POLY) own = (A.kb_ * d_row + A.kc * fmaf(d_row, d_row, own)) * A.inv_s2;
-              A.diag_out[U.z * A.step_diag + row] = own;
+          for (int j = 0; j < 32; ++j)
+            if (j == lane) {
+              mine = __uint_as_float(r[j]);
+              v[j] = 0.0f;
             }
-          }
-          unsigned short* out = A.out_hi + U.z * A.step_out;
-          if (in) or_store(out + row * A.ld_out + col0, v, DT_FP16);
-          if (U.mirror) or_store_mirror(out + col0 * A.ld_out + row0, A.ld_out, v, A.N - col0, lane);
-        } else if (!A.last) {
           if (in) {
-            const int64_t o = U.z * A.step_out + row * A.ld_out + col0;
-            or_store(A.out_hi + o, v, DT_FP16);
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const uint32_t h = pack2(v[j], v[j + 1], DT_FP16);
-              v[j] -= lo16(h, DT_FP16);
-              v[j + 1] -= hi16(h, DT_FP16);
-            }
-            or_store(A.out_lo + o, v, DT_FP16);
+            if (MODE == OR_POLY) mine = (A.kb_ * d_row + A.kc * fmaf(d_row, d_row, mine)) * A.inv_s2;
+            A.diag_out[U.z * A.step_diag + row] = mine;
           }
-        } else {
-          unsigned short* out = A.last + U.z * A.step_last + col0;
+        }
+        if (MODE == OR_APPLY && A.final) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] *= A.inv_s;
-          if (A.vec_last && col0 + 32 <= A.N) {
-            if (in) or_store(out + row * A.ld_last, v, DT_BF16);
-          } else {
-            // rows that 32-byte stores do not fit: a lane a column, by way of shared memory
-            uint4* w = reinterpret_cast<uint4*>(st + lane * 80);
+        }
+        uint4 w[4];
+        or_pack(v, MODE == OR_APPLY && A.final ? DT_BF16 : DT_FP16, w);
+        unsigned short* piece = own + (c >> 5) * (MODE == OR_APPLY ? 2048 : 1024);
+        if (MODE == OR_GRAM) or_save(piece, w, lane);
+        if (MODE == OR_APPLY && !A.final) {
+          or_save(piece, w, lane);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              w[j] = make_uint4(pack2(v[8 * j], v[8 * j + 1], DT_BF16), pack2(v[8 * j + 2], v[8 * j + 3], DT_BF16),
-                                pack2(v[8 * j + 4], v[8 * j + 5], DT_BF16), pack2(v[8 * j + 6], v[8 * j + 7], DT_BF16));
-            __syncwarp();
-            if (col0 + lane < A.N) {
-              const int rows = min(32, A.M - row0);
+          for (int j = 0; j < 32; ++j) v[j] -= or_value(w, j);
+          uint4 l[4];
+          or_pack(v, DT_FP16, l);
+          or_save(piece + 1024, l, lane);
+        }
+        if (MODE == OR_APPLY && A.final && A.last) {
+          // rows that tensor copies cannot write: a lane a column
+          or_stage(st, w, lane);
+          __syncwarp();
+          if (col0 + lane < A.N) {
+            unsigned short* out = A.last + U.z * A.step_last + row0 * A.ld_last + col0 + lane;
+            const int rows = min(32, A.M - row0);
 #pragma unroll 8
-              for (int i = 0; i < rows; ++i)
-                out[(row0 + i) * A.ld_last + lane] = *reinterpret_cast<const unsigned short*>(st + i * 80 + lane * 2);
+            for (int i = 0; i < rows; ++i) {
+              unsigned short x;
+              asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x) : "r"(or_at(st, i, lane >> 3) + static_cast<uint32_t>(lane & 7) * 2));
+              out[i * A.ld_last] = x;
             }
-            __syncwarp();
           }
+          __syncwarp();
+          continue;
+        }
+        if (lane == 0) tma_store_read();   // the piece before has left shared memory
+        __syncwarp();
+        or_stage(st, w, lane);
+        if (SYM && U.mirror) or_stage_mirror(st + 2048, v, lane);
+        tma_store_fence();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(&A.to, st, col0, row0, U.z);
+          if (SYM && U.mirror) tma_store_3d(&A.to, st + 2048, row0, col0, U.z);
+          tma_store_commit();
         }
       }
     }
+    if (lane == 0) tma_store_done();
   }
   tm_fence_before();
   __syncthreads();
@@ -409,7 +428,7 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
 // the start: X = s G / (|G| + eps)
 // ---------------------------------------------------------------------------
 
-constexpr int OR_NORM_CTAS = 128;   // partial sums of a matrix at most
+constexpr int OR_NORM_CTAS = 608;   // partial sums of a matrix at most
 
 struct OrthoStart {
   const void* g;
@@ -417,8 +436,11 @@ struct OrthoStart {
   int64_t ldg, step_g;
   int M, N, ctas;           // CTAs a matrix
   float* part;              // [matrix][OR_NORM_CTAS][3]
-  unsigned short *hi, *lo;
+  unsigned short* hi;       // X as the tensor copies read it
   int64_t ld_x, step_x;
+  unsigned short* own;      // X as the epilogues do
+  int64_t step_own;
+  int own_cols;
   int vec;                  // elements of a row come eight at a time
   double s, eps;
 };
@@ -446,6 +468,31 @@ __device__ __forceinline__ void or_read(const OrthoStart& A, int64_t at, int lef
     v[j] = j >= left ? 0.0f : A.dt == 2 ? static_cast<const float*>(A.g)[at + j] : ld16(A.g, at + j, A.dt);
 }
 
+// A warp's unit: 8 rows of 32 columns, a lane has 8 of them (row lane / 4).  f(row, column,
+// values) for the units of this CTA in turn, four of them under way at a time.
+template <typename F>
+__device__ __forceinline__ void or_elements(const OrthoStart& A, int z, F&& f) {
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = (lane & 3) * 8;
+  const int cols = (A.N + 31) / 32;
+  const int n = (A.M + 7) / 8 * cols;   // (at most 4096 * 1024)
+  const int step = static_cast<int>(gridDim.x) * 8;
+  for (int u = static_cast<int>(blockIdx.x) * 8 + (threadIdx.x >> 5); u < n; u += 4 * step) {
+    float v[4][8];
+    int row[4], col[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = u + k * step, b = i / cols;
+      row[k] = b * 8 + r;
+      col[k] = (i - b * cols) * 32 + c;
+      if (i >= n || row[k] >= A.M || col[k] >= A.N) row[k] = -1;
+      if (row[k] >= 0) or_read(A, z * A.step_g + row[k] * A.ldg + col[k], A.N - col[k], v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (row[k] >= 0) f(row[k], col[k], v[k]);
+  }
+}
+
 // Squares summed in fp32 in three ranges (of 2^-40 and 2^40), each scaled into the
 // middle: a square of any fp32 value neither overflows nor vanishes.
 __global__ void __launch_bounds__(256) k_ortho_norm(const OrthoStart A) {
@@ -454,13 +501,7 @@ __global__ void __launch_bounds__(256) k_ortho_norm(const OrthoStart A) {
   asm volatile("griddepcontrol.launch_dependents;");
   const int z = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float s[3] = {0.0f, 0.0f, 0.0f};
-  const int q = (A.N + 7) / 8;
-  const int64_t n = static_cast<int64_t>(A.M) * q;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t r = i / q;
-    const int c = static_cast<int>(i - r * q) * 8;
-    float v[8];
-    or_read(A, z * A.step_g + r * A.ldg + c, A.N - c, v);
+  or_elements(A, z, [&](int, int, const float (&v)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float x = fabsf(v[j]);
@@ -472,7 +513,7 @@ __global__ void __launch_bounds__(256) k_ortho_norm(const OrthoStart A) {
         s[1] = fmaf(x, x, s[1]);   // (NaN too)
       }
     }
-  }
+  });
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
 #pragma unroll
@@ -518,13 +559,7 @@ __global__ void __launch_bounds__(256) k_ortho_start(const OrthoStart A) {
   }
   __syncthreads();
   const float f0 = factor[0], f1 = factor[1];
-  const int q = (A.N + 7) / 8;
-  const int64_t n = static_cast<int64_t>(A.M) * q;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t r = i / q;
-    const int c = static_cast<int>(i - r * q) * 8;
-    float v[8];
-    or_read(A, z * A.step_g + r * A.ldg + c, A.N - c, v);
+  or_elements(A, z, [&](int row, int col, const float (&v)[8]) {
     uint32_t h[4], l[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -532,10 +567,13 @@ __global__ void __launch_bounds__(256) k_ortho_start(const OrthoStart A) {
       h[j] = pack2(a, b, DT_FP16);
       l[j] = pack2(a - lo16(h[j], DT_FP16), b - hi16(h[j], DT_FP16), DT_FP16);
     }
-    const int64_t o = z * A.step_x + r * A.ld_x + c;   // (rows are padded to 32 elements)
-    *reinterpret_cast<uint4*>(A.hi + o) = make_uint4(h[0], h[1], h[2], h[3]);
-    *reinterpret_cast<uint4*>(A.lo + o) = make_uint4(l[0], l[1], l[2], l[3]);
-  }
+    const uint4 hw = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(A.hi + z * A.step_x + row * A.ld_x + col) = hw;   // (rows are padded to 32 elements)
+    unsigned short* p = A.own + z * A.step_own + (static_cast<int64_t>(row >> 5) * A.own_cols + (col >> 5)) * 2048 +
+                        ((col >> 3) & 3) * 256 + (row & 31) * 8;
+    *reinterpret_cast<uint4*>(p) = hw;
+    *reinterpret_cast<uint4*>(p + 1024) = make_uint4(l[0], l[1], l[2], l[3]);
+  });
 }
 
 }  // namespace moe_op
