@@ -12,15 +12,22 @@
 using namespace moe_op;
 
 struct moe_ortho : OpHandle {
-  int64_t own_step_x() const { return (cfg.rows + 31) / 32 * (ld_x / 32) * 2048; }
-  int64_t own_step_a() const { return (m + 31) / 32 * (ld_a / 32) * 1024; }
   moe_ortho_config cfg{};
   int m = 0;                        // the smaller side: A and B are [m, m]
   int64_t ld_x = 0, ld_a = 0;       // row strides of X and of A, B
   int q = 0;                        // scale of X: 2^q
+  int workers[3] = {0, 0, 0};       // resident CTAs, and pairs of them, by the CTAs of a tile
   unsigned short *hi[2] = {nullptr, nullptr}, *a = nullptr, *b = nullptr;   // rows, as tensor copies read them
   unsigned short *own_x = nullptr, *own_a = nullptr;   // 32 x 32 pieces, as epilogues do
   float *d = nullptr, *e = nullptr, *sums = nullptr;
+  unsigned* done = nullptr;
+  int* arrived = nullptr;
+  CUtensorMap lx[2], la, lb, sx[2], sa, sb;
+  bool tall() const { return cfg.rows > cfg.cols; }
+  int64_t step_x() const { return cfg.rows * ld_x; }
+  int64_t step_a() const { return m * ld_a; }
+  int64_t step_own_x() const { return (cfg.rows + 31) / 32 * (ld_x / 32) * 2048; }
+  int64_t step_own_a() const { return (m + 31) / 32 * (ld_a / 32) * 1024; }
 };
 
 namespace {
@@ -29,6 +36,8 @@ thread_local std::string g_error;
 
 constexpr int kMaxSide = 32768;
 constexpr int kMaxSteps = 64;
+// counters of split tiles: K is split where all splits run at once
+int arrived_of(int sms) { return 3 * sms * OR_EPI_WARPS; }
 
 // The largest |singular value| and |b l + c l^2| (l its square) that the steps can
 // reach from singular values in [0, 1].  Each step maps [0, top] by p on a grid.
@@ -84,49 +93,61 @@ moe_status validate(const moe_ortho_config* c, std::string* why) {
 
 using Kernel = void (*)(const OrthoArgs);
 
-// of a mode and, for GRAM and APPLY, of tall matrices
-Kernel kernel_of(int mode, bool tall, int cg) {
-  if (mode == OR_POLY) return cg == 2 ? k_ortho<2, false, false, OR_POLY> : k_ortho<1, false, false, OR_POLY>;
-  if (mode == OR_GRAM) {
-    if (tall) return cg == 2 ? k_ortho<2, true, true, OR_GRAM> : k_ortho<1, true, true, OR_GRAM>;
-    return cg == 2 ? k_ortho<2, false, false, OR_GRAM> : k_ortho<1, false, false, OR_GRAM>;
-  }
-  if (tall) return cg == 2 ? k_ortho<2, false, false, OR_APPLY> : k_ortho<1, false, false, OR_APPLY>;
-  return cg == 2 ? k_ortho<2, false, true, OR_APPLY> : k_ortho<1, false, true, OR_APPLY>;
+Kernel kernel_of(int cg, bool tall) {
+  if (tall) return cg == 2 ? k_ortho<2, true> : k_ortho<1, true>;
+  return cg == 2 ? k_ortho<2, false> : k_ortho<1, false>;
 }
 
-// Tiles of 256 x 256 on pairs, or 128 x 128: those with fewer waves.  A 64-wide K block of
-// either takes a CTA as long (its bytes are the same), a wave of pairs does four times
-// the work of a wave's half.
-int group_of(bool sym, int M, int N, int n, int sms) {
-  const int64_t u1 = sym ? or_units<1, true>(M, N, n) : or_units<1, false>(M, N, n);
-  const int64_t u2 = sym ? or_units<2, true>(M, N, n) : or_units<2, false>(M, N, n);
-  return tiles(u2, sms / 2) <= tiles(u1, sms) ? 2 : 1;
-}
+constexpr int kMaxSplit = 16;
 
-cudaError_t launch(moe_ortho* h, int mode, bool tall, OrthoArgs a, int k, const void* pa, int64_t lda, const void* pb, int64_t ldb,
-                   cudaStream_t s, std::string* why) {
-  const bool sym = mode != OR_APPLY;
-  const int cg = group_of(sym, a.M, a.N, a.batches, h->num_sms);
-  const bool amn = mode == OR_GRAM && tall, bmn = (mode == OR_GRAM && tall) || (mode == OR_APPLY && !tall);
-  a.kb = (k + 63) / 64;
-  a.sub = cg == 2 ? 1 : 2;
-  a.stages = OR_MAX_STAGES;
-  while (or_smem_bytes(a.stages, a.sub) > OR_SMEM_MAX) --a.stages;
-  const int64_t xs = h->cfg.rows * h->ld_x, as = h->m * h->ld_a;
-  const bool ok = (amn ? encode_stack16(&a.ta, pa, a.M, k, lda, a.batches, xs, 64, 64)
-                       : encode_stack16(&a.ta, pa, k, a.M, lda, a.batches, mode == OR_GRAM || (mode == OR_APPLY && tall) ? xs : as, 64, 128)) &&
-                  (bmn ? encode_stack16(&a.tb, pb, a.N, k, ldb, a.batches, xs, 64, 64)
-                       : encode_stack16(&a.tb, pb, k, a.N, ldb, a.batches, mode == OR_GRAM ? xs : as, 64, 128));
-  if (!ok) {
-    *why = "tensor map refused";
-    return cudaErrorInvalidValue;
+// How n matrices are taken: CTAs of a tile (1: 128 x 128, 2: 256 x 256) and the K splits of
+// the three products.
+struct Plan {
+  int cg = 1;
+  int ks[3] = {1, 1, 1};
+  double clocks = 1e30;
+  int tiles[3], kb[3];
+  size_t part_bytes(int n) const {
+    size_t t = 0;
+    for (int p = 0; p < 3; ++p)
+      if (ks[p] > 1) t += static_cast<size_t>(n) * tiles[p] * ks[p] * cg * or_part_floats(cg) * 4;
+    return t;
   }
-  const int64_t units = sym ? (cg == 2 ? or_units<2, true>(a.M, a.N, a.batches) : or_units<1, true>(a.M, a.N, a.batches))
-                            : (cg == 2 ? or_units<2, false>(a.M, a.N, a.batches) : or_units<1, false>(a.M, a.N, a.batches));
-  const int64_t workers = std::min<int64_t>(units, h->num_sms / cg);
-  ++h->last_launches;
-  return launch_chained(kernel_of(mode, tall, cg), workers * cg, OR_THREADS, static_cast<size_t>(or_smem_bytes(a.stages, a.sub)), cg, s, a);
+};
+
+// The least estimated time in SM clocks.  A product takes its tiles over the workers (whole
+// rounds of them for one matrix; several matrices' products fill each other's last
+// rounds) times a tile's K blocks (512 clocks, the MMAs of a pair's 256 x 256 x 64 or the
+// bytes of a CTA's 128 x 128 x 64), then the way of its last tile to whoever waits for it;
+// a K split adds its partial sums' way through memory.
+Plan plan_of(const moe_ortho_config& c, int n, const int (&workers)[3]) {
+  Plan best;
+  const int m = std::min(c.rows, c.cols);
+  for (int cg = 1; cg <= 2; ++cg) {
+    Plan p;
+    p.cg = cg;
+    p.clocks = 0.0;
+    const int W = workers[cg];
+    for (int mode = 0; mode < 3; ++mode) {
+      p.tiles[mode] = mode == OR_APPLY ? or_tiles(mode, cg, c.rows, c.cols) : or_tiles(mode, cg, m, m);
+      p.kb[mode] = ((mode == OR_GRAM ? std::max(c.rows, c.cols) : m) + 63) / 64;
+      const double T = static_cast<double>(p.tiles[mode]) * n;
+      double least = 1e30;
+      for (int ks = 1; ks <= kMaxSplit; ++ks) {
+        if (ks > 1 && (T * ks > W || p.kb[mode] / ks < 2)) break;
+        const double rounds = n > 1 ? std::max(1.0, T * ks / W) : std::ceil(T * ks / W);
+        const double t = rounds * ((p.kb[mode] + ks - 1) / ks) * 512.0 + (cg == 2 ? 9000.0 : 6000.0) +
+                         (ks > 1 ? (cg == 2 ? 5000.0 : 2500.0) + ks * 300.0 : 0.0);
+        if (t < least) {
+          least = t;
+          p.ks[mode] = ks;
+        }
+      }
+      p.clocks += least;
+    }
+    if (p.clocks < best.clocks) best = p;
+  }
+  return best;
 }
 
 int64_t span(int64_t n, int64_t step, int64_t rows, int64_t ld, int64_t cols) { return (n - 1) * step + (rows - 1) * ld + cols; }
@@ -157,9 +178,7 @@ moe_status forward(moe_ortho* h, const void* g, int64_t ldg, int64_t step_g, int
   DeviceScope dev(h->device);
   if (!dev.ok) return fail(MOE_ERR_DEVICE, "the handle's device cannot be made current");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool tall = R > C;
   const int m = h->m;
-  const int64_t xs = R * h->ld_x, as = m * h->ld_a, ds = (m + 31) / 32 * 32;
   const double scale = std::ldexp(1.0, h->q);
 
   OrthoStart t{};
@@ -174,13 +193,16 @@ moe_status forward(moe_ortho* h, const void* g, int64_t ldg, int64_t step_g, int
   t.part = h->sums;
   t.hi = h->hi[0];
   t.own = h->own_x;
-  t.step_own = h->own_step_x();
+  t.step_own = h->step_own_x();
   t.own_cols = static_cast<int>(h->ld_x / 32);
   t.ld_x = h->ld_x;
-  t.step_x = xs;
+  t.step_x = h->step_x();
   t.vec = reinterpret_cast<uintptr_t>(g) % 16 == 0 && (R == 1 || ldg * gb % 16 == 0) && step_g * gb % 16 == 0;
   t.s = scale;
   t.eps = c.eps;
+  t.done = h->done;
+  t.arrived = h->arrived;
+  t.n_arrived = arrived_of(h->num_sms);
   cudaError_t e = cudaSuccess;
   std::string why;
   for (int z = 0; z < n && e == cudaSuccess; z += 65535) {   // (a grid's second dimension)
@@ -188,66 +210,92 @@ moe_status forward(moe_ortho* h, const void* g, int64_t ldg, int64_t step_g, int
     OrthoStart p = t;
     p.g = gp + z * step_g * gb;
     p.part += static_cast<int64_t>(z) * OR_NORM_CTAS * 3;
-    p.hi += z * xs;
+    p.hi += z * t.step_x;
     p.own += z * t.step_own;
+    p.done += 3ll * z;
     const dim3 grid(static_cast<unsigned>(t.ctas), static_cast<unsigned>(nz));
     e = launch_chained(k_ortho_norm, grid, 256, 0, 1, s, p);
     if (e == cudaSuccess) e = launch_chained(k_ortho_start, grid, 256, 0, 1, s, p);
     h->last_launches += 2;
   }
 
-  OrthoArgs base{};
-  base.batches = n;
-  base.ka = c.a;
-  base.kb_ = c.b;
-  base.kc = static_cast<float>(c.c / (scale * scale));
-  base.inv_s = static_cast<float>(1.0 / scale);
-  base.inv_s2 = static_cast<float>(1.0 / (scale * scale));
-  base.step_diag = ds;
-  base.status = h->status;
-  // where the epilogues' tensor copies write: pieces of 32 x 32
-  auto rows_of = [&](CUtensorMap* map, const void* p, int64_t cols, int64_t rows, int64_t ld, int64_t step) {
-    if (encode_stack16(map, p, cols, rows, ld, n, step, 32, 32)) return true;
-    why = "tensor map refused";
-    e = cudaErrorInvalidValue;
-    return false;
-  };
-  for (int i = 0; i < c.steps && e == cudaSuccess; ++i) {
-    const unsigned short* x = h->hi[i & 1];
-    OrthoArgs a = base;      // O = X X^T without its diagonal
-    a.M = a.N = m;
-    a.own = h->own_a;
-    a.step_own = h->own_step_a();
-    a.own_cols = static_cast<int>(h->ld_a / 32);
-    a.diag_out = h->d;
-    if (!rows_of(&a.to, h->a, m, m, h->ld_a, as)) break;
-    e = launch(h, OR_GRAM, tall, a, tall ? c.rows : c.cols, x, h->ld_x, x, h->ld_x, s, &why);
-    if (e != cudaSuccess) break;
-    a.diag = h->d;           // P = b A + c A A without its diagonal
-    a.diag_out = h->e;
-    if (!rows_of(&a.to, h->b, m, m, h->ld_a, as)) break;
-    e = launch(h, OR_POLY, tall, a, m, h->a, h->ld_a, h->a, h->ld_a, s, &why);
-    if (e != cudaSuccess) break;
-    a = base;
-    a.M = c.rows;
-    a.N = c.cols;
-    a.own = h->own_x;
-    a.step_own = t.step_own;
-    a.own_cols = t.own_cols;
-    a.diag = h->e;
-    a.e_by_row = !tall;
-    a.final = i + 1 == c.steps;
-    if (!a.final) {
-      if (!rows_of(&a.to, h->hi[(i + 1) & 1], C, R, h->ld_x, xs)) break;
-    } else if (reinterpret_cast<uintptr_t>(out) % 16 == 0 && ldo % 8 == 0 && step_o % 8 == 0) {
-      if (!rows_of(&a.to, out, C, R, ldo, n > 1 ? step_o : (R * ldo + 7) / 8 * 8)) break;
-    } else {
-      a.last = static_cast<unsigned short*>(out);
-      a.ld_last = ldo;
-      a.step_last = step_o;
+  const Plan P = plan_of(c, n, h->workers);
+  OrthoArgs a{};
+  for (int i = 0; i < 2; ++i) {
+    a.lx[i] = h->lx[i];
+    a.sx[i] = h->sx[i];
+  }
+  a.la = h->la;
+  a.lb = h->lb;
+  a.sa = h->sa;
+  a.sb = h->sb;
+  if (reinterpret_cast<uintptr_t>(out) % 16 == 0 && ldo % 8 == 0 && step_o % 8 == 0) {
+    if (e == cudaSuccess && !encode_stack16(&a.out, out, C, R, ldo, n, n > 1 ? step_o : (R * ldo + 7) / 8 * 8, 32, 32)) {
+      why = "tensor map refused";
+      e = cudaErrorInvalidValue;
     }
-    e = tall ? launch(h, OR_APPLY, true, a, m, x, h->ld_x, h->b, h->ld_a, s, &why)
-             : launch(h, OR_APPLY, false, a, m, h->b, h->ld_a, x, h->ld_x, s, &why);
+  } else {
+    a.last = static_cast<unsigned short*>(out);
+    a.ld_last = ldo;
+    a.step_last = step_o;
+  }
+  float* part = h->part;
+  int* arrived = h->arrived;
+  int64_t units = 0;
+  for (int p = 0; p < 3; ++p) {
+    OrthoPhase& f = a.ph[p];
+    f.M = p == OR_APPLY ? c.rows : m;
+    f.N = p == OR_APPLY ? c.cols : m;
+    f.tiles = P.tiles[p];
+    f.kb = P.kb[p];
+    f.ks = P.ks[p];
+    f.units = n * f.tiles * f.ks;
+    units = std::max<int64_t>(units, f.units);
+    f.part = part;
+    f.arrived = arrived;
+    if (f.ks > 1) {
+      part += static_cast<int64_t>(f.units) * P.cg * or_part_floats(P.cg);
+      arrived += n * f.tiles * P.cg * OR_EPI_WARPS;
+    }
+  }
+  a.steps = c.steps;
+  a.sub = P.cg == 2 ? 1 : 2;
+  a.stages = OR_MAX_STAGES;
+  while (or_smem_bytes(a.stages, a.sub) > OR_SMEM_MAX) --a.stages;
+  a.own_a = h->own_a;
+  a.own_x = h->own_x;
+  a.step_own_a = h->step_own_a();
+  a.step_own_x = h->step_own_x();
+  a.cols_a = static_cast<int>(h->ld_a / 32);
+  a.cols_x = static_cast<int>(h->ld_x / 32);
+  a.d = h->d;
+  a.e = h->e;
+  a.step_diag = h->ld_a;
+  a.ka = c.a;
+  a.kb = c.b;
+  a.kc = static_cast<float>(c.c / (scale * scale));
+  a.inv_s = static_cast<float>(1.0 / scale);
+  a.inv_s2 = static_cast<float>(1.0 / (scale * scale));
+  a.done = h->done;
+  a.status = h->status;
+  if (e == cudaSuccess) {
+    // all CTAs resident at once: they wait for one another
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(units, h->workers[P.cg]) * P.cg));
+    cfg.blockDim = dim3(OR_THREADS);
+    cfg.dynamicSmemBytes = static_cast<size_t>(or_smem_bytes(a.stages, a.sub));
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeCooperative;
+    at[0].val.cooperative = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = static_cast<unsigned>(P.cg);
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = P.cg > 1 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kernel_of(P.cg, h->tall()), a);
+    ++h->last_launches;
   }
   if (e != cudaSuccess) {
     h->last_error = why.empty() ? std::string("launch: ") + cudaGetErrorString(e) : why;
@@ -290,19 +338,44 @@ moe_status create(const moe_ortho_config* cfg, moe_ortho** out, moe_ortho*& h) {
   if (e == cudaSuccess) e = cudaMemset(h->status, 0, 64);
   for (unsigned short** p : {&h->hi[0], &h->hi[1]})
     if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(p), x);
-  if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->own_x), n * h->own_step_x() * 2);
-  if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->own_a), n * h->own_step_a() * 2);
+  if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->own_x), n * h->step_own_x() * 2);
+  if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->own_a), n * h->step_own_a() * 2);
   for (unsigned short** p : {&h->a, &h->b})
     if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(p), a);
   for (float** p : {&h->d, &h->e})
     if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(p), n * h->ld_a * 4);
   if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->sums), n * OR_NORM_CTAS * 3 * 4);
-  for (int mode = 0; mode < 3; ++mode)
-    for (int cg = 1; cg <= 2; ++cg)
-      for (int tall = 0; tall < 2; ++tall)
-        if (e == cudaSuccess)
-          e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel_of(mode, tall, cg)),
-                                   cudaFuncAttributeMaxDynamicSharedMemorySize, OR_SMEM_MAX);
+  if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->done), n * 3 * 4);
+  if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->arrived), static_cast<size_t>(arrived_of(sms)) * 4);
+  for (int cg = 1; cg <= 2 && e == cudaSuccess; ++cg) {
+    const Kernel k = kernel_of(cg, h->tall());
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize, OR_SMEM_MAX);
+    if (e != cudaSuccess) break;
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3(static_cast<unsigned>(sms / cg * cg));
+    lc.blockDim = dim3(OR_THREADS);
+    lc.dynamicSmemBytes = OR_SMEM_MAX;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = static_cast<unsigned>(cg);
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    lc.attrs = at;
+    lc.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&h->workers[cg], k, &lc);
+    h->workers[cg] = std::min(h->workers[cg], sms / cg);
+    if (e == cudaSuccess && h->workers[cg] < 1) e = cudaErrorInvalidConfiguration;
+  }
+  for (int i = 1; i <= std::min(c.max_matrices, sms) && e == cudaSuccess; ++i)   // (more matrices: no splits)
+    h->part_bytes = std::max(h->part_bytes, plan_of(c, i, h->workers).part_bytes(i));
+  if (e == cudaSuccess && h->part_bytes) e = h->alloc(reinterpret_cast<void**>(&h->part), h->part_bytes);
+  auto rows_of = [&](CUtensorMap* load, CUtensorMap* store, const void* p, int64_t cols, int64_t rows, int64_t ld) {
+    return encode_stack16(load, p, cols, rows, ld, c.max_matrices, rows * ld, 64, 64) &&
+           encode_stack16(store, p, cols, rows, ld, c.max_matrices, rows * ld, 32, 32);
+  };
+  if (e == cudaSuccess &&
+      !(rows_of(&h->lx[0], &h->sx[0], h->hi[0], c.cols, c.rows, h->ld_x) && rows_of(&h->lx[1], &h->sx[1], h->hi[1], c.cols, c.rows, h->ld_x) &&
+        rows_of(&h->la, &h->sa, h->a, h->m, h->m, h->ld_a) && rows_of(&h->lb, &h->sb, h->b, h->m, h->m, h->ld_a)))
+    e = cudaErrorInvalidValue;
   if (e == cudaSuccess) e = cudaDeviceSynchronize();   // the status word's clear runs on the default stream
   if (e != cudaSuccess) {
     g_error = std::string("create: ") + cudaGetErrorString(e);

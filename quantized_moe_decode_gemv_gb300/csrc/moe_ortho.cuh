@@ -21,10 +21,20 @@
 //     what rounding leaves of X lies in directions that X itself may not have, where p
 //     multiplies by a = 3.4 a step; without lo a gradient of 9 tokens was off by 4e-2.
 //
+// All steps are one launch (k_ortho).  The tiles of all products, (step, product, matrix,
+// tile), are one list that CTAs (pairs, for 256 x 256 tiles) take in turn; a tile waits
+// until the products that it reads are done, by counters of finished epilogues for each
+// matrix and product.  Tiles only wait for tiles before them in the list and all CTAs are
+// resident (a cooperative launch), so somebody always can go on.  As launches of their
+// own, products were 2.1 waves taken as 3 (16 matrices of 1856 x 1024, tiles of 256 x
+// 256 on 76 pairs), and each paid for its launch, its pipeline's filling and its
+// epilogues' end.
+//
 // Roles of a CTA's 12 warps, as in k_gemm16: tensor copies, MMAs, tensor memory, and
-// eight epilogue warps; accumulators double-buffered, CTAs (pairs) persistent.  Tiles are
-// square, CG * 128 on a side; a symmetric product computes those on and below the
-// diagonal and stores the others as their transposes.
+// eight epilogue warps; accumulators double-buffered.  Tiles are square, CG * 128 on a
+// side; a symmetric product computes those on and below the diagonal and stores the
+// others as their transposes.  Where tiles are fewer than CTAs, K is split; the last of a
+// tile's splits to arrive, warp by warp, adds the partial sums in order.
 //
 // An epilogue warp's piece is 32 x 32 values, a row a lane.  Memory that lanes address by
 // their rows is 32 lines an instruction, and that paced the epilogues (17 thousand clocks
@@ -48,24 +58,32 @@ constexpr int OR_EPI_BYTES = OR_EPI_WARPS * 4096;   // a warp's 32 x 32 values a
 constexpr int OR_SMEM_MAX = 227 * 1024;
 enum : int { OR_GRAM = 0, OR_POLY = 1, OR_APPLY = 2 };
 
+// A product of every step: output rows and columns, tiles of a matrix, K blocks and their
+// splits.  (Partial sums have a place for each product: one matrix may be a product ahead
+// of another.)
+struct OrthoPhase {
+  int M, N, tiles, kb, ks, units;   // units: of all matrices
+  float* part;              // [unit][CG][4][BN / 32][32 x 32]: partial sums of a split K
+  int* arrived;             // [tile][CG][8]: splits that have left theirs
+};
+
 struct OrthoArgs {
-  CUtensorMap ta, tb;       // 3-D: columns, rows, matrix
-  int M, N, kb;             // output rows and columns, 64-wide K blocks
-  int batches;
+  CUtensorMap lx[2], la, lb;         // loads (64 x 64): X of even and odd steps, O, P
+  CUtensorMap sx[2], sa, sb, out;    // stores (32 x 32): the same, and the caller's matrices
+  OrthoPhase ph[3];
+  int steps;
   int stages, sub;          // slots of the ring and K blocks a slot
-  CUtensorMap to;           // GRAM: O; POLY: P (B without its diagonal); APPLY: X's hi, or the caller's matrices
-  unsigned short* own;      // pieces of 32 x 32 values: O (GRAM writes, POLY reads), X as hi and lo (APPLY)
-  int64_t step_own;
-  int own_cols;             // pieces in a row of them
-  const float* diag;        // POLY: d; APPLY: e
+  // pieces of 32 x 32 values as epilogues read them: O (written by GRAM, read by POLY), X as hi and lo (APPLY)
+  unsigned short *own_a, *own_x;
+  int64_t step_own_a, step_own_x;
+  int cols_a, cols_x;       // pieces in a row of them
+  float *d, *e;             // the diagonals
   int64_t step_diag;
-  float* diag_out;          // GRAM: d; POLY: e
-  int final;                // APPLY: the last step, whose result is the caller's
   unsigned short* last;     // the caller's bf16 matrices where tensor copies cannot write them, else null
   int64_t ld_last, step_last;
-  int e_by_row;             // APPLY: e belongs to rows (wide) or columns (tall)
-  float ka, kb_, kc, inv_s2;   // a, b, c / s^2, 1 / s^2
+  float ka, kb, kc, inv_s2;   // a, b, c / s^2, 1 / s^2
   float inv_s;
+  unsigned* done;           // [matrix][3]: epilogue warps that have finished a tile of each product
   int* status;
 };
 
@@ -73,23 +91,46 @@ __host__ __device__ inline int or_stage_bytes() { return 2 * 128 * 128; }   // 1
 __host__ __device__ inline int or_smem_bytes(int stages, int sub) {
   return stages * sub * or_stage_bytes() + OR_EPI_BYTES + 8 * (2 * OR_MAX_STAGES + 6) + 1024;
 }
+// Partial sums of a CTA's part of a tile: 128 rows, CG * 128 columns.
+__host__ __device__ constexpr int or_part_floats(int cg) { return 128 * 128 * cg; }
+__host__ __device__ inline int or_tiles(int mode, int cg, int M, int N) {
+  const int tm = (M + cg * 128 - 1) / (cg * 128), tn = (N + cg * 128 - 1) / (cg * 128);
+  return mode == OR_APPLY ? tm * tn : tm * (tm + 1) / 2;
+}
 
 struct OrthoUnit {
-  int z, m0, n0;
+  int mode, step, z, m0, n0, kb0, nkb, ks;
+  int tile;     // of the product, over all matrices
+  int unit;     // the same with its split
   bool mirror;
 };
 
-// Unit u: matrices, then tiles.  Symmetric: tile rows one after the other, each up to
-// the diagonal; else in groups of 8 tile rows, rows fastest.
-template <int CG, bool SYM>
-__device__ __forceinline__ OrthoUnit or_unit(const OrthoArgs& A, int u) {
+// Unit g of the list: steps, products, matrices, tiles, K splits.  Symmetric: tile rows
+// one after the other, each up to the diagonal; else in groups of 8 tile rows, rows fastest.
+template <int CG>
+__device__ __forceinline__ OrthoUnit or_unit(const OrthoArgs& A, int64_t g) {
   constexpr int TS = CG * 128;
-  const int tm = (A.M + TS - 1) / TS, tn = (A.N + TS - 1) / TS;
-  const int tiles = SYM ? tm * (tm + 1) / 2 : tm * tn;
   OrthoUnit U;
-  U.z = u / tiles;
-  int t = u - U.z * tiles;
-  if (SYM) {
+  const int per = A.ph[0].units + A.ph[1].units + A.ph[2].units;
+  U.step = static_cast<int>(g / per);
+  int r = static_cast<int>(g - static_cast<int64_t>(U.step) * per);
+  U.mode = OR_GRAM;
+  if (r >= A.ph[0].units) {
+    r -= A.ph[0].units;
+    U.mode = OR_POLY;
+    if (r >= A.ph[1].units) {
+      r -= A.ph[1].units;
+      U.mode = OR_APPLY;
+    }
+  }
+  const OrthoPhase& P = A.ph[U.mode];
+  U.ks = P.ks;
+  U.unit = r;
+  U.tile = r / P.ks;
+  const int split = r - U.tile * P.ks;
+  U.z = U.tile / P.tiles;
+  int t = U.tile - U.z * P.tiles;
+  if (U.mode != OR_APPLY) {
     int i = static_cast<int>((sqrtf(8.0f * t + 1.0f) - 1.0f) * 0.5f);
     while (i * (i + 1) / 2 > t) --i;
     while ((i + 1) * (i + 2) / 2 <= t) ++i;
@@ -98,19 +139,39 @@ __device__ __forceinline__ OrthoUnit or_unit(const OrthoArgs& A, int u) {
     U.n0 = j * TS;
     U.mirror = i != j;
   } else {
-    const int g = t / (8 * tn), rows = min(8, tm - 8 * g);
-    t -= g * 8 * tn;
-    U.m0 = (8 * g + t % rows) * TS;
+    const int tm = (P.M + TS - 1) / TS, tn = (P.N + TS - 1) / TS;
+    const int gr = t / (8 * tn), rows = min(8, tm - 8 * gr);
+    t -= gr * 8 * tn;
+    U.m0 = (8 * gr + t % rows) * TS;
     U.n0 = (t / rows) * TS;
     U.mirror = false;
   }
+  U.kb0 = split * P.kb / P.ks;
+  U.nkb = (split + 1) * P.kb / P.ks - U.kb0;
   return U;
 }
 
-template <int CG, bool SYM>
-__host__ __device__ inline int64_t or_units(int M, int N, int batches) {
-  const int64_t tm = (M + CG * 128 - 1) / (CG * 128), tn = (N + CG * 128 - 1) / (CG * 128);
-  return batches * (SYM ? tm * (tm + 1) / 2 : tm * tn);
+// The counter that a unit's inputs are done by, and the value it has to reach.
+template <int CG>
+__device__ __forceinline__ const unsigned* or_needs(const OrthoArgs& A, const OrthoUnit& U, unsigned* count) {
+  const int from = U.mode == OR_GRAM ? OR_APPLY : U.mode - 1;
+  const int rounds = U.mode == OR_GRAM ? U.step : U.step + 1;
+  *count = static_cast<unsigned>(rounds) * static_cast<unsigned>(A.ph[from].tiles) * (OR_EPI_WARPS * CG);
+  return A.done + U.z * 3 + from;
+}
+// Bounded wait of a warp until other CTAs have counted so far; what they wrote before is
+// seen by this warp's loads and by tensor copies that it issues.
+__device__ __forceinline__ bool or_wait_count(const unsigned* p, unsigned count) {
+  const long long t0 = clock64();
+  do {
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    if (__all_sync(0xFFFFFFFFu, v >= count)) {
+      asm volatile("fence.proxy.async.global;" ::: "memory");
+      return true;
+    }
+  } while (clock64() - t0 < WAIT_CLOCKS);
+  return false;
 }
 
 // A warp's piece in shared memory as a tensor copy of 32 columns reads it: rows of 64
@@ -158,9 +219,8 @@ __device__ __forceinline__ float or_value(const uint4 (&w)[4], int j) {
   return j & 1 ? hi16(x, DT_FP16) : lo16(x, DT_FP16);
 }
 
-template <int CG, bool AMN, bool BMN, int MODE>
+template <int CG, bool TALL>
 __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__ OrthoArgs A) {
-  constexpr bool SYM = MODE != OR_APPLY;
   constexpr int BN = CG * 128;
   extern __shared__ __align__(1024) char or_smem[];
   char* base = or_smem + ((1024u - (smem_u32(or_smem) & 1023u)) & 1023u);
@@ -173,7 +233,7 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
   const int worker = blockIdx.x / CG, nworkers = gridDim.x / CG;
-  const int units = static_cast<int>(or_units<CG, SYM>(A.M, A.N, A.batches));
+  const int64_t units = static_cast<int64_t>(A.ph[0].units + A.ph[1].units + A.ph[2].units) * A.steps;
   constexpr uint32_t tm_cols = 2 * BN;
 
   if (warp == 2) tm_alloc<CG>(smem_u32(holder), tm_cols);
@@ -194,15 +254,17 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
   if (CG == 2) cluster_sync();
   tm_fence_after();
   const uint32_t tmem = *holder;
-  // everything above may run while the kernel before this one in the stream ends
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
   bool ok = true;
-  auto wait = [&](uint64_t* b, uint32_t parity) {
-    if (bar_wait(smem_u32(b), parity)) return true;
+  auto gave_up = [&] {
     atomicOr(A.status, STATUS_TIMEOUT);
     ok = false;
     return false;
+  };
+  auto wait = [&](uint64_t* b, uint32_t parity) { return bar_wait(smem_u32(b), parity) || gave_up(); };
+  auto wait_inputs = [&](const OrthoUnit& U) {
+    unsigned count;
+    const unsigned* p = or_needs<CG>(A, U, &count);
+    return count == 0 || or_wait_count(p, count) || gave_up();
   };
 
   if (warp == 0) {
@@ -210,11 +272,17 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
     RingPos R;
     bool again = false;   // slots have been used before
     uint32_t q = 0;
-    for (int u = worker; ok && u < units; u += nworkers) {
-      const OrthoUnit U = or_unit<CG, SYM>(A, u);
+    for (int64_t g = worker; ok && g < units; g += nworkers) {
+      const OrthoUnit U = or_unit<CG>(A, g);
       const int am = U.m0 + static_cast<int>(rank) * 128, bn = U.n0 + static_cast<int>(rank) * 128;
-      for (int i = 0; i < A.kb; i += A.sub, ++q) {
-        const int s = R.slot, nk = min(A.sub, A.kb - i);
+      // boxes of 64 x 64: K-major, k across and 64 rows each; MN-major, 64 rows across and k down
+      const CUtensorMap* x = &A.lx[U.step & 1];
+      const CUtensorMap* ma = U.mode == OR_GRAM ? x : U.mode == OR_POLY ? &A.la : TALL ? x : &A.lb;
+      const CUtensorMap* mb = U.mode == OR_GRAM ? x : U.mode == OR_POLY ? &A.la : TALL ? &A.lb : x;
+      const bool amn = TALL && U.mode == OR_GRAM, bmn = TALL ? U.mode == OR_GRAM : U.mode == OR_APPLY;
+      if (!wait_inputs(U)) break;
+      for (int i = 0; i < U.nkb; i += A.sub, ++q) {
+        const int s = R.slot, nk = min(A.sub, U.nkb - i);
         if (again && !wait(&empty[s], R.parity ^ 1u)) break;
         R.next(S);
         again = again || R.slot == 0;
@@ -223,20 +291,12 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
         if (elect_lane()) {
           if (rank == 0) bar_expect_tx(own, static_cast<uint32_t>(CG * stage_bytes * nk));
           for (int j = 0; j < nk; ++j) {
-            const int k0 = (i + j) * 64;
+            const int k0 = (U.kb0 + i + j) * 64;
             const uint32_t da = smem_u32(base + s * slot_bytes + j * stage_bytes), db = da + 128 * 128;
-            if (AMN) {
-              tma_3d<CG>(da, &A.ta, am, k0, U.z, fb);
-              tma_3d<CG>(da + 8192, &A.ta, am + 64, k0, U.z, fb);
-            } else {
-              tma_3d<CG>(da, &A.ta, k0, am, U.z, fb);
-            }
-            if (BMN) {
-              tma_3d<CG>(db, &A.tb, bn, k0, U.z, fb);
-              tma_3d<CG>(db + 8192, &A.tb, bn + 64, k0, U.z, fb);
-            } else {
-              tma_3d<CG>(db, &A.tb, k0, bn, U.z, fb);
-            }
+            tma_3d<CG>(da, ma, amn ? am : k0, amn ? k0 : am, U.z, fb);
+            tma_3d<CG>(da + 8192, ma, amn ? am + 64 : k0, amn ? k0 : am + 64, U.z, fb);
+            tma_3d<CG>(db, mb, bmn ? bn : k0, bmn ? k0 : bn, U.z, fb);
+            tma_3d<CG>(db + 8192, mb, bmn ? bn + 64 : k0, bmn ? k0 : bn + 64, U.z, fb);
           }
         }
         __syncwarp();
@@ -256,28 +316,29 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
   } else if (warp == 1) {
     // ---------------- MMAs (the pair's even CTA) ----------------
     if (rank == 0) {
-      const uint32_t idesc = f16_idesc(CG * 128, BN, DT_FP16, AMN, BMN);
       RingPos R;
       uint32_t n = 0;
-      for (int u = worker; ok && u < units; u += nworkers, ++n) {
+      for (int64_t g = worker; ok && g < units; g += nworkers, ++n) {
+        const OrthoUnit U = or_unit<CG>(A, g);
+        const bool amn = TALL && U.mode == OR_GRAM, bmn = TALL ? U.mode == OR_GRAM : U.mode == OR_APPLY;
+        const uint32_t idesc = f16_idesc(CG * 128, BN, DT_FP16, amn, bmn);
+        const uint32_t la = amn ? 8192 : 16, lb = bmn ? 8192 : 16, ka = amn ? 2048 : 32, kb = bmn ? 2048 : 32;
         const int buf = n & 1;
         if (n >= 2 && !wait(&acce[buf], ((n >> 1) - 1) & 1)) break;
         tm_fence_after();
         const uint32_t d = tmem + static_cast<uint32_t>(buf * BN);
-        for (int i = 0; i < A.kb; i += A.sub) {
-          const int s = R.slot, nk = min(A.sub, A.kb - i);
-          if (!wait(&full[s], R.parity)) break;
+        for (int i = 0; i < U.nkb; i += A.sub) {
+          const int s = R.slot, nk = min(A.sub, U.nkb - i);
+          // (a CTA may have to wait for others between its units: two limits, not one)
+          if (!bar_wait(smem_u32(&full[s]), R.parity) && !wait(&full[s], R.parity)) break;
           R.next(S);
           tm_fence_after();
           if (elect_lane()) {
             for (int j = 0; j < nk; ++j) {
               const uint32_t sa = smem_u32(base + s * slot_bytes + j * stage_bytes), sb = sa + 128 * 128;
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint64_t da = AMN ? sw128_desc(sa + k * 2048, 8192) : sw128_desc(sa + k * 32, 16);
-                const uint64_t db = BMN ? sw128_desc(sb + k * 2048, 8192) : sw128_desc(sb + k * 32, 16);
-                tm_mma<CG>(d, da, db, idesc, (i | j | k) != 0);
-              }
+              for (uint32_t k = 0; k < 4; ++k)
+                tm_mma<CG>(d, sw128_desc(sa + k * ka, la), sw128_desc(sb + k * kb, lb), idesc, (i | j | k) != 0);
             }
             tm_commit<CG>(smem_u32(&empty[s]));
           }
@@ -297,119 +358,176 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
     const int ew = warp & 3, half = (warp - 4) >> 2;
     const uint32_t st = smem_u32(epi + (warp - 4) * 4096);
     uint32_t n = 0;
-    for (int u = worker; ok && u < units; u += nworkers, ++n) {
-      const OrthoUnit U = or_unit<CG, SYM>(A, u);
+    for (int64_t g = worker; ok && g < units; g += nworkers, ++n) {
+      const OrthoUnit U = or_unit<CG>(A, g);
+      const OrthoPhase& P = A.ph[U.mode];
       const int buf = n & 1;
+      const bool apply = U.mode == OR_APPLY, poly = U.mode == OR_POLY, final = apply && U.step + 1 == A.steps;
       const uint32_t tcol = tmem + (static_cast<uint32_t>(ew * 32) << 16) + static_cast<uint32_t>(buf * BN);
       const int row0 = U.m0 + static_cast<int>(rank) * 128 + ew * 32, row = row0 + lane;
-      const float* diag = A.diag + U.z * A.step_diag;
-      const bool in = row < A.M;
-      const float d_row = (MODE == OR_POLY || (MODE == OR_APPLY && A.e_by_row)) && in ? diag[row] : 0.0f;
+      const bool in = row < P.M, rows_live = row0 < P.M;
+      const float* diag = (apply ? A.e : A.d) + U.z * A.step_diag;
+      const int64_t at = static_cast<int64_t>(row0 >> 5) * (apply ? A.cols_x : A.cols_a) + (U.n0 >> 5);
+      unsigned short* own = apply ? A.own_x + U.z * A.step_own_x + at * 2048 : A.own_a + U.z * A.step_own_a + at * 1024;
+      if (!wait_inputs(U)) break;
+      const float d_row = (poly || (apply && !TALL)) && in ? diag[row] : 0.0f;
       // what a piece needs of its own elements is under way before its accumulators are
-      unsigned short* own = A.own + U.z * A.step_own + (static_cast<int64_t>(row0 >> 5) * A.own_cols + (U.n0 >> 5)) *
-                                                           (MODE == OR_APPLY ? 2048 : 1024);
       uint4 hi[4], lo[4];
       auto fetch = [&](int c) {
-        if (MODE == OR_GRAM || row0 >= A.M || U.n0 + c >= A.N) return;
-        const unsigned short* p = own + (c >> 5) * (MODE == OR_APPLY ? 2048 : 1024);
+        if (U.mode == OR_GRAM || !rows_live || U.n0 + c >= P.N) return;
+        const unsigned short* p = own + (c >> 5) * (apply ? 2048 : 1024);
         or_load(p, hi, lane);
-        if (MODE == OR_APPLY) or_load(p + 1024, lo, lane);
+        if (apply) or_load(p + 1024, lo, lane);
       };
       fetch(32 * half);
-      if (!wait(&accf[buf], (n >> 1) & 1)) break;
+      if (!bar_wait(smem_u32(&accf[buf]), (n >> 1) & 1) && !wait(&accf[buf], (n >> 1) & 1)) break;
       tm_fence_after();
-      for (int c = 32 * half; c < BN; c += 64) {
-        const int col0 = U.n0 + c;
-        const bool live = row0 < A.M && col0 < A.N;
-        float dc[32];
-        if ((MODE == OR_POLY || (MODE == OR_APPLY && !A.e_by_row)) && live) {
+      // K split: first this unit's partial sums to memory, then, for the tile's last unit, all of them
+      float* part = P.part + (static_cast<int64_t>(U.unit) * CG + rank) * or_part_floats(CG) + ew * (BN / 32) * 1024 + lane * 4;
+      bool finish = U.ks == 1;
+      for (int round = U.ks == 1 ? 1 : 0; round < 2; ++round) {
+        if (round == 1 && !finish) break;
+        for (int c = 32 * half; c < BN; c += 64) {
+          const int col0 = U.n0 + c;
+          const bool live = rows_live && col0 < P.N;
+          float r[32];
+          if (round == 0 || U.ks == 1) {
+            uint32_t a[32];
+            tm_ld32(tcol + c, a);
+            tm_wait_ld();
+            if (c + 64 >= BN) {
+              // the accumulators are in registers: the buffer may be rewritten
+              tm_fence_before();
+              __syncwarp();
+              if (lane == 0) {
+                if (CG == 2) bar_arrive_cluster(smem_u32(&acce[buf]), 0);
+                else bar_arrive(smem_u32(&acce[buf]));
+              }
+            }
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(dc + j) = *reinterpret_cast<const float4*>(diag + col0 + j);
-        }
-        uint32_t r[32];
-        tm_ld32(tcol + c, r);
-        tm_wait_ld();
-        if (c + 64 >= BN) {
-          // the accumulators are in registers: the buffer may be rewritten
-          tm_fence_before();
+            for (int j = 0; j < 32; ++j) r[j] = __uint_as_float(a[j]);
+          }
+          if (!live) continue;
+          float* mine = part + (c >> 5) * 1024;
+          if (round == 0) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(mine + j * 32) = make_float4(r[j], r[j + 1], r[j + 2], r[j + 3]);
+            continue;
+          }
+          if (U.ks > 1) {
+            const float* p = mine - static_cast<int64_t>(U.unit - U.tile * U.ks) * CG * or_part_floats(CG);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[j] = 0.0f;
+            for (int s = 0; s < U.ks; ++s, p += CG * or_part_floats(CG)) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                const float4 f = __ldcg(reinterpret_cast<const float4*>(p + j * 32));
+                r[j] += f.x, r[j + 1] += f.y, r[j + 2] += f.z, r[j + 3] += f.w;
+              }
+            }
+          }
+          float v[32];
+          if (U.mode == OR_GRAM) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = r[j];
+          } else {
+            float dc[32];
+            if (poly || TALL) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(dc + j) = *reinterpret_cast<const float4*>(diag + col0 + j);
+            }
+            if (poly) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const float o = or_value(hi, j);
+                v[j] = fmaf(A.kb, o, A.kc * fmaf(o, d_row + dc[j], r[j]));
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                v[j] = fmaf(A.ka + (TALL ? dc[j] : d_row), or_value(hi, j), fmaf(A.ka, or_value(lo, j), A.inv_s2 * r[j]));
+            }
+          }
+          if (c + 64 < BN) fetch(c + 64);
+          if (!apply && row0 == col0) {   // the diagonal: kept apart, in fp32
+            float x = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j == lane) {
+                x = r[j];
+                v[j] = 0.0f;
+              }
+            if (in) {
+              if (poly) x = (A.kb * d_row + A.kc * fmaf(d_row, d_row, x)) * A.inv_s2;
+              (poly ? A.e : A.d)[U.z * A.step_diag + row] = x;
+            }
+          }
+          if (final) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] *= A.inv_s;
+          }
+          uint4 w[4];
+          or_pack(v, final ? DT_BF16 : DT_FP16, w);
+          unsigned short* piece = own + (c >> 5) * (apply ? 2048 : 1024);
+          if (U.mode == OR_GRAM) or_save(piece, w, lane);
+          if (apply && !final) {
+            or_save(piece, w, lane);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] -= or_value(w, j);
+            uint4 l[4];
+            or_pack(v, DT_FP16, l);
+            or_save(piece + 1024, l, lane);
+          }
+          if (lane == 0) tma_store_read();   // the piece before has left shared memory
+          __syncwarp();
+          or_stage(st, w, lane);
+          if (U.mirror) or_stage_mirror(st + 2048, v, lane);
+          if (final && A.last) {
+            // rows that tensor copies cannot write: a lane a column
+            __syncwarp();
+            if (col0 + lane < P.N) {
+              unsigned short* out = A.last + U.z * A.step_last + row0 * A.ld_last + col0 + lane;
+              const int rows = min(32, P.M - row0);
+#pragma unroll 8
+              for (int i = 0; i < rows; ++i) {
+                unsigned short x;
+                asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x) : "r"(or_at(st, i, lane >> 3) + static_cast<uint32_t>(lane & 7) * 2));
+                out[i * A.ld_last] = x;
+              }
+            }
+            __syncwarp();
+            continue;
+          }
+          tma_store_fence();
           __syncwarp();
           if (lane == 0) {
-            if (CG == 2) bar_arrive_cluster(smem_u32(&acce[buf]), 0);
-            else bar_arrive(smem_u32(&acce[buf]));
+            const CUtensorMap* to = final ? &A.out : apply ? &A.sx[(U.step + 1) & 1] : poly ? &A.sb : &A.sa;
+            tma_store_3d(to, st, col0, row0, U.z);
+            if (U.mirror) tma_store_3d(to, st + 2048, row0, col0, U.z);
+            tma_store_commit();
           }
         }
-        if (!live) continue;
-        float v[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float acc = __uint_as_float(r[j]);
-          if (MODE == OR_GRAM) {
-            v[j] = acc;
-          } else if (MODE == OR_POLY) {
-            const float o = or_value(hi, j);
-            v[j] = fmaf(A.kb_, o, A.kc * fmaf(o, d_row + dc[j], acc));
-          } else {
-            const float e = A.e_by_row ? d_row : dc[j];
-            v[j] = fmaf(A.ka + e, or_value(hi, j), fmaf(A.ka, or_value(lo, j), A.inv_s2 * acc));
-          }
-        }
-        if (c + 64 < BN) fetch(c + 64);
-        if (SYM && row0 == col0) {   // the diagonal: kept apart, in fp32
-          float mine = 0.0f;
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (j == lane) {
-              mine = __uint_as_float(r[j]);
-              v[j] = 0.0f;
-            }
-          if (in) {
-            if (MODE == OR_POLY) mine = (A.kb_ * d_row + A.kc * fmaf(d_row, d_row, mine)) * A.inv_s2;
-            A.diag_out[U.z * A.step_diag + row] = mine;
-          }
-        }
-        if (MODE == OR_APPLY && A.final) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] *= A.inv_s;
-        }
-        uint4 w[4];
-        or_pack(v, MODE == OR_APPLY && A.final ? DT_BF16 : DT_FP16, w);
-        unsigned short* piece = own + (c >> 5) * (MODE == OR_APPLY ? 2048 : 1024);
-        if (MODE == OR_GRAM) or_save(piece, w, lane);
-        if (MODE == OR_APPLY && !A.final) {
-          or_save(piece, w, lane);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] -= or_value(w, j);
-          uint4 l[4];
-          or_pack(v, DT_FP16, l);
-          or_save(piece + 1024, l, lane);
-        }
-        if (MODE == OR_APPLY && A.final && A.last) {
-          // rows that tensor copies cannot write: a lane a column
-          or_stage(st, w, lane);
+        if (round == 0) {
           __syncwarp();
-          if (col0 + lane < A.N) {
-            unsigned short* out = A.last + U.z * A.step_last + row0 * A.ld_last + col0 + lane;
-            const int rows = min(32, A.M - row0);
-#pragma unroll 8
-            for (int i = 0; i < rows; ++i) {
-              unsigned short x;
-              asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x) : "r"(or_at(st, i, lane >> 3) + static_cast<uint32_t>(lane & 7) * 2));
-              out[i * A.ld_last] = x;
-            }
+          int others = 0;
+          if (lane == 0) {
+            int* count = P.arrived + (U.tile * CG + static_cast<int>(rank)) * OR_EPI_WARPS + warp - 4;
+            __threadfence();
+            others = atomicAdd(count, 1);
+            if (others == U.ks - 1) *count = 0;   // (nobody looks again before this tile's next product)
+            __threadfence();
           }
-          __syncwarp();
-          continue;
+          finish = __shfl_sync(0xFFFFFFFFu, others, 0) == U.ks - 1;
         }
-        if (lane == 0) tma_store_read();   // the piece before has left shared memory
-        __syncwarp();
-        or_stage(st, w, lane);
-        if (SYM && U.mirror) or_stage_mirror(st + 2048, v, lane);
-        tma_store_fence();
+      }
+      if (finish && !final) {
+        // this warp's part of the tile is in memory: stores of its lanes, then tensor copies
         __syncwarp();
         if (lane == 0) {
-          tma_store_3d(&A.to, st, col0, row0, U.z);
-          if (SYM && U.mirror) tma_store_3d(&A.to, st + 2048, row0, col0, U.z);
-          tma_store_commit();
+          tma_store_done();
+          asm volatile("fence.proxy.async.global;" ::: "memory");
+          __threadfence();
+          asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(A.done + U.z * 3 + U.mode) : "memory");
         }
       }
     }
@@ -443,6 +561,9 @@ struct OrthoStart {
   int own_cols;
   int vec;                  // elements of a row come eight at a time
   double s, eps;
+  unsigned* done;           // [matrix][3], cleared
+  int* arrived;             // cleared by the first matrix
+  int n_arrived;
 };
 
 // Up to eight elements from column c of a row (zeros past the last one).
@@ -556,6 +677,11 @@ __global__ void __launch_bounds__(256) k_ortho_start(const OrthoStart A) {
         factor[1] = static_cast<float>(r);
       }
     }
+  }
+  if (blockIdx.x == 0) {
+    if (threadIdx.x < 3) A.done[z * 3 + threadIdx.x] = 0;
+    if (z == 0)
+      for (int i = threadIdx.x; i < A.n_arrived; i += 256) A.arrived[i] = 0;
   }
   __syncthreads();
   const float f0 = factor[0], f1 = factor[1];

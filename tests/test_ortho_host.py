@@ -95,11 +95,22 @@ def test_the_precision_held_is_enough(kind, rows, cols):
 def test_chained_kernels_promise_no_constant_inputs():
     path = os.path.join(os.path.dirname(_capi.__file__), "csrc", "moe_ortho.cuh")
     text = re.sub(r"//[^\n]*", lambda m: m.group(0) if "-----" in m.group(0) else "", open(path).read())
-    kernels = re.split(r"__global__", text)[1:]
-    assert len(kernels) == 3
-    for kernel in kernels:
-        head, body = kernel.split("{", 1)
-        assert "griddepcontrol.wait" in body and "__restrict__" not in head
-    # bounded waits of every role begin after the kernel before has ended
-    body = kernels[0]
-    assert body.index("griddepcontrol.wait") < body.index("tensor copies ----") < body.index("MMAs (") < body.index("epilogue ----")
+    kernels = {re.search(r"\bk_\w+", k).group(0): k.split("{", 1) for k in re.split(r"__global__", text)[1:]}
+    assert set(kernels) == {"k_ortho", "k_ortho_norm", "k_ortho_start"}
+    for name, (head, body) in kernels.items():
+        # (k_ortho is launched after its inputs' kernel has ended, and its CTAs write what others read)
+        assert ("griddepcontrol.wait" in body) == (name != "k_ortho") and "__restrict__" not in head
+
+
+def test_waits_for_other_tiles_come_before_what_they_guard():
+    """Copies and epilogues of a tile begin after the products that it reads are done."""
+    path = os.path.join(os.path.dirname(_capi.__file__), "csrc", "moe_ortho.cuh")
+    text = open(path).read()
+    text = text[text.index("k_ortho(const"):]
+    copies = text[text.index("tensor copies ----"):text.index("MMAs (")]
+    assert copies.index("wait_inputs") < copies.index("tma_3d")
+    epilogue = text[text.index("epilogue ----"):]
+    first = min(epilogue.index(s) for s in ("diag[row]", "or_load(p", "tma_store_3d"))
+    assert epilogue.index("wait_inputs(U)") < first
+    # and a tile counts as done after its stores
+    assert epilogue.index("tma_store_done()") < epilogue.index("red.release.gpu")
