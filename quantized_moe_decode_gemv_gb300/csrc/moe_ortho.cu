@@ -21,7 +21,7 @@ struct moe_ortho : OpHandle {
   unsigned short *own_x = nullptr, *own_a = nullptr;   // 32 x 32 pieces, as epilogues do
   float *d = nullptr, *e = nullptr, *sums = nullptr;
   unsigned* done = nullptr;
-  int* arrived = nullptr;
+  unsigned* arrived = nullptr;
   CUtensorMap lx[2], la, lb, sx[2], sa, sb;
   bool tall() const { return cfg.rows > cfg.cols; }
   int64_t step_x() const { return cfg.rows * ld_x; }
@@ -240,7 +240,7 @@ moe_status forward(moe_ortho* h, const void* g, int64_t ldg, int64_t step_g, int
     a.step_last = step_o;
   }
   float* part = h->part;
-  int* arrived = h->arrived;
+  unsigned* arrived = h->arrived;
   int64_t units = 0;
   for (int p = 0; p < 3; ++p) {
     OrthoPhase& f = a.ph[p];
@@ -259,9 +259,8 @@ moe_status forward(moe_ortho* h, const void* g, int64_t ldg, int64_t step_g, int
     }
   }
   a.steps = c.steps;
-  a.sub = P.cg == 2 ? 1 : 2;
   a.stages = OR_MAX_STAGES;
-  while (or_smem_bytes(a.stages, a.sub) > OR_SMEM_MAX) --a.stages;
+  while (or_smem_bytes(a.stages) > OR_SMEM_MAX) --a.stages;
   a.own_a = h->own_a;
   a.own_x = h->own_x;
   a.step_own_a = h->step_own_a();
@@ -283,7 +282,7 @@ moe_status forward(moe_ortho* h, const void* g, int64_t ldg, int64_t step_g, int
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(units, h->workers[P.cg]) * P.cg));
     cfg.blockDim = dim3(OR_THREADS);
-    cfg.dynamicSmemBytes = static_cast<size_t>(or_smem_bytes(a.stages, a.sub));
+    cfg.dynamicSmemBytes = static_cast<size_t>(or_smem_bytes(a.stages));
     cfg.stream = s;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeCooperative;

@@ -54,7 +54,8 @@ namespace moe_op {
 constexpr int OR_THREADS = 384;
 constexpr int OR_EPI_WARPS = 8;
 constexpr int OR_MAX_STAGES = 8;
-constexpr int OR_EPI_BYTES = OR_EPI_WARPS * 4096;   // a warp's 32 x 32 values and their transpose
+constexpr int OR_EPI_BYTES = OR_EPI_WARPS * 8192;   // a warp's 32 x 32 values and their transpose; hi and lo of its next piece
+constexpr int OR_BARS = 2 * OR_MAX_STAGES + 9 + OR_EPI_WARPS;
 constexpr int OR_SMEM_MAX = 227 * 1024;
 enum : int { OR_GRAM = 0, OR_POLY = 1, OR_APPLY = 2 };
 
@@ -64,7 +65,7 @@ enum : int { OR_GRAM = 0, OR_POLY = 1, OR_APPLY = 2 };
 struct OrthoPhase {
   int M, N, tiles, kb, ks, units;   // units: of all matrices
   float* part;              // [unit][CG][4][BN / 32][32 x 32]: partial sums of a split K
-  int* arrived;             // [tile][CG][8]: splits that have left theirs
+  unsigned* arrived;        // [tile][CG][8]: splits that have left theirs, in all steps so far
 };
 
 struct OrthoArgs {
@@ -72,7 +73,7 @@ struct OrthoArgs {
   CUtensorMap sx[2], sa, sb, out;    // stores (32 x 32): the same, and the caller's matrices
   OrthoPhase ph[3];
   int steps;
-  int stages, sub;          // slots of the ring and K blocks a slot
+  int stages;               // slots of the ring, a K block each
   // pieces of 32 x 32 values as epilogues read them: O (written by GRAM, read by POLY), X as hi and lo (APPLY)
   unsigned short *own_a, *own_x;
   int64_t step_own_a, step_own_x;
@@ -83,14 +84,12 @@ struct OrthoArgs {
   int64_t ld_last, step_last;
   float ka, kb, kc, inv_s2;   // a, b, c / s^2, 1 / s^2
   float inv_s;
-  unsigned* done;           // [matrix][3]: epilogue warps that have finished a tile of each product
+  unsigned* done;           // [matrix][3]: epilogue warps that are through with a unit of each product
   int* status;
 };
 
 __host__ __device__ inline int or_stage_bytes() { return 2 * 128 * 128; }   // 128 rows of A and of B (CG 2: a half of it)
-__host__ __device__ inline int or_smem_bytes(int stages, int sub) {
-  return stages * sub * or_stage_bytes() + OR_EPI_BYTES + 8 * (2 * OR_MAX_STAGES + 6) + 1024;
-}
+__host__ __device__ inline int or_smem_bytes(int stages) { return stages * or_stage_bytes() + OR_EPI_BYTES + 8 * (OR_BARS + 1) + 1024; }
 // Partial sums of a CTA's part of a tile: 128 rows, CG * 128 columns.
 __host__ __device__ constexpr int or_part_floats(int cg) { return 128 * 128 * cg; }
 __host__ __device__ inline int or_tiles(int mode, int cg, int M, int N) {
@@ -99,7 +98,7 @@ __host__ __device__ inline int or_tiles(int mode, int cg, int M, int N) {
 }
 
 struct OrthoUnit {
-  int mode, step, z, m0, n0, kb0, nkb, ks;
+  int mode, step, z, m0, n0, kb0, nkb, ks, split;
   int tile;     // of the product, over all matrices
   int unit;     // the same with its split
   bool mirror;
@@ -127,7 +126,7 @@ __device__ __forceinline__ OrthoUnit or_unit(const OrthoArgs& A, int64_t g) {
   U.ks = P.ks;
   U.unit = r;
   U.tile = r / P.ks;
-  const int split = r - U.tile * P.ks;
+  U.split = r - U.tile * P.ks;
   U.z = U.tile / P.tiles;
   int t = U.tile - U.z * P.tiles;
   if (U.mode != OR_APPLY) {
@@ -146,8 +145,8 @@ __device__ __forceinline__ OrthoUnit or_unit(const OrthoArgs& A, int64_t g) {
     U.n0 = (t / rows) * TS;
     U.mirror = false;
   }
-  U.kb0 = split * P.kb / P.ks;
-  U.nkb = (split + 1) * P.kb / P.ks - U.kb0;
+  U.kb0 = U.split * P.kb / P.ks;
+  U.nkb = (U.split + 1) * P.kb / P.ks - U.kb0;
   return U;
 }
 
@@ -156,7 +155,7 @@ template <int CG>
 __device__ __forceinline__ const unsigned* or_needs(const OrthoArgs& A, const OrthoUnit& U, unsigned* count) {
   const int from = U.mode == OR_GRAM ? OR_APPLY : U.mode - 1;
   const int rounds = U.mode == OR_GRAM ? U.step : U.step + 1;
-  *count = static_cast<unsigned>(rounds) * static_cast<unsigned>(A.ph[from].tiles) * (OR_EPI_WARPS * CG);
+  *count = static_cast<unsigned>(rounds) * static_cast<unsigned>(A.ph[from].tiles * A.ph[from].ks) * (OR_EPI_WARPS * CG);
   return A.done + U.z * 3 + from;
 }
 // Bounded wait of a warp until other CTAs have counted so far; what they wrote before is
@@ -205,9 +204,12 @@ __device__ __forceinline__ void or_pack(const float (&v)[32], int dt, uint4 (&w)
                       pack2(v[8 * j + 4], v[8 * j + 5], dt), pack2(v[8 * j + 6], v[8 * j + 7], dt));
 }
 // Half of a piece (hi or lo): a lane's row as four words, those of the lanes side by side.
-__device__ __forceinline__ void or_load(const unsigned short* p, uint4 (&w)[4], int lane) {
+__device__ __forceinline__ void or_load(uint32_t p, uint4 (&w)[4], int lane) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const uint4*>(p + j * 256 + lane * 8);
+  for (int j = 0; j < 4; ++j)
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[j].x), "=r"(w[j].y), "=r"(w[j].z), "=r"(w[j].w)
+                 : "r"(p + static_cast<uint32_t>(j * 512 + lane * 16)));
 }
 __device__ __forceinline__ void or_save(unsigned short* p, const uint4 (&w)[4], int lane) {
 #pragma unroll
@@ -225,11 +227,12 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
   extern __shared__ __align__(1024) char or_smem[];
   char* base = or_smem + ((1024u - (smem_u32(or_smem) & 1023u)) & 1023u);
   const int S = A.stages;
-  const int stage_bytes = or_stage_bytes(), slot_bytes = A.sub * stage_bytes;
-  char* epi = base + S * slot_bytes;
+  const int stage_bytes = or_stage_bytes();
+  char* epi = base + S * stage_bytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(epi + OR_EPI_BYTES);
-  uint64_t *full = bars, *empty = bars + OR_MAX_STAGES, *accf = bars + 2 * OR_MAX_STAGES, *acce = accf + 2, *drain = acce + 2;
-  uint32_t* holder = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t *full = bars, *empty = bars + OR_MAX_STAGES, *accf = bars + 2 * OR_MAX_STAGES, *acce = accf + 2, *drain = acce + 2,
+           *stored = drain + 1, *piece_in = stored + 4;
+  uint32_t* holder = reinterpret_cast<uint32_t*>(bars + OR_BARS);
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
   const int worker = blockIdx.x / CG, nworkers = gridDim.x / CG;
@@ -247,6 +250,8 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
       bar_init(smem_u32(&acce[b]), OR_EPI_WARPS * CG);
     }
     bar_init(smem_u32(drain), 1);
+    for (int i = 0; i < 4; ++i) bar_init(smem_u32(&stored[i]), OR_EPI_WARPS);
+    for (int i = 0; i < OR_EPI_WARPS; ++i) bar_init(smem_u32(&piece_in[i]), 1);
     bar_fence_init();
   }
   tm_fence_before();
@@ -261,6 +266,8 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
     return false;
   };
   auto wait = [&](uint64_t* b, uint32_t parity) { return bar_wait(smem_u32(b), parity) || gave_up(); };
+  // (a CTA may have to wait for others between its units: two limits, so that the one that waits for them gives up first)
+  auto wait_long = [&](uint64_t* b, uint32_t parity) { return bar_wait(smem_u32(b), parity) || wait(b, parity); };
   auto wait_inputs = [&](const OrthoUnit& U) {
     unsigned count;
     const unsigned* p = or_needs<CG>(A, U, &count);
@@ -281,23 +288,21 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
       const CUtensorMap* mb = U.mode == OR_GRAM ? x : U.mode == OR_POLY ? &A.la : TALL ? &A.lb : x;
       const bool amn = TALL && U.mode == OR_GRAM, bmn = TALL ? U.mode == OR_GRAM : U.mode == OR_APPLY;
       if (!wait_inputs(U)) break;
-      for (int i = 0; i < U.nkb; i += A.sub, ++q) {
-        const int s = R.slot, nk = min(A.sub, U.nkb - i);
+      for (int i = 0; i < U.nkb; ++i, ++q) {
+        const int s = R.slot;
         if (again && !wait(&empty[s], R.parity ^ 1u)) break;
         R.next(S);
         again = again || R.slot == 0;
         // both CTAs' copies complete on the even CTA's barrier
         const uint32_t own = smem_u32(&full[s]), fb = CG == 2 ? cluster_addr(own, 0) : own;
         if (elect_lane()) {
-          if (rank == 0) bar_expect_tx(own, static_cast<uint32_t>(CG * stage_bytes * nk));
-          for (int j = 0; j < nk; ++j) {
-            const int k0 = (U.kb0 + i + j) * 64;
-            const uint32_t da = smem_u32(base + s * slot_bytes + j * stage_bytes), db = da + 128 * 128;
-            tma_3d<CG>(da, ma, amn ? am : k0, amn ? k0 : am, U.z, fb);
-            tma_3d<CG>(da + 8192, ma, amn ? am + 64 : k0, amn ? k0 : am + 64, U.z, fb);
-            tma_3d<CG>(db, mb, bmn ? bn : k0, bmn ? k0 : bn, U.z, fb);
-            tma_3d<CG>(db + 8192, mb, bmn ? bn + 64 : k0, bmn ? k0 : bn + 64, U.z, fb);
-          }
+          if (rank == 0) bar_expect_tx(own, static_cast<uint32_t>(CG * stage_bytes));
+          const int k0 = (U.kb0 + i) * 64;
+          const uint32_t da = smem_u32(base + s * stage_bytes), db = da + 128 * 128;
+          tma_3d<CG>(da, ma, amn ? am : k0, amn ? k0 : am, U.z, fb);
+          tma_3d<CG>(da + 8192, ma, amn ? am + 64 : k0, amn ? k0 : am + 64, U.z, fb);
+          tma_3d<CG>(db, mb, bmn ? bn : k0, bmn ? k0 : bn, U.z, fb);
+          tma_3d<CG>(db + 8192, mb, bmn ? bn + 64 : k0, bmn ? k0 : bn + 64, U.z, fb);
         }
         __syncwarp();
       }
@@ -327,19 +332,16 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
         if (n >= 2 && !wait(&acce[buf], ((n >> 1) - 1) & 1)) break;
         tm_fence_after();
         const uint32_t d = tmem + static_cast<uint32_t>(buf * BN);
-        for (int i = 0; i < U.nkb; i += A.sub) {
-          const int s = R.slot, nk = min(A.sub, U.nkb - i);
-          // (a CTA may have to wait for others between its units: two limits, not one)
-          if (!bar_wait(smem_u32(&full[s]), R.parity) && !wait(&full[s], R.parity)) break;
+        for (int i = 0; i < U.nkb; ++i) {
+          const int s = R.slot;
+          if (!wait_long(&full[s], R.parity)) break;
           R.next(S);
           tm_fence_after();
           if (elect_lane()) {
-            for (int j = 0; j < nk; ++j) {
-              const uint32_t sa = smem_u32(base + s * slot_bytes + j * stage_bytes), sb = sa + 128 * 128;
+            const uint32_t sa = smem_u32(base + s * stage_bytes), sb = sa + 128 * 128;
 #pragma unroll
-              for (uint32_t k = 0; k < 4; ++k)
-                tm_mma<CG>(d, sw128_desc(sa + k * ka, la), sw128_desc(sb + k * kb, lb), idesc, (i | j | k) != 0);
-            }
+            for (uint32_t k = 0; k < 4; ++k)
+              tm_mma<CG>(d, sw128_desc(sa + k * ka, la), sw128_desc(sb + k * kb, lb), idesc, (i | k) != 0);
             tm_commit<CG>(smem_u32(&empty[s]));
           }
           __syncwarp();
@@ -353,11 +355,35 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
         bar_wait(smem_u32(drain), 0);
       }
     }
+  } else if (warp == 3) {
+    // ---------------- counts of finished units, for other CTAs ----------------
+    uint32_t n = 0;
+    for (int64_t g = worker; ok && g < units; g += nworkers, ++n) {
+      const OrthoUnit U = or_unit<CG>(A, g);
+      if (!wait_long(&stored[n & 3], (n >> 2) & 1)) break;
+      if (lane == 0)
+        asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(A.done + U.z * 3 + U.mode), "n"(OR_EPI_WARPS) : "memory");
+      __syncwarp();
+    }
   } else if (warp >= 4) {
     // ---------------- epilogue ----------------
-    const int ew = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t st = smem_u32(epi + (warp - 4) * 4096);
-    uint32_t n = 0;
+    constexpr int NP = BN / 64;   // pieces of a warp
+    const int w8 = warp - 4, ew = warp & 3, half = w8 >> 2;
+    const uint32_t st = smem_u32(epi + w8 * 8192), st_in = st + 4096, in_bar = smem_u32(&piece_in[w8]);
+    uint32_t n = 0, in_parity = 0;
+    // A unit counts as done when its stores are: with the next unit's first piece, unless the
+    // next unit is not there yet.
+    int pending = -1;
+    auto flush = [&](bool all) {
+      if (pending < 0) return;
+      __syncwarp();
+      if (lane == 0) {
+        if (all) tma_store_done<0>();
+        else tma_store_done<1>();
+        bar_arrive(smem_u32(&stored[pending]));
+      }
+      pending = -1;
+    };
     for (int64_t g = worker; ok && g < units; g += nworkers, ++n) {
       const OrthoUnit U = or_unit<CG>(A, g);
       const OrthoPhase& P = A.ph[U.mode];
@@ -369,169 +395,182 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
       const float* diag = (apply ? A.e : A.d) + U.z * A.step_diag;
       const int64_t at = static_cast<int64_t>(row0 >> 5) * (apply ? A.cols_x : A.cols_a) + (U.n0 >> 5);
       unsigned short* own = apply ? A.own_x + U.z * A.step_own_x + at * 2048 : A.own_a + U.z * A.step_own_a + at * 1024;
-      if (!wait_inputs(U)) break;
-      const float d_row = (poly || (apply && !TALL)) && in ? diag[row] : 0.0f;
-      // what a piece needs of its own elements is under way before its accumulators are
-      uint4 hi[4], lo[4];
-      auto fetch = [&](int c) {
-        if (U.mode == OR_GRAM || !rows_live || U.n0 + c >= P.N) return;
-        const unsigned short* p = own + (c >> 5) * (apply ? 2048 : 1024);
-        or_load(p, hi, lane);
-        if (apply) or_load(p + 1024, lo, lane);
+      // pieces that this warp finishes: all of its own, or its split's share
+      auto live = [&](int i) { return rows_live && U.n0 + 32 * half + 64 * i < P.N; };
+      auto takes = [&](int i) { return live(i) && (U.ks == 1 || (w8 * NP + i) % U.ks == U.split); };
+      // what a piece needs of its own elements is on its way before its accumulators are there
+      auto fetch = [&](int i) {
+        if (U.mode == OR_GRAM) return;
+        while (i < NP && !takes(i)) ++i;
+        __syncwarp();   // the piece before has been read
+        if (i < NP && lane == 0) {
+          const uint32_t bytes = apply ? 4096u : 2048u;
+          bar_expect_tx(in_bar, bytes);
+          bulk_load(st_in, own + ((32 * half + 64 * i) >> 5) * (apply ? 2048 : 1024), bytes, in_bar);
+        }
       };
-      fetch(32 * half);
-      if (!bar_wait(smem_u32(&accf[buf]), (n >> 1) & 1) && !wait(&accf[buf], (n >> 1) & 1)) break;
+      if (!__all_sync(0xFFFFFFFFu, bar_over(smem_u32(&accf[buf]), (n >> 1) & 1))) flush(true);
+      if (!wait_inputs(U)) break;
+      fetch(0);
+      const float d_row = (poly || (apply && !TALL)) && in ? diag[row] : 0.0f;
+      float d_col[NP];
+#pragma unroll
+      for (int i = 0; i < NP; ++i) d_col[i] = (poly || (apply && TALL)) && live(i) ? diag[U.n0 + 32 * half + 64 * i + lane] : 0.0f;
+      if (!wait_long(&accf[buf], (n >> 1) & 1)) break;
       tm_fence_after();
-      // K split: first this unit's partial sums to memory, then, for the tile's last unit, all of them
-      float* part = P.part + (static_cast<int64_t>(U.unit) * CG + rank) * or_part_floats(CG) + ew * (BN / 32) * 1024 + lane * 4;
-      bool finish = U.ks == 1;
-      for (int round = U.ks == 1 ? 1 : 0; round < 2; ++round) {
-        if (round == 1 && !finish) break;
-        for (int c = 32 * half; c < BN; c += 64) {
-          const int col0 = U.n0 + c;
-          const bool live = rows_live && col0 < P.N;
-          float r[32];
-          if (round == 0 || U.ks == 1) {
-            uint32_t a[32];
-            tm_ld32(tcol + c, a);
-            tm_wait_ld();
-            if (c + 64 >= BN) {
-              // the accumulators are in registers: the buffer may be rewritten
-              tm_fence_before();
-              __syncwarp();
-              if (lane == 0) {
-                if (CG == 2) bar_arrive_cluster(smem_u32(&acce[buf]), 0);
-                else bar_arrive(smem_u32(&acce[buf]));
-              }
-            }
-#pragma unroll
-            for (int j = 0; j < 32; ++j) r[j] = __uint_as_float(a[j]);
-          }
-          if (!live) continue;
-          float* mine = part + (c >> 5) * 1024;
-          if (round == 0) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(mine + j * 32) = make_float4(r[j], r[j + 1], r[j + 2], r[j + 3]);
-            continue;
-          }
-          if (U.ks > 1) {
-            const float* p = mine - static_cast<int64_t>(U.unit - U.tile * U.ks) * CG * or_part_floats(CG);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) r[j] = 0.0f;
-            for (int s = 0; s < U.ks; ++s, p += CG * or_part_floats(CG)) {
-#pragma unroll
-              for (int j = 0; j < 32; j += 4) {
-                const float4 f = __ldcg(reinterpret_cast<const float4*>(p + j * 32));
-                r[j] += f.x, r[j + 1] += f.y, r[j + 2] += f.z, r[j + 3] += f.w;
-              }
-            }
-          }
-          float v[32];
-          if (U.mode == OR_GRAM) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = r[j];
-          } else {
-            float dc[32];
-            if (poly || TALL) {
-#pragma unroll
-              for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(dc + j) = *reinterpret_cast<const float4*>(diag + col0 + j);
-            }
-            if (poly) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const float o = or_value(hi, j);
-                v[j] = fmaf(A.kb, o, A.kc * fmaf(o, d_row + dc[j], r[j]));
-              }
-            } else {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                v[j] = fmaf(A.ka + (TALL ? dc[j] : d_row), or_value(hi, j), fmaf(A.ka, or_value(lo, j), A.inv_s2 * r[j]));
-            }
-          }
-          if (c + 64 < BN) fetch(c + 64);
-          if (!apply && row0 == col0) {   // the diagonal: kept apart, in fp32
-            float x = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j == lane) {
-                x = r[j];
-                v[j] = 0.0f;
-              }
-            if (in) {
-              if (poly) x = (A.kb * d_row + A.kc * fmaf(d_row, d_row, x)) * A.inv_s2;
-              (poly ? A.e : A.d)[U.z * A.step_diag + row] = x;
-            }
-          }
-          if (final) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] *= A.inv_s;
-          }
-          uint4 w[4];
-          or_pack(v, final ? DT_BF16 : DT_FP16, w);
-          unsigned short* piece = own + (c >> 5) * (apply ? 2048 : 1024);
-          if (U.mode == OR_GRAM) or_save(piece, w, lane);
-          if (apply && !final) {
-            or_save(piece, w, lane);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] -= or_value(w, j);
-            uint4 l[4];
-            or_pack(v, DT_FP16, l);
-            or_save(piece + 1024, l, lane);
-          }
-          if (lane == 0) tma_store_read();   // the piece before has left shared memory
-          __syncwarp();
-          or_stage(st, w, lane);
-          if (U.mirror) or_stage_mirror(st + 2048, v, lane);
-          if (final && A.last) {
-            // rows that tensor copies cannot write: a lane a column
-            __syncwarp();
-            if (col0 + lane < P.N) {
-              unsigned short* out = A.last + U.z * A.step_last + row0 * A.ld_last + col0 + lane;
-              const int rows = min(32, P.M - row0);
-#pragma unroll 8
-              for (int i = 0; i < rows; ++i) {
-                unsigned short x;
-                asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x) : "r"(or_at(st, i, lane >> 3) + static_cast<uint32_t>(lane & 7) * 2));
-                out[i * A.ld_last] = x;
-              }
-            }
-            __syncwarp();
-            continue;
-          }
-          tma_store_fence();
-          __syncwarp();
-          if (lane == 0) {
-            const CUtensorMap* to = final ? &A.out : apply ? &A.sx[(U.step + 1) & 1] : poly ? &A.sb : &A.sa;
-            tma_store_3d(to, st, col0, row0, U.z);
-            if (U.mirror) tma_store_3d(to, st + 2048, row0, col0, U.z);
-            tma_store_commit();
-          }
-        }
-        if (round == 0) {
-          __syncwarp();
-          int others = 0;
-          if (lane == 0) {
-            int* count = P.arrived + (U.tile * CG + static_cast<int>(rank)) * OR_EPI_WARPS + warp - 4;
-            __threadfence();
-            others = atomicAdd(count, 1);
-            if (others == U.ks - 1) *count = 0;   // (nobody looks again before this tile's next product)
-            __threadfence();
-          }
-          finish = __shfl_sync(0xFFFFFFFFu, others, 0) == U.ks - 1;
-        }
-      }
-      if (finish && !final) {
-        // this warp's part of the tile is in memory: stores of its lanes, then tensor copies
+      // the accumulators are in registers: the buffer may be rewritten
+      auto release = [&] {
+        tm_fence_before();
         __syncwarp();
         if (lane == 0) {
-          tma_store_done();
-          asm volatile("fence.proxy.async.global;" ::: "memory");
-          __threadfence();
-          asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(A.done + U.z * 3 + U.mode) : "memory");
+          if (CG == 2) bar_arrive_cluster(smem_u32(&acce[buf]), 0);
+          else bar_arrive(smem_u32(&acce[buf]));
         }
+      };
+      // K split: this unit's partial sums to memory, and a wait for the tile's other splits
+      float* part = P.part + (static_cast<int64_t>(U.unit) * CG + rank) * or_part_floats(CG) + (ew * (BN / 32) + half) * 1024 + lane * 4;
+      if (U.ks > 1) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          uint32_t a[32];
+          tm_ld32(tcol + 32 * half + 64 * i, a);
+          tm_wait_ld();
+          if (i == NP - 1) release();
+          if (live(i))
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) *reinterpret_cast<uint4*>(part + i * 2048 + j * 32) = make_uint4(a[j], a[j + 1], a[j + 2], a[j + 3]);
+        }
+        flush(true);
+        unsigned* count = P.arrived + (U.tile * CG + static_cast<int>(rank)) * OR_EPI_WARPS + w8;
+        __syncwarp();
+        if (lane == 0) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(count) : "memory");
+        __syncwarp();
+        if (!or_wait_count(count, static_cast<unsigned>(U.ks) * static_cast<unsigned>(U.step + 1))) {
+          gave_up();
+          break;
+        }
+        part -= static_cast<int64_t>(U.split) * CG * or_part_floats(CG);   // the first split's
       }
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const int c = 32 * half + 64 * i, col0 = U.n0 + c;
+        float r[32];
+        if (U.ks == 1) {
+          uint32_t a[32];
+          tm_ld32(tcol + c, a);
+          tm_wait_ld();
+          if (i == NP - 1) release();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) r[j] = __uint_as_float(a[j]);
+        }
+        if (!takes(i)) continue;
+        if (U.ks > 1) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) r[j] = 0.0f;
+          const float* p = part + i * 2048;
+#pragma unroll 2
+          for (int s = 0; s < U.ks; ++s, p += CG * or_part_floats(CG)) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(p + j * 32);
+              r[j] += f.x, r[j + 1] += f.y, r[j + 2] += f.z, r[j + 3] += f.w;
+            }
+          }
+        }
+        float v[32];
+        if (U.mode == OR_GRAM) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = r[j];
+        } else {
+          if (!bar_wait(in_bar, in_parity)) {
+            gave_up();
+            break;
+          }
+          in_parity ^= 1u;
+          uint4 hi[4];
+          or_load(st_in, hi, lane);
+          if (poly) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float o = or_value(hi, j);
+              v[j] = fmaf(A.kb, o, A.kc * fmaf(o, d_row + __shfl_sync(0xFFFFFFFFu, d_col[i], j), r[j]));
+            }
+          } else {
+            uint4 lo[4];
+            or_load(st_in + 2048, lo, lane);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float e = TALL ? __shfl_sync(0xFFFFFFFFu, d_col[i], j) : d_row;
+              v[j] = fmaf(A.ka + e, or_value(hi, j), fmaf(A.ka, or_value(lo, j), A.inv_s2 * r[j]));
+            }
+          }
+          fetch(i + 1);
+        }
+        if (!apply && row0 == col0) {   // the diagonal: kept apart, in fp32
+          float x = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (j == lane) {
+              x = r[j];
+              v[j] = 0.0f;
+            }
+          if (in) {
+            if (poly) x = (A.kb * d_row + A.kc * fmaf(d_row, d_row, x)) * A.inv_s2;
+            (poly ? A.e : A.d)[U.z * A.step_diag + row] = x;
+          }
+        }
+        if (final) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] *= A.inv_s;
+        }
+        uint4 w[4];
+        or_pack(v, final ? DT_BF16 : DT_FP16, w);
+        unsigned short* piece = own + (c >> 5) * (apply ? 2048 : 1024);
+        if (U.mode == OR_GRAM) or_save(piece, w, lane);
+        if (lane == 0) tma_store_read();   // the piece before has left shared memory
+        __syncwarp();
+        or_stage(st, w, lane);
+        if (U.mirror) or_stage_mirror(st + 2048, v, lane);
+        if (apply && !final) {
+          or_save(piece, w, lane);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] -= or_value(w, j);
+          uint4 l[4];
+          or_pack(v, DT_FP16, l);
+          or_save(piece + 1024, l, lane);
+        }
+        if (final && A.last) {
+          // rows that tensor copies cannot write: a lane a column
+          __syncwarp();
+          if (col0 + lane < P.N) {
+            unsigned short* out = A.last + U.z * A.step_last + row0 * A.ld_last + col0 + lane;
+            const int rows = min(32, P.M - row0);
+#pragma unroll 8
+            for (int k = 0; k < rows; ++k) {
+              unsigned short x;
+              asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x) : "r"(or_at(st, k, lane >> 3) + static_cast<uint32_t>(lane & 7) * 2));
+              out[k * A.ld_last] = x;
+            }
+          }
+          __syncwarp();
+          continue;
+        }
+        tma_store_fence();
+        __syncwarp();
+        if (lane == 0) {
+          const CUtensorMap* to = final ? &A.out : apply ? &A.sx[(U.step + 1) & 1] : poly ? &A.sb : &A.sa;
+          tma_store_3d(to, st, col0, row0, U.z);
+          if (U.mirror) tma_store_3d(to, st + 2048, row0, col0, U.z);
+          tma_store_commit();
+        }
+        flush(false);   // (the unit before)
+      }
+      if (!ok) break;
+      flush(true);
+      pending = static_cast<int>(n & 3);
     }
-    if (lane == 0) tma_store_done();
+    flush(true);
+    if (lane == 0) tma_store_done<0>();
   }
   tm_fence_before();
   __syncthreads();
@@ -562,7 +601,7 @@ struct OrthoStart {
   int vec;                  // elements of a row come eight at a time
   double s, eps;
   unsigned* done;           // [matrix][3], cleared
-  int* arrived;             // cleared by the first matrix
+  unsigned* arrived;        // cleared by the first matrix
   int n_arrived;
 };
 

@@ -109,8 +109,11 @@ def test_waits_for_other_tiles_come_before_what_they_guard():
     text = text[text.index("k_ortho(const"):]
     copies = text[text.index("tensor copies ----"):text.index("MMAs (")]
     assert copies.index("wait_inputs") < copies.index("tma_3d")
-    epilogue = text[text.index("epilogue ----"):]
-    first = min(epilogue.index(s) for s in ("diag[row]", "or_load(p", "tma_store_3d"))
-    assert epilogue.index("wait_inputs(U)") < first
+    counts, epilogue = text[text.index("counts of finished"):text.index("epilogue ----")], text[text.index("epilogue ----"):]
+    assert epilogue.index("wait_inputs(U)") < min(epilogue.index(s) for s in ("fetch(0)", "diag[row]", "tma_store_3d"))
     # and a tile counts as done after its stores
-    assert epilogue.index("tma_store_done()") < epilogue.index("red.release.gpu")
+    flush = epilogue[epilogue.index("auto flush"):]
+    assert flush.index("tma_store_done<0>()") < flush.index("tma_store_done<1>()") < flush.index("bar_arrive(smem_u32(&stored")
+    assert counts.index("wait_long(&stored") < counts.index("red.release.gpu")
+    # a split's partial sums are added after those of all splits have arrived, which nobody holds up
+    assert epilogue.index("flush(true);\n        unsigned* count") < epilogue.index("or_wait_count(count") < epilogue.index("part -=")
