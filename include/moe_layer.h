@@ -612,8 +612,8 @@ typedef struct moe_ortho moe_ortho;
  * than 2^24 tiles of 128 x 128 in all matrices, coefficients that let a singular value
  * of 0..1 grow above 4 (or |b l + c l^2|, l its square, above 64). */
 moe_status moe_ortho_validate(const moe_ortho_config *cfg);
-/* Create on the current CUDA device: a workspace of about 8 bytes an element of G and
- * 6 an element of G G^T (of the smaller side), for max_matrices of them.  Synchronises the device, so not
+/* Create on the current CUDA device: a workspace of about 6 bytes an element of G and
+ * 4 an element of G G^T (of the smaller side), for max_matrices of them.  Synchronises the device, so not
  * inside a stream capture. */
 moe_status moe_ortho_create(const moe_ortho_config *cfg, moe_ortho **out);
 

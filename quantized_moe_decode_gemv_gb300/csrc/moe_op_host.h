@@ -146,10 +146,8 @@ cudaError_t gemm16_join(const JoinCall& c, cudaStream_t s);
 // outside read as zero.  False when the driver refuses it.  Needs encoder_found().
 bool encode_rows16(CUtensorMap* m, const void* p, int64_t cols, int64_t rows, int64_t ld, int box_rows);
 
-// The same of n matrices `step` elements apart (their number the third coordinate),
-// in boxes of 64 columns (swizzled by 128 bytes) or 32 (by 64).
-bool encode_stack16(CUtensorMap* m, const void* p, int64_t cols, int64_t rows, int64_t ld, int n, int64_t step, int box_cols,
-                    int box_rows);
+// The same of n matrices `step` elements apart (their number the third coordinate).
+bool encode_stack16(CUtensorMap* m, const void* p, int64_t cols, int64_t rows, int64_t ld, int n, int64_t step, int box_rows);
 
 // Whether the driver has a tensor-map encoder (looked up once); false with the reason.
 bool encoder_found(std::string* why);

@@ -18,16 +18,15 @@ struct moe_ortho : OpHandle {
   int q = 0;                        // scale of X: 2^q
   int workers[3] = {0, 0, 0};       // resident CTAs, and pairs of them, by the CTAs of a tile
   unsigned short *hi[2] = {nullptr, nullptr}, *a = nullptr, *b = nullptr;   // rows, as tensor copies read them
-  unsigned short *own_x = nullptr, *own_a = nullptr;   // 32 x 32 pieces, as epilogues do
+  unsigned short* lo = nullptr;     // X's second term in 32 x 32 pieces, as epilogues read it
   float *d = nullptr, *e = nullptr, *sums = nullptr;
   unsigned* done = nullptr;
   unsigned* arrived = nullptr;
-  CUtensorMap lx[2], la, lb, sx[2], sa, sb;
+  CUtensorMap tx[2], ta, tb;
   bool tall() const { return cfg.rows > cfg.cols; }
   int64_t step_x() const { return cfg.rows * ld_x; }
   int64_t step_a() const { return m * ld_a; }
-  int64_t step_own_x() const { return (cfg.rows + 31) / 32 * (ld_x / 32) * 2048; }
-  int64_t step_own_a() const { return (m + 31) / 32 * (ld_a / 32) * 1024; }
+  int64_t step_lo() const { return (cfg.rows + 31) / 32 * (ld_x / 32) * 1024; }
 };
 
 namespace {
@@ -192,9 +191,9 @@ moe_status forward(moe_ortho* h, const void* g, int64_t ldg, int64_t step_g, int
   t.ctas = static_cast<int>(std::min<int64_t>({OR_NORM_CTAS, (pieces + 1023) / 1024, tiles(8ll * h->num_sms, n)}));
   t.part = h->sums;
   t.hi = h->hi[0];
-  t.own = h->own_x;
-  t.step_own = h->step_own_x();
-  t.own_cols = static_cast<int>(h->ld_x / 32);
+  t.lo = h->lo;
+  t.step_lo = h->step_lo();
+  t.cols_lo = static_cast<int>(h->ld_x / 32);
   t.ld_x = h->ld_x;
   t.step_x = h->step_x();
   t.vec = reinterpret_cast<uintptr_t>(g) % 16 == 0 && (R == 1 || ldg * gb % 16 == 0) && step_g * gb % 16 == 0;
@@ -204,14 +203,13 @@ moe_status forward(moe_ortho* h, const void* g, int64_t ldg, int64_t step_g, int
   t.arrived = h->arrived;
   t.n_arrived = arrived_of(h->num_sms);
   cudaError_t e = cudaSuccess;
-  std::string why;
   for (int z = 0; z < n && e == cudaSuccess; z += 65535) {   // (a grid's second dimension)
     const int nz = std::min(n - z, 65535);
     OrthoStart p = t;
     p.g = gp + z * step_g * gb;
     p.part += static_cast<int64_t>(z) * OR_NORM_CTAS * 3;
     p.hi += z * t.step_x;
-    p.own += z * t.step_own;
+    p.lo += z * t.step_lo;
     p.done += 3ll * z;
     const dim3 grid(static_cast<unsigned>(t.ctas), static_cast<unsigned>(nz));
     e = launch_chained(k_ortho_norm, grid, 256, 0, 1, s, p);
@@ -222,23 +220,21 @@ moe_status forward(moe_ortho* h, const void* g, int64_t ldg, int64_t step_g, int
   const Plan P = plan_of(c, n, h->workers);
   OrthoArgs a{};
   for (int i = 0; i < 2; ++i) {
-    a.lx[i] = h->lx[i];
-    a.sx[i] = h->sx[i];
+    a.tx[i] = h->tx[i];
+    a.x[i] = h->hi[i];
   }
-  a.la = h->la;
-  a.lb = h->lb;
-  a.sa = h->sa;
-  a.sb = h->sb;
-  if (reinterpret_cast<uintptr_t>(out) % 16 == 0 && ldo % 8 == 0 && step_o % 8 == 0) {
-    if (e == cudaSuccess && !encode_stack16(&a.out, out, C, R, ldo, n, n > 1 ? step_o : (R * ldo + 7) / 8 * 8, 32, 32)) {
-      why = "tensor map refused";
-      e = cudaErrorInvalidValue;
-    }
-  } else {
-    a.last = static_cast<unsigned short*>(out);
-    a.ld_last = ldo;
-    a.step_last = step_o;
-  }
+  a.ta = h->ta;
+  a.tb = h->tb;
+  a.a = h->a;
+  a.b = h->b;
+  a.ld_x = h->ld_x;
+  a.ld_a = h->ld_a;
+  a.step_x = h->step_x();
+  a.step_a = h->step_a();
+  a.out = static_cast<unsigned short*>(out);
+  a.ld_out = ldo;
+  a.step_out = step_o;
+  a.vec_out = reinterpret_cast<uintptr_t>(out) % 32 == 0 && ldo % 16 == 0 && step_o % 16 == 0;
   float* part = h->part;
   unsigned* arrived = h->arrived;
   int64_t units = 0;
@@ -261,12 +257,9 @@ moe_status forward(moe_ortho* h, const void* g, int64_t ldg, int64_t step_g, int
   a.steps = c.steps;
   a.stages = OR_MAX_STAGES;
   while (or_smem_bytes(a.stages) > OR_SMEM_MAX) --a.stages;
-  a.own_a = h->own_a;
-  a.own_x = h->own_x;
-  a.step_own_a = h->step_own_a();
-  a.step_own_x = h->step_own_x();
-  a.cols_a = static_cast<int>(h->ld_a / 32);
-  a.cols_x = static_cast<int>(h->ld_x / 32);
+  a.lo = h->lo;
+  a.step_lo = t.step_lo;
+  a.cols_lo = t.cols_lo;
   a.d = h->d;
   a.e = h->e;
   a.step_diag = h->ld_a;
@@ -297,7 +290,7 @@ moe_status forward(moe_ortho* h, const void* g, int64_t ldg, int64_t step_g, int
     ++h->last_launches;
   }
   if (e != cudaSuccess) {
-    h->last_error = why.empty() ? std::string("launch: ") + cudaGetErrorString(e) : why;
+    h->last_error = std::string("launch: ") + cudaGetErrorString(e);
     return MOE_ERR_CUDA;
   }
   return MOE_OK;
@@ -337,8 +330,7 @@ moe_status create(const moe_ortho_config* cfg, moe_ortho** out, moe_ortho*& h) {
   if (e == cudaSuccess) e = cudaMemset(h->status, 0, 64);
   for (unsigned short** p : {&h->hi[0], &h->hi[1]})
     if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(p), x);
-  if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->own_x), n * h->step_own_x() * 2);
-  if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->own_a), n * h->step_own_a() * 2);
+  if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->lo), n * h->step_lo() * 2);
   for (unsigned short** p : {&h->a, &h->b})
     if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(p), a);
   for (float** p : {&h->d, &h->e})
@@ -367,13 +359,11 @@ moe_status create(const moe_ortho_config* cfg, moe_ortho** out, moe_ortho*& h) {
   for (int i = 1; i <= std::min(c.max_matrices, sms) && e == cudaSuccess; ++i)   // (more matrices: no splits)
     h->part_bytes = std::max(h->part_bytes, plan_of(c, i, h->workers).part_bytes(i));
   if (e == cudaSuccess && h->part_bytes) e = h->alloc(reinterpret_cast<void**>(&h->part), h->part_bytes);
-  auto rows_of = [&](CUtensorMap* load, CUtensorMap* store, const void* p, int64_t cols, int64_t rows, int64_t ld) {
-    return encode_stack16(load, p, cols, rows, ld, c.max_matrices, rows * ld, 64, 64) &&
-           encode_stack16(store, p, cols, rows, ld, c.max_matrices, rows * ld, 32, 32);
+  auto rows_of = [&](CUtensorMap* map, const void* p, int64_t cols, int64_t rows, int64_t ld) {
+    return encode_stack16(map, p, cols, rows, ld, c.max_matrices, rows * ld, 64);
   };
-  if (e == cudaSuccess &&
-      !(rows_of(&h->lx[0], &h->sx[0], h->hi[0], c.cols, c.rows, h->ld_x) && rows_of(&h->lx[1], &h->sx[1], h->hi[1], c.cols, c.rows, h->ld_x) &&
-        rows_of(&h->la, &h->sa, h->a, h->m, h->m, h->ld_a) && rows_of(&h->lb, &h->sb, h->b, h->m, h->m, h->ld_a)))
+  if (e == cudaSuccess && !(rows_of(&h->tx[0], h->hi[0], c.cols, c.rows, h->ld_x) && rows_of(&h->tx[1], h->hi[1], c.cols, c.rows, h->ld_x) &&
+                            rows_of(&h->ta, h->a, h->m, h->m, h->ld_a) && rows_of(&h->tb, h->b, h->m, h->m, h->ld_a)))
     e = cudaErrorInvalidValue;
   if (e == cudaSuccess) e = cudaDeviceSynchronize();   // the status word's clear runs on the default stream
   if (e != cudaSuccess) {

@@ -32,16 +32,18 @@
 //
 // Roles of a CTA's 12 warps, as in k_gemm16: tensor copies, MMAs, tensor memory, and
 // eight epilogue warps; accumulators double-buffered.  Tiles are square, CG * 128 on a
-// side; a symmetric product computes those on and below the diagonal and stores the
-// others as their transposes.  Where tiles are fewer than CTAs, K is split; the last of a
-// tile's splits to arrive, warp by warp, adds the partial sums in order.
+// side; of a symmetric matrix those on and below the diagonal are computed and stored, and
+// who reads one above it reads its transpose, an MN-major operand instead of a K-major one
+// (both are what a tensor copy makes of rows; the majors are part of each MMA's descriptor).
+// Where tiles are fewer than CTAs, K is split; each split then adds the partial sums, in
+// order, of a share of the tile's pieces.
 //
-// An epilogue warp's piece is 32 x 32 values, a row a lane.  Memory that lanes address by
-// their rows is 32 lines an instruction, and that paced the epilogues (17 thousand clocks
-// for a 256 x 256 tile, more than the MMAs of K = 1024).  So what an epilogue reads of its
-// own element, X for the linear term and O for b A, lies a second time in pieces as lanes
-// read them (16 bytes of 32 lanes side by side), and rows are written by tensor copies
-// from shared memory.
+// An epilogue warp's piece is 32 x 32 values, a row a lane.  What paced the epilogues was
+// what they wrote (all CTAs at once: 6 KB a piece, X twice and symmetric tiles twice, took 8 us
+// for 256 x 256 values, XXX with the 4 and 2 KB of now; its MMAs take 4.3 at K = 1024).
+// So X's hi is its operand's rows and nothing else, its lo lies as lanes read it, and
+// symmetric tiles are stored once.  What a piece reads comes two pieces ahead by the lanes'
+// own asynchronous copies; tensor copies would queue behind those of the ring.
 //
 // Every wait is bounded; a role whose wait runs out sets the timeout bit of the status
 // word and winds down.
@@ -54,8 +56,8 @@ namespace moe_op {
 constexpr int OR_THREADS = 384;
 constexpr int OR_EPI_WARPS = 8;
 constexpr int OR_MAX_STAGES = 8;
-constexpr int OR_EPI_BYTES = OR_EPI_WARPS * 8192;   // a warp's 32 x 32 values and their transpose; hi and lo of its next piece
-constexpr int OR_BARS = 2 * OR_MAX_STAGES + 9 + OR_EPI_WARPS;
+constexpr int OR_EPI_BYTES = OR_EPI_WARPS * 8192;   // hi and lo of a warp's next two pieces
+constexpr int OR_BARS = 2 * OR_MAX_STAGES + 9;
 constexpr int OR_SMEM_MAX = 227 * 1024;
 enum : int { OR_GRAM = 0, OR_POLY = 1, OR_APPLY = 2 };
 
@@ -69,19 +71,20 @@ struct OrthoPhase {
 };
 
 struct OrthoArgs {
-  CUtensorMap lx[2], la, lb;         // loads (64 x 64): X of even and odd steps, O, P
-  CUtensorMap sx[2], sa, sb, out;    // stores (32 x 32): the same, and the caller's matrices
+  CUtensorMap tx[2], ta, tb;         // boxes of 64 x 64: X of even and odd steps, O, P
   OrthoPhase ph[3];
   int steps;
   int stages;               // slots of the ring, a K block each
-  // pieces of 32 x 32 values as epilogues read them: O (written by GRAM, read by POLY), X as hi and lo (APPLY)
-  unsigned short *own_a, *own_x;
-  int64_t step_own_a, step_own_x;
-  int cols_a, cols_x;       // pieces in a row of them
+  unsigned short* lo;       // X's second term in pieces of 32 x 32, a lane's 16-byte words side by side
+  int64_t step_lo;
+  int cols_lo;              // pieces in a row of them
   float *d, *e;             // the diagonals
   int64_t step_diag;
-  unsigned short* last;     // the caller's bf16 matrices where tensor copies cannot write them, else null
-  int64_t ld_last, step_last;
+  unsigned short *x[2], *a, *b;   // the same as rows
+  int64_t ld_x, ld_a, step_x, step_a;
+  unsigned short* out;      // the caller's bf16 matrices
+  int64_t ld_out, step_out;
+  int vec_out;              // their rows take 32-byte stores
   float ka, kb, kc, inv_s2;   // a, b, c / s^2, 1 / s^2
   float inv_s;
   unsigned* done;           // [matrix][3]: epilogue warps that are through with a unit of each product
@@ -101,7 +104,6 @@ struct OrthoUnit {
   int mode, step, z, m0, n0, kb0, nkb, ks, split;
   int tile;     // of the product, over all matrices
   int unit;     // the same with its split
-  bool mirror;
 };
 
 // Unit g of the list: steps, products, matrices, tiles, K splits.  Symmetric: tile rows
@@ -136,18 +138,27 @@ __device__ __forceinline__ OrthoUnit or_unit(const OrthoArgs& A, int64_t g) {
     const int j = t - i * (i + 1) / 2;
     U.m0 = i * TS;
     U.n0 = j * TS;
-    U.mirror = i != j;
   } else {
     const int tm = (P.M + TS - 1) / TS, tn = (P.N + TS - 1) / TS;
     const int gr = t / (8 * tn), rows = min(8, tm - 8 * gr);
     t -= gr * 8 * tn;
     U.m0 = (8 * gr + t % rows) * TS;
     U.n0 = (t / rows) * TS;
-    U.mirror = false;
   }
   U.kb0 = U.split * P.kb / P.ks;
   U.nkb = (U.split + 1) * P.kb / P.ks - U.kb0;
   return U;
+}
+
+// Whether K block k0 of the unit's A or B (TALL: of tall matrices) is an MN-major operand: X where
+// its rows are K, and the tiles of a symmetric matrix that are stored as their transposes.
+template <int CG, bool TALL>
+__device__ __forceinline__ bool or_a_mn(const OrthoUnit& U, int k0) {
+  return U.mode == OR_GRAM ? TALL : (U.mode == OR_POLY || !TALL) && k0 >= U.m0 + CG * 128;
+}
+template <int CG, bool TALL>
+__device__ __forceinline__ bool or_b_mn(const OrthoUnit& U, int k0) {
+  return U.mode == OR_GRAM ? TALL : U.mode == OR_APPLY && !TALL ? true : k0 >= U.n0 + CG * 128;
 }
 
 // The counter that a unit's inputs are done by, and the value it has to reach.
@@ -173,43 +184,46 @@ __device__ __forceinline__ bool or_wait_count(const unsigned* p, unsigned count)
   return false;
 }
 
-// A warp's piece in shared memory as a tensor copy of 32 columns reads it: rows of 64
-// bytes, their 16-byte words exchanged by the row (64-byte swizzle).
-__device__ __forceinline__ uint32_t or_at(uint32_t st, int row, int word) {
-  return st + static_cast<uint32_t>(row * 64 + ((word ^ (row >> 1 & 3)) << 4));
-}
-__device__ __forceinline__ void or_stage(uint32_t st, const uint4 (&w)[4], int lane) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(or_at(st, lane, j)), "r"(w[j].x), "r"(w[j].y), "r"(w[j].z), "r"(w[j].w)
-                 : "memory");
-}
-// Its transpose.  Neighbouring lanes trade one of two columns, so that a lane writes two
-// rows' values of a column at once.
-__device__ __forceinline__ void or_stage_mirror(uint32_t st, const float (&v)[32], int lane) {
-  const int odd = lane & 1;
-#pragma unroll
-  for (int j = 0; j < 32; j += 2) {
-    const float give = odd ? v[j] : v[j + 1];
-    const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 1);
-    const uint32_t w = odd ? pack2(got, v[j + 1], DT_FP16) : pack2(v[j], got, DT_FP16);
-    asm volatile("st.shared.b32 [%0], %1;" ::"r"(or_at(st, j + odd, lane >> 3) + static_cast<uint32_t>(lane & 6) * 2), "r"(w) : "memory");
-  }
-}
-
 __device__ __forceinline__ void or_pack(const float (&v)[32], int dt, uint4 (&w)[4]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     w[j] = make_uint4(pack2(v[8 * j], v[8 * j + 1], dt), pack2(v[8 * j + 2], v[8 * j + 3], dt),
                       pack2(v[8 * j + 4], v[8 * j + 5], dt), pack2(v[8 * j + 6], v[8 * j + 7], dt));
 }
-// Half of a piece (hi or lo): a lane's row as four words, those of the lanes side by side.
+// A lane's row of a piece to global memory: 64 bytes, 32-byte aligned.
+__device__ __forceinline__ void or_store(unsigned short* p, const uint4 (&w)[4]) {
+  stg32(p, w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w);
+  stg32(p + 16, w[2].x, w[2].y, w[2].z, w[2].w, w[3].x, w[3].y, w[3].z, w[3].w);
+}
+// A piece of rows ld apart into shared memory, 16-byte words of a row exchanged by the
+// row so that lanes read their rows without bank conflicts.  Rows from `rows` on are zero.
+__device__ __forceinline__ void or_copy_rows(uint32_t to, const unsigned short* p, int64_t ld, int rows, int lane) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = j * 8 + (lane >> 2), w = lane & 3;
+    copy16(to + static_cast<uint32_t>(r * 64 + ((w ^ (r >> 1 & 3)) << 4)), p + (r < rows ? r * ld : 0) + w * 8, r < rows);
+  }
+}
+__device__ __forceinline__ void or_load_rows(uint32_t p, uint4 (&w)[4], int lane) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[j].x), "=r"(w[j].y), "=r"(w[j].z), "=r"(w[j].w)
+                 : "r"(p + static_cast<uint32_t>(lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)))
+                 : "memory");
+}
+// A piece that lies as lanes read it: each copies, reads and writes its own words.
+__device__ __forceinline__ void or_copy(uint32_t to, const unsigned short* p, int lane) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) copy16(to + static_cast<uint32_t>(j * 512 + lane * 16), p + j * 256 + lane * 8, true);
+}
 __device__ __forceinline__ void or_load(uint32_t p, uint4 (&w)[4], int lane) {
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(w[j].x), "=r"(w[j].y), "=r"(w[j].z), "=r"(w[j].w)
-                 : "r"(p + static_cast<uint32_t>(j * 512 + lane * 16)));
+                 : "r"(p + static_cast<uint32_t>(j * 512 + lane * 16))
+                 : "memory");
 }
 __device__ __forceinline__ void or_save(unsigned short* p, const uint4 (&w)[4], int lane) {
 #pragma unroll
@@ -230,8 +244,7 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
   const int stage_bytes = or_stage_bytes();
   char* epi = base + S * stage_bytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(epi + OR_EPI_BYTES);
-  uint64_t *full = bars, *empty = bars + OR_MAX_STAGES, *accf = bars + 2 * OR_MAX_STAGES, *acce = accf + 2, *drain = acce + 2,
-           *stored = drain + 1, *piece_in = stored + 4;
+  uint64_t *full = bars, *empty = bars + OR_MAX_STAGES, *accf = bars + 2 * OR_MAX_STAGES, *acce = accf + 2, *drain = acce + 2, *stored = drain + 1;
   uint32_t* holder = reinterpret_cast<uint32_t*>(bars + OR_BARS);
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
@@ -251,7 +264,6 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
     }
     bar_init(smem_u32(drain), 1);
     for (int i = 0; i < 4; ++i) bar_init(smem_u32(&stored[i]), OR_EPI_WARPS);
-    for (int i = 0; i < OR_EPI_WARPS; ++i) bar_init(smem_u32(&piece_in[i]), 1);
     bar_fence_init();
   }
   tm_fence_before();
@@ -283,10 +295,9 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
       const OrthoUnit U = or_unit<CG>(A, g);
       const int am = U.m0 + static_cast<int>(rank) * 128, bn = U.n0 + static_cast<int>(rank) * 128;
       // boxes of 64 x 64: K-major, k across and 64 rows each; MN-major, 64 rows across and k down
-      const CUtensorMap* x = &A.lx[U.step & 1];
-      const CUtensorMap* ma = U.mode == OR_GRAM ? x : U.mode == OR_POLY ? &A.la : TALL ? x : &A.lb;
-      const CUtensorMap* mb = U.mode == OR_GRAM ? x : U.mode == OR_POLY ? &A.la : TALL ? &A.lb : x;
-      const bool amn = TALL && U.mode == OR_GRAM, bmn = TALL ? U.mode == OR_GRAM : U.mode == OR_APPLY;
+      const CUtensorMap* x = &A.tx[U.step & 1];
+      const CUtensorMap* ma = U.mode == OR_GRAM ? x : U.mode == OR_POLY ? &A.ta : TALL ? x : &A.tb;
+      const CUtensorMap* mb = U.mode == OR_GRAM ? x : U.mode == OR_POLY ? &A.ta : TALL ? &A.tb : x;
       if (!wait_inputs(U)) break;
       for (int i = 0; i < U.nkb; ++i, ++q) {
         const int s = R.slot;
@@ -298,6 +309,7 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
         if (elect_lane()) {
           if (rank == 0) bar_expect_tx(own, static_cast<uint32_t>(CG * stage_bytes));
           const int k0 = (U.kb0 + i) * 64;
+          const bool amn = or_a_mn<CG, TALL>(U, k0), bmn = or_b_mn<CG, TALL>(U, k0);
           const uint32_t da = smem_u32(base + s * stage_bytes), db = da + 128 * 128;
           tma_3d<CG>(da, ma, amn ? am : k0, amn ? k0 : am, U.z, fb);
           tma_3d<CG>(da + 8192, ma, amn ? am + 64 : k0, amn ? k0 : am + 64, U.z, fb);
@@ -325,15 +337,15 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
       uint32_t n = 0;
       for (int64_t g = worker; ok && g < units; g += nworkers, ++n) {
         const OrthoUnit U = or_unit<CG>(A, g);
-        const bool amn = TALL && U.mode == OR_GRAM, bmn = TALL ? U.mode == OR_GRAM : U.mode == OR_APPLY;
-        const uint32_t idesc = f16_idesc(CG * 128, BN, DT_FP16, amn, bmn);
-        const uint32_t la = amn ? 8192 : 16, lb = bmn ? 8192 : 16, ka = amn ? 2048 : 32, kb = bmn ? 2048 : 32;
         const int buf = n & 1;
         if (n >= 2 && !wait(&acce[buf], ((n >> 1) - 1) & 1)) break;
         tm_fence_after();
         const uint32_t d = tmem + static_cast<uint32_t>(buf * BN);
         for (int i = 0; i < U.nkb; ++i) {
-          const int s = R.slot;
+          const int s = R.slot, k0 = (U.kb0 + i) * 64;
+          const bool amn = or_a_mn<CG, TALL>(U, k0), bmn = or_b_mn<CG, TALL>(U, k0);
+          const uint32_t idesc = f16_idesc(CG * 128, BN, DT_FP16, amn, bmn);
+          const uint32_t la = amn ? 8192 : 16, lb = bmn ? 8192 : 16, ka = amn ? 2048 : 32, kb = bmn ? 2048 : 32;
           if (!wait_long(&full[s], R.parity)) break;
           R.next(S);
           tm_fence_after();
@@ -369,21 +381,8 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
     // ---------------- epilogue ----------------
     constexpr int NP = BN / 64;   // pieces of a warp
     const int w8 = warp - 4, ew = warp & 3, half = w8 >> 2;
-    const uint32_t st = smem_u32(epi + w8 * 8192), st_in = st + 4096, in_bar = smem_u32(&piece_in[w8]);
-    uint32_t n = 0, in_parity = 0;
-    // A unit counts as done when its stores are: with the next unit's first piece, unless the
-    // next unit is not there yet.
-    int pending = -1;
-    auto flush = [&](bool all) {
-      if (pending < 0) return;
-      __syncwarp();
-      if (lane == 0) {
-        if (all) tma_store_done<0>();
-        else tma_store_done<1>();
-        bar_arrive(smem_u32(&stored[pending]));
-      }
-      pending = -1;
-    };
+    const uint32_t st = smem_u32(epi + w8 * 8192);
+    uint32_t n = 0;
     for (int64_t g = worker; ok && g < units; g += nworkers, ++n) {
       const OrthoUnit U = or_unit<CG>(A, g);
       const OrthoPhase& P = A.ph[U.mode];
@@ -393,29 +392,27 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
       const int row0 = U.m0 + static_cast<int>(rank) * 128 + ew * 32, row = row0 + lane;
       const bool in = row < P.M, rows_live = row0 < P.M;
       const float* diag = (apply ? A.e : A.d) + U.z * A.step_diag;
-      const int64_t at = static_cast<int64_t>(row0 >> 5) * (apply ? A.cols_x : A.cols_a) + (U.n0 >> 5);
-      unsigned short* own = apply ? A.own_x + U.z * A.step_own_x + at * 2048 : A.own_a + U.z * A.step_own_a + at * 1024;
+      // the piece's own rows of X (apply: read, and written for the next step), of O (read by poly, written by gram) and of P
+      const int64_t at_x = U.z * A.step_x + row0 * A.ld_x, at_a = U.z * A.step_a + row0 * A.ld_a;
+      const unsigned short* from = apply ? A.x[U.step & 1] + at_x : A.a + at_a;
+      unsigned short* lo_pieces = A.lo + U.z * A.step_lo + (static_cast<int64_t>(row0 >> 5) * A.cols_lo + (U.n0 >> 5)) * 1024;
       // pieces that this warp finishes: all of its own, or its split's share
       auto live = [&](int i) { return rows_live && U.n0 + 32 * half + 64 * i < P.N; };
       auto takes = [&](int i) { return live(i) && (U.ks == 1 || (w8 * NP + i) % U.ks == U.split); };
-      // what a piece needs of its own elements is on its way before its accumulators are there
+      // what a piece needs of its own elements, into the buffer of its number's parity
       auto fetch = [&](int i) {
-        if (U.mode == OR_GRAM) return;
-        while (i < NP && !takes(i)) ++i;
-        __syncwarp();   // the piece before has been read
-        if (i < NP && lane == 0) {
-          const uint32_t bytes = apply ? 4096u : 2048u;
-          bar_expect_tx(in_bar, bytes);
-          bulk_load(st_in, own + ((32 * half + 64 * i) >> 5) * (apply ? 2048 : 1024), bytes, in_bar);
+        if (i < NP && U.mode != OR_GRAM && takes(i)) {
+          or_copy_rows(st + (i & 1) * 4096, from + U.n0 + 32 * half + 64 * i, apply ? A.ld_x : A.ld_a, P.M - row0, lane);
+          if (apply) or_copy(st + (i & 1) * 4096 + 2048, lo_pieces + half * 1024 + i * 2048, lane);
         }
+        copies_commit();
       };
-      if (!__all_sync(0xFFFFFFFFu, bar_over(smem_u32(&accf[buf]), (n >> 1) & 1))) flush(true);
       if (!wait_inputs(U)) break;
       fetch(0);
+      fetch(1);
       const float d_row = (poly || (apply && !TALL)) && in ? diag[row] : 0.0f;
-      float d_col[NP];
-#pragma unroll
-      for (int i = 0; i < NP; ++i) d_col[i] = (poly || (apply && TALL)) && live(i) ? diag[U.n0 + 32 * half + 64 * i + lane] : 0.0f;
+      auto col_diag = [&](int i) { return (poly || (apply && TALL)) && i < NP && live(i) ? diag[U.n0 + 32 * half + 64 * i + lane] : 0.0f; };
+      float d_next = col_diag(0);
       if (!wait_long(&accf[buf], (n >> 1) & 1)) break;
       tm_fence_after();
       // the accumulators are in registers: the buffer may be rewritten
@@ -430,7 +427,7 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
       // K split: this unit's partial sums to memory, and a wait for the tile's other splits
       float* part = P.part + (static_cast<int64_t>(U.unit) * CG + rank) * or_part_floats(CG) + (ew * (BN / 32) + half) * 1024 + lane * 4;
       if (U.ks > 1) {
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < NP; ++i) {
           uint32_t a[32];
           tm_ld32(tcol + 32 * half + 64 * i, a);
@@ -440,7 +437,6 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
 #pragma unroll
             for (int j = 0; j < 32; j += 4) *reinterpret_cast<uint4*>(part + i * 2048 + j * 32) = make_uint4(a[j], a[j + 1], a[j + 2], a[j + 3]);
         }
-        flush(true);
         unsigned* count = P.arrived + (U.tile * CG + static_cast<int>(rank)) * OR_EPI_WARPS + w8;
         __syncwarp();
         if (lane == 0) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(count) : "memory");
@@ -451,9 +447,12 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
         }
         part -= static_cast<int64_t>(U.split) * CG * or_part_floats(CG);   // the first split's
       }
-#pragma unroll
+      // (not unrolled: the code of every piece and product once is what fits the instruction cache)
+#pragma unroll 1
       for (int i = 0; i < NP; ++i) {
         const int c = 32 * half + 64 * i, col0 = U.n0 + c;
+        const float d_col = d_next;
+        d_next = col_diag(i + 1);
         float r[32];
         if (U.ks == 1) {
           uint32_t a[32];
@@ -463,7 +462,10 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
 #pragma unroll
           for (int j = 0; j < 32; ++j) r[j] = __uint_as_float(a[j]);
         }
-        if (!takes(i)) continue;
+        if (!takes(i)) {
+          fetch(i + 2);
+          continue;
+        }
         if (U.ks > 1) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) r[j] = 0.0f;
@@ -472,7 +474,7 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
           for (int s = 0; s < U.ks; ++s, p += CG * or_part_floats(CG)) {
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(p + j * 32);
+              const float4 f = __ldcg(reinterpret_cast<const float4*>(p + j * 32));
               r[j] += f.x, r[j + 1] += f.y, r[j + 2] += f.z, r[j + 3] += f.w;
             }
           }
@@ -482,29 +484,26 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = r[j];
         } else {
-          if (!bar_wait(in_bar, in_parity)) {
-            gave_up();
-            break;
-          }
-          in_parity ^= 1u;
+          copies_wait_n<1>();
+          __syncwarp();
+          const uint32_t mine = st + (i & 1) * 4096;
           uint4 hi[4];
-          or_load(st_in, hi, lane);
+          or_load_rows(mine, hi, lane);
           if (poly) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               const float o = or_value(hi, j);
-              v[j] = fmaf(A.kb, o, A.kc * fmaf(o, d_row + __shfl_sync(0xFFFFFFFFu, d_col[i], j), r[j]));
+              v[j] = fmaf(A.kb, o, A.kc * fmaf(o, d_row + __shfl_sync(0xFFFFFFFFu, d_col, j), r[j]));
             }
           } else {
             uint4 lo[4];
-            or_load(st_in + 2048, lo, lane);
+            or_load(mine + 2048, lo, lane);
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-              const float e = TALL ? __shfl_sync(0xFFFFFFFFu, d_col[i], j) : d_row;
+              const float e = TALL ? __shfl_sync(0xFFFFFFFFu, d_col, j) : d_row;
               v[j] = fmaf(A.ka + e, or_value(hi, j), fmaf(A.ka, or_value(lo, j), A.inv_s2 * r[j]));
             }
           }
-          fetch(i + 1);
         }
         if (!apply && row0 == col0) {   // the diagonal: kept apart, in fp32
           float x = 0.0f;
@@ -523,54 +522,53 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] *= A.inv_s;
         }
+        // (the caller's rows that 32-byte stores do not fit go by way of this piece's buffer)
+        const bool staged = final && !(A.vec_out && col0 + 32 <= P.N);
+        if (!staged) {
+          __syncwarp();   // this piece's buffer has been read
+          fetch(i + 2);
+        }
         uint4 w[4];
         or_pack(v, final ? DT_BF16 : DT_FP16, w);
-        unsigned short* piece = own + (c >> 5) * (apply ? 2048 : 1024);
-        if (U.mode == OR_GRAM) or_save(piece, w, lane);
-        if (lane == 0) tma_store_read();   // the piece before has left shared memory
-        __syncwarp();
-        or_stage(st, w, lane);
-        if (U.mirror) or_stage_mirror(st + 2048, v, lane);
-        if (apply && !final) {
-          or_save(piece, w, lane);
+        if (!apply) {
+          if (in) or_store((poly ? A.b : A.a) + at_a + lane * A.ld_a + col0, w);
+        } else if (!final) {
+          if (in) or_store(A.x[(U.step + 1) & 1] + at_x + lane * A.ld_x + col0, w);
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] -= or_value(w, j);
-          uint4 l[4];
-          or_pack(v, DT_FP16, l);
-          or_save(piece + 1024, l, lane);
-        }
-        if (final && A.last) {
-          // rows that tensor copies cannot write: a lane a column
+          or_pack(v, DT_FP16, w);
+          or_save(lo_pieces + half * 1024 + i * 2048, w, lane);
+        } else if (!staged) {
+          if (in) or_store(A.out + U.z * A.step_out + row * A.ld_out + col0, w);
+        } else {
+          const uint32_t mine = st + (i & 1) * 4096;
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(mine + static_cast<uint32_t>(lane * 80 + j * 16)), "r"(w[j].x),
+                         "r"(w[j].y), "r"(w[j].z), "r"(w[j].w)
+                         : "memory");
           __syncwarp();
           if (col0 + lane < P.N) {
-            unsigned short* out = A.last + U.z * A.step_last + row0 * A.ld_last + col0 + lane;
+            unsigned short* out = A.out + U.z * A.step_out + row0 * A.ld_out + col0 + lane;
             const int rows = min(32, P.M - row0);
 #pragma unroll 8
             for (int k = 0; k < rows; ++k) {
               unsigned short x;
-              asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x) : "r"(or_at(st, k, lane >> 3) + static_cast<uint32_t>(lane & 7) * 2));
-              out[k * A.ld_last] = x;
+              asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x) : "r"(mine + static_cast<uint32_t>(k * 80 + lane * 2)) : "memory");
+              out[k * A.ld_out] = x;
             }
           }
           __syncwarp();
-          continue;
+          fetch(i + 2);
         }
-        tma_store_fence();
-        __syncwarp();
-        if (lane == 0) {
-          const CUtensorMap* to = final ? &A.out : apply ? &A.sx[(U.step + 1) & 1] : poly ? &A.sb : &A.sa;
-          tma_store_3d(to, st, col0, row0, U.z);
-          if (U.mirror) tma_store_3d(to, st + 2048, row0, col0, U.z);
-          tma_store_commit();
-        }
-        flush(false);   // (the unit before)
       }
-      if (!ok) break;
-      flush(true);
-      pending = static_cast<int>(n & 3);
+      // this warp's part is on its way to memory: tensor copies of other CTAs may read it
+      // once warp 3 has said so
+      asm volatile("fence.proxy.async.global;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) bar_arrive(smem_u32(&stored[n & 3]));
     }
-    flush(true);
-    if (lane == 0) tma_store_done<0>();
   }
   tm_fence_before();
   __syncthreads();
@@ -595,9 +593,9 @@ struct OrthoStart {
   float* part;              // [matrix][OR_NORM_CTAS][3]
   unsigned short* hi;       // X as the tensor copies read it
   int64_t ld_x, step_x;
-  unsigned short* own;      // X as the epilogues do
-  int64_t step_own;
-  int own_cols;
+  unsigned short* lo;       // and its second term, in pieces
+  int64_t step_lo;
+  int cols_lo;
   int vec;                  // elements of a row come eight at a time
   double s, eps;
   unsigned* done;           // [matrix][3], cleared
@@ -732,12 +730,10 @@ __global__ void __launch_bounds__(256) k_ortho_start(const OrthoStart A) {
       h[j] = pack2(a, b, DT_FP16);
       l[j] = pack2(a - lo16(h[j], DT_FP16), b - hi16(h[j], DT_FP16), DT_FP16);
     }
-    const uint4 hw = make_uint4(h[0], h[1], h[2], h[3]);
-    *reinterpret_cast<uint4*>(A.hi + z * A.step_x + row * A.ld_x + col) = hw;   // (rows are padded to 32 elements)
-    unsigned short* p = A.own + z * A.step_own + (static_cast<int64_t>(row >> 5) * A.own_cols + (col >> 5)) * 2048 +
+    *reinterpret_cast<uint4*>(A.hi + z * A.step_x + row * A.ld_x + col) = make_uint4(h[0], h[1], h[2], h[3]);   // (rows are padded to 32 elements)
+    unsigned short* p = A.lo + z * A.step_lo + (static_cast<int64_t>(row >> 5) * A.cols_lo + (col >> 5)) * 1024 +
                         ((col >> 3) & 3) * 256 + (row & 31) * 8;
-    *reinterpret_cast<uint4*>(p) = hw;
-    *reinterpret_cast<uint4*>(p + 1024) = make_uint4(l[0], l[1], l[2], l[3]);
+    *reinterpret_cast<uint4*>(p) = make_uint4(l[0], l[1], l[2], l[3]);
   });
 }
 

@@ -110,10 +110,9 @@ def test_waits_for_other_tiles_come_before_what_they_guard():
     copies = text[text.index("tensor copies ----"):text.index("MMAs (")]
     assert copies.index("wait_inputs") < copies.index("tma_3d")
     counts, epilogue = text[text.index("counts of finished"):text.index("epilogue ----")], text[text.index("epilogue ----"):]
-    assert epilogue.index("wait_inputs(U)") < min(epilogue.index(s) for s in ("fetch(0)", "diag[row]", "tma_store_3d"))
+    assert epilogue.index("wait_inputs(U)") < min(epilogue.index(s) for s in ("fetch(0)", "diag[row]", "or_store("))
     # and a tile counts as done after its stores
-    flush = epilogue[epilogue.index("auto flush"):]
-    assert flush.index("tma_store_done<0>()") < flush.index("tma_store_done<1>()") < flush.index("bar_arrive(smem_u32(&stored")
+    assert epilogue.rindex("out[k * A.ld_out]") < epilogue.index("fence.proxy.async") < epilogue.index("bar_arrive(smem_u32(&stored")
     assert counts.index("wait_long(&stored") < counts.index("red.release.gpu")
-    # a split's partial sums are added after those of all splits have arrived, which nobody holds up
-    assert epilogue.index("flush(true);\n        unsigned* count") < epilogue.index("or_wait_count(count") < epilogue.index("part -=")
+    # a split's partial sums are added after those of all splits have arrived
+    assert epilogue.index("red.release.gpu") < epilogue.index("or_wait_count(count") < epilogue.index("part -=")
