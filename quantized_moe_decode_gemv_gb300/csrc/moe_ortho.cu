@@ -103,6 +103,7 @@ constexpr int kMaxSplit = 16;
 // the three products.
 struct Plan {
   int cg = 1;
+  int group = 1;
   int ks[3] = {1, 1, 1};
   double clocks = 1e30;
   int tiles[3], kb[3];
@@ -114,11 +115,19 @@ struct Plan {
   }
 };
 
+// What a matrix keeps in the L2 while it goes through its steps.
+int64_t resident_bytes(const moe_ortho_config& c) {
+  const int64_t m = std::min(c.rows, c.cols);
+  return 6ll * c.rows * c.cols + 4 * m * m;
+}
+constexpr int64_t kResident = 100ll << 20;   // of 129 MB
+
 // The least estimated time in SM clocks.  A product takes its tiles over the workers (whole
 // rounds of them for one matrix; several matrices' products fill each other's last
-// rounds) times a tile's K blocks (512 clocks, the MMAs of a pair's 256 x 256 x 64 or the
-// bytes of a CTA's 128 x 128 x 64), then the way of its last tile to whoever waits for it;
-// a K split adds its partial sums' way through memory.
+// rounds) times a tile's K blocks, then the way of its last tile to whoever waits for it;
+// a K split adds its partial sums' way through memory.  Measured on 1024 x 4096: a K block
+// of a 128 x 128 tile 440 clocks with all CTAs at work (its bytes; its MMAs take 256), a
+// pair's of 256 x 256 550 (512); joining 4 splits 3.5 us.
 Plan plan_of(const moe_ortho_config& c, int n, const int (&workers)[3]) {
   Plan best;
   const int m = std::min(c.rows, c.cols);
@@ -130,19 +139,28 @@ Plan plan_of(const moe_ortho_config& c, int n, const int (&workers)[3]) {
     for (int mode = 0; mode < 3; ++mode) {
       p.tiles[mode] = mode == OR_APPLY ? or_tiles(mode, cg, c.rows, c.cols) : or_tiles(mode, cg, m, m);
       p.kb[mode] = ((mode == OR_GRAM ? std::max(c.rows, c.cols) : m) + 63) / 64;
-      const double T = static_cast<double>(p.tiles[mode]) * n;
+    }
+    // groups: as few as the L2 allows, of about one size, each with two rounds of tiles of its
+    // smaller products, so that a matrix's products finish while others' run (16 of 1856 x
+    // 1024, 250 MB: 605 us in one group of 2.1 rounds, 652 in two of one)
+    const int64_t fit = std::max<int64_t>(kResident / resident_bytes(c), tiles(2 * W, p.tiles[OR_GRAM]));
+    const int64_t groups = tiles(n, static_cast<int>(std::min<int64_t>(fit, n)));
+    p.group = static_cast<int>(tiles(n, static_cast<int>(groups)));
+    for (int mode = 0; mode < 3; ++mode) {
+      const double T = static_cast<double>(p.tiles[mode]) * p.group;
       double least = 1e30;
       for (int ks = 1; ks <= kMaxSplit; ++ks) {
-        if (ks > 1 && (T * ks > W || p.kb[mode] / ks < 2)) break;
+        if (ks > 1 && (groups > 1 || T * ks > W || p.kb[mode] / ks < 2)) break;
         const double rounds = n > 1 ? std::max(1.0, T * ks / W) : std::ceil(T * ks / W);
-        const double t = rounds * ((p.kb[mode] + ks - 1) / ks) * 512.0 + (cg == 2 ? 9000.0 : 6000.0) +
-                         (ks > 1 ? (cg == 2 ? 5000.0 : 2500.0) + ks * 300.0 : 0.0);
+        const double kb = cg == 2 ? 550.0 : 260.0 + 180.0 * std::min(1.0, T * ks / W);
+        const double t = rounds * ((p.kb[mode] + ks - 1) / ks) * kb + (cg == 2 ? 9000.0 : 6000.0) +
+                         (ks > 1 ? (cg == 2 ? 9000.0 : 5000.0) + ks * 300.0 : 0.0);
         if (t < least) {
           least = t;
           p.ks[mode] = ks;
         }
       }
-      p.clocks += least;
+      p.clocks += least * groups;
     }
     if (p.clocks < best.clocks) best = p;
   }
@@ -245,16 +263,18 @@ moe_status forward(moe_ortho* h, const void* g, int64_t ldg, int64_t step_g, int
     f.tiles = P.tiles[p];
     f.kb = P.kb[p];
     f.ks = P.ks[p];
-    f.units = n * f.tiles * f.ks;
-    units = std::max<int64_t>(units, f.units);
+    const int64_t all = static_cast<int64_t>(P.group) * f.tiles * f.ks;
+    units = std::max(units, all);
     f.part = part;
     f.arrived = arrived;
     if (f.ks > 1) {
-      part += static_cast<int64_t>(f.units) * P.cg * or_part_floats(P.cg);
+      part += all * P.cg * or_part_floats(P.cg);
       arrived += n * f.tiles * P.cg * OR_EPI_WARPS;
     }
   }
   a.steps = c.steps;
+  a.matrices = n;
+  a.group = P.group;
   a.stages = OR_MAX_STAGES;
   while (or_smem_bytes(a.stages) > OR_SMEM_MAX) --a.stages;
   a.lo = h->lo;

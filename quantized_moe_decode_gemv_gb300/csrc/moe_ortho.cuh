@@ -21,14 +21,14 @@
 //     what rounding leaves of X lies in directions that X itself may not have, where p
 //     multiplies by a = 3.4 a step; without lo a gradient of 9 tokens was off by 4e-2.
 //
-// All steps are one launch (k_ortho).  The tiles of all products, (step, product, matrix,
-// tile), are one list that CTAs (pairs, for 256 x 256 tiles) take in turn; a tile waits
+// All steps are one launch (k_ortho).  The tiles of all products, (group of matrices, step,
+// product, matrix, tile), are one list that CTAs (pairs, for 256 x 256 tiles) take in turn; a tile waits
 // until the products that it reads are done, by counters of finished epilogues for each
 // matrix and product.  Tiles only wait for tiles before them in the list and all CTAs are
 // resident (a cooperative launch), so somebody always can go on.  As launches of their
 // own, products were 2.1 waves taken as 3 (16 matrices of 1856 x 1024, tiles of 256 x
 // 256 on 76 pairs), and each paid for its launch, its pipeline's filling and its
-// epilogues' end.
+// epilogues' end.  (A group is a stack's matrices that the L2 holds, if they are enough.)
 //
 // Roles of a CTA's 12 warps, as in k_gemm16: tensor copies, MMAs, tensor memory, and
 // eight epilogue warps; accumulators double-buffered.  Tiles are square, CG * 128 on a
@@ -40,7 +40,8 @@
 //
 // An epilogue warp's piece is 32 x 32 values, a row a lane.  What paced the epilogues was
 // what they wrote (all CTAs at once: 6 KB a piece, X twice and symmetric tiles twice, took 8 us
-// for 256 x 256 values, XXX with the 4 and 2 KB of now; its MMAs take 4.3 at K = 1024).
+// for 256 x 256 values, 6 with the 4 KB of X and 3.5 with the 2 KB of O; MMAs take 4.3 at
+// K = 1024).
 // So X's hi is its operand's rows and nothing else, its lo lies as lanes read it, and
 // symmetric tiles are stored once.  What a piece reads comes two pieces ahead by the lanes'
 // own asynchronous copies; tensor copies would queue behind those of the ring.
@@ -65,7 +66,7 @@ enum : int { OR_GRAM = 0, OR_POLY = 1, OR_APPLY = 2 };
 // splits.  (Partial sums have a place for each product: one matrix may be a product ahead
 // of another.)
 struct OrthoPhase {
-  int M, N, tiles, kb, ks, units;   // units: of all matrices
+  int M, N, tiles, kb, ks;
   float* part;              // [unit][CG][4][BN / 32][32 x 32]: partial sums of a split K
   unsigned* arrived;        // [tile][CG][8]: splits that have left theirs, in all steps so far
 };
@@ -73,7 +74,7 @@ struct OrthoPhase {
 struct OrthoArgs {
   CUtensorMap tx[2], ta, tb;         // boxes of 64 x 64: X of even and odd steps, O, P
   OrthoPhase ph[3];
-  int steps;
+  int steps, matrices, group;   // matrices that go through the steps together
   int stages;               // slots of the ring, a K block each
   unsigned short* lo;       // X's second term in pieces of 32 x 32, a lane's 16-byte words side by side
   int64_t step_lo;
@@ -102,25 +103,29 @@ __host__ __device__ inline int or_tiles(int mode, int cg, int M, int N) {
 
 struct OrthoUnit {
   int mode, step, z, m0, n0, kb0, nkb, ks, split;
-  int tile;     // of the product, over all matrices
+  int tile;     // of the product, over the group's matrices
   int unit;     // the same with its split
 };
 
-// Unit g of the list: steps, products, matrices, tiles, K splits.  Symmetric: tile rows
-// one after the other, each up to the diagonal; else in groups of 8 tile rows, rows fastest.
+// Unit g of the list: groups, steps, products, matrices, tiles, K splits.  Symmetric: tile
+// rows one after the other, each up to the diagonal; else in groups of 8 tile rows, rows fastest.
 template <int CG>
 __device__ __forceinline__ OrthoUnit or_unit(const OrthoArgs& A, int64_t g) {
   constexpr int TS = CG * 128;
   OrthoUnit U;
-  const int per = A.ph[0].units + A.ph[1].units + A.ph[2].units;
+  const int u0 = A.ph[0].tiles * A.ph[0].ks, u1 = A.ph[1].tiles * A.ph[1].ks, u2 = A.ph[2].tiles * A.ph[2].ks;   // of a matrix
+  const int64_t whole = static_cast<int64_t>(u0 + u1 + u2) * A.group * A.steps;
+  const int z0 = static_cast<int>(g / whole) * A.group, nz = min(A.group, A.matrices - z0);
+  g -= g / whole * whole;
+  const int per = (u0 + u1 + u2) * nz;
   U.step = static_cast<int>(g / per);
   int r = static_cast<int>(g - static_cast<int64_t>(U.step) * per);
   U.mode = OR_GRAM;
-  if (r >= A.ph[0].units) {
-    r -= A.ph[0].units;
+  if (r >= u0 * nz) {
+    r -= u0 * nz;
     U.mode = OR_POLY;
-    if (r >= A.ph[1].units) {
-      r -= A.ph[1].units;
+    if (r >= u1 * nz) {
+      r -= u1 * nz;
       U.mode = OR_APPLY;
     }
   }
@@ -131,6 +136,7 @@ __device__ __forceinline__ OrthoUnit or_unit(const OrthoArgs& A, int64_t g) {
   U.split = r - U.tile * P.ks;
   U.z = U.tile / P.tiles;
   int t = U.tile - U.z * P.tiles;
+  U.z += z0;
   if (U.mode != OR_APPLY) {
     int i = static_cast<int>((sqrtf(8.0f * t + 1.0f) - 1.0f) * 0.5f);
     while (i * (i + 1) / 2 > t) --i;
@@ -249,7 +255,8 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
   const int worker = blockIdx.x / CG, nworkers = gridDim.x / CG;
-  const int64_t units = static_cast<int64_t>(A.ph[0].units + A.ph[1].units + A.ph[2].units) * A.steps;
+  const int64_t units = static_cast<int64_t>(A.ph[0].tiles * A.ph[0].ks + A.ph[1].tiles * A.ph[1].ks + A.ph[2].tiles * A.ph[2].ks) *
+                        A.matrices * A.steps;
   constexpr uint32_t tm_cols = 2 * BN;
 
   if (warp == 2) tm_alloc<CG>(smem_u32(holder), tm_cols);
@@ -626,13 +633,13 @@ __device__ __forceinline__ void or_read(const OrthoStart& A, int64_t at, int lef
     v[j] = j >= left ? 0.0f : A.dt == 2 ? static_cast<const float*>(A.g)[at + j] : ld16(A.g, at + j, A.dt);
 }
 
-// A warp's unit: 8 rows of 32 columns, a lane has 8 of them (row lane / 4).  f(row, column,
+// A warp's unit: 4 rows of 64 columns, a lane has 8 of them (row lane / 8).  f(row, column,
 // values) for the units of this CTA in turn, four of them under way at a time.
 template <typename F>
 __device__ __forceinline__ void or_elements(const OrthoStart& A, int z, F&& f) {
-  const int lane = threadIdx.x & 31, r = lane >> 2, c = (lane & 3) * 8;
-  const int cols = (A.N + 31) / 32;
-  const int n = (A.M + 7) / 8 * cols;   // (at most 4096 * 1024)
+  const int lane = threadIdx.x & 31, r = lane >> 3, c = (lane & 7) * 8;
+  const int cols = (A.N + 63) / 64;
+  const int n = (A.M + 3) / 4 * cols;   // (at most 8192 * 512)
   const int step = static_cast<int>(gridDim.x) * 8;
   for (int u = static_cast<int>(blockIdx.x) * 8 + (threadIdx.x >> 5); u < n; u += 4 * step) {
     float v[4][8];
@@ -640,8 +647,8 @@ __device__ __forceinline__ void or_elements(const OrthoStart& A, int z, F&& f) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int i = u + k * step, b = i / cols;
-      row[k] = b * 8 + r;
-      col[k] = (i - b * cols) * 32 + c;
+      row[k] = b * 4 + r;
+      col[k] = (i - b * cols) * 64 + c;
       if (i >= n || row[k] >= A.M || col[k] >= A.N) row[k] = -1;
       if (row[k] >= 0) or_read(A, z * A.step_g + row[k] * A.ldg + col[k], A.N - col[k], v[k]);
     }

@@ -91,9 +91,14 @@ int row_threads(int T, int H, int vec, int sms) {
 using RowKernel = void (*)(const RowArgs);
 
 RowKernel take_kernel(int vec) { return vec == 8 ? k_rows_take<8> : vec == 2 ? k_rows_take<2> : k_rows_take<1>; }
-RowKernel combine_kernel(int vec) {
-  return vec == 8 ? k_rows_combine<8> : vec == 2 ? k_rows_combine<2> : k_rows_combine<1>;
+// as many rows under way as a token has (odd widths: eight)
+RowKernel combine_kernel(int vec, int k) {
+  if (vec == 8) return k <= 4 ? k_rows_combine<8, 4> : k <= 8 ? k_rows_combine<8, 8> : k <= 10 ? k_rows_combine<8, 10> : k_rows_combine<8, 16>;
+  return vec == 2 ? k_rows_combine<2, 8> : k_rows_combine<1, 8>;
 }
+using SmallKernel = void (*)(const PlanArgs, const RowArgs);
+SmallKernel small_kernel(int vec) { return vec == 8 ? k_rows_small<8> : vec == 2 ? k_rows_small<2> : k_rows_small<1>; }
+int small_smem(int E, int P) { return (rw_plan_smem(E) + 15) / 16 * 16 + 4 * P; }
 template <bool Y, bool W>
 RowKernel grad_kernel_t(int vec) {
   return vec == 8 ? k_rows_grad<8, Y, W> : vec == 2 ? k_rows_grad<2, Y, W> : k_rows_grad<1, Y, W>;
@@ -139,22 +144,24 @@ moe_status check_ids(moe_rows* h, const void* ids, int32_t id_bytes, const int32
   return MOE_OK;
 }
 
-cudaError_t launch_plan(moe_rows* h, const void* ids, int32_t id_bytes, int32_t T, int32_t* offsets, int32_t* order,
-                        int32_t* place, cudaStream_t s) {
-  const int E = h->cfg.n_experts;
-  if (T == 0) return cudaMemsetAsync(offsets, 0, static_cast<size_t>(E + 1) * 4, s);
+PlanArgs plan_args(moe_rows* h, const void* ids, int32_t id_bytes, int32_t T, int32_t* offsets, int32_t* order, int32_t* place) {
   PlanArgs a{};
   a.ids = ids;
   a.id64 = id_bytes == 8;
   a.P = T * h->cfg.top_k;
-  a.E = E;
+  a.E = h->cfg.n_experts;
   a.chunks = (a.P + RW_CHUNK - 1) / RW_CHUNK;
   a.totals = h->totals;
   a.offsets = offsets;
   a.order = order;
   a.place = place;
   a.status = h->status;
-  const size_t smem = static_cast<size_t>(rw_plan_smem(E));
+  return a;
+}
+
+cudaError_t launch_plan(moe_rows* h, const PlanArgs& a, cudaStream_t s) {
+  if (a.P == 0) return cudaMemsetAsync(a.offsets, 0, static_cast<size_t>(a.E + 1) * 4, s);
+  const size_t smem = static_cast<size_t>(rw_plan_smem(a.E));
   cudaError_t e = cudaSuccess;
   if (a.chunks > 1) {
     e = launch_chained(k_rows_plan<true>, a.chunks, RW_PLAN_THREADS, smem, 1, s, a);
@@ -167,13 +174,8 @@ cudaError_t launch_plan(moe_rows* h, const void* ids, int32_t id_bytes, int32_t 
   return e;
 }
 
-cudaError_t launch_take(moe_rows* h, const Rows& x, const Rows& rows, int32_t T, int32_t width, const int32_t* offsets,
-                        const int32_t* place, cudaStream_t s) {
+RowArgs row_args(moe_rows* h, int32_t T, int32_t width, const int32_t* offsets, const int32_t* place) {
   RowArgs a{};
-  a.tok = static_cast<const unsigned short*>(x.p);
-  a.ld_tok = x.ld;
-  a.row_out = static_cast<unsigned short*>(const_cast<void*>(rows.p));
-  a.ld_row_out = rows.ld;
   a.offsets = offsets;
   a.place = place;
   a.T = T;
@@ -182,10 +184,11 @@ cudaError_t launch_take(moe_rows* h, const Rows& x, const Rows& rows, int32_t T,
   a.E = h->cfg.n_experts;
   a.dt = h->cfg.act_dtype;
   a.status = h->status;
-  const int vec = vector_of({x, rows});
-  ++h->last_launches;
-  return launch_chained(take_kernel(vec), T, row_threads(T, width, vec, h->num_sms), 0, 1, s, a);
+  return a;
 }
+
+// CTAs that go through tokens: as many as run at once.
+int token_ctas(int T, int threads, int sms) { return std::min(T, sms * (2048 / threads)); }
 
 moe_status plan(moe_rows* h, const void* ids, int32_t id_bytes, int32_t T, int32_t* offsets, int32_t* order, int32_t* place,
                 void* stream) {
@@ -199,7 +202,7 @@ moe_status plan(moe_rows* h, const void* ids, int32_t id_bytes, int32_t T, int32
   DeviceScope dev(h->device);
   if (!dev.ok) return fail(h, MOE_ERR_DEVICE, "the handle's device cannot be made current");
   h->last_launches = 0;
-  return launched(h, launch_plan(h, ids, id_bytes, T, offsets, order, place, static_cast<cudaStream_t>(stream)));
+  return launched(h, launch_plan(h, plan_args(h, ids, id_bytes, T, offsets, order, place), static_cast<cudaStream_t>(stream)));
 }
 
 // The rows alone (ids NULL), or the plan and the rows.
@@ -229,8 +232,24 @@ moe_status take(moe_rows* h, bool with_plan, const void* x, int64_t ldx, int32_t
   DeviceScope dev(h->device);
   if (!dev.ok) return fail(h, MOE_ERR_DEVICE, "the handle's device cannot be made current");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = with_plan ? launch_plan(h, ids, id_bytes, T, offsets, order, place, s) : cudaSuccess;
-  if (e == cudaSuccess && T > 0) e = launch_take(h, in, out, T, width, offsets, place, s);
+  RowArgs a = row_args(h, T, width, offsets, place);
+  a.tok = static_cast<const unsigned short*>(x);
+  a.ld_tok = ldx;
+  a.row_out = static_cast<unsigned short*>(rows);
+  a.ld_row_out = ld_rows;
+  const int vec = T > 0 ? vector_of({in, out}) : 1;
+  if (with_plan && T > 0 && P <= RW_CHUNK) {
+    const int64_t pieces = static_cast<int64_t>(T) * ((width + 32 * vec - 1) / (32 * vec));
+    ++h->last_launches;
+    return launched(h, launch_chained(small_kernel(vec), std::min<int64_t>(h->num_sms, (pieces + 31) / 32), RW_PLAN_THREADS,
+                                      static_cast<size_t>(small_smem(a.E, static_cast<int>(P))), 1, s,
+                                      plan_args(h, ids, id_bytes, T, offsets, order, place), a));
+  }
+  cudaError_t e = with_plan ? launch_plan(h, plan_args(h, ids, id_bytes, T, offsets, order, place), s) : cudaSuccess;
+  if (e == cudaSuccess && T > 0) {
+    ++h->last_launches;
+    e = launch_chained(take_kernel(vec), T, row_threads(T, width, vec, h->num_sms), 0, 1, s, a);
+  }
   return launched(h, e);
 }
 
@@ -253,23 +272,16 @@ moe_status combine(moe_rows* h, const void* y, int64_t ldy, int32_t T, int32_t w
     return fail(h, MOE_ERR_INVALID_ARG, "out overlaps an input");
   DeviceScope dev(h->device);
   if (!dev.ok) return fail(h, MOE_ERR_DEVICE, "the handle's device cannot be made current");
-  RowArgs a{};
+  RowArgs a = row_args(h, T, width, nullptr, place);
   a.row = static_cast<const unsigned short*>(y);
   a.ld_row = ldy;
   a.tok_out = static_cast<unsigned short*>(out);
   a.ld_tok = ldo;
   a.w = w;
   a.w_dt = w_dtype;
-  a.place = place;
-  a.T = T;
-  a.k = h->cfg.top_k;
-  a.H = width;
-  a.E = h->cfg.n_experts;
-  a.dt = h->cfg.act_dtype;
-  a.status = h->status;
-  const int vec = vector_of({in, to});
+  const int vec = vector_of({in, to}), threads = row_threads(T, width, vec, h->num_sms);
   ++h->last_launches;
-  return launched(h, launch_chained(combine_kernel(vec), T, row_threads(T, width, vec, h->num_sms), 0, 1,
+  return launched(h, launch_chained(combine_kernel(vec, a.k), token_ctas(T, threads, h->num_sms), threads, 0, 1,
                                     static_cast<cudaStream_t>(stream), a));
 }
 
@@ -298,7 +310,7 @@ moe_status combine_backward(moe_rows* h, const void* d_out, int64_t ldd, int32_t
     return fail(h, MOE_ERR_INVALID_ARG, "a gradient overlaps an input or the other gradient");
   DeviceScope dev(h->device);
   if (!dev.ok) return fail(h, MOE_ERR_DEVICE, "the handle's device cannot be made current");
-  RowArgs a{};
+  RowArgs a = row_args(h, T, width, offsets, place);
   a.tok = static_cast<const unsigned short*>(d_out);
   a.ld_tok = ldd;
   a.row = static_cast<const unsigned short*>(in.p);
@@ -308,18 +320,10 @@ moe_status combine_backward(moe_rows* h, const void* d_out, int64_t ldd, int32_t
   a.w = w;
   a.d_w = d_w;
   a.w_dt = w_dtype;
-  a.offsets = offsets;
-  a.place = place;
-  a.T = T;
-  a.k = h->cfg.top_k;
-  a.H = width;
-  a.E = h->cfg.n_experts;
-  a.dt = h->cfg.act_dtype;
-  a.status = h->status;
-  const int vec = vector_of({e, in, to});
+  const int vec = vector_of({e, in, to}), threads = row_threads(T, width, vec, h->num_sms);
   ++h->last_launches;
-  return launched(h, launch_chained(grad_kernel(vec, d_y != nullptr, d_w != nullptr), T,
-                                    row_threads(T, width, vec, h->num_sms), 0, 1, static_cast<cudaStream_t>(stream), a));
+  return launched(h, launch_chained(grad_kernel(vec, d_y != nullptr, d_w != nullptr), token_ctas(T, threads, h->num_sms), threads,
+                                    0, 1, static_cast<cudaStream_t>(stream), a));
 }
 
 // (h: the handle while it is not the caller's, for the entry point to free when an exception ends this)
@@ -352,6 +356,10 @@ moe_status create(const moe_rows_config* cfg, moe_rows** out, moe_rows*& h) {
     e = h->alloc(reinterpret_cast<void**>(&h->totals), static_cast<size_t>(chunks) * (cfg->n_experts + 1) * 4);
   for (const void* k : {reinterpret_cast<const void*>(k_rows_plan<true>), reinterpret_cast<const void*>(k_rows_plan<false>)})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, rw_plan_smem(RW_MAX_E));
+  for (int vec : {1, 2, 8})
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(reinterpret_cast<const void*>(small_kernel(vec)), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               small_smem(RW_MAX_E, RW_CHUNK));
   if (e == cudaSuccess) e = cudaDeviceSynchronize();   // the status word's clear runs on the default stream
   if (e != cudaSuccess) {
     g_error = std::string("create: ") + cudaGetErrorString(e);

@@ -31,54 +31,95 @@ struct PlanArgs {
 
 __host__ __device__ inline int rw_plan_smem(int E) { return 32 * (E + 1) * 2 + (E + 1) * 4 + 32 * 4 + 16; }
 
+// What a CTA of the plan finds out about its picks first + 32 r: their bins (-1: past the
+// last pick) and how many of their bins the warp had before them; counters in shared memory.
+struct PlanPicks {
+  int first;
+  int bin[RW_ROUNDS], before[RW_ROUNDS];
+};
+
+// Exclusive sum over the bins: a thread has all of a bin's picks and those of the CTAs
+// before this one; base[bin] becomes this CTA's first row of it.
+__device__ __forceinline__ void rw_starts(const PlanArgs& A, bool write, char* smem, int all, int low) {
+  int* base = reinterpret_cast<int*>(smem);
+  int* sums = base + A.E + 1;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int incl = all;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+    if (lane >= d) incl += v;
+  }
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    int s = sums[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, s, d);
+      if (lane >= d) s += v;
+    }
+    sums[lane] = s;
+  }
+  __syncthreads();
+  const int start = incl - all + (warp ? sums[warp - 1] : 0);
+  if (tid < A.E) {
+    base[tid] = start + low;
+    if (write) A.offsets[tid] = start;
+  }
+  if (tid == A.E - 1) {   // (E <= 1024 threads)
+    base[A.E] += start + all;
+    if (write) A.offsets[A.E] = start + all;
+  }
+  __syncthreads();
+}
+
 // Stable sort of the picks by expert, E + 1 bins (the last one: no expert).  A warp has
 // 128 consecutive picks and counts them bin by bin, 32 at a time, in its own row of
 // counters: lanes of equal bin find each other (match), so a pick knows how many of its
 // bin came before it in the warp.  Sums over the warps before, the CTAs before and the
 // bins below give its row.  COUNT: totals of every CTA alone, for picks of several CTAs.
+// WRITE: this CTA writes offsets.
 template <bool COUNT>
-__global__ void __launch_bounds__(RW_PLAN_THREADS) k_rows_plan(const PlanArgs A) {
-  extern __shared__ __align__(16) char rw_smem[];
+__device__ __forceinline__ void rw_plan(const PlanArgs& A, int chunk, bool write, char* smem, PlanPicks& K) {
   const int nb = A.E + 1;
-  int* base = reinterpret_cast<int*>(rw_smem);
-  int* sums = base + nb;
-  unsigned short* count = reinterpret_cast<unsigned short*>(sums + 32);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, chunk = blockIdx.x;
-  for (int i = tid; i < 32 * nb; i += RW_PLAN_THREADS) count[i] = 0;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
-  const int first = chunk * RW_CHUNK + warp * 32 * RW_ROUNDS + lane;
-  int bin[RW_ROUNDS], before[RW_ROUNDS];
+  int* base = reinterpret_cast<int*>(smem);
+  unsigned short* count = reinterpret_cast<unsigned short*>(base + nb + 32);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  K.first = chunk * RW_CHUNK + warp * 32 * RW_ROUNDS + lane;
   bool bad = false;
 #pragma unroll
   for (int r = 0; r < RW_ROUNDS; ++r) {
-    const int i = first + 32 * r;
-    bin[r] = -1;
+    const int i = K.first + 32 * r;
+    K.bin[r] = -1;
     if (i < A.P) {
       const long long e = A.id64 ? static_cast<const long long*>(A.ids)[i] : static_cast<const int*>(A.ids)[i];
       bad = bad || e < -1 || e >= A.E;
-      bin[r] = e < 0 || e >= A.E ? A.E : static_cast<int>(e);
+      K.bin[r] = e < 0 || e >= A.E ? A.E : static_cast<int>(e);
     }
   }
   if (bad && !COUNT) atomicOr(A.status, STATUS_INDEX);
-  __syncthreads();
+  __syncthreads();   // the counters are zero
   unsigned short* mine = count + warp * nb;
 #pragma unroll
   for (int r = 0; r < RW_ROUNDS; ++r) {
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, bin[r]);
+    K.before[r] = 0;
+    if (chunk * RW_CHUNK + warp * 32 * RW_ROUNDS + 32 * r >= A.P) continue;   // (the whole warp)
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, K.bin[r]);
     const int rank = __popc(same & ((1u << lane) - 1u));
-    const int old = bin[r] >= 0 ? mine[bin[r]] : 0;
+    const int old = K.bin[r] >= 0 ? mine[K.bin[r]] : 0;
     __syncwarp();
-    if (bin[r] >= 0 && rank == 0) mine[bin[r]] = static_cast<unsigned short>(old + __popc(same));
+    if (K.bin[r] >= 0 && rank == 0) mine[K.bin[r]] = static_cast<unsigned short>(old + __popc(same));
     __syncwarp();
-    before[r] = old + rank;
+    K.before[r] = old + rank;
   }
   __syncthreads();
+  const int warps = min(32, (A.P - chunk * RW_CHUNK + 32 * RW_ROUNDS - 1) / (32 * RW_ROUNDS));   // those with picks
   int all = 0, low = 0;
   for (int b = tid; b < nb; b += RW_PLAN_THREADS) {
     int run = 0;
 #pragma unroll 8
-    for (int w = 0; w < 32; ++w) {
+    for (int w = 0; w < warps; ++w) {
       const int v = count[w * nb + b];
       count[w * nb + b] = static_cast<unsigned short>(run);
       run += v;
@@ -104,43 +145,38 @@ __global__ void __launch_bounds__(RW_PLAN_THREADS) k_rows_plan(const PlanArgs A)
       base[b] = ahead;
     }
   }
-  if (COUNT) return;
-  // exclusive sum over the bins
-  int incl = all;
+  if constexpr (!COUNT) rw_starts(A, write, smem, all, low);
+}
+
+// The row of a pick (those without an expert: behind all others).
+__device__ __forceinline__ int rw_row(const PlanPicks& K, int r, int nb, const char* smem) {
+  const int* base = reinterpret_cast<const int*>(smem);
+  const unsigned short* count = reinterpret_cast<const unsigned short*>(base + nb + 32);
+  const int b = K.bin[r];
+  return base[b] + count[(threadIdx.x >> 5) * nb + b] + K.before[r];
+}
+
+__device__ __forceinline__ void rw_clear_counts(char* smem, int nb) {
+  uint32_t* count = reinterpret_cast<uint32_t*>(smem + nb * 4 + 32 * 4);
+  for (int i = threadIdx.x; i < 16 * nb; i += RW_PLAN_THREADS) count[i] = 0;
+}
+
+template <bool COUNT>
+__global__ void __launch_bounds__(RW_PLAN_THREADS) k_rows_plan(const PlanArgs A) {
+  extern __shared__ __align__(16) char rw_smem[];
+  rw_clear_counts(rw_smem, A.E + 1);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  PlanPicks K;
+  rw_plan<COUNT>(A, blockIdx.x, !COUNT && blockIdx.x == 0, rw_smem, K);
+  if constexpr (!COUNT) {
 #pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const int v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-    if (lane >= d) incl += v;
-  }
-  if (lane == 31) sums[warp] = incl;
-  __syncthreads();
-  if (warp == 0) {
-    int s = sums[lane];
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const int v = __shfl_up_sync(0xFFFFFFFFu, s, d);
-      if (lane >= d) s += v;
+    for (int r = 0; r < RW_ROUNDS; ++r) {
+      if (K.bin[r] < 0) continue;
+      const int i = K.first + 32 * r, row = rw_row(K, r, A.E + 1, rw_smem);
+      A.order[row] = K.bin[r] < A.E ? i : -1;
+      A.place[i] = K.bin[r] < A.E ? row : -1;
     }
-    sums[lane] = s;
-  }
-  __syncthreads();
-  const int start = incl - all + (warp ? sums[warp - 1] : 0);
-  if (tid < A.E) {
-    base[tid] = start + low;
-    if (chunk == 0) A.offsets[tid] = start;
-  }
-  if (tid == A.E - 1) {   // (E <= 1024 threads)
-    base[A.E] += start + all;
-    if (chunk == 0) A.offsets[A.E] = start + all;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int r = 0; r < RW_ROUNDS; ++r) {
-    const int i = first + 32 * r, b = bin[r];
-    if (b < 0) continue;
-    const int row = base[b] + mine[b] + before[r];
-    A.order[row] = b < A.E ? i : -1;
-    A.place[i] = b < A.E ? row : -1;
   }
 }
 
@@ -234,7 +270,7 @@ __device__ __forceinline__ int rw_place(const RowArgs& A, int t, int lane) {
 template <int VEC>
 __device__ __forceinline__ void rw_clear_tail(const RowArgs& A) {
   const int P = A.T * A.k;
-  for (int64_t r = max(A.offsets[A.E], 0) + static_cast<int64_t>(blockIdx.x); r < P; r += A.T)
+  for (int64_t r = max(A.offsets[A.E], 0) + static_cast<int64_t>(blockIdx.x); r < P; r += gridDim.x)
     for (int c = threadIdx.x * VEC; c < A.H; c += blockDim.x * VEC) rw_store<VEC>(A.row_out + r * A.ld_row_out + c, rw_zero<VEC>());
 }
 
@@ -256,107 +292,168 @@ __global__ void __launch_bounds__(512) k_rows_take(const RowArgs A) {
   rw_clear_tail<VEC>(A);
 }
 
-// out[t] = sum over j, in order, of w[t, j] y[place[t, j]] in fp32, rounded once.  The
-// rows of eight picks are under way at a time.
+// The plan and the rows of up to RW_CHUNK picks in one launch: every CTA makes the plan
+// for itself (some 3 us, as long as a second launch and its wait take), the first one
+// writes it, and each takes some of the tokens' pieces.
 template <int VEC>
+__global__ void __launch_bounds__(RW_PLAN_THREADS) k_rows_small(const PlanArgs P, const RowArgs A) {
+  extern __shared__ __align__(16) char rw_smem[];
+  const int nb = P.E + 1;
+  int* place = reinterpret_cast<int*>(rw_smem + (rw_plan_smem(P.E) + 15) / 16 * 16);
+  rw_clear_counts(rw_smem, nb);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  PlanPicks K;
+  rw_plan<false>(P, 0, blockIdx.x == 0, rw_smem, K);
+  const int present = reinterpret_cast<const int*>(rw_smem)[P.E];
+#pragma unroll
+  for (int r = 0; r < RW_ROUNDS; ++r) {
+    if (K.bin[r] < 0) continue;
+    const int i = K.first + 32 * r, row = rw_row(K, r, nb, rw_smem);
+    place[i] = K.bin[r] < P.E ? row : -1;
+    if (blockIdx.x == 0) {
+      P.order[row] = K.bin[r] < P.E ? i : -1;
+      P.place[i] = K.bin[r] < P.E ? row : -1;
+    }
+  }
+  __syncthreads();
+  // a warp takes a piece of a token's row
+  const int lane = threadIdx.x & 31, pieces = (A.H + 32 * VEC - 1) / (32 * VEC), warps = gridDim.x * (RW_PLAN_THREADS / 32);
+  for (int u = blockIdx.x * (RW_PLAN_THREADS / 32) + (threadIdx.x >> 5); u < A.T * pieces; u += warps) {
+    const int t = u / pieces, c = (u - t * pieces) * 32 * VEC + lane * VEC;
+    if (c >= A.H) continue;
+    const RowPiece<VEC> v = rw_load<VEC>(A.tok + t * A.ld_tok + c);
+    for (int j = 0; j < A.k; ++j) {
+      const int r = place[t * A.k + j];
+      if (r >= 0) rw_store<VEC>(A.row_out + r * A.ld_row_out + c, v);
+    }
+  }
+  for (int64_t r = present + blockIdx.x; r < P.P; r += gridDim.x)
+    for (int c = threadIdx.x * VEC; c < A.H; c += RW_PLAN_THREADS * VEC) rw_store<VEC>(A.row_out + r * A.ld_row_out + c, rw_zero<VEC>());
+}
+
+// out[t] = sum over j, in order, of w[t, j] y[place[t, j]] in fp32, rounded once.  CTAs
+// go through tokens; the rows of NB picks are under way at a time, and the next
+// token's places and weights with them.
+template <int VEC, int NB>
 __global__ void __launch_bounds__(512) k_rows_combine(const RowArgs A) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  const int t = blockIdx.x, lane = threadIdx.x & 31;
-  const int place = rw_place(A, t, lane);
-  const float weight = lane < A.k && A.w ? rw_weight(A.w, static_cast<int64_t>(t) * A.k + lane, A.w_dt) : 1.0f;
-  for (int c = threadIdx.x * VEC; c - lane * VEC < A.H; c += blockDim.x * VEC) {
-    const bool in = c < A.H;
-    float sum[VEC];
+  const int lane = threadIdx.x & 31;
+  auto place_of = [&](int t) { return t < A.T ? rw_place(A, t, lane) : -1; };
+  auto weight_of = [&](int t) {
+    return t < A.T && lane < A.k && A.w ? rw_weight(A.w, static_cast<int64_t>(t) * A.k + lane, A.w_dt) : 1.0f;
+  };
+  int next_place = place_of(blockIdx.x);
+  float next_weight = weight_of(blockIdx.x);
+  for (int t = blockIdx.x; t < A.T; t += gridDim.x) {
+    const int place = next_place;
+    const float weight = place >= 0 ? next_weight : 0.0f;   // (a pick without an expert: 0 times 0)
+    next_place = place_of(t + gridDim.x);
+    next_weight = weight_of(t + gridDim.x);
+    for (int c = threadIdx.x * VEC; c - lane * VEC < A.H; c += blockDim.x * VEC) {
+      const bool in = c < A.H;
+      float sum[VEC];
 #pragma unroll
-    for (float& s : sum) s = 0.0f;
-    for (int j0 = 0; j0 < A.k; j0 += 8) {
-      RowPiece<VEC> v[8];
-      int r[8];
+      for (float& s : sum) s = 0.0f;
+      for (int j0 = 0; j0 < A.k; j0 += NB) {
+        RowPiece<VEC> v[NB];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        r[j] = __shfl_sync(0xFFFFFFFFu, place, j0 + j);   // (lanes from k on: -1)
-        if (in && r[j] >= 0) v[j] = rw_load<VEC>(A.row + r[j] * A.ld_row + c);
+        for (int j = 0; j < NB; ++j) {
+          const int r = __shfl_sync(0xFFFFFFFFu, place, j0 + j);   // (lanes from k on: -1)
+          v[j] = in && r >= 0 ? rw_load<VEC>(A.row + r * A.ld_row + c) : rw_zero<VEC>();
+        }
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          const float f = __shfl_sync(0xFFFFFFFFu, weight, j0 + j);
+          float y[VEC];
+          rw_float<VEC>(v[j], A.dt, y);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) sum[i] = fmaf(f, y[i], sum[i]);
+        }
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float f = __shfl_sync(0xFFFFFFFFu, weight, j0 + j);
-        if (!in || r[j] < 0) continue;
-        float y[VEC];
-        rw_float<VEC>(v[j], A.dt, y);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) sum[i] = fmaf(f, y[i], sum[i]);
-      }
+      if (in) rw_store<VEC>(A.tok_out + t * A.ld_tok + c, rw_pack<VEC>(sum, A.dt));
     }
-    if (in) rw_store<VEC>(A.tok_out + t * A.ld_tok + c, rw_pack<VEC>(sum, A.dt));
   }
 }
 
 // d_y[place[t, j]] = w[t, j] d_out[t];  d_w[t, j] = <d_out[t], y[place[t, j]]>: a lane's
 // part of all k sums stays in registers over the row; lanes and warps are added in a
-// fixed order.  (W: d_w is wanted; Y: d_y is.)
+// fixed order.  (W: d_w is wanted; Y: d_y is.)  CTAs go through tokens as above.
 template <int VEC, bool Y, bool W>
 __global__ void __launch_bounds__(512) k_rows_grad(const RowArgs A) {
-  __shared__ float part[16][RW_MAX_K];
+  constexpr int NB = VEC == 8 ? 8 : 4;   // rows under way at a time
+  __shared__ float part[2][16][RW_MAX_K];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int place = rw_place(A, t, lane);
-  const float weight = Y && lane < A.k ? rw_weight(A.w, static_cast<int64_t>(t) * A.k + lane, A.w_dt) : 0.0f;
-  float dot[RW_MAX_K];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto place_of = [&](int t) { return t < A.T ? rw_place(A, t, lane) : -1; };
+  auto weight_of = [&](int t) {
+    return Y && t < A.T && lane < A.k ? rw_weight(A.w, static_cast<int64_t>(t) * A.k + lane, A.w_dt) : 0.0f;
+  };
+  int next_place = place_of(blockIdx.x), turn = 0;
+  float next_weight = weight_of(blockIdx.x);
+  for (int t = blockIdx.x; t < A.T; t += gridDim.x, turn ^= 1) {
+    const int place = next_place;
+    const float weight = next_weight;
+    next_place = place_of(t + gridDim.x);
+    next_weight = weight_of(t + gridDim.x);
+    float dot[RW_MAX_K];
 #pragma unroll
-  for (float& d : dot) d = 0.0f;
-  for (int c = threadIdx.x * VEC; c - lane * VEC < A.H; c += blockDim.x * VEC) {
-    const bool in = c < A.H;
-    float e[VEC];
-    rw_float<VEC>(in ? rw_load<VEC>(A.tok + t * A.ld_tok + c) : rw_zero<VEC>(), A.dt, e);
+    for (float& d : dot) d = 0.0f;
+    for (int c = threadIdx.x * VEC; c - lane * VEC < A.H; c += blockDim.x * VEC) {
+      const bool in = c < A.H;
+      float e[VEC];
+      rw_float<VEC>(in ? rw_load<VEC>(A.tok + t * A.ld_tok + c) : rw_zero<VEC>(), A.dt, e);
 #pragma unroll
-    for (int j0 = 0; j0 < RW_MAX_K; j0 += 8) {
-      if (j0 >= A.k) break;
-      RowPiece<VEC> v[8];
-      int r[8];
+      for (int j0 = 0; j0 < RW_MAX_K; j0 += NB) {
+        if (j0 >= A.k) break;
+        RowPiece<VEC> v[NB];
+        int r[NB];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        r[j] = __shfl_sync(0xFFFFFFFFu, place, j0 + j);
-        if (W && in && r[j] >= 0) v[j] = rw_load<VEC>(A.row + r[j] * A.ld_row + c);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float f = Y ? __shfl_sync(0xFFFFFFFFu, weight, j0 + j) : 0.0f;
-        if (!in || r[j] < 0) continue;
-        if (Y) {
-          float g[VEC];
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) g[i] = f * e[i];
-          rw_store<VEC>(A.row_out + r[j] * A.ld_row_out + c, rw_pack<VEC>(g, A.dt));
+        for (int j = 0; j < NB; ++j) {
+          r[j] = __shfl_sync(0xFFFFFFFFu, place, j0 + j);
+          if (W && in && r[j] >= 0) v[j] = rw_load<VEC>(A.row + r[j] * A.ld_row + c);
         }
-        if (W) {
-          float y[VEC];
-          rw_float<VEC>(v[j], A.dt, y);
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) dot[j0 + j] = fmaf(e[i], y[i], dot[j0 + j]);
+        for (int j = 0; j < NB; ++j) {
+          const float f = Y ? __shfl_sync(0xFFFFFFFFu, weight, j0 + j) : 0.0f;
+          if (!in || r[j] < 0) continue;
+          if (Y) {
+            float g[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) g[i] = f * e[i];
+            rw_store<VEC>(A.row_out + r[j] * A.ld_row_out + c, rw_pack<VEC>(g, A.dt));
+          }
+          if (W) {
+            float y[VEC];
+            rw_float<VEC>(v[j], A.dt, y);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) dot[j0 + j] = fmaf(e[i], y[i], dot[j0 + j]);
+          }
         }
       }
     }
-  }
-  if (Y) rw_clear_tail<VEC>(A);
-  if (!W) return;
+    if constexpr (W) {
 #pragma unroll
-  for (int j = 0; j < RW_MAX_K; ++j) {
-    if (j >= A.k) break;
-    float d = dot[j];
+      for (int j = 0; j < RW_MAX_K; ++j) {
+        if (j >= A.k) break;
+        float d = dot[j];
 #pragma unroll
-    for (int s = 16; s > 0; s /= 2) d += __shfl_xor_sync(0xFFFFFFFFu, d, s);
-    if (lane == 0) part[warp][j] = d;
+        for (int s = 16; s > 0; s /= 2) d += __shfl_xor_sync(0xFFFFFFFFu, d, s);
+        if (lane == 0) part[turn][warp][j] = d;
+      }
+      __syncthreads();   // (the other turn's sums have been read: their reader has come here since)
+      if (warp == 0 && lane < A.k) {
+        float d = 0.0f;
+        for (int v = 0; v < static_cast<int>(blockDim.x) / 32; ++v) d += part[turn][v][lane];
+        const int64_t i = static_cast<int64_t>(t) * A.k + lane;
+        if (A.w_dt == 2) static_cast<float*>(A.d_w)[i] = d;
+        else static_cast<unsigned short*>(A.d_w)[i] = pack1(d, A.w_dt);
+      }
+    }
   }
-  __syncthreads();
-  if (warp == 0 && lane < A.k) {
-    float d = 0.0f;
-    for (int v = 0; v < static_cast<int>(blockDim.x) / 32; ++v) d += part[v][lane];
-    const int64_t i = static_cast<int64_t>(t) * A.k + lane;
-    if (A.w_dt == 2) static_cast<float*>(A.d_w)[i] = d;
-    else static_cast<unsigned short*>(A.d_w)[i] = pack1(d, A.w_dt);
-  }
+  if constexpr (Y) rw_clear_tail<VEC>(A);
 }
 
 }  // namespace moe_op

@@ -49,7 +49,7 @@ def test_kinds(pkg, kind, rows, cols, dtype):
     orf.check(op(g), g, kind)
 
 
-@pytest.mark.parametrize("n,rows,cols", [(3, 130, 70), (20, 64, 300), (2, 513, 1030), (33, 40, 40), (5, 1024, 600)])
+@pytest.mark.parametrize("n,rows,cols", [(3, 130, 70), (20, 64, 300), (2, 513, 1030), (33, 40, 40), (5, 1024, 600), (19, 1000, 1100)])
 def test_stacks(pkg, n, rows, cols):
     """A stack's matrices come out as each alone; fewer than the handle holds, too."""
     op, one = handle(pkg, rows, cols, n + 1, "fp32"), handle(pkg, rows, cols, 1, "fp32")
