@@ -91,22 +91,37 @@ int row_threads(int T, int H, int vec, int sms) {
 using RowKernel = void (*)(const RowArgs);
 
 RowKernel take_kernel(int vec) { return vec == 8 ? k_rows_take<8> : vec == 2 ? k_rows_take<2> : k_rows_take<1>; }
-// as many rows under way as a token has (odd widths: eight)
-RowKernel combine_kernel(int vec, int k) {
-  if (vec == 8) return k <= 4 ? k_rows_combine<8, 4> : k <= 8 ? k_rows_combine<8, 8> : k <= 10 ? k_rows_combine<8, 10> : k_rows_combine<8, 16>;
-  return vec == 2 ? k_rows_combine<2, 8> : k_rows_combine<1, 8>;
-}
+// (rows and widths of whole 16-byte words go by way of shared memory instead)
+RowKernel combine_kernel(int vec) { return vec == 2 ? k_rows_combine<2> : k_rows_combine<1>; }
 using SmallKernel = void (*)(const PlanArgs, const RowArgs);
 SmallKernel small_kernel(int vec) { return vec == 8 ? k_rows_small<8> : vec == 2 ? k_rows_small<2> : k_rows_small<1>; }
 int small_smem(int E, int P) { return (rw_plan_smem(E) + 15) / 16 * 16 + 4 * P; }
 template <bool Y, bool W>
-RowKernel grad_kernel_t(int vec) {
-  return vec == 8 ? k_rows_grad<8, Y, W> : vec == 2 ? k_rows_grad<2, Y, W> : k_rows_grad<1, Y, W>;
-}
+RowKernel grad_kernel_t(int vec) { return vec == 2 ? k_rows_grad<2, Y, W> : k_rows_grad<1, Y, W>; }
 RowKernel grad_kernel(int vec, bool y, bool w) {
-  return y ? (w ? grad_kernel_t<true, true>(vec) : grad_kernel_t<true, false>(vec)) : grad_kernel_t<false, true>(vec);
+  if (!w) return vec == 8 ? k_rows_grad<8, true, false> : grad_kernel_t<true, false>(vec);
+  return y ? grad_kernel_t<true, true>(vec) : grad_kernel_t<false, true>(vec);
 }
 
+// A CTA's warps and slots of `rows` rows.  One piece under way a warp and many warps beat
+// several and few: on 8192 tokens of 9 rows of 1024, 2 slots (20 warps an SM) 31.5 us, 3 (12
+// warps) 41; few rows take more slots, 2 KB under way a warp.
+constexpr int kStreamSmem = 8 * 2 * (RW_MAX_K + 1) * 512;   // the most it may be
+struct StreamShape {
+  int threads, slots, smem, ctas;
+};
+StreamShape stream_shape(int T, int H, int rows, int sms) {
+  StreamShape s;
+  const int pieces = (H + 255) / 256;
+  // (up to 16 warps a token where tokens alone do not fill the SMs)
+  const int warps = std::min(pieces, T < 2 * sms && 16 * std::max(2, 2048 / (rows * 512) + 1) * rows * 512 <= kStreamSmem ? 16 : 8);
+  s.threads = 32 * warps;
+  s.slots = std::max(2, 2048 / (rows * 512) + 1);   // (at most 5)
+  s.smem = warps * s.slots * rows * 512;
+  const int fit = std::max(1, std::min({2048 / s.threads, 220 * 1024 / (s.smem + 2048), 32}));
+  s.ctas = std::min(T, sms * fit);
+  return s;
+}
 bool misaligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 
 moe_status fail(moe_rows* h, moe_status st, const char* msg) {
@@ -164,11 +179,15 @@ cudaError_t launch_plan(moe_rows* h, const PlanArgs& a, cudaStream_t s) {
   const size_t smem = static_cast<size_t>(rw_plan_smem(a.E));
   cudaError_t e = cudaSuccess;
   if (a.chunks > 1) {
-    e = launch_chained(k_rows_plan<true>, a.chunks, RW_PLAN_THREADS, smem, 1, s, a);
+    e = launch_chained(k_rows_count, a.chunks, RW_CHUNK, 0, 1, s, a);
     ++h->last_launches;
+    if (e == cudaSuccess && a.chunks > RW_DIRECT_CHUNKS) {
+      e = launch_chained(k_rows_scan, (a.E + 32) / 32, RW_CHUNK, 0, 1, s, a);
+      ++h->last_launches;
+    }
   }
   if (e == cudaSuccess) {
-    e = launch_chained(k_rows_plan<false>, a.chunks, RW_PLAN_THREADS, smem, 1, s, a);
+    e = launch_chained(k_rows_plan, a.chunks, RW_CHUNK, smem, 1, s, a);
     ++h->last_launches;
   }
   return e;
@@ -241,7 +260,7 @@ moe_status take(moe_rows* h, bool with_plan, const void* x, int64_t ldx, int32_t
   if (with_plan && T > 0 && P <= RW_CHUNK) {
     const int64_t pieces = static_cast<int64_t>(T) * ((width + 32 * vec - 1) / (32 * vec));
     ++h->last_launches;
-    return launched(h, launch_chained(small_kernel(vec), std::min<int64_t>(h->num_sms, (pieces + 31) / 32), RW_PLAN_THREADS,
+    return launched(h, launch_chained(small_kernel(vec), std::min<int64_t>(h->num_sms, (pieces + 7) / 8), RW_CHUNK,
                                       static_cast<size_t>(small_smem(a.E, static_cast<int>(P))), 1, s,
                                       plan_args(h, ids, id_bytes, T, offsets, order, place), a));
   }
@@ -281,7 +300,12 @@ moe_status combine(moe_rows* h, const void* y, int64_t ldy, int32_t T, int32_t w
   a.w_dt = w_dtype;
   const int vec = vector_of({in, to}), threads = row_threads(T, width, vec, h->num_sms);
   ++h->last_launches;
-  return launched(h, launch_chained(combine_kernel(vec, a.k), token_ctas(T, threads, h->num_sms), threads, 0, 1,
+  if (vec == 8) {
+    const StreamShape f = stream_shape(T, width, a.k, h->num_sms);
+    return launched(h, launch_chained(k_rows_combine_stream, f.ctas, f.threads, static_cast<size_t>(f.smem), 1,
+                                      static_cast<cudaStream_t>(stream), a, f.slots));
+  }
+  return launched(h, launch_chained(combine_kernel(vec), token_ctas(T, threads, h->num_sms), threads, 0, 1,
                                     static_cast<cudaStream_t>(stream), a));
 }
 
@@ -322,6 +346,11 @@ moe_status combine_backward(moe_rows* h, const void* d_out, int64_t ldd, int32_t
   a.w_dt = w_dtype;
   const int vec = vector_of({e, in, to}), threads = row_threads(T, width, vec, h->num_sms);
   ++h->last_launches;
+  if (d_w && vec == 8) {
+    const StreamShape f = stream_shape(T, width, a.k + 1, h->num_sms);
+    return launched(h, launch_chained(d_y ? k_rows_grad_stream<true> : k_rows_grad_stream<false>, f.ctas, f.threads,
+                                      static_cast<size_t>(f.smem), 1, static_cast<cudaStream_t>(stream), a, f.slots));
+  }
   return launched(h, launch_chained(grad_kernel(vec, d_y != nullptr, d_w != nullptr), token_ctas(T, threads, h->num_sms), threads,
                                     0, 1, static_cast<cudaStream_t>(stream), a));
 }
@@ -353,13 +382,16 @@ moe_status create(const moe_rows_config* cfg, moe_rows** out, moe_rows*& h) {
   if (e == cudaSuccess) e = cudaMemset(h->status, 0, 64);
   const int64_t chunks = (static_cast<int64_t>(cfg->max_tokens) * cfg->top_k + RW_CHUNK - 1) / RW_CHUNK;
   if (e == cudaSuccess && chunks > 1)
-    e = h->alloc(reinterpret_cast<void**>(&h->totals), static_cast<size_t>(chunks) * (cfg->n_experts + 1) * 4);
-  for (const void* k : {reinterpret_cast<const void*>(k_rows_plan<true>), reinterpret_cast<const void*>(k_rows_plan<false>)})
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, rw_plan_smem(RW_MAX_E));
+    e = h->alloc(reinterpret_cast<void**>(&h->totals), static_cast<size_t>(chunks + 1) * (cfg->n_experts + 1) * 4);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k_rows_plan), cudaFuncAttributeMaxDynamicSharedMemorySize, rw_plan_smem(RW_MAX_E));
   for (int vec : {1, 2, 8})
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(reinterpret_cast<const void*>(small_kernel(vec)), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                small_smem(RW_MAX_E, RW_CHUNK));
+  for (const void* k : {reinterpret_cast<const void*>(k_rows_combine_stream), reinterpret_cast<const void*>(k_rows_grad_stream<true>),
+                        reinterpret_cast<const void*>(k_rows_grad_stream<false>)})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();   // the status word's clear runs on the default stream
   if (e != cudaSuccess) {
     g_error = std::string("create: ") + cudaGetErrorString(e);

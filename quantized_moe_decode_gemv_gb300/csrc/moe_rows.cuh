@@ -15,28 +15,33 @@ namespace moe_op {
 
 constexpr int RW_MAX_K = 16;
 constexpr int RW_MAX_E = 1024;
-constexpr int RW_PLAN_THREADS = 1024;
-constexpr int RW_ROUNDS = 4;             // picks a thread of the plan
-constexpr int RW_CHUNK = RW_PLAN_THREADS * RW_ROUNDS;   // picks a CTA
+constexpr int RW_CHUNK = 1024;           // picks of a CTA of the plan, one a thread
+constexpr int RW_DIRECT_CHUNKS = 128;    // up to so many, every CTA adds the chunks before it by itself
 
 struct PlanArgs {
   const void* ids;
   int id64;              // ids of 64 bits
   int P, E;
   int chunks;
-  int* totals;           // [chunks][E + 1] picks of every expert (several chunks only)
+  int* totals;           // [chunks + 1][E + 1]: picks of every bin in a chunk; after k_rows_scan before it, and in all
   int *offsets, *order, *place;
   int* status;
 };
 
-__host__ __device__ inline int rw_plan_smem(int E) { return 32 * (E + 1) * 2 + (E + 1) * 4 + 32 * 4 + 16; }
+// Counters of a CTA: [E + 1] first rows, [32] sums of warps, [32][E + 1] 16-bit counts of warps.
+__host__ __device__ inline int rw_plan_smem(int E) { return (E + 1) * 4 + 32 * 4 + 32 * (E + 1) * 2 + 16; }
 
-// What a CTA of the plan finds out about its picks first + 32 r: their bins (-1: past the
-// last pick) and how many of their bins the warp had before them; counters in shared memory.
-struct PlanPicks {
-  int first;
-  int bin[RW_ROUNDS], before[RW_ROUNDS];
-};
+// A pick's bin, and whether its id is neither -1 nor an expert.
+__device__ __forceinline__ int rw_bin(const PlanArgs& A, int i, bool* bad) {
+  const long long e = A.id64 ? static_cast<const long long*>(A.ids)[i] : static_cast<const int*>(A.ids)[i];
+  *bad = e < -1 || e >= A.E;
+  return e < 0 || e >= A.E ? A.E : static_cast<int>(e);
+}
+
+__device__ __forceinline__ void rw_clear_counts(char* smem, int nb) {
+  uint32_t* count = reinterpret_cast<uint32_t*>(smem + nb * 4 + 32 * 4);
+  for (int i = threadIdx.x; i < 16 * nb; i += RW_CHUNK) count[i] = 0;
+}
 
 // Exclusive sum over the bins: a thread has all of a bin's picks and those of the CTAs
 // before this one; base[bin] becomes this CTA's first row of it.
@@ -74,66 +79,47 @@ __device__ __forceinline__ void rw_starts(const PlanArgs& A, bool write, char* s
   __syncthreads();
 }
 
-// Stable sort of the picks by expert, E + 1 bins (the last one: no expert).  A warp has
-// 128 consecutive picks and counts them bin by bin, 32 at a time, in its own row of
-// counters: lanes of equal bin find each other (match), so a pick knows how many of its
-// bin came before it in the warp.  Sums over the warps before, the CTAs before and the
-// bins below give its row.  COUNT: totals of every CTA alone, for picks of several CTAs.
-// WRITE: this CTA writes offsets.
-template <bool COUNT>
-__device__ __forceinline__ void rw_plan(const PlanArgs& A, int chunk, bool write, char* smem, PlanPicks& K) {
+// Stable sort of the picks by expert, E + 1 bins (the last one: no expert); a thread has
+// pick i = chunk * 1024 + tid, and is told its bin and row (-1: no such pick).  Lanes of
+// equal bin find each other (match), and a warp's counts of its bins go to its row of
+// counters; sums over the lanes and warps before, the chunks before and the bins below
+// give the row.  `write`: this CTA writes offsets.  Picks of several chunks have been
+// counted by the kernels before; what comes ahead of the totals needs nothing of those
+// and begins while they run (they have waited for whoever wrote the ids).
+// (Four picks a thread and a quarter of the CTAs took 12.4 us for 8192 x 9 picks, this 11.6;
+// 10.7 and 7.4 for 4096 x 8.)
+__device__ __forceinline__ void rw_plan(const PlanArgs& A, int chunk, bool write, char* smem, int* bin, int* row) {
   const int nb = A.E + 1;
   int* base = reinterpret_cast<int*>(smem);
   unsigned short* count = reinterpret_cast<unsigned short*>(base + nb + 32);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  K.first = chunk * RW_CHUNK + warp * 32 * RW_ROUNDS + lane;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, i = chunk * RW_CHUNK + tid;
   bool bad = false;
-#pragma unroll
-  for (int r = 0; r < RW_ROUNDS; ++r) {
-    const int i = K.first + 32 * r;
-    K.bin[r] = -1;
-    if (i < A.P) {
-      const long long e = A.id64 ? static_cast<const long long*>(A.ids)[i] : static_cast<const int*>(A.ids)[i];
-      bad = bad || e < -1 || e >= A.E;
-      K.bin[r] = e < 0 || e >= A.E ? A.E : static_cast<int>(e);
-    }
-  }
-  if (bad && !COUNT) atomicOr(A.status, STATUS_INDEX);
+  *bin = i < A.P ? rw_bin(A, i, &bad) : -1;
+  if (bad) atomicOr(A.status, STATUS_INDEX);
+  const uint32_t same = __match_any_sync(0xFFFFFFFFu, *bin);
+  const int rank = __popc(same & ((1u << lane) - 1u));
   __syncthreads();   // the counters are zero
-  unsigned short* mine = count + warp * nb;
-#pragma unroll
-  for (int r = 0; r < RW_ROUNDS; ++r) {
-    K.before[r] = 0;
-    if (chunk * RW_CHUNK + warp * 32 * RW_ROUNDS + 32 * r >= A.P) continue;   // (the whole warp)
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, K.bin[r]);
-    const int rank = __popc(same & ((1u << lane) - 1u));
-    const int old = K.bin[r] >= 0 ? mine[K.bin[r]] : 0;
-    __syncwarp();
-    if (K.bin[r] >= 0 && rank == 0) mine[K.bin[r]] = static_cast<unsigned short>(old + __popc(same));
-    __syncwarp();
-    K.before[r] = old + rank;
-  }
+  if (*bin >= 0 && rank == 0) count[warp * nb + *bin] = static_cast<unsigned short>(__popc(same));
   __syncthreads();
-  const int warps = min(32, (A.P - chunk * RW_CHUNK + 32 * RW_ROUNDS - 1) / (32 * RW_ROUNDS));   // those with picks
+  if (A.chunks > 1) asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int warps = min(32, (A.P - chunk * RW_CHUNK + 31) / 32);   // those with picks
   int all = 0, low = 0;
-  for (int b = tid; b < nb; b += RW_PLAN_THREADS) {
-    int run = 0;
+  for (int b = tid; b < nb; b += RW_CHUNK) {
+    int sum = 0, ahead = 0;
 #pragma unroll 8
     for (int w = 0; w < warps; ++w) {
       const int v = count[w * nb + b];
-      count[w * nb + b] = static_cast<unsigned short>(run);
-      run += v;
+      count[w * nb + b] = static_cast<unsigned short>(sum);
+      sum += v;
     }
-    if (COUNT) {
-      A.totals[static_cast<int64_t>(chunk) * nb + b] = run;
-      continue;
-    }
-    int sum = run, ahead = 0;
-    if (A.chunks > 1) {
+    if (A.chunks > RW_DIRECT_CHUNKS) {
+      ahead = A.totals[static_cast<int64_t>(chunk) * nb + b];
+      sum = A.totals[static_cast<int64_t>(A.chunks) * nb + b];
+    } else if (A.chunks > 1) {
       sum = 0;
 #pragma unroll 8
       for (int c = 0; c < A.chunks; ++c) {
-        const int v = A.totals[static_cast<int64_t>(c) * nb + b];
+        const int v = A.totals[c * nb + b];
         sum += v;
         ahead += c < chunk ? v : 0;
       }
@@ -145,39 +131,64 @@ __device__ __forceinline__ void rw_plan(const PlanArgs& A, int chunk, bool write
       base[b] = ahead;
     }
   }
-  if constexpr (!COUNT) rw_starts(A, write, smem, all, low);
+  rw_starts(A, write, smem, all, low);
+  *row = *bin >= 0 ? base[*bin] + count[warp * nb + *bin] + rank : -1;
 }
 
-// The row of a pick (those without an expert: behind all others).
-__device__ __forceinline__ int rw_row(const PlanPicks& K, int r, int nb, const char* smem) {
-  const int* base = reinterpret_cast<const int*>(smem);
-  const unsigned short* count = reinterpret_cast<const unsigned short*>(base + nb + 32);
-  const int b = K.bin[r];
-  return base[b] + count[(threadIdx.x >> 5) * nb + b] + K.before[r];
-}
-
-__device__ __forceinline__ void rw_clear_counts(char* smem, int nb) {
-  uint32_t* count = reinterpret_cast<uint32_t*>(smem + nb * 4 + 32 * 4);
-  for (int i = threadIdx.x; i < 16 * nb; i += RW_PLAN_THREADS) count[i] = 0;
-}
-
-template <bool COUNT>
-__global__ void __launch_bounds__(RW_PLAN_THREADS) k_rows_plan(const PlanArgs A) {
-  extern __shared__ __align__(16) char rw_smem[];
-  rw_clear_counts(rw_smem, A.E + 1);
+// totals[chunk]: how many picks of every bin a chunk has.
+__global__ void __launch_bounds__(RW_CHUNK, 1) k_rows_count(const PlanArgs A) {
+  __shared__ int count[RW_MAX_E + 1];
+  const int nb = A.E + 1;
+  for (int b = threadIdx.x; b < nb; b += RW_CHUNK) count[b] = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  PlanPicks K;
-  rw_plan<COUNT>(A, blockIdx.x, !COUNT && blockIdx.x == 0, rw_smem, K);
-  if constexpr (!COUNT) {
-#pragma unroll
-    for (int r = 0; r < RW_ROUNDS; ++r) {
-      if (K.bin[r] < 0) continue;
-      const int i = K.first + 32 * r, row = rw_row(K, r, A.E + 1, rw_smem);
-      A.order[row] = K.bin[r] < A.E ? i : -1;
-      A.place[i] = K.bin[r] < A.E ? row : -1;
+  __syncthreads();
+  const int i = blockIdx.x * RW_CHUNK + threadIdx.x;
+  bool bad;
+  if (i < A.P) atomicAdd(&count[rw_bin(A, i, &bad)], 1);
+  __syncthreads();
+  for (int b = threadIdx.x; b < nb; b += RW_CHUNK) A.totals[static_cast<int64_t>(blockIdx.x) * nb + b] = count[b];
+}
+
+// Many chunks: totals of the chunks before each, and of all, in their place.  A lane has a
+// bin, a warp a 32nd of the chunks.
+__global__ void __launch_bounds__(RW_CHUNK, 1) k_rows_scan(const PlanArgs A) {
+  __shared__ int sums[32][32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nb = A.E + 1, b = blockIdx.x * 32 + lane;
+  const int per = (A.chunks + 31) / 32, c0 = min(warp * per, A.chunks), c1 = min(c0 + per, A.chunks);
+  int* t = A.totals + b;
+  int sum = 0;
+  if (b < nb)
+#pragma unroll 8
+    for (int c = c0; c < c1; ++c) sum += t[static_cast<int64_t>(c) * nb];
+  sums[warp][lane] = sum;
+  __syncthreads();
+  int run = 0;
+  for (int w = 0; w < warp; ++w) run += sums[w][lane];
+  if (b < nb) {
+#pragma unroll 8
+    for (int c = c0; c < c1; ++c) {
+      const int v = t[static_cast<int64_t>(c) * nb];
+      t[static_cast<int64_t>(c) * nb] = run;
+      run += v;
     }
+    if (warp == 31) t[static_cast<int64_t>(A.chunks) * nb] = run;
   }
+}
+
+__global__ void __launch_bounds__(RW_CHUNK, 1) k_rows_plan(const PlanArgs A) {
+  extern __shared__ __align__(16) char rw_smem[];
+  rw_clear_counts(rw_smem, A.E + 1);
+  if (A.chunks == 1) asm volatile("griddepcontrol.wait;" ::: "memory");   // (else in rw_plan)
+  int bin, row;
+  rw_plan(A, blockIdx.x, blockIdx.x == 0, rw_smem, &bin, &row);
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (bin < 0) return;
+  const int i = blockIdx.x * RW_CHUNK + threadIdx.x;
+  A.order[row] = bin < A.E ? i : -1;
+  A.place[i] = bin < A.E ? row : -1;
 }
 
 // VEC 16-bit elements of a lane, as words (VEC 1: the low half).
@@ -293,50 +304,54 @@ __global__ void __launch_bounds__(512) k_rows_take(const RowArgs A) {
 }
 
 // The plan and the rows of up to RW_CHUNK picks in one launch: every CTA makes the plan
-// for itself (some 3 us, as long as a second launch and its wait take), the first one
-// writes it, and each takes some of the tokens' pieces.
+// for itself, the first one writes it, and each takes some of the tokens' pieces.  One
+// token 3.3 us and a launch's 2 us of the host less; as two launches 4.2.
 template <int VEC>
-__global__ void __launch_bounds__(RW_PLAN_THREADS) k_rows_small(const PlanArgs P, const RowArgs A) {
+__global__ void __launch_bounds__(RW_CHUNK, 1) k_rows_small(const PlanArgs P, const RowArgs A) {
   extern __shared__ __align__(16) char rw_smem[];
   const int nb = P.E + 1;
   int* place = reinterpret_cast<int*>(rw_smem + (rw_plan_smem(P.E) + 15) / 16 * 16);
   rw_clear_counts(rw_smem, nb);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  PlanPicks K;
-  rw_plan<false>(P, 0, blockIdx.x == 0, rw_smem, K);
-  const int present = reinterpret_cast<const int*>(rw_smem)[P.E];
-#pragma unroll
-  for (int r = 0; r < RW_ROUNDS; ++r) {
-    if (K.bin[r] < 0) continue;
-    const int i = K.first + 32 * r, row = rw_row(K, r, nb, rw_smem);
-    place[i] = K.bin[r] < P.E ? row : -1;
+  // a warp takes a piece of a token's row: the first one is under way while the plan is made
+  const int lane = threadIdx.x & 31, pieces = (A.H + 32 * VEC - 1) / (32 * VEC), warps = gridDim.x * (RW_CHUNK / 32);
+  int u = blockIdx.x * (RW_CHUNK / 32) + (threadIdx.x >> 5);
+  auto column = [&](int unit) { return unit % pieces * 32 * VEC + lane * VEC; };
+  auto load = [&](int unit) {
+    const int c = column(unit);
+    return unit < A.T * pieces && c < A.H ? rw_load<VEC>(A.tok + unit / pieces * A.ld_tok + c) : rw_zero<VEC>();
+  };
+  RowPiece<VEC> v = load(u);
+  int bin, row;
+  rw_plan(P, 0, blockIdx.x == 0, rw_smem, &bin, &row);
+  const int present = reinterpret_cast<const int*>(rw_smem)[P.E];   // (the only CTA of the plan: no pick lies before it)
+  if (bin >= 0) {
+    place[threadIdx.x] = bin < P.E ? row : -1;
     if (blockIdx.x == 0) {
-      P.order[row] = K.bin[r] < P.E ? i : -1;
-      P.place[i] = K.bin[r] < P.E ? row : -1;
+      P.order[row] = bin < P.E ? static_cast<int>(threadIdx.x) : -1;
+      P.place[threadIdx.x] = bin < P.E ? row : -1;
     }
   }
   __syncthreads();
-  // a warp takes a piece of a token's row
-  const int lane = threadIdx.x & 31, pieces = (A.H + 32 * VEC - 1) / (32 * VEC), warps = gridDim.x * (RW_PLAN_THREADS / 32);
-  for (int u = blockIdx.x * (RW_PLAN_THREADS / 32) + (threadIdx.x >> 5); u < A.T * pieces; u += warps) {
-    const int t = u / pieces, c = (u - t * pieces) * 32 * VEC + lane * VEC;
-    if (c >= A.H) continue;
-    const RowPiece<VEC> v = rw_load<VEC>(A.tok + t * A.ld_tok + c);
+  for (; u < A.T * pieces; u += warps, v = load(u)) {
+    const int t = u / pieces, c = column(u);
+    const int mine = lane < A.k ? place[t * A.k + lane] : -1;
     for (int j = 0; j < A.k; ++j) {
-      const int r = place[t * A.k + j];
-      if (r >= 0) rw_store<VEC>(A.row_out + r * A.ld_row_out + c, v);
+      const int r = __shfl_sync(0xFFFFFFFFu, mine, j);
+      if (r >= 0 && c < A.H) rw_store<VEC>(A.row_out + r * A.ld_row_out + c, v);
     }
   }
   for (int64_t r = present + blockIdx.x; r < P.P; r += gridDim.x)
-    for (int c = threadIdx.x * VEC; c < A.H; c += RW_PLAN_THREADS * VEC) rw_store<VEC>(A.row_out + r * A.ld_row_out + c, rw_zero<VEC>());
+    for (int c = threadIdx.x * VEC; c < A.H; c += RW_CHUNK * VEC) rw_store<VEC>(A.row_out + r * A.ld_row_out + c, rw_zero<VEC>());
 }
 
 // out[t] = sum over j, in order, of w[t, j] y[place[t, j]] in fp32, rounded once.  CTAs
 // go through tokens; the rows of NB picks are under way at a time, and the next
 // token's places and weights with them.
-template <int VEC, int NB>
+template <int VEC>
 __global__ void __launch_bounds__(512) k_rows_combine(const RowArgs A) {
+  constexpr int NB = 8;   // rows under way at a time
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   const int lane = threadIdx.x & 31;
@@ -454,6 +469,172 @@ __global__ void __launch_bounds__(512) k_rows_grad(const RowArgs A) {
     }
   }
   if constexpr (Y) rw_clear_tail<VEC>(A);
+}
+
+// ---------------------------------------------------------------------------
+// the same for many tokens: rows by way of shared memory
+// ---------------------------------------------------------------------------
+//
+// With rows in registers a warp has one batch of them under way, and the next only when
+// that has come: 8192 tokens of 9 rows of 1024 came at 2.9 TB/s with 20 warps an SM. Here
+// a warp has a ring of S slots of its own, each a piece (256 columns) of all k rows (and
+// of the token's, for the gradient), filled by the lanes' asynchronous copies (zeros where a
+// pick has no expert) S - 1 pieces ahead; every lane reads what it copied itself.
+// A CTA goes through tokens, its warps through a row's pieces.
+
+struct RowStream {
+  const RowArgs& A;
+  uint32_t smem;                    // this warp's ring
+  int slots, rows;                  // pieces ahead + 1, rows of a slot
+  int warps, warp, lane;
+  int t, piece, slot = 0;           // next piece to be fetched
+  int place, next_place;            // of token t and of the one after
+
+  __device__ __forceinline__ RowStream(const RowArgs& a, char* base, int slots_, int rows_)
+      : A(a), slots(slots_), rows(rows_), warps(blockDim.x >> 5), warp(threadIdx.x >> 5), lane(threadIdx.x & 31) {
+    smem = smem_u32(base) + static_cast<uint32_t>(warp * slots * rows * 512);
+    t = blockIdx.x;
+    piece = warp;
+    place = place_of(t);
+    next_place = place_of(t + gridDim.x);
+  }
+  __device__ __forceinline__ int place_of(int u) const { return u < A.T ? rw_place(A, u, lane) : -1; }
+  // Row `row` of a slot, this lane's 16 bytes.
+  __device__ __forceinline__ uint32_t at(int s, int row) const { return smem + static_cast<uint32_t>((s * rows + row) * 512 + lane * 16); }
+  // The next piece into the next slot: the k rows, and for TOK the token's own behind them.
+  template <bool TOK>
+  __device__ __forceinline__ void fetch() {
+    if (t < A.T) {
+      const int c = (piece * 32 + lane) * 8;
+      const bool in = c < A.H;
+      for (int j = 0; j < A.k; ++j) {
+        const int r = __shfl_sync(0xFFFFFFFFu, place, j);
+        copy16(at(slot, j), A.row + max(r, 0) * A.ld_row + (in ? c : 0), in && r >= 0);
+      }
+      if (TOK) copy16(at(slot, A.k), A.tok + t * A.ld_tok + (in ? c : 0), in);
+      piece += warps;
+      if (piece * 256 >= A.H) {
+        piece = warp;
+        t += gridDim.x;
+        place = next_place;
+        next_place = place_of(t + gridDim.x);
+      }
+    }
+    copies_commit();
+    slot = slot + 1 == slots ? 0 : slot + 1;
+  }
+};
+
+__device__ __forceinline__ RowPiece<8> rw_shared(uint32_t p) {
+  RowPiece<8> v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]) : "r"(p) : "memory");
+  return v;
+}
+
+// As k_rows_combine.  Rows and widths of whole 16-byte words.
+__global__ void __launch_bounds__(512) k_rows_combine_stream(const RowArgs A, int slots) {
+  extern __shared__ __align__(16) char rw_smem[];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  RowStream S(A, rw_smem, slots, A.k);
+  for (int i = 0; i < slots - 1; ++i) S.fetch<false>();
+  const int lane = S.lane;
+  auto weight_of = [&](int t) {
+    return t < A.T && lane < A.k && A.w ? rw_weight(A.w, static_cast<int64_t>(t) * A.k + lane, A.w_dt) : 1.0f;
+  };
+  float next_weight = weight_of(blockIdx.x);
+  int next_place = S.place_of(blockIdx.x), slot = 0;
+  for (int t = blockIdx.x; t < A.T; t += gridDim.x) {
+    const float weight = next_place >= 0 ? next_weight : 0.0f;   // (a pick without an expert: 0 times 0)
+    next_weight = weight_of(t + gridDim.x);
+    next_place = S.place_of(t + gridDim.x);
+    for (int piece = S.warp; piece * 256 < A.H; piece += S.warps) {
+      S.fetch<false>();
+      copies_wait(slots - 1);
+      float sum[8];
+#pragma unroll
+      for (float& s : sum) s = 0.0f;
+#pragma unroll 4
+      for (int j = 0; j < A.k; ++j) {
+        const float f = __shfl_sync(0xFFFFFFFFu, weight, j);
+        float y[8];
+        rw_float<8>(rw_shared(S.at(slot, j)), A.dt, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] = fmaf(f, y[i], sum[i]);
+      }
+      slot = slot + 1 == slots ? 0 : slot + 1;
+      const int c = (piece * 32 + lane) * 8;
+      if (c < A.H) rw_store<8>(A.tok_out + t * A.ld_tok + c, rw_pack<8>(sum, A.dt));
+    }
+  }
+}
+
+// As k_rows_grad with W.
+template <bool Y>
+__global__ void __launch_bounds__(512) k_rows_grad_stream(const RowArgs A, int slots) {
+  extern __shared__ __align__(16) char rw_smem[];
+  __shared__ float part[2][16][RW_MAX_K];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  RowStream S(A, rw_smem, slots, A.k + 1);
+  for (int i = 0; i < slots - 1; ++i) S.fetch<true>();
+  const int lane = S.lane;
+  auto weight_of = [&](int t) {
+    return Y && t < A.T && lane < A.k ? rw_weight(A.w, static_cast<int64_t>(t) * A.k + lane, A.w_dt) : 0.0f;
+  };
+  float next_weight = weight_of(blockIdx.x);
+  int next_place = S.place_of(blockIdx.x), slot = 0, turn = 0;
+  for (int t = blockIdx.x; t < A.T; t += gridDim.x, turn ^= 1) {
+    const float weight = next_weight;
+    const int place = next_place;
+    next_weight = weight_of(t + gridDim.x);
+    next_place = S.place_of(t + gridDim.x);
+    float dot[RW_MAX_K];
+#pragma unroll
+    for (float& d : dot) d = 0.0f;
+    for (int piece = S.warp; piece * 256 < A.H; piece += S.warps) {
+      S.fetch<true>();
+      copies_wait(slots - 1);
+      const int c = (piece * 32 + lane) * 8;
+      float e[8];
+      rw_float<8>(rw_shared(S.at(slot, A.k)), A.dt, e);
+#pragma unroll
+      for (int j = 0; j < RW_MAX_K; ++j) {
+        if (j >= A.k) break;
+        float y[8];
+        rw_float<8>(rw_shared(S.at(slot, j)), A.dt, y);
+        const int r = __shfl_sync(0xFFFFFFFFu, place, j);
+        if (Y) {
+          const float f = __shfl_sync(0xFFFFFFFFu, weight, j);
+          float g[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) g[i] = f * e[i];
+          if (c < A.H && r >= 0) rw_store<8>(A.row_out + r * A.ld_row_out + c, rw_pack<8>(g, A.dt));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dot[j] = fmaf(e[i], y[i], dot[j]);
+      }
+      slot = slot + 1 == slots ? 0 : slot + 1;
+    }
+#pragma unroll
+    for (int j = 0; j < RW_MAX_K; ++j) {
+      if (j >= A.k) break;
+      float d = dot[j];
+#pragma unroll
+      for (int s = 16; s > 0; s /= 2) d += __shfl_xor_sync(0xFFFFFFFFu, d, s);
+      if (lane == 0) part[turn][S.warp][j] = d;
+    }
+    __syncthreads();   // (the other turn's sums have been read: their reader has come here since)
+    if (S.warp == 0 && lane < A.k) {
+      float d = 0.0f;
+      for (int v = 0; v < S.warps; ++v) d += part[turn][v][lane];
+      if (place < 0) d = 0.0f;   // (an infinite d_out times no row's zeros)
+      const int64_t i = static_cast<int64_t>(t) * A.k + lane;
+      if (A.w_dt == 2) static_cast<float*>(A.d_w)[i] = d;
+      else static_cast<unsigned short*>(A.d_w)[i] = pack1(d, A.w_dt);
+    }
+  }
+  if constexpr (Y) rw_clear_tail<8>(A);
 }
 
 }  // namespace moe_op

@@ -124,7 +124,18 @@ def test_chained_kernels_promise_no_constant_inputs():
     path = os.path.join(os.path.dirname(_capi.__file__), "csrc", "moe_rows.cuh")
     text = re.sub(r"//[^\n]*", "", open(path).read())
     kernels = re.split(r"__global__", text)[1:]
-    assert len(kernels) == 5
+    assert len(kernels) == 9
     for kernel in kernels:
         head, body = kernel.split("{", 1)
         assert "griddepcontrol.wait" in body and "__restrict__" not in head
+
+
+def test_chunks_are_waited_for_before_their_totals():
+    """The plan of several chunks begins while they are counted, and waits before it adds them."""
+    text = open(os.path.join(os.path.dirname(_capi.__file__), "csrc", "moe_rows.cuh")).read()
+    body = text[text.index("void rw_plan("):]
+    assert body.index("griddepcontrol.wait") < body.index("A.totals[") < body.index("rw_starts(A, write")
+    # and whoever counts has waited for the ids before it lets the plan begin
+    for kernel in ("k_rows_count(", "k_rows_scan("):
+        k = text[text.index("void __launch_bounds__(RW_CHUNK, 1) " + kernel):]
+        assert k.index("griddepcontrol.wait") < k.index("griddepcontrol.launch_dependents") < k.index("A.totals")

@@ -15,6 +15,8 @@ CASES = [
     (455, 9, 496, 1024, "bf16", 0.03, 64), (456, 9, 31, 40, "bf16", 0.0, 3), (1025, 4, 1024, 16, "bf16", 0.05, 0),
     (3001, 7, 257, 72, "fp16", 0.02, 0), (20000, 9, 496, 8, "bf16", 0.01, 0), (40, 5, 9, 4104, "bf16", 0.3, 0),
     (600, 3, 8, 8200, "fp16", 0.0, 0), (16, 2, 1, 32, "bf16", 0.0, 0),
+    (128, 8, 40, 48, "bf16", 0.1, 0), (129, 8, 1024, 48, "bf16", 0.1, 0), (16384, 8, 77, 16, "fp16", 0.02, 0),
+    (16385, 8, 1000, 16, "bf16", 0.1, 0), (100, 16, 64, 2056, "bf16", 0.05, 8), (700, 16, 20, 520, "fp16", 0.0, 0),
 ]
 
 
@@ -380,6 +382,24 @@ def test_offsets_past_32_bits(pkg):
     assert torch.equal(out, x)        # eight equal rows: exact
     d = op.combine_backward(out, rows, w, plan, need=("y",))
     assert torch.equal(d.y[-3000:], (x[tail // k].float() * 0.125).bfloat16())
+    assert op.device_status() == 0
+
+
+@pytest.mark.parametrize("T,k,E", [(1 << 20, 16, 1024), (200001, 7, 300)])
+def test_millions_of_picks(pkg, T, k, E):
+    op = handle(pkg, T, k, E, "bf16")
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    ids = torch.randint(-1, E, (T, k), generator=gen, device="cuda", dtype=torch.int32)
+    x = torch.arange(T, device="cuda", dtype=torch.int32).view(torch.int16).reshape(T, 2).view(torch.bfloat16)   # a row's number
+    rows, plan = op.dispatch(x, ids)
+    key = torch.where(ids < 0, E, ids).reshape(-1)
+    order = torch.argsort(key, stable=True)
+    n = int((key < E).sum())
+    assert plan.offsets.tolist() == torch.searchsorted(key[order].contiguous(), torch.arange(E + 1, device="cuda", dtype=torch.int32)).tolist()
+    assert torch.equal(plan.order[:n].long(), order[:n]) and (plan.order[n:] == -1).all()
+    assert torch.equal(plan.place.reshape(-1)[order[:n]].long(), torch.arange(n, device="cuda"))
+    assert (plan.place[ids < 0] == -1).all()
+    assert torch.equal(rows[:n].view(torch.int16), x[order[:n] // k].view(torch.int16)) and not rows[n:].view(torch.int16).any()
     assert op.device_status() == 0
 
 
