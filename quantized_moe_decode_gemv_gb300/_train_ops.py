@@ -93,63 +93,72 @@ class ExpertRows(_Handle):
         self._i32, self._id_bytes = torch.int32, {torch.int32: 4, torch.int64: 8}
         self._w_types = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
-    def _rows_of(self, x, what: str, rows=None):
-        """(row stride, width) of a 2-D tensor of ``rows`` rows."""
-        shape = x.shape
-        if len(shape) != 2 or (rows is not None and shape[0] != rows):
-            raise MoEError(_SHAPE, f"{what} must be [{'T' if rows is None else rows}, H], not {list(shape)}")
-        return self._stride(x, shape[1], what), shape[1]
+    # A decode call's kernel takes a few microseconds: arguments are checked by plain comparisons,
+    # and reasons are found when one fails.
 
-    def _ids(self, ids):
-        if len(ids.shape) != 2 or ids.shape[1] != self._k:
-            raise MoEError(_SHAPE, f"ids must be [T, {self._k}], not {list(ids.shape)}")
+    def _ids(self, ids) -> int:
+        shape = ids.shape
+        if len(shape) != 2 or shape[1] != self._k:
+            raise MoEError(_SHAPE, f"ids must be [T, {self._k}], not {list(shape)}")
         if ids.dtype not in self._id_bytes or ids.device != self.device or not ids.is_contiguous():
             raise MoEError(_INVALID_ARG, f"ids must be a contiguous int32 or int64 tensor on {self.device}")
-        if ids.shape[0] > self.config.max_tokens:
-            raise MoEError(_INVALID_ARG, f"{ids.shape[0]} tokens, max_tokens is {self.config.max_tokens}")
-        return ids.shape[0]
+        if shape[0] > self.config.max_tokens:
+            raise MoEError(_INVALID_ARG, f"{shape[0]} tokens, max_tokens is {self.config.max_tokens}")
+        return shape[0]
 
-    def _plan(self, plan, T=None):
-        """T of a plan, its tensors checked."""
-        offsets, order, place = plan
-        if T is None:
-            T = place.shape[0]
-        for t, shape, what in ((offsets, (self._E + 1,), "offsets"), (order, (T * self._k,), "order"),
-                               (place, (T, self._k), "place")):
+    def _width(self, x, rows: int, what: str) -> int:
+        shape = x.shape
+        if len(shape) != 2 or shape[0] != rows:
+            raise MoEError(_SHAPE, f"{what} must be [{rows}, H], not {list(shape)}")
+        return shape[1]
+
+    def _bad_plan(self, plan, T):
+        for t, shape, what in zip(plan, ((self._E + 1,), (T * self._k,), (T, self._k)), RowPlan._fields):
             if t.shape != shape:
                 raise MoEError(_SHAPE, f"the plan's {what} must be {list(shape)}, not {list(t.shape)}")
-            if t.dtype is not self._i32 or t.device != self.device or not t.is_contiguous():
-                raise MoEError(_INVALID_ARG, f"the plan's {what} must be a contiguous int32 tensor on {self.device}")
+        raise MoEError(_INVALID_ARG, f"the plan must be three contiguous int32 tensors on {self.device}")
+
+    def _plan(self, plan) -> int:
+        """T of a plan, its tensors checked."""
+        offsets, order, place = plan
+        T, i32, device = place.shape[0], self._i32, self.device
+        if not (place.shape == (T, self._k) and order.shape == (T * self._k,) and offsets.shape == (self._E + 1,) and
+                place.dtype is i32 and order.dtype is i32 and offsets.dtype is i32 and place.device == device and
+                order.device == device and offsets.device == device and place.is_contiguous() and order.is_contiguous() and
+                offsets.is_contiguous()):
+            self._bad_plan(plan, T)
+        if T > self.config.max_tokens:
+            raise MoEError(_INVALID_ARG, f"a plan of {T} tokens, max_tokens is {self.config.max_tokens}")
         return T
 
-    def _weights(self, w, T):
+    def _weights(self, w, T: int) -> int:
         if w.shape != (T, self._k):
             raise MoEError(_SHAPE, f"w must be [{T}, {self._k}], not {list(w.shape)}")
         if w.dtype not in self._w_types or w.device != self.device or not w.is_contiguous():
             raise MoEError(_INVALID_ARG, f"w must be a contiguous fp32, bf16 or fp16 tensor on {self.device}")
         return self._w_types[w.dtype]
 
-    def _out(self, out, rows, H, what, where):
-        """(tensor, row stride) of an output that may be given."""
-        if out is None:
-            with where:
-                return self._empty((rows, H), dtype=self._dtype, device=self.device), H
-        ld = self._stride(out, H, what)
+    def _given(self, out, rows: int, H: int) -> int:
+        """Row stride of an output that the caller gives."""
+        ld = self._stride(out, H, "out")
         if out.shape[0] != rows:
-            raise MoEError(_SHAPE, f"{what} has {out.shape[0]} rows, not {rows}")
-        return out, ld
+            raise MoEError(_SHAPE, f"out has {out.shape[0]} rows, not {rows}")
+        return ld
 
-    def _new_plan(self, T, where) -> RowPlan:
-        empty, device, i32 = self._empty, self.device, self._i32
-        with where:
-            return RowPlan(empty((self._E + 1,), dtype=i32, device=device),
-                           empty((T * self._k,), dtype=i32, device=device), empty((T, self._k), dtype=i32, device=device))
+    def _new_plan(self, T: int) -> RowPlan:
+        k, empty, i32, device = self._k, self._empty, self._i32, self.device
+        return RowPlan(empty((self._E + 1,), dtype=i32, device=device), empty((T * k,), dtype=i32, device=device),
+                       empty((T, k), dtype=i32, device=device))
+
+    def _new(self, rows: int, H: int):
+        return self._empty((rows, H), dtype=self._dtype, device=self.device)
 
     def plan(self, ids, stream=None) -> RowPlan:
         """The plan of ids [T, k] alone."""
         T = self._ids(ids)
         s, where = self._stream(stream, ids)
-        p = self._new_plan(T, where)
+        with where:
+            p = self._new_plan(T)
         status = self._lib.moe_rows_plan(self.handle, ids.data_ptr(), self._id_bytes[ids.dtype], T, p[0].data_ptr(),
                                          p[1].data_ptr(), p[2].data_ptr(), s)
         if status:
@@ -159,10 +168,15 @@ class ExpertRows(_Handle):
     def dispatch(self, x, ids, out=None, stream=None):
         """(rows [T k, H], plan) of x [T, H] (rows may be strided) and ids [T, k]."""
         T = self._ids(ids)
-        ldx, H = self._rows_of(x, "x", T)
+        H = ldo = self._width(x, T, "x")
+        ldx = self._stride(x, H, "x")
+        if out is not None:
+            ldo = self._given(out, T * self._k, H)
         s, where = self._stream(stream, x, ids, out)
-        out, ldo = self._out(out, T * self._k, H, "out", where)
-        p = self._new_plan(T, where)
+        with where:
+            if out is None:
+                out = self._new(T * self._k, H)
+            p = self._new_plan(T)
         status = self._lib.moe_rows_dispatch(self.handle, x.data_ptr(), ldx, T, H, ids.data_ptr(), self._id_bytes[ids.dtype],
                                              p[0].data_ptr(), p[1].data_ptr(), p[2].data_ptr(), out.data_ptr(), ldo, s)
         if status:
@@ -172,9 +186,14 @@ class ExpertRows(_Handle):
     def take(self, x, plan, out=None, stream=None):
         """rows [T k, H] of x [T, H] by a plan that is there already."""
         T = self._plan(plan)
-        ldx, H = self._rows_of(x, "x", T)
+        H = ldo = self._width(x, T, "x")
+        ldx = self._stride(x, H, "x")
+        if out is not None:
+            ldo = self._given(out, T * self._k, H)
         s, where = self._stream(stream, x, out, *plan)
-        out, ldo = self._out(out, T * self._k, H, "out", where)
+        if out is None:
+            with where:
+                out = self._new(T * self._k, H)
         status = self._lib.moe_rows_take(self.handle, x.data_ptr(), ldx, T, H, plan[0].data_ptr(), plan[2].data_ptr(),
                                          out.data_ptr(), ldo, s)
         if status:
@@ -183,10 +202,15 @@ class ExpertRows(_Handle):
 
     def _combine(self, y, w, plan, out, stream, what):
         T = self._plan(plan)
-        ldy, H = self._rows_of(y, what, T * self._k)
+        H = ldo = self._width(y, T * self._k, what)
+        ldy = self._stride(y, H, what)
         wt = 2 if w is None else self._weights(w, T)
+        if out is not None:
+            ldo = self._given(out, T, H)
         s, where = self._stream(stream, y, w, out, *plan)
-        out, ldo = self._out(out, T, H, "out", where)
+        if out is None:
+            with where:
+                out = self._new(T, H)
         status = self._lib.moe_rows_combine(self.handle, y.data_ptr(), ldy, T, H, None if w is None else w.data_ptr(), wt,
                                             plan[2].data_ptr(), out.data_ptr(), ldo, s)
         if status:
@@ -209,14 +233,16 @@ class ExpertRows(_Handle):
             if n not in RowGrads._fields:
                 raise MoEError(_INVALID_ARG, f"need names {', '.join(RowGrads._fields)}")
         T = self._plan(plan)
-        ldd, H = self._rows_of(d_out, "d_out", T)
-        ldy, Hy = self._rows_of(y, "y", T * self._k)
-        if Hy != H:
-            raise MoEError(_SHAPE, f"y is {Hy} wide, d_out {H}")
+        P = T * self._k
+        H = self._width(d_out, T, "d_out")
+        ldd = self._stride(d_out, H, "d_out")
+        if self._width(y, P, "y") != H:
+            raise MoEError(_SHAPE, f"y is {y.shape[1]} wide, d_out {H}")
+        ldy = self._stride(y, H, "y")
         wt = self._weights(w, T)
         s, where = self._stream(stream, d_out, y, w, *plan)
         with where:
-            d_y = self._empty((T * self._k, H), dtype=self._dtype, device=self.device) if "y" in need else None
+            d_y = self._new(P, H) if "y" in need else None
             d_w = self._empty((T, self._k), dtype=w.dtype, device=self.device) if "w" in need else None
         status = self._lib.moe_rows_combine_backward(
             self.handle, d_out.data_ptr(), ldd, T, H, y.data_ptr(), ldy, w.data_ptr(), wt, plan[0].data_ptr(),
