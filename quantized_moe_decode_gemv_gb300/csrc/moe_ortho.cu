@@ -206,7 +206,8 @@ moe_status forward(moe_ortho* h, const void* g, int64_t ldg, int64_t step_g, int
   t.M = c.rows;
   t.N = c.cols;
   const int64_t pieces = R * ((C + 7) / 8);
-  t.ctas = static_cast<int>(std::min<int64_t>({OR_NORM_CTAS, (pieces + 1023) / 1024, tiles(8ll * h->num_sms, n)}));
+  // (a CTA for up to 32 K elements: a second kernel and its wait would take longer)
+  t.ctas = pieces <= 4096 ? 1 : static_cast<int>(std::min<int64_t>({OR_NORM_CTAS, (pieces + 1023) / 1024, tiles(8ll * h->num_sms, n)}));
   t.part = h->sums;
   t.hi = h->hi[0];
   t.lo = h->lo;
@@ -230,9 +231,12 @@ moe_status forward(moe_ortho* h, const void* g, int64_t ldg, int64_t step_g, int
     p.lo += z * t.step_lo;
     p.done += 3ll * z;
     const dim3 grid(static_cast<unsigned>(t.ctas), static_cast<unsigned>(nz));
-    e = launch_chained(k_ortho_norm, grid, 256, 0, 1, s, p);
+    if (t.ctas > 1) {
+      e = launch_chained(k_ortho_norm, grid, 256, 0, 1, s, p);
+      ++h->last_launches;
+    }
     if (e == cudaSuccess) e = launch_chained(k_ortho_start, grid, 256, 0, 1, s, p);
-    h->last_launches += 2;
+    ++h->last_launches;
   }
 
   const Plan P = plan_of(c, n, h->workers);

@@ -658,15 +658,20 @@ __device__ __forceinline__ void or_elements(const OrthoStart& A, int z, F&& f) {
   }
 }
 
-// Squares summed in fp32 in three ranges (of 2^-40 and 2^40), each scaled into the
-// middle: a square of any fp32 value neither overflows nor vanishes.
-__global__ void __launch_bounds__(256) k_ortho_norm(const OrthoStart A) {
-  __shared__ float sums[8][3];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
-  const int z = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// A CTA's share of a matrix's squares, summed in fp32: eight at a time where their sum is far
+// from fp32's ends, else each in one of three ranges (of 2^-40 and 2^40) that is scaled
+// into the middle, so that no square overflows or vanishes.  sums[0..2]: the ranges.
+__device__ __forceinline__ void or_squares(const OrthoStart& A, int z, float (*warps)[3], float* sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float s[3] = {0.0f, 0.0f, 0.0f};
   or_elements(A, z, [&](int, int, const float (&v)[8]) {
+    float t = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t = fmaf(v[j], v[j], t);
+    if (t > 0x1p-80f && t < 0x1p80f) {
+      s[1] += t;
+      return;
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float x = fabsf(v[j]);
@@ -683,29 +688,42 @@ __global__ void __launch_bounds__(256) k_ortho_norm(const OrthoStart A) {
   for (int k = 0; k < 3; ++k) {
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) s[k] += __shfl_xor_sync(0xFFFFFFFFu, s[k], d);
-    if (lane == 0) sums[warp][k] = s[k];
+    if (lane == 0) warps[warp][k] = s[k];
   }
   __syncthreads();
   if (threadIdx.x < 3) {
     float t = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) t += sums[w][threadIdx.x];
-    A.part[(static_cast<int64_t>(z) * OR_NORM_CTAS + blockIdx.x) * 3 + threadIdx.x] = t;
+    for (int w = 0; w < 8; ++w) t += warps[w][threadIdx.x];
+    sums[threadIdx.x] = t;
   }
 }
 
-// X = hi + lo in fp16.  Every CTA adds the matrix's partial sums in order; the factor
-// s / (|G| + eps) is applied as two, so that it has 64-bit numbers' range.
+__global__ void __launch_bounds__(256) k_ortho_norm(const OrthoStart A) {
+  __shared__ float warps[8][3];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  or_squares(A, blockIdx.y, warps, A.part + (static_cast<int64_t>(blockIdx.y) * OR_NORM_CTAS + blockIdx.x) * 3);
+}
+
+// X = hi + lo in fp16.  Every CTA adds the matrix's partial sums in order (one that has the
+// matrix alone makes them); the factor s / (|G| + eps) is applied as two, so that it has
+// 64-bit numbers' range.
 __global__ void __launch_bounds__(256) k_ortho_start(const OrthoStart A) {
-  __shared__ float factor[2];
+  __shared__ float factor[2], warps[8][3], alone[3];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   const int z = blockIdx.y;
+  if (A.ctas == 1) {
+    or_squares(A, z, warps, alone);
+    __syncthreads();
+  }
   if (threadIdx.x < 32) {
+    const float* part = A.ctas == 1 ? alone : A.part + static_cast<int64_t>(z) * OR_NORM_CTAS * 3;
     double t[3] = {0.0, 0.0, 0.0};
     for (int i = threadIdx.x; i < A.ctas; i += 32)
 #pragma unroll
-      for (int k = 0; k < 3; ++k) t[k] += A.part[(static_cast<int64_t>(z) * OR_NORM_CTAS + i) * 3 + k];
+      for (int k = 0; k < 3; ++k) t[k] += part[i * 3 + k];
     double sum = t[0] * 0x1p-120 + t[1] + t[2] * 0x1p120;
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
