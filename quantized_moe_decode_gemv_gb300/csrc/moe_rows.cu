@@ -74,54 +74,46 @@ bool meet(const Rows& a, const Rows& b) {
   return a.ld != b.ld || rows_overlap(a.p, a.ld, a.cols, b.p, b.ld, b.cols, std::max(a.n, b.n));
 }
 
-// As many elements a lane as all rows' addresses allow: 8, 2 or 1.
-int vector_of(std::initializer_list<Rows> all) {
+// Whether all rows are whole 16-byte words.
+bool whole_words(std::initializer_list<Rows> all) {
   int64_t bits = all.begin()->cols * 2;
   for (const Rows& r : all)
     if (r.p) bits |= static_cast<int64_t>(reinterpret_cast<uintptr_t>(r.p)) | (r.n > 1 ? r.ld * 2 : 0);
-  return bits % 16 == 0 ? 8 : bits % 4 == 0 ? 2 : 1;
+  return bits % 16 == 0;
 }
 
-// A warp for each piece of a row, up to 8; up to 16 where tokens alone do not fill the SMs.
-int row_threads(int T, int H, int vec, int sms) {
-  const int pieces = (H + 32 * vec - 1) / (32 * vec);
-  return 32 * std::min(pieces, T < 2 * sms ? 16 : 8);
-}
+// A CTA's warps: one for each 256 columns, up to 8; up to 16 where tokens alone do not fill the SMs.
+int row_warps(int T, int H, int sms) { return std::min((H + 255) / 256, T < 2 * sms ? 16 : 8); }
 
-using RowKernel = void (*)(const RowArgs);
-
-RowKernel take_kernel(int vec) { return vec == 8 ? k_rows_take<8> : vec == 2 ? k_rows_take<2> : k_rows_take<1>; }
-// (rows and widths of whole 16-byte words go by way of shared memory instead)
-RowKernel combine_kernel(int vec) { return vec == 2 ? k_rows_combine<2> : k_rows_combine<1>; }
-using SmallKernel = void (*)(const PlanArgs, const RowArgs);
-SmallKernel small_kernel(int vec) { return vec == 8 ? k_rows_small<8> : vec == 2 ? k_rows_small<2> : k_rows_small<1>; }
 int small_smem(int E, int P) { return (rw_plan_smem(E) + 15) / 16 * 16 + 4 * P; }
-template <bool Y, bool W>
-RowKernel grad_kernel_t(int vec) { return vec == 2 ? k_rows_grad<2, Y, W> : k_rows_grad<1, Y, W>; }
-RowKernel grad_kernel(int vec, bool y, bool w) {
-  if (!w) return vec == 8 ? k_rows_grad<8, true, false> : grad_kernel_t<true, false>(vec);
-  return y ? grad_kernel_t<true, true>(vec) : grad_kernel_t<false, true>(vec);
+using RowKernel = void (*)(const RowArgs);
+using StreamKernel = void (*)(const RowArgs, int);
+
+StreamKernel grad_kernel(bool aligned, bool y) {
+  if (aligned) return y ? k_rows_grad<true, true> : k_rows_grad<true, false>;
+  return y ? k_rows_grad<false, true> : k_rows_grad<false, false>;
 }
 
 // A CTA's warps and slots of `rows` rows.  One piece under way a warp and many warps beat
 // several and few: on 8192 tokens of 9 rows of 1024, 2 slots (20 warps an SM) 31.5 us, 3 (12
 // warps) 41; few rows take more slots, 2 KB under way a warp.
-constexpr int kStreamSmem = 8 * 2 * (RW_MAX_K + 1) * 512;   // the most it may be
+constexpr int kStreamSmem = 8 * 2 * (RW_MAX_K + 1) * rw_slot_row(false);   // the most it may be
 struct StreamShape {
   int threads, slots, smem, ctas;
 };
-StreamShape stream_shape(int T, int H, int rows, int sms) {
+StreamShape stream_shape(int T, int H, int rows, bool aligned, int sms) {
   StreamShape s;
-  const int pieces = (H + 255) / 256;
-  // (up to 16 warps a token where tokens alone do not fill the SMs)
-  const int warps = std::min(pieces, T < 2 * sms && 16 * std::max(2, 2048 / (rows * 512) + 1) * rows * 512 <= kStreamSmem ? 16 : 8);
-  s.threads = 32 * warps;
   s.slots = std::max(2, 2048 / (rows * 512) + 1);   // (at most 5)
-  s.smem = warps * s.slots * rows * 512;
+  const int slot = rows * rw_slot_row(aligned);
+  int warps = row_warps(T, H, sms);
+  if (warps * s.slots * slot > kStreamSmem) warps = 8;
+  s.threads = 32 * warps;
+  s.smem = warps * s.slots * slot;
   const int fit = std::max(1, std::min({2048 / s.threads, 220 * 1024 / (s.smem + 2048), 32}));
   s.ctas = std::min(T, sms * fit);
   return s;
 }
+
 bool misaligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 
 moe_status fail(moe_rows* h, moe_status st, const char* msg) {
@@ -206,9 +198,6 @@ RowArgs row_args(moe_rows* h, int32_t T, int32_t width, const int32_t* offsets, 
   return a;
 }
 
-// CTAs that go through tokens: as many as run at once.
-int token_ctas(int T, int threads, int sms) { return std::min(T, sms * (2048 / threads)); }
-
 moe_status plan(moe_rows* h, const void* ids, int32_t id_bytes, int32_t T, int32_t* offsets, int32_t* order, int32_t* place,
                 void* stream) {
   if (!h) return MOE_ERR_INVALID_ARG;
@@ -256,18 +245,19 @@ moe_status take(moe_rows* h, bool with_plan, const void* x, int64_t ldx, int32_t
   a.ld_tok = ldx;
   a.row_out = static_cast<unsigned short*>(rows);
   a.ld_row_out = ld_rows;
-  const int vec = T > 0 ? vector_of({in, out}) : 1;
+  const bool aligned = whole_words({in, out});
   if (with_plan && T > 0 && P <= RW_CHUNK) {
-    const int64_t pieces = static_cast<int64_t>(T) * ((width + 32 * vec - 1) / (32 * vec));
+    const int64_t pieces = static_cast<int64_t>(T) * ((width + 255) / 256);
     ++h->last_launches;
-    return launched(h, launch_chained(small_kernel(vec), std::min<int64_t>(h->num_sms, (pieces + 7) / 8), RW_CHUNK,
+    return launched(h, launch_chained(aligned ? k_rows_small<true> : k_rows_small<false>, std::min<int64_t>(h->num_sms, (pieces + 7) / 8), RW_CHUNK,
                                       static_cast<size_t>(small_smem(a.E, static_cast<int>(P))), 1, s,
                                       plan_args(h, ids, id_bytes, T, offsets, order, place), a));
   }
   cudaError_t e = with_plan ? launch_plan(h, plan_args(h, ids, id_bytes, T, offsets, order, place), s) : cudaSuccess;
   if (e == cudaSuccess && T > 0) {
     ++h->last_launches;
-    e = launch_chained(take_kernel(vec), T, row_threads(T, width, vec, h->num_sms), 0, 1, s, a);
+    const RowKernel k = aligned ? k_rows_take<true> : k_rows_take<false>;
+    e = launch_chained(k, T, 32 * row_warps(T, width, h->num_sms), 0, 1, s, a);
   }
   return launched(h, e);
 }
@@ -298,15 +288,11 @@ moe_status combine(moe_rows* h, const void* y, int64_t ldy, int32_t T, int32_t w
   a.ld_tok = ldo;
   a.w = w;
   a.w_dt = w_dtype;
-  const int vec = vector_of({in, to}), threads = row_threads(T, width, vec, h->num_sms);
+  const bool aligned = whole_words({in, to});
+  const StreamShape f = stream_shape(T, width, a.k, aligned, h->num_sms);
   ++h->last_launches;
-  if (vec == 8) {
-    const StreamShape f = stream_shape(T, width, a.k, h->num_sms);
-    return launched(h, launch_chained(k_rows_combine_stream, f.ctas, f.threads, static_cast<size_t>(f.smem), 1,
-                                      static_cast<cudaStream_t>(stream), a, f.slots));
-  }
-  return launched(h, launch_chained(combine_kernel(vec), token_ctas(T, threads, h->num_sms), threads, 0, 1,
-                                    static_cast<cudaStream_t>(stream), a));
+  return launched(h, launch_chained(aligned ? k_rows_combine<true> : k_rows_combine<false>, f.ctas, f.threads,
+                                    static_cast<size_t>(f.smem), 1, static_cast<cudaStream_t>(stream), a, f.slots));
 }
 
 moe_status combine_backward(moe_rows* h, const void* d_out, int64_t ldd, int32_t T, int32_t width, const void* y, int64_t ldy,
@@ -344,15 +330,15 @@ moe_status combine_backward(moe_rows* h, const void* d_out, int64_t ldd, int32_t
   a.w = w;
   a.d_w = d_w;
   a.w_dt = w_dtype;
-  const int vec = vector_of({e, in, to}), threads = row_threads(T, width, vec, h->num_sms);
+  const bool aligned = whole_words({e, in, to});
   ++h->last_launches;
-  if (d_w && vec == 8) {
-    const StreamShape f = stream_shape(T, width, a.k + 1, h->num_sms);
-    return launched(h, launch_chained(d_y ? k_rows_grad_stream<true> : k_rows_grad_stream<false>, f.ctas, f.threads,
-                                      static_cast<size_t>(f.smem), 1, static_cast<cudaStream_t>(stream), a, f.slots));
+  if (!d_w) {
+    const RowKernel k = aligned ? k_rows_scale<true> : k_rows_scale<false>;
+    return launched(h, launch_chained(k, T, 32 * row_warps(T, width, h->num_sms), 0, 1, static_cast<cudaStream_t>(stream), a));
   }
-  return launched(h, launch_chained(grad_kernel(vec, d_y != nullptr, d_w != nullptr), token_ctas(T, threads, h->num_sms), threads,
-                                    0, 1, static_cast<cudaStream_t>(stream), a));
+  const StreamShape f = stream_shape(T, width, a.k + 1, aligned, h->num_sms);
+  return launched(h, launch_chained(grad_kernel(aligned, d_y != nullptr), f.ctas, f.threads, static_cast<size_t>(f.smem), 1,
+                                    static_cast<cudaStream_t>(stream), a, f.slots));
 }
 
 // (h: the handle while it is not the caller's, for the entry point to free when an exception ends this)
@@ -385,13 +371,14 @@ moe_status create(const moe_rows_config* cfg, moe_rows** out, moe_rows*& h) {
     e = h->alloc(reinterpret_cast<void**>(&h->totals), static_cast<size_t>(chunks + 1) * (cfg->n_experts + 1) * 4);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k_rows_plan), cudaFuncAttributeMaxDynamicSharedMemorySize, rw_plan_smem(RW_MAX_E));
-  for (int vec : {1, 2, 8})
+  for (auto k : {k_rows_small<true>, k_rows_small<false>})
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(reinterpret_cast<const void*>(small_kernel(vec)), cudaFuncAttributeMaxDynamicSharedMemorySize,
+      e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                small_smem(RW_MAX_E, RW_CHUNK));
-  for (const void* k : {reinterpret_cast<const void*>(k_rows_combine_stream), reinterpret_cast<const void*>(k_rows_grad_stream<true>),
-                        reinterpret_cast<const void*>(k_rows_grad_stream<false>)})
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem);
+  for (StreamKernel k : {k_rows_combine<true>, k_rows_combine<false>, grad_kernel(true, true), grad_kernel(true, false),
+                         grad_kernel(false, true), grad_kernel(false, false)})
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();   // the status word's clear runs on the default stream
   if (e != cudaSuccess) {
     g_error = std::string("create: ") + cudaGetErrorString(e);

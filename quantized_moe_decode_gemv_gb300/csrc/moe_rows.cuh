@@ -191,55 +191,26 @@ __global__ void __launch_bounds__(RW_CHUNK, 1) k_rows_plan(const PlanArgs A) {
   A.place[i] = bin < A.E ? row : -1;
 }
 
-// VEC 16-bit elements of a lane, as words (VEC 1: the low half).
-template <int VEC>
+// Eight 16-bit elements of a lane, as four words.
 struct RowPiece {
-  uint32_t w[VEC > 1 ? VEC / 2 : 1];
+  uint32_t w[4];
 };
-template <int VEC>
-__device__ __forceinline__ RowPiece<VEC> rw_load(const unsigned short* p) {
-  RowPiece<VEC> v;
-  if constexpr (VEC == 8) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    v.w[0] = u.x, v.w[1] = u.y, v.w[2] = u.z, v.w[3] = u.w;
-  } else if constexpr (VEC == 2) {
-    v.w[0] = *reinterpret_cast<const uint32_t*>(p);
-  } else {
-    v.w[0] = *p;
-  }
-  return v;
+__device__ __forceinline__ RowPiece rw_load(const unsigned short* p) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  return RowPiece{{u.x, u.y, u.z, u.w}};
 }
-template <int VEC>
-__device__ __forceinline__ void rw_store(unsigned short* p, const RowPiece<VEC>& v) {
-  if constexpr (VEC == 8) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
-  } else if constexpr (VEC == 2) {
-    *reinterpret_cast<uint32_t*>(p) = v.w[0];
-  } else {
-    *p = static_cast<unsigned short>(v.w[0]);
-  }
+__device__ __forceinline__ void rw_store(unsigned short* p, const RowPiece& v) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
 }
-template <int VEC>
-__device__ __forceinline__ RowPiece<VEC> rw_zero() {
-  RowPiece<VEC> v;
+__device__ __forceinline__ RowPiece rw_zero() { return RowPiece{{0, 0, 0, 0}}; }
+__device__ __forceinline__ void rw_float(const RowPiece& v, int dt, float (&f)[8]) {
 #pragma unroll
-  for (uint32_t& w : v.w) w = 0;
-  return v;
+  for (int j = 0; j < 8; ++j) f[j] = j & 1 ? hi16(v.w[j / 2], dt) : lo16(v.w[j / 2], dt);
 }
-template <int VEC>
-__device__ __forceinline__ void rw_float(const RowPiece<VEC>& v, int dt, float (&f)[VEC]) {
+__device__ __forceinline__ RowPiece rw_pack(const float (&f)[8], int dt) {
+  RowPiece v;
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) f[j] = j & 1 ? hi16(v.w[j / 2], dt) : lo16(v.w[j / 2], dt);
-}
-template <int VEC>
-__device__ __forceinline__ RowPiece<VEC> rw_pack(const float (&f)[VEC], int dt) {
-  RowPiece<VEC> v;
-  if constexpr (VEC == 1) {
-    v.w[0] = pack1(f[0], dt);
-  } else {
-#pragma unroll
-    for (int j = 0; j < VEC; j += 2) v.w[j / 2] = pack2(f[j], f[j + 1], dt);
-  }
+  for (int j = 0; j < 8; j += 2) v.w[j / 2] = pack2(f[j], f[j + 1], dt);
   return v;
 }
 
@@ -276,37 +247,115 @@ __device__ __forceinline__ int rw_place(const RowArgs& A, int t, int lane) {
   return r;
 }
 
-// Rows from offsets[E] on belong to no pick: zero, so that what is summed over all rows
-// later (a weight gradient) needs to know no length.
-template <int VEC>
-__device__ __forceinline__ void rw_clear_tail(const RowArgs& A) {
+// ---------------------------------------------------------------------------
+// rows of any address and width, 256 columns a warp at a time
+// ---------------------------------------------------------------------------
+//
+// A lane has 8 consecutive elements of a piece as four words.  Where all rows are whole
+// 16-byte words (ALIGNED) it loads and stores just those.  Else rows begin anywhere in a
+// word of 16 bytes: a piece is read as the 33 whole words that hold it, and a lane cuts its
+// elements out of two of them; it is stored as whole words, made of two lanes' elements, with
+// the ends of a piece element by element.  (An element a lane at a time, 8192 tokens of 9
+// rows of 1001 came back in 117 us and went out in 51; XXX and XXX this way.)
+
+// Eight elements from word 0..4 on, `odd`: from its second half.
+__device__ __forceinline__ RowPiece rw_cut(const uint32_t (&x)[5], bool odd) {
+  RowPiece v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v.w[i] = odd ? __funnelshift_r(x[i], x[i + 1], 16) : x[i];
+  return v;
+}
+
+// How many elements into its 16-byte word a row begins.
+__device__ __forceinline__ int rw_shift(const unsigned short* p) { return static_cast<int>((reinterpret_cast<uintptr_t>(p) >> 1) & 7); }
+
+// A piece's elements to `row` (its first column: piece * 256; H columns in all) by the
+// whole warp.
+template <bool ALIGNED>
+__device__ __forceinline__ void rw_put(unsigned short* row, int piece, int H, const RowPiece& v, int lane) {
+  const int c = (piece * 32 + lane) * 8;
+  if (ALIGNED) {
+    if (c < H) rw_store(row + c, v);
+    return;
+  }
+  const int shift = rw_shift(row);
+  // the lane's word of 16 bytes: `shift` elements of the lane before, then its own
+  uint32_t x[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = __shfl_up_sync(0xFFFFFFFFu, v.w[i], 1);
+    x[4 + i] = v.w[i];
+  }
+  // from element 8 - shift of these 16 on: whole words by halves, then the odd element
+  const int from = 8 - shift;
+#pragma unroll
+  for (int d = 4; d > 0; d /= 2)
+    if (from / 2 & d)
+#pragma unroll
+      for (int i = 0; i < 8 - d; ++i) x[i] = x[i + d];
+  const uint32_t y[5] = {x[0], x[1], x[2], x[3], x[4]};   // (the fifth counts for odd shifts only)
+  const RowPiece g = rw_cut(y, from & 1);
+  unsigned short* word = row + c - shift;
+  if ((lane > 0 || shift == 0) && c + 8 - shift <= H) {
+    rw_store(word, g);
+  } else if (c < H || lane > 0) {   // the first word of a piece, and what is left of the row
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if ((lane > 0 || i >= shift) && c - shift + i < H) word[i] = static_cast<unsigned short>(i & 1 ? g.w[i / 2] >> 16 : g.w[i / 2]);
+  }
+  if (lane == 31 && shift) {   // the last elements of the piece: the next word's first
+#pragma unroll
+    for (int i = 1; i < 8; ++i)
+      if (i >= from && c + i < H) row[c + i] = static_cast<unsigned short>(i & 1 ? v.w[i / 2] >> 16 : v.w[i / 2]);
+  }
+}
+
+// A lane's elements of a row of x, zeros past the last.
+template <bool ALIGNED>
+__device__ __forceinline__ RowPiece rw_get(const unsigned short* row, int piece, int H, int lane) {
+  const int c = (piece * 32 + lane) * 8;
+  RowPiece v = rw_zero();
+  if (ALIGNED) {
+    if (c < H) v = rw_load(row + c);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < H) v.w[i / 2] |= static_cast<uint32_t>(row[c + i]) << (i & 1 ? 16 : 0);
+  }
+  return v;
+}
+
+// Rows from `first` on belong to no pick: zero, so that what is summed over all rows later (a
+// weight gradient) needs to know no length.
+template <bool ALIGNED>
+__device__ __forceinline__ void rw_clear_tail(const RowArgs& A, int first) {
   const int P = A.T * A.k;
-  for (int64_t r = max(A.offsets[A.E], 0) + static_cast<int64_t>(blockIdx.x); r < P; r += gridDim.x)
-    for (int c = threadIdx.x * VEC; c < A.H; c += blockDim.x * VEC) rw_store<VEC>(A.row_out + r * A.ld_row_out + c, rw_zero<VEC>());
+  for (int64_t r = max(first, 0) + static_cast<int64_t>(blockIdx.x); r < P; r += gridDim.x)
+    for (int piece = threadIdx.x >> 5; piece * 256 < A.H; piece += blockDim.x >> 5)
+      rw_put<ALIGNED>(A.row_out + r * A.ld_row_out, piece, A.H, rw_zero(), threadIdx.x & 31);
 }
 
 // rows[place[t, j]] = x[t].
-template <int VEC>
-__global__ void __launch_bounds__(512) k_rows_take(const RowArgs A) {
+template <bool ALIGNED>
+__global__ void __launch_bounds__(512, 1) k_rows_take(const RowArgs A) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   const int t = blockIdx.x, lane = threadIdx.x & 31;
   const int place = rw_place(A, t, lane);
-  for (int c = threadIdx.x * VEC; c - lane * VEC < A.H; c += blockDim.x * VEC) {
-    const bool in = c < A.H;
-    const RowPiece<VEC> v = in ? rw_load<VEC>(A.tok + t * A.ld_tok + c) : rw_zero<VEC>();
+  for (int piece = threadIdx.x >> 5; piece * 256 < A.H; piece += blockDim.x >> 5) {
+    const RowPiece v = rw_get<ALIGNED>(A.tok + t * A.ld_tok, piece, A.H, lane);
     for (int j = 0; j < A.k; ++j) {
       const int r = __shfl_sync(0xFFFFFFFFu, place, j);
-      if (in && r >= 0) rw_store<VEC>(A.row_out + r * A.ld_row_out + c, v);
+      if (r >= 0) rw_put<ALIGNED>(A.row_out + r * A.ld_row_out, piece, A.H, v, lane);
     }
   }
-  rw_clear_tail<VEC>(A);
+  rw_clear_tail<ALIGNED>(A, A.offsets[A.E]);
 }
 
 // The plan and the rows of up to RW_CHUNK picks in one launch: every CTA makes the plan
 // for itself, the first one writes it, and each takes some of the tokens' pieces.  One
 // token 3.3 us and a launch's 2 us of the host less; as two launches 4.2.
-template <int VEC>
+template <bool ALIGNED>
 __global__ void __launch_bounds__(RW_CHUNK, 1) k_rows_small(const PlanArgs P, const RowArgs A) {
   extern __shared__ __align__(16) char rw_smem[];
   const int nb = P.E + 1;
@@ -315,14 +364,12 @@ __global__ void __launch_bounds__(RW_CHUNK, 1) k_rows_small(const PlanArgs P, co
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   // a warp takes a piece of a token's row: the first one is under way while the plan is made
-  const int lane = threadIdx.x & 31, pieces = (A.H + 32 * VEC - 1) / (32 * VEC), warps = gridDim.x * (RW_CHUNK / 32);
+  const int lane = threadIdx.x & 31, pieces = (A.H + 255) / 256, warps = gridDim.x * (RW_CHUNK / 32);
   int u = blockIdx.x * (RW_CHUNK / 32) + (threadIdx.x >> 5);
-  auto column = [&](int unit) { return unit % pieces * 32 * VEC + lane * VEC; };
   auto load = [&](int unit) {
-    const int c = column(unit);
-    return unit < A.T * pieces && c < A.H ? rw_load<VEC>(A.tok + unit / pieces * A.ld_tok + c) : rw_zero<VEC>();
+    return unit < A.T * pieces ? rw_get<ALIGNED>(A.tok + unit / pieces * A.ld_tok, unit % pieces, A.H, lane) : rw_zero();
   };
-  RowPiece<VEC> v = load(u);
+  RowPiece v = load(u);
   int bin, row;
   rw_plan(P, 0, blockIdx.x == 0, rw_smem, &bin, &row);
   const int present = reinterpret_cast<const int*>(rw_smem)[P.E];   // (the only CTA of the plan: no pick lies before it)
@@ -335,154 +382,32 @@ __global__ void __launch_bounds__(RW_CHUNK, 1) k_rows_small(const PlanArgs P, co
   }
   __syncthreads();
   for (; u < A.T * pieces; u += warps, v = load(u)) {
-    const int t = u / pieces, c = column(u);
+    const int t = u / pieces;
     const int mine = lane < A.k ? place[t * A.k + lane] : -1;
     for (int j = 0; j < A.k; ++j) {
       const int r = __shfl_sync(0xFFFFFFFFu, mine, j);
-      if (r >= 0 && c < A.H) rw_store<VEC>(A.row_out + r * A.ld_row_out + c, v);
+      if (r >= 0) rw_put<ALIGNED>(A.row_out + r * A.ld_row_out, u % pieces, A.H, v, lane);
     }
   }
-  for (int64_t r = present + blockIdx.x; r < P.P; r += gridDim.x)
-    for (int c = threadIdx.x * VEC; c < A.H; c += RW_CHUNK * VEC) rw_store<VEC>(A.row_out + r * A.ld_row_out + c, rw_zero<VEC>());
+  rw_clear_tail<ALIGNED>(A, present);
 }
 
-// out[t] = sum over j, in order, of w[t, j] y[place[t, j]] in fp32, rounded once.  CTAs
-// go through tokens; the rows of NB picks are under way at a time, and the next
-// token's places and weights with them.
-template <int VEC>
-__global__ void __launch_bounds__(512) k_rows_combine(const RowArgs A) {
-  constexpr int NB = 8;   // rows under way at a time
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
-  const int lane = threadIdx.x & 31;
-  auto place_of = [&](int t) { return t < A.T ? rw_place(A, t, lane) : -1; };
-  auto weight_of = [&](int t) {
-    return t < A.T && lane < A.k && A.w ? rw_weight(A.w, static_cast<int64_t>(t) * A.k + lane, A.w_dt) : 1.0f;
-  };
-  int next_place = place_of(blockIdx.x);
-  float next_weight = weight_of(blockIdx.x);
-  for (int t = blockIdx.x; t < A.T; t += gridDim.x) {
-    const int place = next_place;
-    const float weight = place >= 0 ? next_weight : 0.0f;   // (a pick without an expert: 0 times 0)
-    next_place = place_of(t + gridDim.x);
-    next_weight = weight_of(t + gridDim.x);
-    for (int c = threadIdx.x * VEC; c - lane * VEC < A.H; c += blockDim.x * VEC) {
-      const bool in = c < A.H;
-      float sum[VEC];
-#pragma unroll
-      for (float& s : sum) s = 0.0f;
-      for (int j0 = 0; j0 < A.k; j0 += NB) {
-        RowPiece<VEC> v[NB];
-#pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          const int r = __shfl_sync(0xFFFFFFFFu, place, j0 + j);   // (lanes from k on: -1)
-          v[j] = in && r >= 0 ? rw_load<VEC>(A.row + r * A.ld_row + c) : rw_zero<VEC>();
-        }
-#pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          const float f = __shfl_sync(0xFFFFFFFFu, weight, j0 + j);
-          float y[VEC];
-          rw_float<VEC>(v[j], A.dt, y);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) sum[i] = fmaf(f, y[i], sum[i]);
-        }
-      }
-      if (in) rw_store<VEC>(A.tok_out + t * A.ld_tok + c, rw_pack<VEC>(sum, A.dt));
-    }
-  }
+// The sums over rows have a ring in shared memory for each warp.  With rows in registers
+// a warp has one batch of them under way, and the next only when that has come: 8192
+// tokens of 9 rows of 1024 came at 2.9 TB/s with 20 warps an SM, 5.3 with the ring.  A slot
+// is a piece of all k rows (and of the token's, for the gradient), filled by the lanes'
+// asynchronous copies, zeros where a pick has no expert, slots - 1 pieces ahead.  A
+// CTA goes through tokens, its warps through a row's pieces.
+
+__device__ __forceinline__ void rw_copy_part(uint32_t dst, const void* src, int bytes) {   // of 16; the others zero
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// d_y[place[t, j]] = w[t, j] d_out[t];  d_w[t, j] = <d_out[t], y[place[t, j]]>: a lane's
-// part of all k sums stays in registers over the row; lanes and warps are added in a
-// fixed order.  (W: d_w is wanted; Y: d_y is.)  CTAs go through tokens as above.
-template <int VEC, bool Y, bool W>
-__global__ void __launch_bounds__(512) k_rows_grad(const RowArgs A) {
-  constexpr int NB = VEC == 8 ? 8 : 4;   // rows under way at a time
-  __shared__ float part[2][16][RW_MAX_K];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  auto place_of = [&](int t) { return t < A.T ? rw_place(A, t, lane) : -1; };
-  auto weight_of = [&](int t) {
-    return Y && t < A.T && lane < A.k ? rw_weight(A.w, static_cast<int64_t>(t) * A.k + lane, A.w_dt) : 0.0f;
-  };
-  int next_place = place_of(blockIdx.x), turn = 0;
-  float next_weight = weight_of(blockIdx.x);
-  for (int t = blockIdx.x; t < A.T; t += gridDim.x, turn ^= 1) {
-    const int place = next_place;
-    const float weight = next_weight;
-    next_place = place_of(t + gridDim.x);
-    next_weight = weight_of(t + gridDim.x);
-    float dot[RW_MAX_K];
-#pragma unroll
-    for (float& d : dot) d = 0.0f;
-    for (int c = threadIdx.x * VEC; c - lane * VEC < A.H; c += blockDim.x * VEC) {
-      const bool in = c < A.H;
-      float e[VEC];
-      rw_float<VEC>(in ? rw_load<VEC>(A.tok + t * A.ld_tok + c) : rw_zero<VEC>(), A.dt, e);
-#pragma unroll
-      for (int j0 = 0; j0 < RW_MAX_K; j0 += NB) {
-        if (j0 >= A.k) break;
-        RowPiece<VEC> v[NB];
-        int r[NB];
-#pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          r[j] = __shfl_sync(0xFFFFFFFFu, place, j0 + j);
-          if (W && in && r[j] >= 0) v[j] = rw_load<VEC>(A.row + r[j] * A.ld_row + c);
-        }
-#pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          const float f = Y ? __shfl_sync(0xFFFFFFFFu, weight, j0 + j) : 0.0f;
-          if (!in || r[j] < 0) continue;
-          if (Y) {
-            float g[VEC];
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) g[i] = f * e[i];
-            rw_store<VEC>(A.row_out + r[j] * A.ld_row_out + c, rw_pack<VEC>(g, A.dt));
-          }
-          if (W) {
-            float y[VEC];
-            rw_float<VEC>(v[j], A.dt, y);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) dot[j0 + j] = fmaf(e[i], y[i], dot[j0 + j]);
-          }
-        }
-      }
-    }
-    if constexpr (W) {
-#pragma unroll
-      for (int j = 0; j < RW_MAX_K; ++j) {
-        if (j >= A.k) break;
-        float d = dot[j];
-#pragma unroll
-        for (int s = 16; s > 0; s /= 2) d += __shfl_xor_sync(0xFFFFFFFFu, d, s);
-        if (lane == 0) part[turn][warp][j] = d;
-      }
-      __syncthreads();   // (the other turn's sums have been read: their reader has come here since)
-      if (warp == 0 && lane < A.k) {
-        float d = 0.0f;
-        for (int v = 0; v < static_cast<int>(blockDim.x) / 32; ++v) d += part[turn][v][lane];
-        const int64_t i = static_cast<int64_t>(t) * A.k + lane;
-        if (A.w_dt == 2) static_cast<float*>(A.d_w)[i] = d;
-        else static_cast<unsigned short*>(A.d_w)[i] = pack1(d, A.w_dt);
-      }
-    }
-  }
-  if constexpr (Y) rw_clear_tail<VEC>(A);
-}
+__host__ __device__ constexpr int rw_slot_row(bool aligned) { return aligned ? 512 : 528; }   // bytes of a piece in a slot
 
-// ---------------------------------------------------------------------------
-// the same for many tokens: rows by way of shared memory
-// ---------------------------------------------------------------------------
-//
-// With rows in registers a warp has one batch of them under way, and the next only when
-// that has come: 8192 tokens of 9 rows of 1024 came at 2.9 TB/s with 20 warps an SM. Here
-// a warp has a ring of S slots of its own, each a piece (256 columns) of all k rows (and
-// of the token's, for the gradient), filled by the lanes' asynchronous copies (zeros where a
-// pick has no expert) S - 1 pieces ahead; every lane reads what it copied itself.
-// A CTA goes through tokens, its warps through a row's pieces.
-
+template <bool ALIGNED>
 struct RowStream {
+  static constexpr int ROW = rw_slot_row(ALIGNED);
   const RowArgs& A;
   uint32_t smem;                    // this warp's ring
   int slots, rows;                  // pieces ahead + 1, rows of a slot
@@ -492,26 +417,45 @@ struct RowStream {
 
   __device__ __forceinline__ RowStream(const RowArgs& a, char* base, int slots_, int rows_)
       : A(a), slots(slots_), rows(rows_), warps(blockDim.x >> 5), warp(threadIdx.x >> 5), lane(threadIdx.x & 31) {
-    smem = smem_u32(base) + static_cast<uint32_t>(warp * slots * rows * 512);
+    smem = smem_u32(base) + static_cast<uint32_t>(warp * slots * rows * ROW);
     t = blockIdx.x;
     piece = warp;
     place = place_of(t);
     next_place = place_of(t + gridDim.x);
   }
   __device__ __forceinline__ int place_of(int u) const { return u < A.T ? rw_place(A, u, lane) : -1; }
-  // Row `row` of a slot, this lane's 16 bytes.
-  __device__ __forceinline__ uint32_t at(int s, int row) const { return smem + static_cast<uint32_t>((s * rows + row) * 512 + lane * 16); }
+  __device__ __forceinline__ uint32_t at(int s, int row) const { return smem + static_cast<uint32_t>((s * rows + row) * ROW); }
+
+  // The piece of one row into a slot (here: there is such a row).
+  __device__ __forceinline__ void copy(uint32_t to, const unsigned short* row, bool here) {
+    const int c = (piece * 32 + lane) * 8;
+    if (ALIGNED) {
+      const bool in = here && c < A.H;
+      copy16(to + static_cast<uint32_t>(lane * 16), row + (in ? c : 0), in);
+    } else {
+      // whole words from the one that the piece begins in: what is read before the row's first element
+      // shares its word, and nothing behind its last one is read
+      const int shift = rw_shift(row);
+      const unsigned short* word = row + c - shift;
+      const int left = here ? (A.H - (c - shift)) * 2 : 0;   // bytes of the row from there on
+      const int own = max(0, min(16, left));
+      rw_copy_part(to + static_cast<uint32_t>(lane * 16), own ? word : row - shift, own);
+      if (lane == 31) {
+        const int next = max(0, min(2 * shift, left - 16));
+        rw_copy_part(to + 512, next ? word + 8 : row - shift, next);
+      }
+    }
+  }
   // The next piece into the next slot: the k rows, and for TOK the token's own behind them.
   template <bool TOK>
   __device__ __forceinline__ void fetch() {
+    if (!ALIGNED) __syncwarp();   // the slot has been read
     if (t < A.T) {
-      const int c = (piece * 32 + lane) * 8;
-      const bool in = c < A.H;
       for (int j = 0; j < A.k; ++j) {
         const int r = __shfl_sync(0xFFFFFFFFu, place, j);
-        copy16(at(slot, j), A.row + max(r, 0) * A.ld_row + (in ? c : 0), in && r >= 0);
+        copy(at(slot, j), A.row + max(r, 0) * A.ld_row, r >= 0);
       }
-      if (TOK) copy16(at(slot, A.k), A.tok + t * A.ld_tok + (in ? c : 0), in);
+      if (TOK) copy(at(slot, A.k), A.tok + t * A.ld_tok, true);
       piece += warps;
       if (piece * 256 >= A.H) {
         piece = warp;
@@ -523,21 +467,38 @@ struct RowStream {
     copies_commit();
     slot = slot + 1 == slots ? 0 : slot + 1;
   }
+  // until the oldest piece has come
+  __device__ __forceinline__ void wait() const {
+    copies_wait(slots - 1);
+    if (!ALIGNED) __syncwarp();
+  }
+  // This lane's elements of a slot's row, which begins at `row` in memory.
+  __device__ __forceinline__ RowPiece read(int s, int j, const unsigned short* row) const {
+    if (ALIGNED) {
+      RowPiece v;
+      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3])
+                   : "r"(at(s, j) + static_cast<uint32_t>(lane * 16))
+                   : "memory");
+      return v;
+    }
+    const int shift = rw_shift(row);
+    const uint32_t p = at(s, j) + static_cast<uint32_t>((shift >> 1) * 4 + lane * 16);
+    uint32_t x[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x[i]) : "r"(p + static_cast<uint32_t>(i * 4)) : "memory");
+    return rw_cut(x, shift & 1);
+  }
 };
 
-__device__ __forceinline__ RowPiece<8> rw_shared(uint32_t p) {
-  RowPiece<8> v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]) : "r"(p) : "memory");
-  return v;
-}
-
-// As k_rows_combine.  Rows and widths of whole 16-byte words.
-__global__ void __launch_bounds__(512) k_rows_combine_stream(const RowArgs A, int slots) {
+// out[t] = sum over j, in order, of w[t, j] y[place[t, j]] in fp32, rounded once.
+template <bool ALIGNED>
+__global__ void __launch_bounds__(512, 1) k_rows_combine(const RowArgs A, int slots) {
   extern __shared__ __align__(16) char rw_smem[];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  RowStream S(A, rw_smem, slots, A.k);
-  for (int i = 0; i < slots - 1; ++i) S.fetch<false>();
+  RowStream<ALIGNED> S(A, rw_smem, slots, A.k);
+  for (int i = 0; i < slots - 1; ++i) S.template fetch<false>();
   const int lane = S.lane;
   auto weight_of = [&](int t) {
     return t < A.T && lane < A.k && A.w ? rw_weight(A.w, static_cast<int64_t>(t) * A.k + lane, A.w_dt) : 1.0f;
@@ -545,39 +506,42 @@ __global__ void __launch_bounds__(512) k_rows_combine_stream(const RowArgs A, in
   float next_weight = weight_of(blockIdx.x);
   int next_place = S.place_of(blockIdx.x), slot = 0;
   for (int t = blockIdx.x; t < A.T; t += gridDim.x) {
-    const float weight = next_place >= 0 ? next_weight : 0.0f;   // (a pick without an expert: 0 times 0)
+    const int place = next_place;
+    const float weight = place >= 0 ? next_weight : 0.0f;   // (a pick without an expert: 0 times 0)
     next_weight = weight_of(t + gridDim.x);
     next_place = S.place_of(t + gridDim.x);
     for (int piece = S.warp; piece * 256 < A.H; piece += S.warps) {
-      S.fetch<false>();
-      copies_wait(slots - 1);
+      S.template fetch<false>();
+      S.wait();
       float sum[8];
 #pragma unroll
       for (float& s : sum) s = 0.0f;
 #pragma unroll 4
       for (int j = 0; j < A.k; ++j) {
         const float f = __shfl_sync(0xFFFFFFFFu, weight, j);
+        const int r = ALIGNED ? 0 : __shfl_sync(0xFFFFFFFFu, place, j);
         float y[8];
-        rw_float<8>(rw_shared(S.at(slot, j)), A.dt, y);
+        rw_float(S.read(slot, j, A.row + max(r, 0) * A.ld_row), A.dt, y);
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum[i] = fmaf(f, y[i], sum[i]);
       }
       slot = slot + 1 == slots ? 0 : slot + 1;
-      const int c = (piece * 32 + lane) * 8;
-      if (c < A.H) rw_store<8>(A.tok_out + t * A.ld_tok + c, rw_pack<8>(sum, A.dt));
+      rw_put<ALIGNED>(A.tok_out + t * A.ld_tok, piece, A.H, rw_pack(sum, A.dt), lane);
     }
   }
 }
 
-// As k_rows_grad with W.
-template <bool Y>
-__global__ void __launch_bounds__(512) k_rows_grad_stream(const RowArgs A, int slots) {
+// d_y[place[t, j]] = w[t, j] d_out[t];  d_w[t, j] = <d_out[t], y[place[t, j]]>: a lane's
+// part of all k sums stays in registers over the row; lanes and warps are added in a
+// fixed order.  (Y: d_y is wanted.)
+template <bool ALIGNED, bool Y>
+__global__ void __launch_bounds__(512, 1) k_rows_grad(const RowArgs A, int slots) {
   extern __shared__ __align__(16) char rw_smem[];
   __shared__ float part[2][16][RW_MAX_K];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  RowStream S(A, rw_smem, slots, A.k + 1);
-  for (int i = 0; i < slots - 1; ++i) S.fetch<true>();
+  RowStream<ALIGNED> S(A, rw_smem, slots, A.k + 1);
+  for (int i = 0; i < slots - 1; ++i) S.template fetch<true>();
   const int lane = S.lane;
   auto weight_of = [&](int t) {
     return Y && t < A.T && lane < A.k ? rw_weight(A.w, static_cast<int64_t>(t) * A.k + lane, A.w_dt) : 0.0f;
@@ -593,23 +557,22 @@ __global__ void __launch_bounds__(512) k_rows_grad_stream(const RowArgs A, int s
 #pragma unroll
     for (float& d : dot) d = 0.0f;
     for (int piece = S.warp; piece * 256 < A.H; piece += S.warps) {
-      S.fetch<true>();
-      copies_wait(slots - 1);
-      const int c = (piece * 32 + lane) * 8;
+      S.template fetch<true>();
+      S.wait();
       float e[8];
-      rw_float<8>(rw_shared(S.at(slot, A.k)), A.dt, e);
+      rw_float(S.read(slot, A.k, A.tok + t * A.ld_tok), A.dt, e);
 #pragma unroll
       for (int j = 0; j < RW_MAX_K; ++j) {
         if (j >= A.k) break;
-        float y[8];
-        rw_float<8>(rw_shared(S.at(slot, j)), A.dt, y);
         const int r = __shfl_sync(0xFFFFFFFFu, place, j);
+        float y[8];
+        rw_float(S.read(slot, j, A.row + max(r, 0) * A.ld_row), A.dt, y);
         if (Y) {
           const float f = __shfl_sync(0xFFFFFFFFu, weight, j);
           float g[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) g[i] = f * e[i];
-          if (c < A.H && r >= 0) rw_store<8>(A.row_out + r * A.ld_row_out + c, rw_pack<8>(g, A.dt));
+          if (r >= 0) rw_put<ALIGNED>(A.row_out + r * A.ld_row_out, piece, A.H, rw_pack(g, A.dt), lane);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) dot[j] = fmaf(e[i], y[i], dot[j]);
@@ -634,7 +597,30 @@ __global__ void __launch_bounds__(512) k_rows_grad_stream(const RowArgs A, int s
       else static_cast<unsigned short*>(A.d_w)[i] = pack1(d, A.w_dt);
     }
   }
-  if constexpr (Y) rw_clear_tail<8>(A);
+  if (Y) rw_clear_tail<ALIGNED>(A, A.offsets[A.E]);
+}
+
+// d_y alone: no row is read.
+template <bool ALIGNED>
+__global__ void __launch_bounds__(512, 1) k_rows_scale(const RowArgs A) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int t = blockIdx.x, lane = threadIdx.x & 31;
+  const int place = rw_place(A, t, lane);
+  const float weight = lane < A.k ? rw_weight(A.w, static_cast<int64_t>(t) * A.k + lane, A.w_dt) : 0.0f;
+  for (int piece = threadIdx.x >> 5; piece * 256 < A.H; piece += blockDim.x >> 5) {
+    float e[8];
+    rw_float(rw_get<ALIGNED>(A.tok + t * A.ld_tok, piece, A.H, lane), A.dt, e);
+    for (int j = 0; j < A.k; ++j) {
+      const int r = __shfl_sync(0xFFFFFFFFu, place, j);
+      const float f = __shfl_sync(0xFFFFFFFFu, weight, j);
+      float g[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[i] = f * e[i];
+      if (r >= 0) rw_put<ALIGNED>(A.row_out + r * A.ld_row_out, piece, A.H, rw_pack(g, A.dt), lane);
+    }
+  }
+  rw_clear_tail<ALIGNED>(A, A.offsets[A.E]);
 }
 
 }  // namespace moe_op

@@ -17,6 +17,8 @@ CASES = [
     (600, 3, 8, 8200, "fp16", 0.0, 0), (16, 2, 1, 32, "bf16", 0.0, 0),
     (128, 8, 40, 48, "bf16", 0.1, 0), (129, 8, 1024, 48, "bf16", 0.1, 0), (16384, 8, 77, 16, "fp16", 0.02, 0),
     (16385, 8, 1000, 16, "bf16", 0.1, 0), (100, 16, 64, 2056, "bf16", 0.05, 8), (700, 16, 20, 520, "fp16", 0.0, 0),
+    (200, 3, 12, 1, "fp16", 0.2, 0), (300, 4, 12, 255, "bf16", 0.3, 1), (300, 4, 12, 257, "fp16", 0.3, 2), (330, 9, 50, 2049, "bf16", 0.1, 5),
+    (90, 5, 12, 4097, "fp16", 0.3, 0),
 ]
 
 
