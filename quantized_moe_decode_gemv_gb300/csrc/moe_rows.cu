@@ -89,11 +89,6 @@ int small_smem(int E, int P) { return (rw_plan_smem(E) + 15) / 16 * 16 + 4 * P; 
 using RowKernel = void (*)(const RowArgs);
 using StreamKernel = void (*)(const RowArgs, int);
 
-StreamKernel grad_kernel(bool aligned, bool y) {
-  if (aligned) return y ? k_rows_grad<true, true> : k_rows_grad<true, false>;
-  return y ? k_rows_grad<false, true> : k_rows_grad<false, false>;
-}
-
 // A CTA's warps and slots of `rows` rows.  One piece under way a warp and many warps beat
 // several and few: on 8192 tokens of 9 rows of 1024, 2 slots (20 warps an SM) 31.5 us, 3 (12
 // warps) 41; few rows take more slots, 2 KB under way a warp.
@@ -330,15 +325,23 @@ moe_status combine_backward(moe_rows* h, const void* d_out, int64_t ldd, int32_t
   a.w = w;
   a.d_w = d_w;
   a.w_dt = w_dtype;
-  const bool aligned = whole_words({e, in, to});
-  ++h->last_launches;
-  if (!d_w) {
-    const RowKernel k = aligned ? k_rows_scale<true> : k_rows_scale<false>;
-    return launched(h, launch_chained(k, T, 32 * row_warps(T, width, h->num_sms), 0, 1, static_cast<cudaStream_t>(stream), a));
+  // Both gradients in one kernel where rows are whole words.  Else cutting and joining words takes
+  // the registers of too many warps: 8192 x 9 x 1001 in one kernel 131 us, in two 57 + 36.
+  const bool aligned = whole_words({e, in, to}), both = aligned && d_y && d_w;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t err = cudaSuccess;
+  if (d_w) {
+    const StreamShape f = stream_shape(T, width, a.k + 1, aligned, h->num_sms);
+    const StreamKernel k = both ? k_rows_grad<true, true> : aligned ? k_rows_grad<true, false> : k_rows_grad<false, false>;
+    ++h->last_launches;
+    err = launch_chained(k, f.ctas, f.threads, static_cast<size_t>(f.smem), 1, s, a, f.slots);
   }
-  const StreamShape f = stream_shape(T, width, a.k + 1, aligned, h->num_sms);
-  return launched(h, launch_chained(grad_kernel(aligned, d_y != nullptr), f.ctas, f.threads, static_cast<size_t>(f.smem), 1,
-                                    static_cast<cudaStream_t>(stream), a, f.slots));
+  if (d_y && !both && err == cudaSuccess) {
+    const RowKernel k = aligned ? k_rows_scale<true> : k_rows_scale<false>;
+    ++h->last_launches;
+    err = launch_chained(k, T, 32 * row_warps(T, width, h->num_sms), 0, 1, s, a);
+  }
+  return launched(h, err);
 }
 
 // (h: the handle while it is not the caller's, for the entry point to free when an exception ends this)
@@ -375,8 +378,8 @@ moe_status create(const moe_rows_config* cfg, moe_rows** out, moe_rows*& h) {
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                small_smem(RW_MAX_E, RW_CHUNK));
-  for (StreamKernel k : {k_rows_combine<true>, k_rows_combine<false>, grad_kernel(true, true), grad_kernel(true, false),
-                         grad_kernel(false, true), grad_kernel(false, false)})
+  for (StreamKernel k : {k_rows_combine<true>, k_rows_combine<false>, k_rows_grad<true, true>, k_rows_grad<true, false>,
+                         k_rows_grad<false, false>})
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();   // the status word's clear runs on the default stream

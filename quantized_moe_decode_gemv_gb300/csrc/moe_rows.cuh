@@ -256,7 +256,8 @@ __device__ __forceinline__ int rw_place(const RowArgs& A, int t, int lane) {
 // word of 16 bytes: a piece is read as the 33 whole words that hold it, and a lane cuts its
 // elements out of two of them; it is stored as whole words, made of two lanes' elements, with
 // the ends of a piece element by element.  (An element a lane at a time, 8192 tokens of 9
-// rows of 1001 came back in 117 us and went out in 51; XXX and XXX this way.)
+// rows of 1001 came back in 117 us and went out in 51; 48 and 36 this way, 31 and 25 at
+// 1024, where the traffic alone takes 25.)
 
 // Eight elements from word 0..4 on, `odd`: from its second half.
 __device__ __forceinline__ RowPiece rw_cut(const uint32_t (&x)[5], bool odd) {
@@ -295,19 +296,18 @@ __device__ __forceinline__ void rw_put(unsigned short* row, int piece, int H, co
       for (int i = 0; i < 8 - d; ++i) x[i] = x[i + d];
   const uint32_t y[5] = {x[0], x[1], x[2], x[3], x[4]};   // (the fifth counts for odd shifts only)
   const RowPiece g = rw_cut(y, from & 1);
-  unsigned short* word = row + c - shift;
-  if ((lane > 0 || shift == 0) && c + 8 - shift <= H) {
-    rw_store(word, g);
-  } else if (c < H || lane > 0) {   // the first word of a piece, and what is left of the row
+  const int c0 = piece * 256, c1 = min(H, c0 + 256);
+  if (c - shift >= c0 && c - shift + 8 <= c1) rw_store(row + c - shift, g);
+  // the elements before the first whole word and behind the last, one a lane: lanes 0 to 7, 8 to 15
+  const int head = shift ? min(from, c1 - c0) : 0, tail = min((c1 + shift) & 7, c1 - c0 - head);
+  const int e = lane < 8 ? lane : c1 - c0 - tail + lane - 8;   // of the piece
+  uint32_t t = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if ((lane > 0 || i >= shift) && c - shift + i < H) word[i] = static_cast<unsigned short>(i & 1 ? g.w[i / 2] >> 16 : g.w[i / 2]);
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t w = __shfl_sync(0xFFFFFFFFu, v.w[q], e >> 3 & 31);
+    if ((e >> 1 & 3) == q) t = w;
   }
-  if (lane == 31 && shift) {   // the last elements of the piece: the next word's first
-#pragma unroll
-    for (int i = 1; i < 8; ++i)
-      if (i >= from && c + i < H) row[c + i] = static_cast<unsigned short>(i & 1 ? v.w[i / 2] >> 16 : v.w[i / 2]);
-  }
+  if (lane < 8 ? lane < head : lane < 8 + tail) row[c0 + e] = static_cast<unsigned short>(e & 1 ? t >> 16 : t);
 }
 
 // A lane's elements of a row of x, zeros past the last.

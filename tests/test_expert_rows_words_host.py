@@ -7,6 +7,7 @@ def put(base, piece, H, values):
     """Elements written for a row that begins at element `base`: {address: value}, by rw_put."""
     shift = base & 7
     start = 8 - shift
+    c0, c1 = piece * 256, min(H, piece * 256 + 256)
     written = {}
 
     def store(at, v):
@@ -26,17 +27,16 @@ def put(base, piece, H, values):
         g = flat[1:9] if start & 1 else flat[:8]
         word = base + c - shift
         assert word % 8 == 0
-        if (lane > 0 or shift == 0) and c + 8 - shift <= H:
+        if c - shift >= c0 and c - shift + 8 <= c1:
             for i in range(8):
                 store(word + i, g[i])
-        elif c < H or lane > 0:
-            for i in range(8):
-                if (lane > 0 or i >= shift) and c - shift + i < H:
-                    store(word + i, g[i])
-        if lane == 31 and shift:
-            for i in range(1, 8):
-                if i >= start and c + i < H:
-                    store(base + c + i, own[lane][i])
+    head = min(start, c1 - c0) if shift else 0
+    tail = min((c1 + shift) & 7, c1 - c0 - head)
+    for lane in range(16):
+        e = lane if lane < 8 else c1 - c0 - tail + lane - 8
+        if lane < head if lane < 8 else lane < 8 + tail:
+            assert 0 <= e < 256
+            store(base + c0 + e, own[e >> 3][e & 7])
     return written
 
 
