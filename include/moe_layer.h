@@ -591,8 +591,10 @@ const char *moe_rows_last_error(const moe_rows *h);
  * (a, b, c) = (3.4445, -4.775, 2.0315) those above some 0.002 come to 0.7 .. 1.2 in five.
  * out is bf16.  Products have fp16 operands (scaled by powers of two, the diagonals of
  * X X^T and of its polynomial apart in fp32, X in two terms where it is multiplied by a
- * alone) and fp32 sums: the error is below that of out's own rounding, some 1e-3 of
- * out's norm for each matrix.  Any finite G: its norm is taken without overflow.  A
+ * alone) and fp32 sums: some 1e-3 of out's norm for each matrix, less than out's own
+ * rounding (nearly singular matrices of a few dozen rows: up to 4e-3).  Elements of X
+ * below 2^-25 / s count as zero (s, the power of two that X is scaled by: 1 to 64, about
+ * the root of the smaller side).  Any finite G: its norm is taken without overflow.  A
  * matrix with a NaN or an infinity becomes NaN, the others of the stack do not.  G = 0
  * gives 0 (with eps = 0: NaN).
  * ------------------------------------------------------------------------- */
