@@ -660,7 +660,8 @@ __device__ __forceinline__ void or_elements(const OrthoStart& A, int z, F&& f) {
 
 // A CTA's share of a matrix's squares, summed in fp32: eight at a time where their sum is far
 // from fp32's ends, else each in one of three ranges (of 2^-40 and 2^40) that is scaled
-// into the middle, so that no square overflows or vanishes.  sums[0..2]: the ranges.
+// so that no square, from 2^-149 to 2^128, vanishes and no sum of 2^30 of them overflows.
+// sums[0..2]: the ranges.
 __device__ __forceinline__ void or_squares(const OrthoStart& A, int z, float (*warps)[3], float* sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float s[3] = {0.0f, 0.0f, 0.0f};
@@ -676,9 +677,9 @@ __device__ __forceinline__ void or_squares(const OrthoStart& A, int z, float (*w
     for (int j = 0; j < 8; ++j) {
       const float x = fabsf(v[j]);
       if (x > 0x1p40f) {
-        s[2] = fmaf(x * 0x1p-60f, x * 0x1p-60f, s[2]);
+        s[2] = fmaf(x * 0x1p-90f, x * 0x1p-90f, s[2]);
       } else if (x < 0x1p-40f) {
-        s[0] = fmaf(x * 0x1p60f, x * 0x1p60f, s[0]);
+        s[0] = fmaf(x * 0x1p85f, x * 0x1p85f, s[0]);
       } else {
         s[1] = fmaf(x, x, s[1]);   // (NaN too)
       }
@@ -724,7 +725,7 @@ __global__ void __launch_bounds__(256) k_ortho_start(const OrthoStart A) {
     for (int i = threadIdx.x; i < A.ctas; i += 32)
 #pragma unroll
       for (int k = 0; k < 3; ++k) t[k] += part[i * 3 + k];
-    double sum = t[0] * 0x1p-120 + t[1] + t[2] * 0x1p120;
+    double sum = t[0] * 0x1p-170 + t[1] + t[2] * 0x1p180;
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
     if (threadIdx.x == 0) {

@@ -4,9 +4,9 @@
 //
 // A pick i = t k + j is token t's j-th expert.  All of it is memory traffic: a token's
 // row is read once and written k times, or k rows are read and one is written, with
-// one multiply-add an element.  So a CTA has one token: its row's pieces of 32 lanes
-// times VEC elements go to the warps in turn, and what a token's k rows have in
-// common (places, weights) is read once a warp and passed by shuffles.
+// one multiply-add an element.  So a CTA has one token at a time: its row's pieces of 256
+// columns go to the warps in turn, and what a token's k rows have in common (places,
+// weights) is read once a warp and passed by shuffles.
 #pragma once
 
 #include "moe_sm103.cuh"

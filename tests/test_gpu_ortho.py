@@ -82,9 +82,10 @@ def test_it_orthogonalises(pkg):
     assert off.abs().max() <= 2 * 2.0 ** -8 + 1e-3
 
 
-@pytest.mark.parametrize("scale", [1e-30, 1e-18, 1e-3, 1e15, 1e34])
+@pytest.mark.parametrize("scale", [1e-41, 1e-30, 1e-18, 1e-3, 1e15, 1e34, 5e37])
 def test_any_magnitude(pkg, scale):
-    g = orf.gradient(70, 90, "fp32", 6, "normal") * (scale * 1e3)
+    g = (orf.gradient(70, 90, "fp32", 6, "normal").double() * (scale * 1e3)).float()   # (1e-41: subnormal numbers)
+    assert torch.isfinite(g).all()
     orf.check(handle(pkg, 70, 90, dtype="fp32", eps=0.0)(g), g, f"{scale}", eps=0.0)
     if scale < 1e-10:    # eps is far above the norm: what is left is small, and linear in the matrix
         got, want = handle(pkg, 70, 90, dtype="fp32")(g), orf.exact(g)
