@@ -29,7 +29,7 @@ def test_shapes(pkg, rows, cols, dtype):
     op = handle(pkg, rows, cols, dtype=dtype)
     g = orf.gradient(rows, cols, dtype, 1)
     orf.check(op(g), g, f"{rows} x {cols}")
-    assert op.device_status() == 0 and op.last_launch_count() == (2 if rows * cols <= 20000 else 3 if rows * cols > 40000 else op.last_launch_count())
+    assert op.device_status() == 0 and op.last_launch_count() == (2 if rows * ((cols + 7) // 8) <= 4096 else 3)
 
 
 @pytest.mark.parametrize("rows,cols", SHAPES)
