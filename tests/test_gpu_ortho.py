@@ -200,6 +200,30 @@ def test_two_handles_on_two_streams(pkg):
         assert all(torch.equal(a, w) for gs, w in zip(got, want) for a in gs)
 
 
+def test_large_matrices_beside_each_other_and_other_work(pkg):
+    """Two handles whose CTAs fill the GPU, on two streams, and products of torch on a third: each
+    launch waits until all of its CTAs are resident, none for the other's."""
+    shapes = [(1500, 4100), (4100, 2050)]
+    ops = [handle(pkg, *s) for s in shapes]
+    g = [orf.gradient(*s, "bf16", i) for i, s in enumerate(shapes)]
+    want = [op(x) for op, x in zip(ops, g)]
+    a = torch.randn(4096, 4096, device="cuda", dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    with torch.cuda.stream(streams[2]):
+        for _ in range(40):
+            b = a @ a
+    got = []
+    for _ in range(6):
+        for op, s, x in zip(ops, streams, g):
+            with torch.cuda.stream(s):
+                got.append(op(x))
+    torch.cuda.synchronize()
+    for i, y in enumerate(got):
+        assert torch.equal(y, want[i % 2])
+    assert torch.isfinite(b).all() and all(op.device_status() == 0 for op in ops)
+
+
 def test_inputs_of_a_given_stream_may_be_dropped(pkg):
     op = handle(pkg, 256, 512)
     g = orf.gradient(256, 512, "bf16", 1)
