@@ -62,7 +62,8 @@ constexpr int OR_THREADS = 384;
 constexpr int OR_EPI_WARPS = 8;
 constexpr int OR_MAX_STAGES = 8;
 constexpr int OR_EPI_BYTES = OR_EPI_WARPS * 8192;   // hi and lo of a warp's next two pieces
-constexpr int OR_BARS = 2 * OR_MAX_STAGES + 9;
+constexpr int OR_STORED = 4;         // units between the epilogue and the warp that counts them, at most
+constexpr int OR_BARS = 2 * OR_MAX_STAGES + 5 + 2 * OR_STORED;
 constexpr int OR_SMEM_MAX = 227 * 1024;
 enum : int { OR_GRAM = 0, OR_POLY = 1, OR_APPLY = 2 };
 
@@ -160,6 +161,20 @@ __device__ __forceinline__ OrthoUnit or_unit(const OrthoArgs& A, int64_t g) {
   return U;
 }
 
+// Where a CTA's unit n stands in the ring of stored units.  Epilogue warps arrive at
+// stored[slot], which completes its phase of `parity`; the warp that counts waits for that
+// and then arrives at taken[slot].  A barrier tells the parity of its phases only, so an
+// epilogue warp that comes to the slot again waits for taken[slot]'s phase before this one:
+// else the counting warp, four units behind, would take a completed phase for one to come.
+struct OrthoSlot {
+  int slot;
+  uint32_t parity;
+  bool again;        // the slot has been used: first wait for taken's phase of parity ^ 1
+};
+__host__ __device__ __forceinline__ OrthoSlot or_slot(uint32_t n) {
+  return OrthoSlot{static_cast<int>(n % OR_STORED), (n / OR_STORED) & 1u, n >= OR_STORED};
+}
+
 // Whether K block k0 of the unit's A or B (TALL: of tall matrices) is an MN-major operand: X where
 // its rows are K, and the tiles of a symmetric matrix that are stored as their transposes.
 template <int CG, bool TALL>
@@ -254,7 +269,7 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
   const int stage_bytes = or_stage_bytes();
   char* epi = base + S * stage_bytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(epi + OR_EPI_BYTES);
-  uint64_t *full = bars, *empty = bars + OR_MAX_STAGES, *accf = bars + 2 * OR_MAX_STAGES, *acce = accf + 2, *drain = acce + 2, *stored = drain + 1;
+  uint64_t *full = bars, *empty = bars + OR_MAX_STAGES, *accf = bars + 2 * OR_MAX_STAGES, *acce = accf + 2, *drain = acce + 2, *stored = drain + 1, *taken = stored + OR_STORED;
   uint32_t* holder = reinterpret_cast<uint32_t*>(bars + OR_BARS);
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
@@ -274,7 +289,10 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
       bar_init(smem_u32(&acce[b]), OR_EPI_WARPS * CG);
     }
     bar_init(smem_u32(drain), 1);
-    for (int i = 0; i < 4; ++i) bar_init(smem_u32(&stored[i]), OR_EPI_WARPS);
+    for (int i = 0; i < OR_STORED; ++i) {
+      bar_init(smem_u32(&stored[i]), OR_EPI_WARPS);
+      bar_init(smem_u32(&taken[i]), 1);
+    }
     bar_fence_init();
   }
   tm_fence_before();
@@ -383,9 +401,13 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
     uint32_t n = 0;
     for (int64_t g = worker; ok && g < units; g += nworkers, ++n) {
       const OrthoUnit U = or_unit<CG>(A, g);
-      if (!wait_long(&stored[n & 3], (n >> 2) & 1)) break;
-      if (lane == 0)
+      const OrthoSlot q = or_slot(n);
+      if (!wait_long(&stored[q.slot], q.parity)) break;
+      __syncwarp();   // (all lanes have seen it)
+      if (lane == 0) {
+        bar_arrive(smem_u32(&taken[q.slot]));
         asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(A.done + U.z * 3 + U.mode), "n"(OR_EPI_WARPS) : "memory");
+      }
       __syncwarp();
     }
   } else if (warp >= 4) {
@@ -578,7 +600,10 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
       // once warp 3 has said so
       asm volatile("fence.proxy.async.global;" ::: "memory");
       __syncwarp();
-      if (lane == 0) bar_arrive(smem_u32(&stored[n & 3]));
+      const OrthoSlot q = or_slot(n);
+      if (q.again && !wait(&taken[q.slot], q.parity ^ 1u)) break;
+      __syncwarp();
+      if (lane == 0) bar_arrive(smem_u32(&stored[q.slot]));
     }
   }
   tm_fence_before();
