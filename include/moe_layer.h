@@ -593,8 +593,8 @@ const char *moe_rows_last_error(const moe_rows *h);
  * X X^T and of its polynomial apart in fp32, X in two terms where it is multiplied by a
  * alone) and fp32 sums: some 1e-3 of out's norm for each matrix, less than out's own
  * rounding (nearly singular matrices of a few dozen rows: up to 4e-3).  Elements of X
- * below 2^-25 / s count as zero (s, the power of two that X is scaled by: 1 to 64, about
- * the root of the smaller side).  Any finite G: its norm is taken without overflow.  A
+ * below 2^-36 / s count as zero, in the products those below 2^-25 / s (s, the power of two
+ * that X is scaled by: 1 to 64, about the root of the smaller side).  Any finite G: its norm is taken without overflow.  A
  * matrix with a NaN or an infinity becomes NaN, the others of the stack do not.  G = 0
  * gives 0 (with eps = 0: NaN).
  * ------------------------------------------------------------------------- */

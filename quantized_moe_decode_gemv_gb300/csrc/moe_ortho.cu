@@ -288,6 +288,7 @@ moe_status forward(moe_ortho* h, const void* g, int64_t ldg, int64_t step_g, int
   a.e = h->e;
   a.step_diag = h->ld_a;
   a.ka = c.a;
+  a.ka_lo = c.a / OR_LO;
   a.kb = c.b;
   a.kc = static_cast<float>(c.c / (scale * scale));
   a.inv_s = static_cast<float>(1.0 / scale);

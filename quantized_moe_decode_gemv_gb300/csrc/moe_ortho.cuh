@@ -17,9 +17,12 @@
 //     in the epilogue.  Near the fixed point A is close to a multiple of 1, so the
 //     diagonal is most of A's norm, and of its rounding: with it in fp16 the error of a
 //     full-rank matrix was 1.5 to 1.7e-3, without 1.0 to 1.2e-3.
-//   - X is kept as two fp16 terms, hi + lo.  Products take hi, the linear term a X both:
+//   - X is kept as two fp16 terms, hi + 2^-11 lo.  Products take hi, the linear term a X both:
 //     what rounding leaves of X lies in directions that X itself may not have, where p
-//     multiplies by a = 3.4 a step; without lo a gradient of 9 tokens was off by 4e-2.
+//     multiplies by a = 3.4 a step; without lo a gradient of 9 tokens was off by 4e-2.  lo is
+//     stored 2^11 times larger, as large as hi: at its own size it would be among fp16's
+//     subnormal numbers and end at 2^-24 (9 tokens, 64 x 8192, eight steps: off by 1.1e-2, this
+//     way 1.4e-3).
 //
 // All steps are one launch (k_ortho).  The tiles of all products, (group of matrices, step,
 // product, matrix, tile), are one list that CTAs (pairs, for 256 x 256 tiles) take in turn; a tile waits
@@ -65,6 +68,7 @@ constexpr int OR_EPI_BYTES = OR_EPI_WARPS * 8192;   // hi and lo of a warp's nex
 constexpr int OR_STORED = 4;         // units between the epilogue and the warp that counts them, at most
 constexpr int OR_BARS = 2 * OR_MAX_STAGES + 5 + 2 * OR_STORED;
 constexpr int OR_SMEM_MAX = 227 * 1024;
+constexpr float OR_LO = 2048.0f;     // X = hi + lo / OR_LO: fp16 has 11 bits
 enum : int { OR_GRAM = 0, OR_POLY = 1, OR_APPLY = 2 };
 
 // A product of every step: output rows and columns, tiles of a matrix, K blocks and their
@@ -81,7 +85,7 @@ struct OrthoArgs {
   OrthoPhase ph[3];
   int steps, matrices, group;   // matrices that go through the steps together
   int stages;               // slots of the ring, a K block each
-  unsigned short* lo;       // X's second term in pieces of 32 x 32, a lane's 16-byte words side by side
+  unsigned short* lo;       // X's second term (times OR_LO) in pieces of 32 x 32, a lane's 16-byte words side by side
   int64_t step_lo;
   int cols_lo;              // pieces in a row of them
   float *d, *e;             // the diagonals
@@ -92,6 +96,7 @@ struct OrthoArgs {
   int64_t ld_out, step_out;
   int vec_out;              // their rows take 32-byte stores
   float ka, kb, kc, inv_s2;   // a, b, c / s^2, 1 / s^2
+  float ka_lo;                // a / OR_LO
   float inv_s;
   unsigned* done;           // [matrix][3]: epilogue warps that are through with a unit of each product
   int* status;
@@ -534,7 +539,7 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               const float e = TALL ? __shfl_sync(0xFFFFFFFFu, d_col, j) : d_row;
-              v[j] = fmaf(A.ka + e, or_value(hi, j), fmaf(A.ka, or_value(lo, j), A.inv_s2 * r[j]));
+              v[j] = fmaf(A.ka + e, or_value(hi, j), fmaf(A.ka_lo, or_value(lo, j), A.inv_s2 * r[j]));
             }
           }
         }
@@ -568,7 +573,7 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
         } else if (!final) {
           if (in) or_store(A.x[(U.step + 1) & 1] + at_x + lane * A.ld_x + col0, w);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] -= or_value(w, j);
+          for (int j = 0; j < 32; ++j) v[j] = OR_LO * (v[j] - or_value(w, j));
           or_pack(v, DT_FP16, w);
           or_save(lo_pieces + half * 1024 + i * 2048, w, lane);
         } else if (!staged) {
@@ -736,7 +741,7 @@ __global__ void __launch_bounds__(256) k_ortho_norm(const OrthoStart A) {
   or_squares(A, blockIdx.y, warps, A.part + (static_cast<int64_t>(blockIdx.y) * OR_NORM_CTAS + blockIdx.x) * 3);
 }
 
-// X = hi + lo in fp16.  Every CTA adds the matrix's partial sums in order (one that has the
+// X = hi + lo / OR_LO in fp16.  Every CTA adds the matrix's partial sums in order (one that has the
 // matrix alone makes them); the factor s / (|G| + eps) is applied as two, so that it has
 // 64-bit numbers' range.
 __global__ void __launch_bounds__(256) k_ortho_start(const OrthoStart A) {
@@ -783,7 +788,7 @@ __global__ void __launch_bounds__(256) k_ortho_start(const OrthoStart A) {
     for (int j = 0; j < 4; ++j) {
       const float a = v[2 * j] * f0 * f1, b = v[2 * j + 1] * f0 * f1;
       h[j] = pack2(a, b, DT_FP16);
-      l[j] = pack2(a - lo16(h[j], DT_FP16), b - hi16(h[j], DT_FP16), DT_FP16);
+      l[j] = pack2(OR_LO * (a - lo16(h[j], DT_FP16)), OR_LO * (b - hi16(h[j], DT_FP16)), DT_FP16);
     }
     *reinterpret_cast<uint4*>(A.hi + z * A.step_x + row * A.ld_x + col) = make_uint4(h[0], h[1], h[2], h[3]);   // (rows are padded to 32 elements)
     unsigned short* p = A.lo + z * A.step_lo + (static_cast<int64_t>(row >> 5) * A.cols_lo + (col >> 5)) * 1024 +
