@@ -603,7 +603,8 @@ typedef struct moe_ortho_config {
   int32_t dtype;          /* BF16|FP16|FP32: G */
   int32_t steps;          /* 1..64 */
   int32_t max_matrices;   /* largest n of a call, >= 1 */
-  float a, b, c;          /* finite, such that no singular value of 0..1 grows above 4 */
+  float a, b, c;          /* finite, such that no singular value of 0..1 grows above 4, nor one
+                             that is 2^-9 too large in each step */
   float eps;              /* >= 0 */
 } moe_ortho_config;
 
@@ -612,7 +613,8 @@ typedef struct moe_ortho moe_ortho;
 /* MOE_ERR_INVALID_ARG: null cfg, sizes or steps < 1, unknown dtype, coefficients or
  * eps not finite, eps < 0.  MOE_ERR_UNSUPPORTED: rows or cols > 32768, steps > 64, more
  * than 2^24 tiles of 128 x 128 in all matrices, coefficients that let a singular value
- * of 0..1 grow above 4 (or |b l + c l^2|, l its square, above 64). */
+ * of 0..1, or 2^-9 above in each step (rounding), grow above 4 (or |b l + c l^2|, l its
+ * square, above 64). */
 moe_status moe_ortho_validate(const moe_ortho_config *cfg);
 /* Create on the current CUDA device: a workspace of about 6 bytes an element of G and
  * 4 an element of G G^T (of the smaller side), for max_matrices of them.  Synchronises the device, so not

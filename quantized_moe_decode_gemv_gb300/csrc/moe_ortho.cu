@@ -39,13 +39,17 @@ constexpr int kMaxSteps = 64;
 int arrived_of(int sms) { return 3 * sms * OR_EPI_WARPS; }
 
 // The largest |singular value| and |b l + c l^2| (l its square) that the steps can
-// reach from singular values in [0, 1].  Each step maps [0, top] by p on a grid.
+// reach from singular values in [0, 1].  Each step maps [0, top] by p on a grid.  Rounding may
+// leave a singular value above the largest that the definition has, by less than 2^-9 of
+// it a step (hi, O and P by 2^-11 each), and where p repels from there the next steps take it away: with
+// (2.5, -3.5, 2), p(1) = 1 and p'(1) = 2, a matrix of rank one went to infinity in 30 steps.
+constexpr double kRounding = 1.0 / 512;
 struct Reach {
   double x = 1.0, b = 0.0;
 };
 Reach reach(const moe_ortho_config& c) {
   Reach R;
-  double top = 1.0;
+  double top = 1.0 + kRounding;
   for (int i = 0; i < c.steps && top < 64.0; ++i) {
     double next = 0.0;
     for (int j = 0; j <= 2048; ++j) {
@@ -54,7 +58,7 @@ Reach reach(const moe_ortho_config& c) {
       R.b = std::max(R.b, std::fabs(b));
     }
     R.x = std::max(R.x, next);
-    top = next;
+    top = next * (1.0 + kRounding);
   }
   return R;
 }
