@@ -591,10 +591,23 @@ const char *moe_rows_last_error(const moe_rows *h);
  * (a, b, c) = (3.4445, -4.775, 2.0315) those above some 0.002 come to 0.7 .. 1.2 in five.
  * out is bf16.  Products have fp16 operands (scaled by powers of two, the diagonals of
  * X X^T and of its polynomial apart in fp32, X in two terms where it is multiplied by a
- * alone) and fp32 sums: some 1e-3 of out's norm for each matrix, less than out's own
- * rounding (nearly singular matrices of a few dozen rows: up to 4e-3).  Elements of X
- * below 2^-36 / s count as zero, in the products those below 2^-25 / s (s, the power of two
- * that X is scaled by: 1 to 64, about the root of the smaller side).  Any finite G: its norm is taken without overflow.  A
+ * alone) and fp32 sums; there is no slower form with more bits.  Off by, as a share of
+ * out's norm for each matrix (out's own rounding is 1.7e-3 of it, and in all of these):
+ *
+ *   with the coefficients above, smaller side 64 and more: about 2e-3 in five steps, 3e-3
+ *     in eight; they never settle, so that each step multiplies the errors of the last
+ *   the same, any smaller side from 16 on: up to 4e-3 in five steps, 5e-3 in six, 8e-3 in
+ *     eight, 3e-2 in twelve, 0.2 in any number
+ *   the same, smaller side below 16, where few errors average: up to eight times that, 0.5
+ *     in any number, about 3e-3 for most matrices
+ *   coefficients that settle at 1 ((1.5, -0.5, 0), (2, -1.5, 0.5)): up to 4e-3 in any number
+ *     of steps (8e-3 below 16)
+ *   in each case besides, where G has fewer directions than its smaller side: up to
+ *     |a|^steps 2^-22 (5e-3 in eight steps of the above, 6e-2 in ten, 0.7 in twelve: what
+ *     rounding leaves in the others is multiplied by a in each, as in any 32-bit form)
+ *
+ * Elements of X below 2^-36 / s count as zero, in the products those below 2^-25 / s (s, the
+ * power of two that X is scaled by: 1 to 64, about the root of the smaller side).  Any finite G: its norm is taken without overflow.  A
  * matrix with a NaN or an infinity becomes NaN, the others of the stack do not.  G = 0
  * gives 0 (with eps = 0: NaN).
  * ------------------------------------------------------------------------- */
