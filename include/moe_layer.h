@@ -629,9 +629,13 @@ typedef struct moe_ortho moe_ortho;
  * of 0..1, or 2^-9 above in each step (rounding), grow above 4 (or |b l + c l^2|, l its
  * square, above 64). */
 moe_status moe_ortho_validate(const moe_ortho_config *cfg);
-/* Create on the current CUDA device: a workspace of about 6 bytes an element of G and
- * 4 an element of G G^T (of the smaller side), for max_matrices of them.  Synchronises the device, so not
- * inside a stream capture. */
+/* Create on the current CUDA device.  The workspace, for max_matrices of them: 6 bytes an
+ * element of G and 4 an element of G G^T (of the smaller side), rows padded to 32 elements (of
+ * 2 of the 6 bytes the columns too); 8 bytes a row of G G^T, 12 a matrix; partial sums of
+ * the norms, 12 bytes for each 8192 elements, at most 12 (8 SMs + max_matrices); and where
+ * a call has too few tiles for the SMs, the partial sums of their K splits, at most 4 bytes x
+ * 128 x 128 x SMs for each of the three products (x 2 where tiles are 256 x 256).
+ * Synchronises the device, so not inside a stream capture. */
 moe_status moe_ortho_create(const moe_ortho_config *cfg, moe_ortho **out);
 
 /* out[n, rows, cols] (bf16) of g[n, rows, cols]; 0 <= n <= max_matrices, n = 0 does

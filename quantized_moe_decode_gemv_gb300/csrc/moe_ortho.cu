@@ -209,9 +209,7 @@ moe_status forward(moe_ortho* h, const void* g, int64_t ldg, int64_t step_g, int
   t.step_g = step_g;
   t.M = c.rows;
   t.N = c.cols;
-  const int64_t pieces = R * ((C + 7) / 8);
-  // (a CTA for up to 32 K elements: a second kernel and its wait would take longer)
-  t.ctas = pieces <= 4096 ? 1 : static_cast<int>(std::min<int64_t>({OR_NORM_CTAS, (pieces + 1023) / 1024, tiles(8ll * h->num_sms, n)}));
+  t.ctas = or_start_ctas(R, C, n, h->num_sms);
   t.part = h->sums;
   t.hi = h->hi[0];
   t.lo = h->lo;
@@ -230,7 +228,7 @@ moe_status forward(moe_ortho* h, const void* g, int64_t ldg, int64_t step_g, int
     const int nz = std::min(n - z, 65535);
     OrthoStart p = t;
     p.g = gp + z * step_g * gb;
-    p.part += static_cast<int64_t>(z) * OR_NORM_CTAS * 3;
+    p.part += static_cast<int64_t>(z) * t.ctas * 3;
     p.hi += z * t.step_x;
     p.lo += z * t.step_lo;
     p.done += 3ll * z;
@@ -364,7 +362,7 @@ moe_status create(const moe_ortho_config* cfg, moe_ortho** out, moe_ortho*& h) {
     if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(p), a);
   for (float** p : {&h->d, &h->e})
     if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(p), n * h->ld_a * 4);
-  if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->sums), n * OR_NORM_CTAS * 3 * 4);
+  if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->sums), static_cast<size_t>(or_norm_parts(c.rows, c.cols, c.max_matrices, sms)) * 3 * 4);
   if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->done), n * 3 * 4);
   if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->arrived), static_cast<size_t>(arrived_of(sms)) * 4);
   for (int cg = 1; cg <= 2 && e == cudaSuccess; ++cg) {

@@ -626,12 +626,28 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
 
 constexpr int OR_NORM_CTAS = 608;   // partial sums of a matrix at most
 
+// CTAs of each of n matrices of R x C for the norm and the start: one for up to 32 K elements (a second
+// kernel and its wait would take longer), else one for 8 K, up to eight an SM in all.
+__host__ __device__ inline int or_start_ctas(int64_t R, int64_t C, int64_t n, int sms) {
+  const int64_t pieces = R * ((C + 7) / 8);
+  if (pieces <= 4096) return 1;
+  int64_t c = (pieces + 1023) / 1024;
+  if (c > (8ll * sms + n - 1) / n) c = (8ll * sms + n - 1) / n;
+  return static_cast<int>(c < OR_NORM_CTAS ? c : OR_NORM_CTAS);
+}
+// Partial sums that calls of up to n matrices need room for: n of them take n times ceil(8 SMs / n) at most.
+__host__ __device__ inline int64_t or_norm_parts(int64_t R, int64_t C, int64_t n, int sms) {
+  const int64_t most = or_start_ctas(R, C, 1, sms);
+  if (most == 1) return 1;   // the start makes its own
+  return n * most < 8ll * sms + n ? n * most : 8ll * sms + n;
+}
+
 struct OrthoStart {
   const void* g;
   int dt;                   // moe_dtype of g
   int64_t ldg, step_g;
   int M, N, ctas;           // CTAs a matrix
-  float* part;              // [matrix][OR_NORM_CTAS][3]
+  float* part;              // [matrix][ctas][3]
   unsigned short* hi;       // X as the tensor copies read it
   int64_t ld_x, step_x;
   unsigned short* lo;       // and its second term, in pieces
@@ -738,7 +754,7 @@ __global__ void __launch_bounds__(256) k_ortho_norm(const OrthoStart A) {
   __shared__ float warps[8][3];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  or_squares(A, blockIdx.y, warps, A.part + (static_cast<int64_t>(blockIdx.y) * OR_NORM_CTAS + blockIdx.x) * 3);
+  or_squares(A, blockIdx.y, warps, A.part + (static_cast<int64_t>(blockIdx.y) * A.ctas + blockIdx.x) * 3);
 }
 
 // X = hi + lo / OR_LO in fp16.  Every CTA adds the matrix's partial sums in order (one that has the
@@ -754,7 +770,7 @@ __global__ void __launch_bounds__(256) k_ortho_start(const OrthoStart A) {
     __syncthreads();
   }
   if (threadIdx.x < 32) {
-    const float* part = A.ctas == 1 ? alone : A.part + static_cast<int64_t>(z) * OR_NORM_CTAS * 3;
+    const float* part = A.ctas == 1 ? alone : A.part + static_cast<int64_t>(z) * A.ctas * 3;
     double t[3] = {0.0, 0.0, 0.0};
     for (int i = threadIdx.x; i < A.ctas; i += 32)
 #pragma unroll
