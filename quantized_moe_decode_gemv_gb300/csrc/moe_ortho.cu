@@ -1,5 +1,5 @@
 // Orthogonalised updates (moe_ortho_* in include/moe_layer.h): host side and C ABI.
-#include "moe_ortho.cuh"
+#include "moe_ortho_plan.h"
 
 #include <cuda_runtime.h>
 
@@ -35,8 +35,6 @@ thread_local std::string g_error;
 
 constexpr int kMaxSide = 32768;
 constexpr int kMaxSteps = 64;
-// counters of split tiles: K is split where all splits run at once
-int arrived_of(int sms) { return 3 * sms * OR_EPI_WARPS; }
 
 // The largest |singular value| and |b l + c l^2| (l its square) that the steps can
 // reach from singular values in [0, 1].  Each step maps [0, top] by p on a grid.  Rounding may
@@ -72,8 +70,6 @@ int scale_of(const moe_ortho_config& c, const Reach& R) {
   return q;
 }
 
-int64_t tiles(int64_t n, int side) { return (n + side - 1) / side; }
-
 moe_status validate(const moe_ortho_config* c, std::string* why) {
   auto fail = [&](moe_status s, const char* msg) {
     *why = msg;
@@ -87,7 +83,7 @@ moe_status validate(const moe_ortho_config* c, std::string* why) {
     return fail(MOE_ERR_INVALID_ARG, "the coefficients and eps must be finite, eps not negative");
   if (c->rows > kMaxSide || c->cols > kMaxSide) return fail(MOE_ERR_UNSUPPORTED, "rows or cols above 32768");
   if (c->steps > kMaxSteps) return fail(MOE_ERR_UNSUPPORTED, "steps above 64");
-  if (tiles(c->rows, 128) * tiles(c->cols, 128) * c->max_matrices > (1 << 24))
+  if (or_parts(c->rows, 128) * or_parts(c->cols, 128) * c->max_matrices > (1 << 24))
     return fail(MOE_ERR_UNSUPPORTED, "more than 2^24 tiles of 128 x 128 in all matrices");
   const Reach R = reach(*c);
   if (R.x > 4.0 || R.b > 64.0) return fail(MOE_ERR_UNSUPPORTED, "the coefficients let singular values of 1 and less grow above 4");
@@ -99,76 +95,6 @@ using Kernel = void (*)(const OrthoArgs);
 Kernel kernel_of(int cg, bool tall) {
   if (tall) return cg == 2 ? k_ortho<2, true> : k_ortho<1, true>;
   return cg == 2 ? k_ortho<2, false> : k_ortho<1, false>;
-}
-
-constexpr int kMaxSplit = 16;
-
-// How n matrices are taken: CTAs of a tile (1: 128 x 128, 2: 256 x 256) and the K splits of
-// the three products.
-struct Plan {
-  int cg = 1;
-  int group = 1;
-  int ks[3] = {1, 1, 1};
-  double clocks = 1e30;
-  int tiles[3], kb[3];
-  size_t part_bytes(int n) const {
-    size_t t = 0;
-    for (int p = 0; p < 3; ++p)
-      if (ks[p] > 1) t += static_cast<size_t>(n) * tiles[p] * ks[p] * cg * or_part_floats(cg) * 4;
-    return t;
-  }
-};
-
-// What a matrix keeps in the L2 while it goes through its steps.
-int64_t resident_bytes(const moe_ortho_config& c) {
-  const int64_t m = std::min(c.rows, c.cols);
-  return 6ll * c.rows * c.cols + 4 * m * m;
-}
-constexpr int64_t kResident = 100ll << 20;   // of 129 MB
-
-// The least estimated time in SM clocks.  A product takes its tiles over the workers (whole
-// rounds of them for one matrix; several matrices' products fill each other's last
-// rounds) times a tile's K blocks, then the way of its last tile to whoever waits for it;
-// a K split adds its partial sums' way through memory.  Measured on 1024 x 4096: a K block
-// of a 128 x 128 tile 440 clocks with all CTAs at work (its bytes; its MMAs take 256), a
-// pair's of 256 x 256 550 (512); joining 4 splits 3.5 us.
-Plan plan_of(const moe_ortho_config& c, int n, const int (&workers)[3]) {
-  Plan best;
-  const int m = std::min(c.rows, c.cols);
-  for (int cg = 1; cg <= 2; ++cg) {
-    Plan p;
-    p.cg = cg;
-    p.clocks = 0.0;
-    const int W = workers[cg];
-    for (int mode = 0; mode < 3; ++mode) {
-      p.tiles[mode] = mode == OR_APPLY ? or_tiles(mode, cg, c.rows, c.cols) : or_tiles(mode, cg, m, m);
-      p.kb[mode] = ((mode == OR_GRAM ? std::max(c.rows, c.cols) : m) + 63) / 64;
-    }
-    // groups: as few as the L2 allows, of about one size, each with two rounds of tiles of its
-    // smaller products, so that a matrix's products finish while others' run (16 of 1856 x
-    // 1024, 250 MB: 605 us in one group of 2.1 rounds, 652 in two of one)
-    const int64_t fit = std::max<int64_t>(kResident / resident_bytes(c), tiles(2 * W, p.tiles[OR_GRAM]));
-    const int64_t groups = tiles(n, static_cast<int>(std::min<int64_t>(fit, n)));
-    p.group = static_cast<int>(tiles(n, static_cast<int>(groups)));
-    for (int mode = 0; mode < 3; ++mode) {
-      const double T = static_cast<double>(p.tiles[mode]) * p.group;
-      double least = 1e30;
-      for (int ks = 1; ks <= kMaxSplit; ++ks) {
-        if (ks > 1 && (groups > 1 || T * ks > W || p.kb[mode] / ks < 2)) break;
-        const double rounds = n > 1 ? std::max(1.0, T * ks / W) : std::ceil(T * ks / W);
-        const double kb = cg == 2 ? 550.0 : 260.0 + 180.0 * std::min(1.0, T * ks / W);
-        const double t = rounds * ((p.kb[mode] + ks - 1) / ks) * kb + (cg == 2 ? 9000.0 : 6000.0) +
-                         (ks > 1 ? (cg == 2 ? 9000.0 : 5000.0) + ks * 300.0 : 0.0);
-        if (t < least) {
-          least = t;
-          p.ks[mode] = ks;
-        }
-      }
-      p.clocks += least * groups;
-    }
-    if (p.clocks < best.clocks) best = p;
-  }
-  return best;
 }
 
 int64_t span(int64_t n, int64_t step, int64_t rows, int64_t ld, int64_t cols) { return (n - 1) * step + (rows - 1) * ld + cols; }
@@ -222,7 +148,7 @@ moe_status forward(moe_ortho* h, const void* g, int64_t ldg, int64_t step_g, int
   t.eps = c.eps;
   t.done = h->done;
   t.arrived = h->arrived;
-  t.n_arrived = arrived_of(h->num_sms);
+  t.n_arrived = ortho_counters(h->num_sms);
   cudaError_t e = cudaSuccess;
   for (int z = 0; z < n && e == cudaSuccess; z += 65535) {   // (a grid's second dimension)
     const int nz = std::min(n - z, 65535);
@@ -241,7 +167,7 @@ moe_status forward(moe_ortho* h, const void* g, int64_t ldg, int64_t step_g, int
     ++h->last_launches;
   }
 
-  const Plan P = plan_of(c, n, h->workers);
+  const OrthoPlan P = ortho_plan(c.rows, c.cols, n, h->workers);
   OrthoArgs a{};
   for (int i = 0; i < 2; ++i) {
     a.tx[i] = h->tx[i];
@@ -259,28 +185,8 @@ moe_status forward(moe_ortho* h, const void* g, int64_t ldg, int64_t step_g, int
   a.ld_out = ldo;
   a.step_out = step_o;
   a.vec_out = reinterpret_cast<uintptr_t>(out) % 32 == 0 && ldo % 16 == 0 && step_o % 16 == 0;
-  float* part = h->part;
-  unsigned* arrived = h->arrived;
-  int64_t units = 0;
-  for (int p = 0; p < 3; ++p) {
-    OrthoPhase& f = a.ph[p];
-    f.M = p == OR_APPLY ? c.rows : m;
-    f.N = p == OR_APPLY ? c.cols : m;
-    f.tiles = P.tiles[p];
-    f.kb = P.kb[p];
-    f.ks = P.ks[p];
-    const int64_t all = static_cast<int64_t>(P.group) * f.tiles * f.ks;
-    units = std::max(units, all);
-    f.part = part;
-    f.arrived = arrived;
-    if (f.ks > 1) {
-      part += all * P.cg * or_part_floats(P.cg);
-      arrived += n * f.tiles * P.cg * OR_EPI_WARPS;
-    }
-  }
+  const int busy = ortho_phases(P, c.rows, c.cols, n, h->workers, h->part, h->arrived, &a);
   a.steps = c.steps;
-  a.matrices = n;
-  a.group = P.group;
   a.stages = OR_MAX_STAGES;
   while (or_smem_bytes(a.stages) > OR_SMEM_MAX) --a.stages;
   a.lo = h->lo;
@@ -300,7 +206,7 @@ moe_status forward(moe_ortho* h, const void* g, int64_t ldg, int64_t step_g, int
   if (e == cudaSuccess) {
     // all CTAs resident at once: they wait for one another
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(units, h->workers[P.cg]) * P.cg));
+    cfg.gridDim = dim3(static_cast<unsigned>(busy * P.cg));
     cfg.blockDim = dim3(OR_THREADS);
     cfg.dynamicSmemBytes = static_cast<size_t>(or_smem_bytes(a.stages));
     cfg.stream = s;
@@ -364,7 +270,7 @@ moe_status create(const moe_ortho_config* cfg, moe_ortho** out, moe_ortho*& h) {
     if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(p), n * h->ld_a * 4);
   if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->sums), static_cast<size_t>(or_norm_parts(c.rows, c.cols, c.max_matrices, sms)) * 3 * 4);
   if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->done), n * 3 * 4);
-  if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->arrived), static_cast<size_t>(arrived_of(sms)) * 4);
+  if (e == cudaSuccess) e = h->alloc(reinterpret_cast<void**>(&h->arrived), static_cast<size_t>(ortho_counters(sms)) * 4);
   for (int cg = 1; cg <= 2 && e == cudaSuccess; ++cg) {
     const Kernel k = kernel_of(cg, h->tall());
     e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize, OR_SMEM_MAX);
@@ -384,7 +290,7 @@ moe_status create(const moe_ortho_config* cfg, moe_ortho** out, moe_ortho*& h) {
     if (e == cudaSuccess && h->workers[cg] < 1) e = cudaErrorInvalidConfiguration;
   }
   for (int i = 1; i <= std::min(c.max_matrices, sms) && e == cudaSuccess; ++i)   // (more matrices: no splits)
-    h->part_bytes = std::max(h->part_bytes, plan_of(c, i, h->workers).part_bytes(i));
+    h->part_bytes = std::max(h->part_bytes, ortho_plan(c.rows, c.cols, i, h->workers).part_bytes(i));
   if (e == cudaSuccess && h->part_bytes) e = h->alloc(reinterpret_cast<void**>(&h->part), h->part_bytes);
   auto rows_of = [&](CUtensorMap* map, const void* p, int64_t cols, int64_t rows, int64_t ld) {
     return encode_stack16(map, p, cols, rows, ld, c.max_matrices, rows * ld, 64);

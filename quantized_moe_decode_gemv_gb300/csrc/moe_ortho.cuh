@@ -120,12 +120,12 @@ struct OrthoUnit {
 // Unit g of the list: groups, steps, products, matrices, tiles, K splits.  Symmetric: tile
 // rows one after the other, each up to the diagonal; else in groups of 8 tile rows, rows fastest.
 template <int CG>
-__device__ __forceinline__ OrthoUnit or_unit(const OrthoArgs& A, int64_t g) {
+__host__ __device__ __forceinline__ OrthoUnit or_unit(const OrthoArgs& A, int64_t g) {
   constexpr int TS = CG * 128;
   OrthoUnit U;
   const int u0 = A.ph[0].tiles * A.ph[0].ks, u1 = A.ph[1].tiles * A.ph[1].ks, u2 = A.ph[2].tiles * A.ph[2].ks;   // of a matrix
   const int64_t whole = static_cast<int64_t>(u0 + u1 + u2) * A.group * A.steps;
-  const int z0 = static_cast<int>(g / whole) * A.group, nz = min(A.group, A.matrices - z0);
+  const int z0 = static_cast<int>(g / whole) * A.group, nz = A.group < A.matrices - z0 ? A.group : A.matrices - z0;
   g -= g / whole * whole;
   const int per = (u0 + u1 + u2) * nz;
   U.step = static_cast<int>(g / per);
@@ -156,7 +156,7 @@ __device__ __forceinline__ OrthoUnit or_unit(const OrthoArgs& A, int64_t g) {
     U.n0 = j * TS;
   } else {
     const int tm = (P.M + TS - 1) / TS, tn = (P.N + TS - 1) / TS;
-    const int gr = t / (8 * tn), rows = min(8, tm - 8 * gr);
+    const int gr = t / (8 * tn), rows = tm - 8 * gr < 8 ? tm - 8 * gr : 8;
     t -= gr * 8 * tn;
     U.m0 = (8 * gr + t % rows) * TS;
     U.n0 = (t / rows) * TS;
@@ -193,7 +193,7 @@ __device__ __forceinline__ bool or_b_mn(const OrthoUnit& U, int k0) {
 
 // The counter that a unit's inputs are done by, and the value it has to reach.
 template <int CG>
-__device__ __forceinline__ const unsigned* or_needs(const OrthoArgs& A, const OrthoUnit& U, unsigned* count) {
+__host__ __device__ __forceinline__ const unsigned* or_needs(const OrthoArgs& A, const OrthoUnit& U, unsigned* count) {
   const int from = U.mode == OR_GRAM ? OR_APPLY : U.mode - 1;
   const int rounds = U.mode == OR_GRAM ? U.step : U.step + 1;
   *count = static_cast<unsigned>(rounds) * static_cast<unsigned>(A.ph[from].tiles * A.ph[from].ks) * (OR_EPI_WARPS * CG);
