@@ -260,15 +260,68 @@ __device__ __forceinline__ int rw_place(const RowArgs& A, int t, int lane) {
 // 1024, where the traffic alone takes 25.)
 
 // Eight elements from word 0..4 on, `odd`: from its second half.
-__device__ __forceinline__ RowPiece rw_cut(const uint32_t (&x)[5], bool odd) {
+__host__ __device__ __forceinline__ RowPiece rw_cut(const uint32_t (&x)[5], bool odd) {
   RowPiece v;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v.w[i] = odd ? __funnelshift_r(x[i], x[i + 1], 16) : x[i];
+  for (int i = 0; i < 4; ++i) {
+#ifdef __CUDA_ARCH__
+    v.w[i] = odd ? __funnelshift_r(x[i], x[i + 1], 16) : x[i];
+#else
+    v.w[i] = odd ? x[i] >> 16 | x[i + 1] << 16 : x[i];
+#endif
+  }
   return v;
 }
 
 // How many elements into its 16-byte word a row begins.
-__device__ __forceinline__ int rw_shift(const unsigned short* p) { return static_cast<int>((reinterpret_cast<uintptr_t>(p) >> 1) & 7); }
+__host__ __device__ __forceinline__ int rw_shift(const unsigned short* p) { return static_cast<int>((reinterpret_cast<uintptr_t>(p) >> 1) & 7); }
+
+// The 16-byte word that a lane writes: the last `shift` elements of the lane before, then its own.
+__host__ __device__ __forceinline__ RowPiece rw_join(const RowPiece& before, const RowPiece& own, int shift) {
+  uint32_t x[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = before.w[i];
+    x[4 + i] = own.w[i];
+  }
+  // from element 8 - shift of these 16 on: whole words by halves, then the odd element
+  const int from = 8 - shift;
+#pragma unroll
+  for (int d = 4; d > 0; d /= 2)
+    if (from / 2 & d)
+#pragma unroll
+      for (int i = 0; i < 8 - d; ++i) x[i] = x[i + d];
+  const uint32_t y[5] = {x[0], x[1], x[2], x[3], x[4]};   // (the fifth counts for odd shifts only)
+  return rw_cut(y, from & 1);
+}
+
+// Columns c0 .. c1 - 1 of a piece, and how many of them lie before its first whole word and behind the last.
+struct RowEnds {
+  int c0, c1, head, tail;
+};
+__host__ __device__ __forceinline__ RowEnds rw_ends(int piece, int H, int shift) {
+  RowEnds e;
+  e.c0 = piece * 256;
+  e.c1 = min(H, e.c0 + 256);
+  e.head = shift ? min(8 - shift, e.c1 - e.c0) : 0;
+  e.tail = min((e.c1 + shift) & 7, e.c1 - e.c0 - e.head);
+  return e;
+}
+// Whether the word that begins `shift` elements before column c is the piece's own.
+__host__ __device__ __forceinline__ bool rw_whole(const RowEnds& e, int c, int shift) { return c - shift >= e.c0 && c - shift + 8 <= e.c1; }
+// The end element of a lane (lanes 0 to 7: the head, 8 to 15: the tail), counted from c0; whether it has one.
+__host__ __device__ __forceinline__ bool rw_end(const RowEnds& e, int lane, int* at) {
+  *at = lane < 8 ? lane : e.c1 - e.c0 - e.tail + lane - 8;
+  return lane < 8 ? lane < e.head : lane < 8 + e.tail;
+}
+
+// Bytes of the row from the word on that begins `shift` elements before column c (0 and less: none); of them in
+// that word, and what lane 31 takes from the word behind it.
+__host__ __device__ __forceinline__ int rw_left(int c, int shift, int H) { return (H - (c - shift)) * 2; }
+__host__ __device__ __forceinline__ int rw_own_bytes(int left) { return max(0, min(16, left)); }
+__host__ __device__ __forceinline__ int rw_next_bytes(int left, int shift) { return max(0, min(2 * shift, left - 16)); }
+// Where the five words that hold a lane's elements begin in a slot, in bytes.
+__host__ __device__ __forceinline__ int rw_slot_at(int lane, int shift) { return (shift >> 1) * 4 + lane * 16; }
 
 // A piece's elements to `row` (its first column: piece * 256; H columns in all) by the
 // whole warp.
@@ -280,34 +333,21 @@ __device__ __forceinline__ void rw_put(unsigned short* row, int piece, int H, co
     return;
   }
   const int shift = rw_shift(row);
-  // the lane's word of 16 bytes: `shift` elements of the lane before, then its own
-  uint32_t x[8];
+  RowPiece before;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[i] = __shfl_up_sync(0xFFFFFFFFu, v.w[i], 1);
-    x[4 + i] = v.w[i];
-  }
-  // from element 8 - shift of these 16 on: whole words by halves, then the odd element
-  const int from = 8 - shift;
-#pragma unroll
-  for (int d = 4; d > 0; d /= 2)
-    if (from / 2 & d)
-#pragma unroll
-      for (int i = 0; i < 8 - d; ++i) x[i] = x[i + d];
-  const uint32_t y[5] = {x[0], x[1], x[2], x[3], x[4]};   // (the fifth counts for odd shifts only)
-  const RowPiece g = rw_cut(y, from & 1);
-  const int c0 = piece * 256, c1 = min(H, c0 + 256);
-  if (c - shift >= c0 && c - shift + 8 <= c1) rw_store(row + c - shift, g);
-  // the elements before the first whole word and behind the last, one a lane: lanes 0 to 7, 8 to 15
-  const int head = shift ? min(from, c1 - c0) : 0, tail = min((c1 + shift) & 7, c1 - c0 - head);
-  const int e = lane < 8 ? lane : c1 - c0 - tail + lane - 8;   // of the piece
+  for (int i = 0; i < 4; ++i) before.w[i] = __shfl_up_sync(0xFFFFFFFFu, v.w[i], 1);
+  const RowPiece g = rw_join(before, v, shift);
+  const RowEnds ends = rw_ends(piece, H, shift);
+  if (rw_whole(ends, c, shift)) rw_store(row + c - shift, g);
+  int e;
+  const bool has = rw_end(ends, lane, &e);
   uint32_t t = 0;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const uint32_t w = __shfl_sync(0xFFFFFFFFu, v.w[q], e >> 3 & 31);
     if ((e >> 1 & 3) == q) t = w;
   }
-  if (lane < 8 ? lane < head : lane < 8 + tail) row[c0 + e] = static_cast<unsigned short>(e & 1 ? t >> 16 : t);
+  if (has) row[ends.c0 + e] = static_cast<unsigned short>(e & 1 ? t >> 16 : t);
 }
 
 // A lane's elements of a row of x, zeros past the last.
@@ -438,11 +478,11 @@ struct RowStream {
       // shares its word, and nothing behind its last one is read
       const int shift = rw_shift(row);
       const unsigned short* word = row + c - shift;
-      const int left = here ? (A.H - (c - shift)) * 2 : 0;   // bytes of the row from there on
-      const int own = max(0, min(16, left));
+      const int left = here ? rw_left(c, shift, A.H) : 0;
+      const int own = rw_own_bytes(left);
       rw_copy_part(to + static_cast<uint32_t>(lane * 16), own ? word : row - shift, own);
       if (lane == 31) {
-        const int next = max(0, min(2 * shift, left - 16));
+        const int next = rw_next_bytes(left, shift);
         rw_copy_part(to + 512, next ? word + 8 : row - shift, next);
       }
     }
@@ -484,7 +524,7 @@ struct RowStream {
       return v;
     }
     const int shift = rw_shift(row);
-    const uint32_t p = at(s, j) + static_cast<uint32_t>((shift >> 1) * 4 + lane * 16);
+    const uint32_t p = at(s, j) + static_cast<uint32_t>(rw_slot_at(lane, shift));
     uint32_t x[5];
 #pragma unroll
     for (int i = 0; i < 5; ++i) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x[i]) : "r"(p + static_cast<uint32_t>(i * 4)) : "memory");
