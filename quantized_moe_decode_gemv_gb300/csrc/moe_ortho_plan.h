@@ -58,11 +58,14 @@ inline OrthoPlan ortho_plan(int rows, int cols, int n, const int (&workers)[3]) 
       p.tiles[mode] = mode == OR_APPLY ? or_tiles(mode, cg, rows, cols) : or_tiles(mode, cg, m, m);
       p.kb[mode] = ((mode == OR_GRAM ? std::max(rows, cols) : m) + 63) / 64;
     }
-    // groups: as few as the L2 allows, of about one size, each with two rounds of tiles of its
-    // smaller products, so that a matrix's products finish while others' run (16 of 1856 x
-    // 1024, 250 MB: 605 us in one group of 2.1 rounds, 652 in two of one)
+    // groups: of the matrices that the L2 holds, or of two rounds of tiles of the smaller products, so
+    // that a matrix's products finish while others' run.  Up to three groups' worth go as one: no last
+    // round of tiles is paid for between groups.  As groups / as one, us: 16 of 1856 x 1024 (1.0 groups)
+    // 669 / 558, 24 of 1024 x 1024 (1.5) 583 / 541, 40 (2.5) 931 / 895, 12 of 1536 x 1536 (1.5) 734 / 710, 3 of 4096 x
+    // 4096 (1.5) 3100 / 2709; 60 of 1856 x 1024 (3.8) 2189 / 2334, 300 of 640 x 640 (11.5) 2386 / 2892, 2000 of
+    // 256 x 256 (13) 2506 / 2687, 200 of 1024 x 1024 (12.5) 4508 / 4733.
     const int64_t fit = std::max<int64_t>(OR_RESIDENT / or_resident_bytes(rows, cols), or_parts(2 * W, p.tiles[OR_GRAM]));
-    const int64_t groups = or_parts(n, static_cast<int>(std::min<int64_t>(fit, n)));
+    const int64_t groups = n <= 3 * fit ? 1 : or_parts(n, static_cast<int>(fit));
     p.group = static_cast<int>(or_parts(n, static_cast<int>(groups)));
     for (int mode = 0; mode < 3; ++mode) {
       const double T = static_cast<double>(p.tiles[mode]) * p.group;

@@ -23,6 +23,7 @@ SHAPES = [
     (760, 9000, 2), (9001, 755, 2), (1270, 6000, 2),
     (300, 4000, 4), (4000, 300, 4), (130, 1100, 3), (1100, 130, 3), (1030, 520, 2), (520, 1030, 2),
     (1856, 1024, 16), (1024, 1856, 16), (1100, 2100, 19), (2100, 1100, 19), (640, 640, 100), (640, 600, 100),
+    (1100, 1300, 50), (1300, 1100, 50),
 ]
 
 PROGRAM = r"""
