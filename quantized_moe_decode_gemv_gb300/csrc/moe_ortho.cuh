@@ -626,8 +626,11 @@ __global__ void __launch_bounds__(OR_THREADS, 1) k_ortho(const __grid_constant__
 
 constexpr int OR_NORM_CTAS = 608;   // partial sums of a matrix at most
 
-// CTAs of each of n matrices of R x C for the norm and the start: one for up to 32 K elements (a second
-// kernel and its wait would take longer), else one for 8 K, up to eight an SM in all.
+// CTAs of each of n matrices of R x C for the norm and the start: one for up to 32 K elements, in one
+// launch, else one for 8 K, up to eight an SM in all.  One launch / two, one step, us: 64 x 64 15.6 / 15.7, 64 x
+// 256 20.6 / 19.2, 128 x 256 28.4 / 21.8, 64 of 64 x 256 23.9 / 22.3, 256 x 512 69.6 / 23.9: equal
+// at 4 K elements; what one launch costs at 32 K is more than the 2.5 us of the host that it saves.  A CTA for 4 K / 8 K / 16 K elements: 256 x 512
+// 22.5 / 23.9 / 27.1, 1024 x 1024 32.7 / 32.3 / 35.4, 1024 x 4096 51.0 / 50.0 / 50.9.
 __host__ __device__ inline int or_start_ctas(int64_t R, int64_t C, int64_t n, int sms) {
   const int64_t pieces = R * ((C + 7) / 8);
   if (pieces <= 4096) return 1;

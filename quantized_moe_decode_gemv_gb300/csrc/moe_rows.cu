@@ -82,7 +82,10 @@ bool whole_words(std::initializer_list<Rows> all) {
   return bits % 16 == 0;
 }
 
-// A CTA's warps: one for each 256 columns, up to 8; up to 16 where tokens alone do not fill the SMs.
+// A CTA's warps: one for each 256 columns, up to 8; up to 16 where tokens alone do not fill the SMs.  8 / 16
+// warps, 8 rows of 6144, us: 152 tokens, out 3.8 / 3.5, back 4.8 / 4.0, d_y 4.4 / 3.9; 228, 5.1 / 5.0, 5.5 / 6.9, 5.5 /
+// 5.4; 303, 5.4 / 5.3, 7.2 / 7.8, 5.8 / 7.0; 330, 6.9 / 8.4, 7.4 / 9.8, 7.2 / 7.0.  Rows of 2560: 16 up to a third faster
+// until 303 (back 4.5 / 3.4), slower at 330 (4.5 / 4.8).
 int row_warps(int T, int H, int sms) { return std::min((H + 255) / 256, T < 2 * sms ? 16 : 8); }
 
 int small_smem(int E, int P) { return (rw_plan_smem(E) + 15) / 16 * 16 + 4 * P; }
@@ -326,7 +329,7 @@ moe_status combine_backward(moe_rows* h, const void* d_out, int64_t ldd, int32_t
   a.d_w = d_w;
   a.w_dt = w_dtype;
   // Both gradients in one kernel where rows are whole words.  Else cutting and joining words takes
-  // the registers of too many warps: 8192 x 9 x 1001 in one kernel 131 us, in two 57 + 36.
+  // the registers of too many warps: 8192 x 9 x 1001 in one kernel 131 us, in two 57 + 41 (100 one after the other).
   const bool aligned = whole_words({e, in, to}), both = aligned && d_y && d_w;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t err = cudaSuccess;

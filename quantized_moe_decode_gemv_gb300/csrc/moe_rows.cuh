@@ -16,7 +16,12 @@ namespace moe_op {
 constexpr int RW_MAX_K = 16;
 constexpr int RW_MAX_E = 1024;
 constexpr int RW_CHUNK = 1024;           // picks of a CTA of the plan, one a thread
-constexpr int RW_DIRECT_CHUNKS = 128;    // up to so many, every CTA adds the chunks before it by itself
+// Up to so many chunks every CTA of the plan adds those before it by itself; more are added by a kernel of
+// their own.  The kernels alone, by itself / with the kernel, us: 256 experts, 32 chunks 6.4 / 6.6, 64 8.1 / 7.0, 128
+// 11.5 / 8.4; 1024 experts, 32 chunks 8.0 / 8.5, 64 10.8 / 8.9, 128 16.6 / 9.7.  But one launch more takes the
+// host 2.5 us: calls one after the other, plan of 128 chunks 15.0 / 17.4, dispatch to rows of 64
+// columns 96 chunks 23.2 / 24.8, 128 28.9 / 26.2, to rows of 1024 64 30.3 / 30.4, 128 57.0 / 54.6 (496 experts).
+constexpr int RW_DIRECT_CHUNKS = 128;
 
 struct PlanArgs {
   const void* ids;
@@ -253,11 +258,12 @@ __device__ __forceinline__ int rw_place(const RowArgs& A, int t, int lane) {
 //
 // A lane has 8 consecutive elements of a piece as four words.  Where all rows are whole
 // 16-byte words (ALIGNED) it loads and stores just those.  Else rows begin anywhere in a
-// word of 16 bytes: a piece is read as the 33 whole words that hold it, and a lane cuts its
-// elements out of two of them; it is stored as whole words, made of two lanes' elements, with
-// the ends of a piece element by element.  (An element a lane at a time, 8192 tokens of 9
-// rows of 1001 came back in 117 us and went out in 51; 48 and 36 this way, 31 and 25 at
-// 1024, where the traffic alone takes 25.)
+// word of 16 bytes.  Rows that are summed (RowStream: the combine, d_w) are read as the 33 whole
+// words that hold a piece, and a lane cuts its elements out of two of them; a token's row
+// that goes to its k places (rw_get: dispatch, take, d_y) is read element by element, once.  Both are
+// stored as whole words, made of two lanes' elements, with the ends of a piece element by
+// element.  (An element a lane at a time, 8192 tokens of 9 rows of 1001 came back in 117 us
+// and went out in 51; 48 and 35 this way, 31 and 25 at 1024, where the traffic alone takes 25.)
 
 // Eight elements from word 0..4 on, `odd`: from its second half.
 __host__ __device__ __forceinline__ RowPiece rw_cut(const uint32_t (&x)[5], bool odd) {
@@ -350,7 +356,7 @@ __device__ __forceinline__ void rw_put(unsigned short* row, int piece, int H, co
   if (has) row[ends.c0 + e] = static_cast<unsigned short>(e & 1 ? t >> 16 : t);
 }
 
-// A lane's elements of a row of x, zeros past the last.
+// A lane's elements of a token's row, zeros past the last (rows that are not whole words: element by element).
 template <bool ALIGNED>
 __device__ __forceinline__ RowPiece rw_get(const unsigned short* row, int piece, int H, int lane) {
   const int c = (piece * 32 + lane) * 8;
