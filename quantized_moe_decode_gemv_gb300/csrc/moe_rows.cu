@@ -68,10 +68,12 @@ bool clash(std::initializer_list<Range> outs, std::initializer_list<Range> ins) 
   return false;
 }
 
-// Whether rows meet rows in memory.  Column ranges of one buffer may interleave.
+// Whether rows meet rows in memory.  Column ranges of one buffer may interleave; a single row
+// has no stride of its own.
 bool meet(const Rows& a, const Rows& b) {
   if (!overlap(a, b)) return false;
-  return a.ld != b.ld || rows_overlap(a.p, a.ld, a.cols, b.p, b.ld, b.cols, std::max(a.n, b.n));
+  const int64_t lda = a.n > 1 ? a.ld : b.ld, ldb = b.n > 1 ? b.ld : a.ld;
+  return lda != ldb || rows_overlap(a.p, lda, a.cols, b.p, ldb, b.cols, std::max(a.n, b.n));
 }
 
 // Whether all rows are whole 16-byte words.
