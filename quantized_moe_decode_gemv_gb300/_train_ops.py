@@ -22,10 +22,11 @@ def _device_of(torch, device):
     return torch.device("cuda", torch.cuda.current_device()) if device.index is None else device
 
 
-def _create(handle, torch, c) -> None:
-    """Validates the C config and creates the handle on its device."""
+def _create(handle, torch, c, device) -> None:
+    """Validates the C config (before a device is looked for) and creates the handle on its device."""
     status = handle._fn("validate")(ctypes.byref(c))
     if status == MOE_OK:
+        handle.device = _device_of(torch, device)
         h = ctypes.c_void_p()
         with torch.cuda.device(handle.device):
             status = handle._fn("create")(ctypes.byref(c), ctypes.byref(h))
@@ -84,12 +85,7 @@ class ExpertRows(_Handle):
         import torch
         self._setup(torch, load_library())
         self.config = config
-        c = config.to_c()
-        status = self._fn("validate")(ctypes.byref(c))
-        if status != MOE_OK:
-            raise MoEError(status, self._fn("last_error")(None).decode())
-        self.device = _device_of(torch, device)
-        _create(self, torch, c)
+        _create(self, torch, config.to_c(), device)
         self._dtype, self._k, self._E = torch_act_dtype(config.act_dtype), config.top_k, config.n_experts
         self._i32, self._id_bytes = torch.int32, {torch.int32: 4, torch.int64: 8}
         self._w_types = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
@@ -295,12 +291,7 @@ class Orthogonalizer(_Handle):
         import torch
         self._setup(torch, load_library())
         self.config = config
-        c = config.to_c()
-        status = self._fn("validate")(ctypes.byref(c))
-        if status != MOE_OK:
-            raise MoEError(status, self._fn("last_error")(None).decode())
-        self.device = _device_of(torch, device)
-        _create(self, torch, c)
+        _create(self, torch, config.to_c(), device)
         self._dtype = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}[config.dtype]
         self._bf16, self._R, self._C, self._call = torch.bfloat16, config.rows, config.cols, self._lib.moe_ortho_forward
 
