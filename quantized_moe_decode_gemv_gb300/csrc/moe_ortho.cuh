@@ -49,9 +49,9 @@
 // symmetric tiles are stored once.  What a piece reads comes two pieces ahead by the lanes'
 // own asynchronous copies; tensor copies would queue behind those of the ring.
 //
-// Measured, five steps, passes back to back: 8192 x 4096 1.69 ms (1.42 PFLOP/s, the symmetric
-// products counted by halves; power and the tensor pipe), 16 x 1856 x 1024 0.57 to 0.61 ms (the L2: 250
-// MB), 1024 x 4096 186 us and 64 x 256 59 us (fifteen products one after the other).
+// Measured, five steps, passes back to back: 8192 x 4096 1.63 to 1.73 ms (1.39 to 1.48 PFLOP/s, the symmetric
+// products counted by halves; power and the tensor pipe), 16 x 1856 x 1024 0.55 to 0.63 ms (the L2: 250
+// MB), 1024 x 4096 186 us and 64 x 256 60 us (fifteen products one after the other).
 //
 // Every wait is bounded; a role whose wait runs out sets the timeout bit of the status
 // word and winds down.
